@@ -336,6 +336,182 @@ const char *ssu_scan_tile_name(int32_t tile);
  * dividing dim). */
 int32_t ssu_scan_select_tile(const ssu_scan_args *args, int64_t chunk);
 
+/* ------------------------------------------------------- linear attention --
+ * Linear attention with a decay for each head, over whole prompts and for
+ * single tokens, on the decode step's state slots. For every sequence, head h
+ * (group g = h / (nheads / ngroups)) and token t in order:
+ *
+ *   S[p,n]   = S[p,n] * exp(log_decay[t,h]) + beta[t,h] * v[t,h,p] * k[t,g,n]
+ *   out[t,p] = bf16( scale * sum_n S[p,n] * q[t,g,n] )
+ *
+ * S starts from state[idx[b], h] and is written back there after the
+ * sequence's last token. With q = C, k = B, v = x, beta = delta and
+ * log_decay = A * delta this is the recurrence of ssu_update (without D), so a
+ * prompt's state can be advanced by either step afterwards; with
+ * log_decay constant in t (stride 0) it is attention with fixed decay rates.
+ *
+ * Numerics: state, decays, sums and the recurrence in fp32 (the decays'
+ * running sums in fp64, where a sum over many tokens would lose digits). Over
+ * prompts the products run on bf16 matrix instructions with fp32 sums; fp32
+ * operands (the state, decayed v) enter as a bf16 pair (value and remainder,
+ * 2^-17 relative), the scores of a chunk as well, so only the output's own
+ * rounding to bf16 is seen. log_decay below -10000 counts as -10000 (exp is 0
+ * from -104 on), so -inf is a reset of the state; NaN and infinite v reach
+ * their own and later tokens of their channel p only, NaN and infinite k
+ * their own and later tokens, NaN and infinite q their own token.
+ */
+typedef struct ssu_linear_args {
+    int32_t batch;      /* sequences, >= 0 (0: no-op) */
+    int32_t nheads;     /* H >= 1 */
+    int32_t headdim;    /* P: a multiple of 16, 16 <= P <= 256 */
+    int32_t dstate;     /* N: 16, 32, 64, 128 or 256 */
+    int32_t ngroups;    /* G >= 1, divides H */
+    int32_t device;     /* HIP device ordinal that launches run on (made current
+                           for the call, then restored); -1: the current one */
+    int64_t ntokens;    /* T >= 0: rows of q, k, v, log_decay, beta and out */
+    int64_t pool_slots; /* slots in the state pool, >= 0 */
+    float scale;        /* finite */
+    int32_t reserved;   /* must be 0 */
+    ssu_view state;      /* [pool_slots, H, P, N] F32, read and written; stride[3] == 1;
+                            pointer and stride[0..2] 16-byte multiples */
+    ssu_view idx;        /* [batch] I32 or I64, stride[0] == 1; ids outside [0, pool_slots)
+                            are padding: neither state nor out is touched */
+    ssu_view cu_seqlens; /* [batch + 1] I32, stride[0] == 1: sequence b is rows
+                            [cu_seqlens[b], cu_seqlens[b+1]), taken inside [0, T); an empty or
+                            reversed range is an empty sequence. Rows of no sequence
+                            are left untouched in out. ssu_linear_attention_step:
+                            ptr NULL, token b belongs to request b */
+    ssu_view q, k;       /* [T, G, N] BF16, stride[2] == 1 */
+    ssu_view v;          /* [T, H, P] BF16, stride[2] == 1 */
+    ssu_view log_decay;  /* [T, H] F32, any strides >= 0 (0: broadcast) */
+    ssu_view beta;       /* [T, H] F32, any strides >= 0; ptr NULL: 1 */
+    ssu_view out;        /* [T, H, P] BF16, written, stride[2] == 1 */
+    void *workspace;     /* device memory, 16-byte aligned; its contents do not matter
+                            before and after the call */
+    int64_t workspace_bytes;
+} ssu_linear_args;
+
+/* Bytes of workspace that ssu_linear_attention needs for `args` (only its sizes
+ * are read; 0 where none is needed, -1 for sizes that it refuses). */
+int64_t ssu_linear_attention_workspace(const ssu_linear_args *args);
+
+/* Enqueue `args`' prompts on `stream`. In-range ids must be distinct and
+ * cu_seqlens must not decrease (neither is checked on the device: with sequences
+ * that share rows or slots the values there are unspecified, every access
+ * stays inside the views). out, state and workspace must not overlap each
+ * other or any input; calls that may run at the same time need workspaces of
+ * their own. Asynchronous, allocation-free and graph-capturable like
+ * ssu_update.
+ * Errors (nothing is launched): SSU_ERR_INVALID_ARGUMENT (null pointers,
+ * negative sizes or strides, wrong dtype tags, non-zero reserved fields, G not
+ * dividing H, a scale that is not finite, a workspace too small),
+ * SSU_ERR_UNSUPPORTED (P, N, inner strides, more than 2^31 tokens or
+ * workgroups), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
+ssu_status ssu_linear_attention(const ssu_linear_args *args, hipStream_t stream);
+
+/* The same for one token per request: ntokens == batch, token b advances
+ * request b; cu_seqlens.ptr and workspace are NULL. Same errors. */
+ssu_status ssu_linear_attention_step(const ssu_linear_args *args, hipStream_t stream);
+
+/* ------------------------------------------ queries and keys of attention --
+ * Norms of queries and keys for each head with the position rotation, for the
+ * attention layers of hybrid models. Each head row x of q and k [D] becomes
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (no weight: factor 1)
+ *   (y[a], y[b]) = (y[a] c_i - y[b] s_i, y[b] c_i + y[a] s_i),  i < rot / 2
+ *
+ * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved, and c_i, s_i
+ * columns i and rot/2 + i of row positions[t] of cos_sin; values from rot on
+ * are only normed. fp32 throughout, one rounding (to nearest even) at the end.
+ * With k_cache and v_cache, token t's keys and values also go into row
+ * slots[t] of a paged cache (page slots[t] / page_size, row slots[t] %
+ * page_size); slots outside the cache are skipped. A token whose position is
+ * outside [0, max_pos) is padding: nothing of it is read or written.
+ */
+typedef struct ssu_qk_args {
+    int64_t ntokens;     /* T >= 0 (0: no-op) */
+    int32_t nq, nk;      /* heads of q (>= 0) and of k (>= 0) */
+    int32_t headdim;     /* D, 1 <= D <= 512 */
+    int32_t rot;         /* even, 0 <= rot <= D (0: norm only) */
+    int32_t interleaved; /* 1 or 0 */
+    int32_t device;      /* as in ssu_linear_args */
+    float eps;           /* >= 0, finite */
+    int32_t page_size;   /* rows of a page, >= 1 (with k_cache) */
+    int64_t max_pos;     /* rows of cos_sin, >= 0 */
+    int64_t num_pages;   /* pages of the caches, >= 0 */
+    ssu_view q, k;       /* [T, nq | nk, D] BF16 or F16, the same for all 16-bit views; stride[2] == 1 */
+    ssu_view q_weight, k_weight; /* [D] F32 or the 16-bit type, stride[0] == 1; ptr NULL: 1 */
+    ssu_view positions;  /* [T] I32 or I64, stride[0] == 1 */
+    ssu_view cos_sin;    /* [max_pos, rot] F32, stride[1] == 1 */
+    ssu_view q_out;      /* [T, nq, D] written, stride[2] == 1; may be q itself */
+    ssu_view k_out;      /* [T, nk, D] written, stride[2] == 1; may be k itself; ptr NULL with
+                            k_cache: keys go to the cache only */
+    ssu_view v;          /* [T, nk, D], stride[2] == 1 (with k_cache) */
+    ssu_view k_cache, v_cache; /* [num_pages, page_size, nk, D] written, stride[3] == 1; both
+                            or neither (ptr NULL) */
+    ssu_view slots;      /* [T] I32 or I64, stride[0] == 1 (with k_cache); in-range slots distinct */
+} ssu_qk_args;
+
+/* Enqueue it on `stream`. Outputs must not overlap inputs or each other, but
+ * q_out may be q and k_out may be k (same pointer and strides). Asynchronous,
+ * allocation-free, graph-capturable. Errors (nothing is launched):
+ * SSU_ERR_INVALID_ARGUMENT (null pointers, sizes, strides, dtype tags),
+ * SSU_ERR_UNSUPPORTED (D > 512, inner strides, more than 2^31 workgroups),
+ * SSU_ERR_MISALIGNED (elements not aligned to their size), SSU_ERR_HIP. */
+ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stream);
+
+/* -------------------------------------------------------- paged attention --
+ * Attention of one new token per request over a paged key-value cache, split
+ * over the cache's length and joined. For request b and query head h, with
+ * K_j, V_j row j % page_size of page block_table[b, j / page_size], head
+ * h / (nq / nk), and n = min(seq_lens[b], max_pages * page_size):
+ *
+ *   w_j = exp(scale q[b,h] . K_j - m),  m = max_j (...)       j < n
+ *   out[b,h] = sum_j w_j V_j / sum_j w_j
+ *   lse[b,h] = m + log(sum_j w_j)
+ *
+ * No visible token, or only scores of -inf: out 0, lse -inf. A negative seq_lens[b] marks a padding
+ * request, whose out and lse are left untouched. Tokens of a page id outside
+ * [0, num_pages) are not visible. fp32 scores, statistics and sums; the
+ * weights w_j enter the product with V as a 16-bit pair (value and
+ * remainder), so that only the output's own rounding is seen. What the cache
+ * holds in rows that no request sees, NaN and infinities too, does not matter.
+ * Results do not depend on other requests of the batch, but on its size and
+ * on max_pages within rounding (they set the split).
+ */
+typedef struct ssu_attn_args {
+    int32_t batch;       /* >= 0 (0: no-op) */
+    int32_t nq, nk;      /* query and key/value heads, nk >= 1 divides nq */
+    int32_t headdim;     /* D: 64, 128 or 256 */
+    int32_t page_size;   /* >= 1 */
+    int32_t device;      /* as in ssu_linear_args */
+    int64_t num_pages;   /* pages of the caches, >= 0 */
+    int64_t max_pages;   /* columns of block_table, >= 0 */
+    float scale;         /* finite */
+    int32_t reserved;    /* must be 0 */
+    ssu_view q;          /* [batch, nq, D] BF16 or F16, stride[2] == 1 */
+    ssu_view k_cache, v_cache; /* [num_pages, page_size, nk, D], q's type, stride[3] == 1 */
+    ssu_view block_table; /* [batch, max_pages] I32, stride[1] == 1 */
+    ssu_view seq_lens;   /* [batch] I32, stride[0] == 1 */
+    ssu_view out;        /* [batch, nq, D] q's type, written, stride[2] == 1 */
+    ssu_view lse;        /* [batch, nq] F32, written; ptr NULL: not wanted */
+    void *workspace;     /* device memory, 16-byte aligned; contents do not matter */
+    int64_t workspace_bytes;
+} ssu_attn_args;
+
+/* Bytes of workspace that ssu_paged_attention needs for `args` (only its sizes
+ * are read; 0 where none is needed, -1 for sizes that it refuses). */
+int64_t ssu_paged_attention_workspace(const ssu_attn_args *args);
+
+/* Enqueue it on `stream`. Rows of 16-byte multiples (pointers and strides) are
+ * read fastest; elements aligned to their size are enough. out, lse and workspace must not overlap each other or any input; calls that
+ * may run at the same time need workspaces of their own. Asynchronous,
+ * allocation-free, graph-capturable. Errors (nothing is launched):
+ * SSU_ERR_INVALID_ARGUMENT (null pointers, sizes, strides, dtype tags, a
+ * workspace too small), SSU_ERR_UNSUPPORTED (D, inner strides, more than 2^31
+ * workgroups), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
+ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream);
+
 /* SSU_ABI_VERSION of the built library. */
 int32_t ssu_abi_version(void);
 

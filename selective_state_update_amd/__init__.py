@@ -17,11 +17,19 @@ per head. Per request b and head h:
     delta = softplus(dt + dt_bias);  a = exp(A * delta)
     state[idx[b], h] = state[idx[b], h] * a + delta * outer(x[b, h], B[b, g])
     out[b, h] = state[idx[b], h] @ C[b, g] + D * x[b, h]      (bf16)
+
+Beside it: several tokens per call, state-block copies and the prefill scan,
+and the sequence operators of the layers around it in hybrid models: linear
+attention with a decay per head on the same state slots (linear_attention over
+prompts, linear_attention_step for single tokens), queries' and keys' norms and
+rotation (qk_norm_rope, also into a paged cache) and attention of one new token
+over that cache (paged_attention).
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -37,6 +45,10 @@ __all__ = [
     "scan_launch",
     "scan_select_tile",
     "scan_tiles",
+    "linear_attention",
+    "linear_attention_step",
+    "qk_norm_rope",
+    "paged_attention",
     "tile_fits",
     "tiles",
     "library_path",
@@ -152,6 +164,12 @@ _lib.ssu_scan_tile_name.argtypes = [_i32]
 _lib.ssu_scan_tile_name.restype = ctypes.c_char_p
 _lib.ssu_scan_select_tile.argtypes = [ctypes.POINTER(ScanArgs), _i64]
 _lib.ssu_scan_select_tile.restype = _i32
+for _name in ("ssu_linear_attention", "ssu_linear_attention_step", "ssu_qk_norm_rope", "ssu_paged_attention"):
+    getattr(_lib, _name).argtypes = [_vp, _vp]
+    getattr(_lib, _name).restype = _i32
+for _name in ("ssu_linear_attention_workspace", "ssu_paged_attention_workspace"):
+    getattr(_lib, _name).argtypes = [_vp]
+    getattr(_lib, _name).restype = _i64
 _lib.ssu_abi_version.argtypes = []
 _lib.ssu_abi_version.restype = _i32
 
@@ -563,3 +581,240 @@ def selective_scan(u, delta, A, B, C, state, D=None, delta_bias=None, delta_soft
     args, out = make_scan_args(u, delta, A, B, C, state, D, delta_bias, delta_softplus, out)
     scan_launch(args, chunk, tile, stream, u.device)
     return out
+
+
+# --------------------------------------------------------------------------- #
+# Sequence operators of hybrid models: ssu_linear_attention(_step),
+# ssu_qk_norm_rope, ssu_paged_attention
+# --------------------------------------------------------------------------- #
+# The arguments' structs as include/ssu.h declares them, packed in one go (a
+# struct field at a time, ctypes takes longer than the smallest calls run).
+_VIEW = "Qii4q"  # ptr, dtype, reserved, strides
+_LINEAR_ARGS = struct.Struct("6i2qfi" + _VIEW * 9 + "Qq")
+_QK_ARGS = struct.Struct("q6ifi2q" + _VIEW * 12)
+_ATTN_ARGS = struct.Struct("6i2qfi" + _VIEW * 7 + "Qq")
+_NO_VIEW = (0, 0, 0, 0, 0, 0, 0)
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+_TAGS = {torch.float32: SSU_F32, torch.bfloat16: SSU_BF16, torch.int32: SSU_I32, torch.int64: SSU_I64,
+         torch.float16: SSU_F16}
+_HALF = (torch.bfloat16, torch.float16)
+_INTS = (torch.int32, torch.int64)
+
+
+def _take(t, name, shape, dtypes, device):
+    """The view fields of tensor ``t`` after checking its shape, dtype and device."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    dtype = t.dtype
+    if dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {dtype} not supported here")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    s = t.stride()
+    return (t.data_ptr(), _TAGS[dtype], 0) + s + _PAD[len(s)]
+
+
+def _inference_only(*tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("inference only: no gradient is recorded; call under torch.no_grad() or detach the inputs")
+
+
+def _gpu_of(t, name):
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU")
+    return device
+
+
+class _On:
+    """Where a call runs: its stream's handle, and memory for it that the
+    caching allocator hands out for that stream."""
+
+    def __init__(self, stream, device):
+        self.device = device
+        self.stream = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.stream = (stream if hasattr(stream, "cuda_stream")
+                           else torch.cuda.ExternalStream(int(stream), device=device))
+            self.handle = self.stream.cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _workspace(given, need, on):
+    """(tensor, pointer, bytes) of a call's workspace: the caller's, or a new one."""
+    if given is not None:
+        if given.device != on.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous, on {on.device}")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if need <= 0:
+        return None, 0, 0
+    ws = on.empty((need,), torch.uint8)
+    return ws, ws.data_ptr(), need
+
+
+def _check(status, where):
+    if status != SSU_OK:
+        raise SSUError(status, where)
+
+
+def _linear(state, q, k, v, log_decay, cu_seqlens, idx, beta, scale, out, workspace, stream, where):
+    device = _gpu_of(state, "state")
+    _inference_only(state, q, k, v, log_decay, beta, out)
+    if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
+        raise ValueError("state must be [pool, H, P, N], q and k [tokens, G, N], v [tokens, H, P]")
+    pool, H, P, N = state.shape
+    T, G = q.shape[0], q.shape[1]
+    if idx.dim() != 1:
+        raise ValueError("state_batch_indices must be [batch]")
+    batch = idx.shape[0]
+    on = _On(stream, device)
+    if out is None:
+        out = on.empty((T, H, P), torch.bfloat16)
+    f32, bf16 = (torch.float32,), (torch.bfloat16,)
+    if log_decay.dim() == 1:  # one rate for each head
+        log_decay = log_decay.expand(T, H) if log_decay.shape[0] == H else log_decay
+    views = (_take(state, "state", (pool, H, P, N), f32, device)
+             + _take(idx, "state_batch_indices", (batch,), _INTS, device)
+             + (_NO_VIEW if cu_seqlens is None
+                else _take(cu_seqlens, "cu_seqlens", (batch + 1,), (torch.int32,), device))
+             + _take(q, "q", (T, G, N), bf16, device) + _take(k, "k", (T, G, N), bf16, device)
+             + _take(v, "v", (T, H, P), bf16, device) + _take(log_decay, "log_decay", (T, H), f32, device)
+             + (_NO_VIEW if beta is None else _take(beta, "beta", (T, H), f32, device))
+             + _take(out, "out", (T, H, P), bf16, device))
+    sizes = (batch, H, P, N, G, device.index, T, pool, scale, 0)
+    ws, ptr, size = None, 0, 0
+    if cu_seqlens is not None:
+        need = _lib.ssu_linear_attention_workspace(_LINEAR_ARGS.pack(*sizes, *views, 0, 0))
+        ws, ptr, size = _workspace(workspace, need, on)
+    args = _LINEAR_ARGS.pack(*sizes, *views, ptr, size)
+    fn = _lib.ssu_linear_attention_step if cu_seqlens is None else _lib.ssu_linear_attention
+    _check(fn(args, on.handle), where)
+    return out
+
+
+def linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta=None, scale=1.0, out=None,
+                     workspace=None, stream=None):
+    """Linear attention with a decay per head over packed prompts (see
+    include/ssu.h, ssu_linear_attention); ``state`` advances in place.
+
+    state [pool, H, P, N] fp32; q, k [T, G, N] bf16; v [T, H, P] bf16 (views into
+    one packed tensor are fine); log_decay [T, H] fp32, or [H] for fixed rates;
+    cu_seqlens [batch + 1] int32, sequence b being rows cu_seqlens[b] to
+    cu_seqlens[b + 1]; state_batch_indices [batch] int32/int64 (ids outside the
+    pool are padding); beta [T, H] fp32 or None for 1. Returns out [T, H, P]
+    bf16 (rows of no sequence are left as they were). ``workspace`` (optional): a
+    contiguous GPU tensor of at least ssu_linear_attention_workspace bytes, not
+    used by another call at the same time. Inference only: no gradient."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    return _linear(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace, stream,
+                   "ssu_linear_attention")
+
+
+def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=None, scale=1.0, out=None, stream=None):
+    """The same for one token per request (ssu_linear_attention_step): q, k
+    [batch, G, N], v [batch, H, P], log_decay [batch, H] or [H], beta [batch, H] or
+    None. Returns out [batch, H, P] bf16."""
+    if q.shape[0] != state_batch_indices.shape[0]:
+        raise ValueError(f"q has {q.shape[0]} tokens for {state_batch_indices.shape[0]} requests")
+    return _linear(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None, stream,
+                   "ssu_linear_attention_step")
+
+
+def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, v=None, k_cache=None, v_cache=None, slots=None, stream=None):
+    """Norm of every query and key head, then the position rotation (see
+    include/ssu.h, ssu_qk_norm_rope). Returns (q_out, k_out).
+
+    q [T, Hq, D], k [T, Hk, D] bf16 or fp16 (views into one packed tensor are
+    fine); positions [T] int32/int64 (outside the table: padding, the token is
+    skipped); cos_sin [max_pos, rot] fp32, cosines then sines; weights [D] (fp32
+    or q's type) or None. q_out and k_out may be q and k themselves. With
+    k_cache and v_cache [pages, page_size, Hk, D], v [T, Hk, D] and slots [T]
+    (int32/int64, outside the cache: skipped; in-range slots distinct), keys and
+    values go into the cache, and k_out is None unless it is given. Inference
+    only: no gradient."""
+    device = _gpu_of(q, "q")
+    _inference_only(q, k, q_weight, k_weight, cos_sin, v, k_cache, v_cache, q_out, k_out)
+    if q.dim() != 3 or k.dim() != 3 or cos_sin.dim() != 2:
+        raise ValueError("q must be [tokens, Hq, D], k [tokens, Hk, D], cos_sin [max_pos, rot]")
+    if q.dtype not in _HALF:
+        raise TypeError(f"q: dtype {q.dtype} not supported here")
+    T, nq, D = q.shape
+    nk = k.shape[1]
+    half, weight = (q.dtype,), (torch.float32, q.dtype)
+    max_pos, rot = cos_sin.shape
+    on = _On(stream, device)
+    with_cache = k_cache is not None
+    if (v_cache is not None) != with_cache or (v is not None) != with_cache or (slots is not None) != with_cache:
+        raise ValueError("v, k_cache, v_cache and slots go together")
+    if q_out is None:
+        q_out = on.empty((T, nq, D), q.dtype)
+    if k_out is None and not with_cache:
+        k_out = on.empty((T, nk, D), q.dtype)
+    pages = page_size = 0
+    cache = _NO_VIEW * 4
+    if with_cache:
+        if k_cache.dim() != 4:
+            raise ValueError("k_cache must be [pages, page_size, Hk, D]")
+        pages, page_size = k_cache.shape[0], k_cache.shape[1]
+        shape = (pages, page_size, nk, D)
+        cache = (_take(v, "v", (T, nk, D), half, device) + _take(k_cache, "k_cache", shape, half, device)
+                 + _take(v_cache, "v_cache", shape, half, device) + _take(slots, "slots", (T,), _INTS, device))
+    args = _QK_ARGS.pack(
+        T, nq, nk, D, rot, 1 if interleaved else 0, device.index, eps, page_size, max_pos, pages,
+        *_take(q, "q", (T, nq, D), half, device), *_take(k, "k", (T, nk, D), half, device),
+        *(_NO_VIEW if q_weight is None else _take(q_weight, "q_weight", (D,), weight, device)),
+        *(_NO_VIEW if k_weight is None else _take(k_weight, "k_weight", (D,), weight, device)),
+        *_take(positions, "positions", (T,), _INTS, device),
+        *_take(cos_sin, "cos_sin", (max_pos, rot), (torch.float32,), device),
+        *_take(q_out, "q_out", (T, nq, D), half, device),
+        *(_NO_VIEW if k_out is None else _take(k_out, "k_out", (T, nk, D), half, device)), *cache)
+    _check(_lib.ssu_qk_norm_rope(args, on.handle), "ssu_qk_norm_rope")
+    return q_out, k_out
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, return_lse=False, workspace=None,
+                    stream=None):
+    """Attention of one new token per request over a paged cache (see
+    include/ssu.h, ssu_paged_attention).
+
+    q [batch, Hq, D] bf16 or fp16; k_cache, v_cache [pages, page_size, Hk, D], q's
+    type; block_table [batch, max_pages] int32; seq_lens [batch] int32, the
+    tokens each request sees (its new one among them; 0: out is 0; negative:
+    padding, out is left as it was); scale: 1 / sqrt(D) by default. Returns out
+    [batch, Hq, D], with return_lse also the logarithms of the softmax sums
+    [batch, Hq] fp32. ``workspace`` as in linear_attention. Inference only: no
+    gradient."""
+    device = _gpu_of(q, "q")
+    _inference_only(q, k_cache, v_cache, out)
+    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [batch, Hq, D], k_cache [pages, page_size, Hk, D], block_table [batch, max_pages]")
+    if q.dtype not in _HALF:
+        raise TypeError(f"q: dtype {q.dtype} not supported here")
+    batch, nq, D = q.shape
+    pages, page_size, nk, _ = k_cache.shape
+    half, i32 = (q.dtype,), (torch.int32,)
+    on = _On(stream, device)
+    if out is None:
+        out = on.empty((batch, nq, D), q.dtype)
+    lse = on.empty((batch, nq), torch.float32) if return_lse else None
+    sizes = (batch, nq, nk, D, page_size, device.index, pages, block_table.shape[1],
+             D ** -0.5 if scale is None else scale, 0)
+    cache = (pages, page_size, nk, D)
+    views = (_take(q, "q", (batch, nq, D), half, device) + _take(k_cache, "k_cache", cache, half, device)
+             + _take(v_cache, "v_cache", cache, half, device)
+             + _take(block_table, "block_table", (batch, block_table.shape[1]), i32, device)
+             + _take(seq_lens, "seq_lens", (batch,), i32, device) + _take(out, "out", (batch, nq, D), half, device)
+             + (_NO_VIEW if lse is None else _take(lse, "lse", (batch, nq), (torch.float32,), device)))
+    need = _lib.ssu_paged_attention_workspace(_ATTN_ARGS.pack(*sizes, *views, 0, 0))
+    ws, ptr, size = _workspace(workspace, need, on)
+    _check(_lib.ssu_paged_attention(_ATTN_ARGS.pack(*sizes, *views, ptr, size), on.handle), "ssu_paged_attention")
+    return (out, lse) if return_lse else out

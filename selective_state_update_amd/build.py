@@ -12,10 +12,13 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", n) for n in ("ssu.hip", "block_copy.hip", "scan.hip")]
+SRCS = [os.path.join(HERE, "csrc", n) for n in ("ssu.hip", "block_copy.hip", "scan.hip", "linear_attention.hip",
+                                                  "qk_norm_rope.hip", "paged_attention.hip")]
 LIB = os.path.join(HERE, "libssu.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -33,20 +36,30 @@ FLAGS = [
 ]
 
 
-def build(extra=(), out: str = LIB, verbose: bool = False) -> str:
-    tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *extra, "-o", tmp, *SRCS]
+def _run(cmd, what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError("libssu build failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+        raise RuntimeError(f"{what} failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
     # hipcc's host pass does not know the packed-fp32 feature and says so; that is harmless
     noise = [ln for ln in res.stderr.splitlines() if ln.strip() and "packed-fp32-ops" not in ln
              and "not a recognized feature" not in ln]
     if noise and verbose:
         sys.stderr.write("\n".join(noise) + "\n")
-    os.replace(tmp, out)
+
+
+def build(extra=(), out: str = LIB, verbose: bool = False) -> str:
+    """Compile every source (side by side, one process each) and link them."""
+    with tempfile.TemporaryDirectory(dir=os.path.dirname(out)) as tmp:
+        objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SRCS]
+        compile_flags = [f for f in FLAGS if f != "-shared"]
+        with ThreadPoolExecutor(max_workers=len(SRCS)) as pool:
+            list(pool.map(lambda so: _run([HIPCC, *compile_flags, *extra, "-c", "-o", so[1], so[0]], "libssu build", verbose),
+                          zip(SRCS, objs)))
+        linked = os.path.join(tmp, "libssu.so")
+        _run([HIPCC, *FLAGS, *extra, "-o", linked, *objs], "libssu link", verbose)
+        os.replace(linked, out)
     return out
 
 

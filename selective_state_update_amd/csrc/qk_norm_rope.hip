@@ -1,0 +1,264 @@
+// qk_norm_rope.hip -- norms of queries and keys for each head with the position
+// rotation, optionally into a paged key-value cache, on MI355X (gfx950):
+// ssu_qk_norm_rope. The operation is stated in include/ssu.h.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "host_checks.h"
+#include "internal.h"
+#include "seq_common.h"
+
+namespace ssu {
+namespace {
+
+constexpr int kMaxHeaddim = 512;
+
+struct QkParams {
+    const uint16_t *q, *k, *v;
+    int64_t q_t, q_h, k_t, k_h, v_t, v_h;
+    const void *q_weight, *k_weight;  // fp32 or the 16-bit type; NULL: 1
+    const void *positions, *slots;
+    const float *cos_sin;
+    int64_t cs_row;
+    uint16_t *q_out, *k_out, *k_cache, *v_cache;
+    int64_t qo_t, qo_h, ko_t, ko_h;
+    int64_t kc_page, kc_row, kc_h, vc_page, vc_row, vc_h;
+    int64_t ntokens, max_pos, num_slots, total;  // total: head rows
+    int32_t nq, nk, rows_per_token, headdim, rot, interleaved, page_size;
+    int32_t pos64, slot64, qw32, kw32;
+    float eps;
+};
+
+template <typename T>
+__device__ __forceinline__ float weight_at(const void *w, int is32, int i)
+{
+    if (!w)
+        return 1.0f;
+    return is32 ? static_cast<const float *>(w)[i] : T::lo(static_cast<const uint16_t *>(w)[i]);
+}
+
+// One wave per head row (a token's query, key and, with a cache, value heads),
+// lane l holding elements l, l + 64, ... and, for the rotation, their pairs'
+// other elements. Any headdim, rotation width and alignment.
+template <typename T>
+__global__ void __launch_bounds__(256) ssu_qk_rows_kernel(const QkParams p)
+{
+    constexpr int M = kMaxHeaddim / 64;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    if (row >= p.total)
+        return;
+    const int64_t t = row / p.rows_per_token;
+    const int r = static_cast<int>(row - t * p.rows_per_token);
+    const int64_t pos = load_index(p.positions, p.pos64, t);
+    if (pos < 0 || pos >= p.max_pos)
+        return;  // padding
+    const bool is_q = r < p.nq, is_v = r >= p.nq + p.nk;
+    const int h = is_q ? r : is_v ? r - p.nq - p.nk : r - p.nq;
+    uint16_t *cache = nullptr;
+    if (!is_q && p.k_cache) {
+        const int64_t slot = load_index(p.slots, p.slot64, t);
+        if (slot >= 0 && slot < p.num_slots) {
+            const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
+            cache = is_v ? p.v_cache + page * p.vc_page + off * p.vc_row + h * p.vc_h
+                         : p.k_cache + page * p.kc_page + off * p.kc_row + h * p.kc_h;
+        }
+    }
+    if (is_v) {
+        const uint16_t *const x = p.v + t * p.v_t + h * p.v_h;
+        if (cache)
+            for (int i = lane; i < p.headdim; i += 64)
+                cache[i] = x[i];
+        return;
+    }
+    const uint16_t *const x = is_q ? p.q + t * p.q_t + h * p.q_h : p.k + t * p.k_t + h * p.k_h;
+    const void *const w = is_q ? p.q_weight : p.k_weight;
+    const int w32 = is_q ? p.qw32 : p.kw32, half = p.rot / 2;
+    const float *const cs = p.cos_sin + pos * p.cs_row;
+    float own[M], other[M], c[M], s[M], sum = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int i = lane + 64 * m;
+        own[m] = other[m] = s[m] = 0.0f;
+        c[m] = 1.0f;
+        if (i < p.headdim) {
+            own[m] = T::lo(x[i]);
+            sum = fmaf(own[m], own[m], sum);
+            own[m] *= weight_at<T>(w, w32, i);
+            if (i < p.rot) {
+                const int pair = p.interleaved ? i >> 1 : i < half ? i : i - half;
+                const bool first = p.interleaved ? !(i & 1) : i < half;
+                const int j = p.interleaved ? i ^ 1 : first ? i + half : i - half;
+                other[m] = T::lo(x[j]) * weight_at<T>(w, w32, j);
+                c[m] = cs[pair];
+                s[m] = first ? -cs[half + pair] : cs[half + pair];
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m /= 2)
+        sum += __shfl_xor(sum, m);
+    const float scale = 1.0f / sqrtf(sum / static_cast<float>(p.headdim) + p.eps);
+    uint16_t y[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        y[m] = T::round((own[m] * c[m] + other[m] * s[m]) * scale);
+    // in place: every element has been read before the first is written
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    uint16_t *const out = is_q ? p.q_out + t * p.qo_t + h * p.qo_h : p.k_out ? p.k_out + t * p.ko_t + h * p.ko_h : nullptr;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (lane + 64 * m < p.headdim) {
+            if (out)
+                out[lane + 64 * m] = y[m];
+            if (cache)
+                cache[lane + 64 * m] = y[m];
+        }
+}
+
+// ------------------------------------------------------------------ host --
+
+ssu_status check_qk(const ssu_qk_args &a)
+{
+    const char *const who = "ssu_qk_norm_rope";
+    if (a.ntokens < 0 || a.nq < 0 || a.nk < 0 || a.max_pos < 0 || a.num_pages < 0)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: negative size", who);
+    if (a.headdim < 1 || a.rot < 0 || a.rot > a.headdim || a.rot % 2)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: headdim %d, rot %d: rot must be even, at most headdim", who,
+                    a.headdim, a.rot);
+    if (a.headdim > kMaxHeaddim)
+        return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d > %d", who, a.headdim, kMaxHeaddim);
+    if (a.interleaved != 0 && a.interleaved != 1)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: interleaved must be 0 or 1", who);
+    if (!(a.eps >= 0.0f) || !std::isfinite(a.eps))
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: eps must be finite and >= 0", who);
+    const bool cache = a.k_cache.ptr || a.v_cache.ptr || a.slots.ptr || a.v.ptr;
+    const int32_t type = a.nq > 0 ? a.q.dtype : a.k.dtype;
+    if (type != SSU_BF16 && type != SSU_F16)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: q and k must be BF16 or F16", who);
+    if (a.ntokens == 0 || a.nq + a.nk == 0)
+        return SSU_OK;
+    const bool nq = a.nq == 0, nk = a.nk == 0;
+    SSU_TRY(check_view(a.q, "q", type, 3, nq));
+    SSU_TRY(check_view(a.q_out, "q_out", type, 3, nq));
+    SSU_TRY(check_view(a.k, "k", type, 3, nk));
+    SSU_TRY(check_view(a.k_out, "k_out", type, 3, nk || cache));
+    SSU_TRY(check_view(a.positions, "positions", a.positions.dtype == SSU_I64 ? SSU_I64 : SSU_I32, 1, false));
+    SSU_TRY(check_view(a.cos_sin, "cos_sin", SSU_F32, 2, a.rot == 0 || a.max_pos == 0));
+    for (const ssu_view *w : {&a.q_weight, &a.k_weight})
+        if (w->ptr) {
+            SSU_TRY(check_view(*w, "weight", w->dtype == SSU_F32 ? SSU_F32 : type, 1, true));
+            if (a.headdim > 1 && w->stride[0] != 1)
+                return fail(SSU_ERR_UNSUPPORTED, "weight: stride must be 1");
+            if (reinterpret_cast<uintptr_t>(w->ptr) % (w->dtype == SSU_F32 ? 4 : 2))
+                return fail(SSU_ERR_MISALIGNED, "weight: pointer must be aligned to its element");
+        }
+    if (cache) {
+        if (a.page_size < 1)
+            return fail(SSU_ERR_INVALID_ARGUMENT, "%s: page_size %d", who, a.page_size);
+        if (a.num_pages > INT64_MAX / a.page_size)
+            return fail(SSU_ERR_INVALID_ARGUMENT, "%s: num_pages * page_size too large", who);
+        const bool none = nk || a.num_pages == 0;
+        SSU_TRY(check_view(a.v, "v", type, 3, nk));
+        SSU_TRY(check_view(a.k_cache, "k_cache", type, 4, none));
+        SSU_TRY(check_view(a.v_cache, "v_cache", type, 4, none));
+        SSU_TRY(check_view(a.slots, "slots", a.slots.dtype == SSU_I64 ? SSU_I64 : SSU_I32, 1, false));
+        if (a.headdim > 1 && ((a.k_cache.ptr && a.k_cache.stride[3] != 1) || (a.v_cache.ptr && a.v_cache.stride[3] != 1)))
+            return fail(SSU_ERR_UNSUPPORTED, "k_cache/v_cache: inner stride must be 1");
+        if (a.slots.stride[0] != 1 && a.ntokens > 1)
+            return fail(SSU_ERR_UNSUPPORTED, "slots: stride must be 1");
+    }
+    SSU_TRY(check_written(a.q_out, "q_out", {a.ntokens, a.nq}));
+    SSU_TRY(check_written(a.k_out, "k_out", {a.ntokens, a.nk}));
+    SSU_TRY(check_written(a.k_cache, "k_cache", {a.num_pages, a.page_size, a.nk}));
+    SSU_TRY(check_written(a.v_cache, "v_cache", {a.num_pages, a.page_size, a.nk}));
+    for (const ssu_view *v : {&a.q, &a.k, &a.v, &a.q_out, &a.k_out})
+        if (v->ptr && a.headdim > 1 && v->stride[2] != 1)
+            return fail(SSU_ERR_UNSUPPORTED, "q/k/v/outputs: inner stride must be 1");
+    if (a.positions.stride[0] != 1 && a.ntokens > 1)
+        return fail(SSU_ERR_UNSUPPORTED, "positions: stride must be 1");
+    if (a.rot > 1 && a.cos_sin.ptr && a.cos_sin.stride[1] != 1)
+        return fail(SSU_ERR_UNSUPPORTED, "cos_sin: inner stride must be 1");
+    for (const ssu_view *v : {&a.q, &a.k, &a.v, &a.q_out, &a.k_out, &a.k_cache, &a.v_cache})
+        if (reinterpret_cast<uintptr_t>(v->ptr) % 2)
+            return fail(SSU_ERR_MISALIGNED, "16-bit operand not 2-byte aligned");
+    if (reinterpret_cast<uintptr_t>(a.cos_sin.ptr) % 4)
+        return fail(SSU_ERR_MISALIGNED, "cos_sin: pointer must be 4-byte aligned");
+    for (const ssu_view *v : {&a.positions, &a.slots})
+        if (reinterpret_cast<uintptr_t>(v->ptr) % (v->dtype == SSU_I64 ? 8 : 4))
+            return fail(SSU_ERR_MISALIGNED, "positions/slots: pointer must be aligned to its element");
+    return SSU_OK;
+}
+
+}  // namespace
+}  // namespace ssu
+
+extern "C" ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stream)
+{
+    using namespace ssu;
+    if (!args)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_qk_norm_rope: null args");
+    const ssu_qk_args &a = *args;
+    SSU_TRY(check_qk(a));
+    if (a.ntokens == 0 || a.nq + a.nk == 0 || a.max_pos == 0)
+        return SSU_OK;
+    QkParams p{};
+    p.q = static_cast<const uint16_t *>(a.q.ptr);
+    p.q_t = a.q.stride[0];
+    p.q_h = a.q.stride[1];
+    p.k = static_cast<const uint16_t *>(a.k.ptr);
+    p.k_t = a.k.stride[0];
+    p.k_h = a.k.stride[1];
+    p.v = static_cast<const uint16_t *>(a.v.ptr);
+    p.v_t = a.v.stride[0];
+    p.v_h = a.v.stride[1];
+    p.q_weight = a.q_weight.ptr;
+    p.qw32 = a.q_weight.dtype == SSU_F32;
+    p.k_weight = a.k_weight.ptr;
+    p.kw32 = a.k_weight.dtype == SSU_F32;
+    p.positions = a.positions.ptr;
+    p.pos64 = a.positions.dtype == SSU_I64;
+    p.slots = a.slots.ptr;
+    p.slot64 = a.slots.dtype == SSU_I64;
+    p.cos_sin = static_cast<const float *>(a.cos_sin.ptr);
+    p.cs_row = a.cos_sin.stride[0];
+    p.q_out = static_cast<uint16_t *>(const_cast<void *>(a.q_out.ptr));
+    p.qo_t = a.q_out.stride[0];
+    p.qo_h = a.q_out.stride[1];
+    p.k_out = static_cast<uint16_t *>(const_cast<void *>(a.k_out.ptr));
+    p.ko_t = a.k_out.stride[0];
+    p.ko_h = a.k_out.stride[1];
+    p.k_cache = static_cast<uint16_t *>(const_cast<void *>(a.k_cache.ptr));
+    p.kc_page = a.k_cache.stride[0];
+    p.kc_row = a.k_cache.stride[1];
+    p.kc_h = a.k_cache.stride[2];
+    p.v_cache = static_cast<uint16_t *>(const_cast<void *>(a.v_cache.ptr));
+    p.vc_page = a.v_cache.stride[0];
+    p.vc_row = a.v_cache.stride[1];
+    p.vc_h = a.v_cache.stride[2];
+    p.ntokens = a.ntokens;
+    p.max_pos = a.max_pos;
+    p.num_slots = p.k_cache ? a.num_pages * a.page_size : 0;
+    p.nq = a.nq;
+    p.nk = a.nk;
+    p.rows_per_token = a.nq + a.nk + (p.k_cache ? a.nk : 0);
+    p.headdim = a.headdim;
+    p.rot = a.rot;
+    p.interleaved = a.interleaved;
+    p.page_size = a.page_size;
+    p.eps = a.eps;
+    if (a.ntokens > INT64_MAX / p.rows_per_token || a.ntokens * p.rows_per_token > int64_t(4) * 0x7fffffff)
+        return fail(SSU_ERR_UNSUPPORTED, "ssu_qk_norm_rope: more than 2^31 workgroups");
+    p.total = a.ntokens * p.rows_per_token;
+    DeviceGuard guard;
+    SSU_TRY(guard.enter(a.device));
+    const bool bf16 = (a.nq > 0 ? a.q.dtype : a.k.dtype) == SSU_BF16;
+    const hipError_t e = launch_kernel(bf16 ? &ssu_qk_rows_kernel<Bf16> : &ssu_qk_rows_kernel<F16>, p, (p.total + 3) / 4,
+                                       256, 0, stream);
+    if (e != hipSuccess)
+        return fail(SSU_ERR_HIP, "launch of the norm and rotation kernel failed: %s", hipGetErrorString(e));
+    return SSU_OK;
+}

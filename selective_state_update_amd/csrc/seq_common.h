@@ -1,0 +1,75 @@
+// seq_common.h -- device helpers shared by the sequence operators
+// (linear_attention.hip, qk_norm_rope.hip, paged_attention.hip; not installed).
+#ifndef SSU_SEQ_COMMON_H
+#define SSU_SEQ_COMMON_H
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace ssu {
+
+constexpr int kNumCUs = 256;  // MI355X
+
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+// Runs of 16-bit elements as one access. The type's alignment is the
+// element's: gfx950 reads and writes 4, 8 and 16 bytes at any 2-byte address,
+// at full speed where the address is a multiple of the size, so views need no
+// alignment beyond their elements'.
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+
+// 16-bit floating types: the fp32 value of bits, and bits rounded to nearest
+// even from fp32 (the conversion is kept opaque to the compiler so that it is
+// never fused with the operation that produces its operand).
+struct Bf16 {
+    static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+    static __device__ __forceinline__ uint16_t round(float f)
+    {
+        asm volatile("" : "+v"(f));
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+    }
+};
+
+struct F16 {
+    static __device__ __forceinline__ float value(uint16_t b)
+    {
+        return static_cast<float>(__builtin_bit_cast(_Float16, b));
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return value(static_cast<uint16_t>(w)); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return value(static_cast<uint16_t>(w >> 16)); }
+    static __device__ __forceinline__ uint16_t round(float f)
+    {
+        asm volatile("" : "+v"(f));
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+    }
+};
+
+// Element i of an index array of 32- or 64-bit integers.
+__device__ __forceinline__ int64_t load_index(const void *p, int is64, int64_t i)
+{
+    return is64 ? static_cast<const int64_t *>(p)[i] : static_cast<int64_t>(static_cast<const int32_t *>(p)[i]);
+}
+
+// Launch a kernel and return its own status (a call that fails leaves no
+// error behind for the caller's next runtime call).
+template <typename P>
+hipError_t launch_kernel(void (*fn)(P), const P &p, int64_t grid, int block, size_t lds, hipStream_t stream)
+{
+    P copy = p;
+    void *args[] = {&copy};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(fn), dim3(static_cast<uint32_t>(grid)),
+                                         dim3(block), args, lds, stream);
+    if (e != hipSuccess)
+        (void)hipGetLastError();
+    return e;
+}
+
+}  // namespace ssu
+
+#endif  // SSU_SEQ_COMMON_H

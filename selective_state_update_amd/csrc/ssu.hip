@@ -49,6 +49,7 @@
 #include <utility>
 #include <vector>
 
+#include "host_checks.h"
 #include "internal.h"
 
 namespace ssu {
@@ -844,6 +845,8 @@ namespace {
 using ssu::DeviceLimits;
 using ssu::device_limits;
 using ssu::fail;
+using ssu::check_view;
+using ssu::DeviceGuard;
 
 bool valid_dstate(int n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
 
@@ -950,29 +953,6 @@ int select_tile(const ssu_config &c, int32_t batch, int32_t ntokens)
     }
     return fallback;
 }
-
-ssu_status check_view(const ssu_view &v, const char *name, int32_t dtype, int rank, bool nullable)
-{
-    if (!v.ptr && !nullable)
-        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: null pointer", name);
-    if (!v.ptr)
-        return SSU_OK;
-    if (v.dtype != dtype)
-        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: dtype tag %d, expected %d", name, v.dtype, dtype);
-    if (v.reserved != 0)
-        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: reserved field must be 0", name);
-    for (int i = 0; i < rank; ++i)
-        if (v.stride[i] < 0)
-            return fail(SSU_ERR_INVALID_ARGUMENT, "%s: negative stride[%d]", name, i);
-    return SSU_OK;
-}
-
-#define SSU_TRY(expr)                    \
-    do {                                 \
-        const ssu_status s_ = (expr);    \
-        if (s_ != SSU_OK)                \
-            return s_;                   \
-    } while (0)
 
 }  // namespace
 
@@ -1098,30 +1078,6 @@ ssu_view with_token_axis(const ssu_view &v)
     w.stride[1] = 0;
     return w;
 }
-
-// Restores the caller's current device on every return path.
-struct DeviceGuard {
-    int prev = -1;
-    bool switched = false;
-    ssu_status enter(int device)
-    {
-        if (device < 0)
-            return SSU_OK;
-        if (hipGetDevice(&prev) != hipSuccess)
-            return fail(SSU_ERR_HIP, "hipGetDevice failed");
-        if (prev != device) {
-            if (hipSetDevice(device) != hipSuccess)
-                return fail(SSU_ERR_HIP, "hipSetDevice(%d) failed", device);
-            switched = true;
-        }
-        return SSU_OK;
-    }
-    ~DeviceGuard()
-    {
-        if (switched)
-            (void)hipSetDevice(prev);
-    }
-};
 
 ssu_status run(const ssu_handle *hd, const Operands &a, hipStream_t stream)
 {
