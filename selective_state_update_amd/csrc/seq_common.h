@@ -50,6 +50,43 @@ struct F16 {
     }
 };
 
+// One wave's product of a 16 x 32 and a 32 x 16 tile on the matrix cores, fp32
+// sums. Lane l holds row (column) l % 16 of a (of b), 8 consecutive places of
+// the contracted axis from 8 * (l / 16); of the result it holds column l % 16,
+// rows 4 * (l / 16) + 0..3. Which values share a place of the contracted axis
+// is free as long as a and b agree.
+template <typename T>
+struct Mma;
+
+template <>
+struct Mma<Bf16> {
+    using Frag = __bf16 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 run(u32x4 a, u32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(Frag, a), __builtin_bit_cast(Frag, b), c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Mma<F16> {
+    using Frag = _Float16 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 run(u32x4 a, u32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(Frag, a), __builtin_bit_cast(Frag, b), c, 0, 0, 0);
+    }
+};
+
+// Two fp32 values as a word of two 16-bit ones.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    return static_cast<uint32_t>(T::round(lo)) | static_cast<uint32_t>(T::round(hi)) << 16;
+}
+
+// The 16-bit halves of two words side by side: the low ones, the high ones.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
 // Element i of an index array of 32- or 64-bit integers.
 __device__ __forceinline__ int64_t load_index(const void *p, int is64, int64_t i)
 {
