@@ -15,10 +15,14 @@
 namespace ssu {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kTile = 32;               // tokens of one wave's step
-constexpr int kRound = kWaves * kTile;  // tokens of one workgroup's step
-constexpr int kMaxSplits = 128;
+constexpr int kTile = 32;     // tokens of one wave's step
+constexpr int kJoinRows = 4;  // rows that a workgroup of the join takes
+
+// Waves of a workgroup. D = 256 needs half the register file per wave: two
+// waves and two workgroups per CU instead of four and one keep one of them
+// loading while the other joins (64 requests up to 4096 tokens, 8 heads of 256:
+// 185 against 208 us).
+constexpr int waves_for(int D) { return D == 256 ? 2 : 4; }
 
 struct AttnParams {
     const uint16_t *q, *k, *v;
@@ -29,32 +33,32 @@ struct AttnParams {
     int64_t o_b, o_h;
     float *lse;
     int64_t l_b, l_h;
-    float *part;  // [batch, splits, nq, D] partial sums, then [batch, splits, nq, 2] (maximum, sum)
-    float *stat;
-    int32_t batch, nq, nk, heads_per_kv, row_tiles, page_size, splits, min_rounds, total;
+    // Workspace: for every workgroup, what the unit that it leaves unfinished
+    // is (Open), and for its first and its last unit 16 rows of sums and of
+    // (maximum, sum).
+    struct Open *open;
+    float *part, *stat;
+    int32_t batch, nq, nk, heads_per_kv, row_tiles, page_size, groups;
     float scale_log2;  // scale * log2(e): weights are powers of 2
 };
 
-// The part of a request's tokens that one split takes: `per` rounds each, the
-// same for all its splits, so that a request's own length is divided evenly
-// whatever the table has room for.
-struct Share {
-    int64_t n, begin, end;  // visible tokens at most; this split's range
-    int active;             // splits that have work (at least 1)
+// A unit (request, key/value head, 16 query heads) whose first steps a
+// workgroup did and whose last ones workgroup `last` does; b < 0: none.
+struct Open {
+    int32_t b, unit, last, reserved;
 };
 
-__device__ __forceinline__ Share share_of(const AttnParams &p, int b, int split)
+// The visible tokens of a request (negative: padding) and its steps; a request
+// without a visible token has one, which writes its zeros.
+__device__ __forceinline__ int64_t visible(const AttnParams &p, int b)
 {
-    Share s;
-    s.n = p.lens[b];
-    if (s.n >= 0)
-        s.n = p.num_pages == 0 ? 0 : min(s.n, p.max_pages * p.page_size);
-    const int rounds = static_cast<int>((s.n + kRound - 1) / kRound);
-    const int per = max((rounds + p.splits - 1) / p.splits, p.min_rounds);
-    s.active = max((rounds + per - 1) / per, 1);
-    s.begin = static_cast<int64_t>(split) * per * kRound;
-    s.end = min(s.n, s.begin + static_cast<int64_t>(per) * kRound);
-    return s;
+    const int64_t n = p.lens[b];
+    return n < 0 ? n : p.num_pages == 0 ? 0 : min(n, p.max_pages * p.page_size);
+}
+
+__device__ __forceinline__ int64_t rounds_of(int64_t n, int round)
+{
+    return n < 0 ? 0 : n == 0 ? 1 : (n + round - 1) / round;
 }
 
 // fp16 weights are scaled by 2^14 (at most 2^14, then): what lies 2^-28 below a
@@ -64,7 +68,21 @@ constexpr float kShift = 0.0f;
 template <>
 constexpr float kShift<F16> = 14.0f;
 
-// One workgroup per (request, split, key/value head, 16 of its query heads).
+template <typename T>
+__device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int d, float y, float sum, float base)
+{
+    p.out[b * p.o_b + h * p.o_h + d] = T::round(sum == 0.0f ? 0.0f : y / sum);
+    if (p.lse && d == 0)
+        p.lse[b * p.l_b + h * p.l_h] = sum == 0.0f ? -INFINITY : (base - kShift<T> + log2f(sum)) * kLn2Hi;
+}
+
+// The steps of all units stand in one line (requests in order, a request's
+// units in order, a unit's steps in order), and every workgroup takes an equal
+// run of it: requests of very different lengths, one long request and many
+// short ones all fill the chip with one set of resident workgroups. A unit
+// that lies across two or more runs is joined by the second kernel; a
+// workgroup leaves at most two of its units unfinished, its first and its last.
+//
 // Memory-bound: every visible K and V row is read once per 16 query heads, so
 // the loads decide, and the products are arranged for them:
 //
@@ -79,13 +97,16 @@ constexpr float kShift<F16> = 14.0f;
 //    for value c * D/16 + m, so a product's fragment is a transposition inside
 //    the lane (byte permutes), and the output comes back in runs of D/16.
 //
-// Every wave takes every fourth 32-token step with statistics of its own; K of
-// the next step is requested before the softmax of this one. PAGE16: pages
-// are a multiple of 16 tokens, a tile lies in one page and its address is
-// uniform; otherwise every lane looks its own token up.
+// V is read past the caches (non-temporal); K is not, because one instruction
+// reads half a cache line of each row and the next the other half. Each wave
+// takes every fourth step of 32 tokens with statistics of its own. PAGE16:
+// pages are a multiple of 16 tokens, a tile lies in one page and its address
+// is uniform; otherwise every lane looks its own token up.
 template <typename T, int D, bool PAGE16>
-__global__ void __launch_bounds__(64 * kWaves) ssu_attn_split_kernel(const AttnParams p)
+__global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
 {
+    constexpr int kWaves = waves_for(D);
+    constexpr int kRound = kWaves * kTile;  // tokens of one workgroup's step
     constexpr int KS = D / 32;      // products along D of a score
     constexpr int E = D / 16;       // values of a V row per lane, products of an output row
     constexpr int EW = E / 2;       // the same in words
@@ -93,247 +114,352 @@ __global__ void __launch_bounds__(64 * kWaves) ssu_attn_split_kernel(const AttnP
     typedef V V_a2 __attribute__((aligned(2)));
     __shared__ float part[kWaves][16][D];
     __shared__ float stat_m[kWaves][16], stat_l[kWaves][16];
+    __shared__ int64_t scan[kWaves];
+    __shared__ int64_t found[3];  // its request, the steps before it, its tokens
 
-    int id = xcd_order(static_cast<int>(blockIdx.x), p.total);
-    const int rt = id % p.row_tiles;
-    id /= p.row_tiles;
-    const int kh = id % p.nk;
-    id /= p.nk;
-    const int split = id % p.splits, b = id / p.splits;
-    const Share sh = share_of(p, b, split);
-    if (sh.n < 0 || split >= sh.active)
-        return;  // padding, or a length that needs fewer splits
-    const int lane = static_cast<int>(threadIdx.x) & 63, c = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    const int rows = min(p.heads_per_kv - rt * 16, 16);  // query heads of this workgroup
-    const int h0 = kh * p.heads_per_kv + rt * 16;
+    const int wg = xcd_order(static_cast<int>(blockIdx.x), p.groups);
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int units = p.nk * p.row_tiles;  // of a request
 
-    u32x4 qf[KS];
+    // this workgroup's run of the line, and the request that it begins in
+    // (up to 256 requests their lengths are read once)
+    const int64_t first_n = tid < p.batch ? visible(p, tid) : -1;
+    int64_t total = rounds_of(first_n, kRound);
+    for (int b = tid + 64 * kWaves; b < p.batch; b += 64 * kWaves)
+        total += rounds_of(visible(p, b), kRound);
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
-        qf[i] = c < rows ? *reinterpret_cast<const u32x4_a2 *>(p.q + b * p.q_b + (h0 + c) * p.q_h + (i * 4 + g) * 8)
-                         : u32x4{0, 0, 0, 0};
-
-    const int32_t *const table = p.table + b * p.t_b;
-    const uint16_t *const kbase = p.k + kh * p.k_h + g * 8, *const vbase = p.v + kh * p.v_h + c * E;
-
-    // A tile of 16 tokens: where it is, and which of its tokens are visible.
-    struct Tile {
-        const uint16_t *k, *v;  // PAGE16: this lane's K row and the tile's first V row
-        int page, off;          // otherwise: this lane's token
-        uint32_t seen;          // uniform, a bit per token
-    };
-    auto locate = [&](int64_t t0) {
-        Tile t;
-        if constexpr (PAGE16) {
-            const int64_t at = min(t0, (sh.n - 1) & ~int64_t(15));
-            const int col = static_cast<int>(at) / p.page_size;
-            const int64_t off = at - static_cast<int64_t>(col) * p.page_size;
-            int64_t page = table[col];
-            const bool good = page >= 0 && page < p.num_pages;
-            page = good ? page : 0;
-            const int64_t left = sh.end - t0;
-            t.seen = !good || left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
-            t.k = kbase + page * p.k_page + (off + c) * p.k_row;
-            t.v = vbase + page * p.v_page + off * p.v_row;
-        } else {
-            const int at = static_cast<int>(min(t0 + c, sh.n - 1));
-            const int col = at / p.page_size;
-            t.off = at - col * p.page_size;
-            t.page = table[col];
-            const bool good = t.page >= 0 && t.page < p.num_pages;
-            t.page = good ? t.page : 0;
-            t.seen = static_cast<uint32_t>(__ballot(good && t0 + c < sh.end)) & 0xffffu;
-            t.k = kbase + t.page * p.k_page + t.off * p.k_row;
+    for (int m = 32; m >= 1; m /= 2)
+        total += __shfl_xor(total, m);
+    if (lane == 0)
+        scan[wave] = total;
+    if (tid == 0)
+        p.open[wg] = Open{-1, 0, 0, 0};
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        total += scan[w] * units;
+    const int64_t per = (total + p.groups - 1) / p.groups;
+    int64_t pos = wg * per;
+    const int64_t stop = min(pos + per, total);
+    if (pos >= stop)
+        return;
+    int64_t before = 0;  // steps of a unit of every earlier request
+    for (int b0 = 0; b0 < p.batch; b0 += 64 * kWaves) {
+        const int b = b0 + tid;
+        const int64_t n = b0 == 0 ? first_n : b < p.batch ? visible(p, b) : -1, own = rounds_of(n, kRound);
+        int64_t sum = own;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int64_t up = __shfl_up(sum, m);
+            sum += lane >= m ? up : 0;
         }
-        return t;
-    };
-    auto load_k = [&](const Tile &t, u32x4 (&f)[KS]) {
+        __syncthreads();
+        if (lane == 63)
+            scan[wave] = sum;
+        __syncthreads();
+        int64_t first = before + sum - own;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            first += w < wave ? scan[w] : 0;
+            before += scan[w];
+        }
+        if (first * units <= pos && pos < (first + own) * units) {
+            found[0] = b;
+            found[1] = first;
+            found[2] = n;
+        }
+        if (before * units > pos)
+            break;
+    }
+    __syncthreads();
+    int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
+    int64_t n = found[2], rounds = rounds_of(n, kRound);
+    int unit = static_cast<int>((pos - found[1] * units) / rounds);
+    int64_t step0 = pos - found[1] * units - unit * rounds;  // of the unit, where this workgroup begins
+
+    for (;;) {
+        const int64_t steps = min(rounds - step0, stop - pos);
+        const struct {
+            int64_t n, begin, end;
+        } sh = {n, step0 * kRound, min(n, (step0 + steps) * kRound)};
+        unit = __builtin_amdgcn_readfirstlane(unit);
+        const int kh = unit / p.row_tiles, rt = unit - kh * p.row_tiles;
+        const int rows = min(p.heads_per_kv - rt * 16, 16);  // query heads of this unit
+        const int h0 = kh * p.heads_per_kv + rt * 16;
+
+        u32x4 qf[KS];
 #pragma unroll
         for (int i = 0; i < KS; ++i)
-            f[i] = *reinterpret_cast<const u32x4_a2 *>(t.k + i * 32);
-    };
-    auto load_v = [&](const Tile &t, V *f) {  // tokens 4g .. 4g+3
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+            qf[i] = c < rows ? *reinterpret_cast<const u32x4_a2 *>(p.q + b * p.q_b + (h0 + c) * p.q_h + (i * 4 + g) * 8)
+                             : u32x4{0, 0, 0, 0};
+        const int32_t *const table = p.table + b * p.t_b;
+        const uint16_t *const kbase = p.k + kh * p.k_h + g * 8, *const vbase = p.v + kh * p.v_h + c * E;
+
+        // A tile of 16 tokens: its page id as the table has it (requested a step
+        // before it is needed), then where it is and which of its tokens are
+        // visible. Uniform with PAGE16 (through the scalar cache: a vector load
+        // would make its reader wait for all K and V loads issued before it),
+        // otherwise of this lane's token.
+        struct Entry {
+            int off;
+            int page;
+        };
+        struct Tile {
+            int64_t k, v;  // PAGE16: the tile's first rows; otherwise this lane's
+            uint32_t seen;  // uniform, a bit per token
+        };
+        auto peek = [&](int64_t t0) {
+            Entry e;
             if constexpr (PAGE16) {
-                f[i] = *reinterpret_cast<const V_a2 *>(t.v + (4 * g + i) * p.v_row);
+                const int at = static_cast<int>(min(t0, (sh.end - 1) & ~int64_t(15)));
+                const int col = __builtin_amdgcn_readfirstlane(at / p.page_size);
+                e.off = at - col * p.page_size;
+                e.page = load_ro(table + col);
             } else {
-                const int64_t page = __shfl(t.page, 4 * g + i), off = __shfl(t.off, 4 * g + i);
-                f[i] = *reinterpret_cast<const V_a2 *>(vbase + page * p.v_page + off * p.v_row);
+                const int at = static_cast<int>(min(t0 + c, sh.end - 1));
+                const int col = at / p.page_size;
+                e.off = at - col * p.page_size;
+                e.page = table[col];
             }
-        }
-    };
-
-    f32x4 o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        o[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -INFINITY, l = 0.0f;  // of query head c (l: this lane's tokens)
-
-    int64_t t0 = sh.begin + wave * kTile;
-    Tile tile[2];
-    u32x4 kf[2][KS];
-    if (t0 < sh.end) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            tile[u] = locate(t0 + 16 * u);
-            load_k(tile[u], kf[u]);
-        }
-    }
-    while (t0 < sh.end) {
-        V vf[8];
-        load_v(tile[0], vf);
-        load_v(tile[1], vf + 4);
-        f32x4 s[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            return e;
+        };
+        auto locate = [&](int64_t t0, const Entry &e) {
+            Tile t;
+            const bool good = e.page >= 0 && e.page < p.num_pages;
+            const int64_t page = good ? e.page : 0;
+            t.k = page * p.k_page + e.off * p.k_row;
+            t.v = page * p.v_page + e.off * p.v_row;
+            if constexpr (PAGE16) {
+                const int64_t left = sh.end - t0;
+                t.seen = !good || left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
+            } else {
+                t.seen = static_cast<uint32_t>(__ballot(good && t0 + c < sh.end)) & 0xffffu;
+            }
+            return t;
+        };
+        const uint16_t *const klane = kbase + (PAGE16 ? c * p.k_row : 0), *const vlane = vbase + (PAGE16 ? 4 * g * p.v_row : 0);
+        auto load_k = [&](const Tile &t, u32x4 (&f)[KS]) {
 #pragma unroll
             for (int i = 0; i < KS; ++i)
-                s[u] = Mma<T>::run(kf[u][i], qf[i], s[u]);
-        }
-        const uint32_t seen[2] = {tile[0].seen, tile[1].seen};
-        t0 += kRound;
+                f[i] = *reinterpret_cast<const u32x4_a2 *>(klane + t.k + i * 32);
+        };
+        auto load_v = [&](const Tile &t, V *f) {  // tokens 4g .. 4g+3
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = PAGE16 ? t.v + i * p.v_row : __shfl(t.v, 4 * g + i);
+                f[i] = __builtin_nontemporal_load(reinterpret_cast<const V_a2 *>(vlane + row));
+            }
+        };
+
+        f32x4 o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        float m = -INFINITY, l = 0.0f;  // of query head c (l: this lane's tokens)
+
+        // One step of 32 tokens, with K (kf) and V (vf) on their way: K of the next
+        // step is requested once the scores have freed its registers, with the page
+        // ids of the step behind it, and the next V after this one's product. Behind
+        // the last step the loads go to the split's last tile again: a condition
+        // around them would make every wait for older loads a wait for all.
+        int64_t t0 = sh.begin + wave * kTile;
+        Tile tile[2];
+        Entry entry[2];
+        u32x4 kf[2][KS];
+        V vf[8];
         if (t0 < sh.end) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                tile[u] = locate(t0 + 16 * u);
+                tile[u] = locate(t0 + 16 * u, peek(t0 + 16 * u));
+                load_k(tile[u], kf[u]);
+                load_v(tile[u], vf + 4 * u);
+                entry[u] = peek(t0 + kRound + 16 * u);
+            }
+        }
+        while (t0 < sh.end) {
+            const uint32_t seen[2] = {tile[0].seen, tile[1].seen};
+            t0 += kRound;
+            f32x4 s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                s[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    s[u] = Mma<T>::run(kf[u][i], qf[i], s[u]);
+            }
+
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                tile[u] = locate(t0 + 16 * u, entry[u]);
+                entry[u] = peek(t0 + kRound + 16 * u);
                 load_k(tile[u], kf[u]);
             }
+
+            // softmax over the step's 32 tokens
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[u][i] *= p.scale_log2;
+                    if (seen[u] != 0xffffu)
+                        s[u][i] = (seen[u] >> (4 * g + i)) & 1 ? s[u][i] : -INFINITY;
+                    top = fmaxf(top, s[u][i]);
+                }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float base = top == -INFINITY ? 0.0f : top;  // scores of -inf weigh nothing
+            const float keep = __builtin_amdgcn_exp2f(m - base);
+            m = top;
+            float w[8], sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[4 * u + i] = __builtin_amdgcn_exp2f(s[u][i] - base + kShift<T>);
+                    sum += w[4 * u + i];
+                }
+            l = fmaf(l, keep, sum);
+            if (__any(keep != 1.0f)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = __shfl(keep, 4 * g + i);  // of the output rows that this lane holds
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        o[e][i] *= f;
+                }
+            }
+            // the weights as a 16-bit pair, value and remainder: rounded once they
+            // would add an error of the output's own rounding's size
+            u32x4 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi[i] = pack2<T>(w[2 * i], w[2 * i + 1]);
+                lo[i] = pack2<T>(w[2 * i] - T::lo(hi[i]), w[2 * i + 1] - T::hi(hi[i]));
+            }
+            if (seen[0] != 0xffffu || seen[1] != 0xffffu) {  // what is not visible may be NaN
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!((seen[i / 4] >> (4 * g + i % 4)) & 1))
+                        vf[i] = V{};
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                u32x4 f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[i] = e % 2 ? high_halves(vf[2 * i][e / 2], vf[2 * i + 1][e / 2])
+                                 : low_halves(vf[2 * i][e / 2], vf[2 * i + 1][e / 2]);
+                o[e] = Mma<T>::run(hi, f, o[e]);
+                o[e] = Mma<T>::run(lo, f, o[e]);
+            }
+            load_v(tile[0], vf);
+            load_v(tile[1], vf + 4);
         }
 
-        // softmax over the step's 32 tokens
-        float top = m;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[u][i] *= p.scale_log2;
-                if (seen[u] != 0xffffu)
-                    s[u][i] = (seen[u] >> (4 * g + i)) & 1 ? s[u][i] : -INFINITY;
-                top = fmaxf(top, s[u][i]);
-            }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float base = top == -INFINITY ? 0.0f : top;  // scores of -inf weigh nothing
-        const float keep = __builtin_amdgcn_exp2f(m - base);
-        m = top;
-        float w[8], sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[4 * u + i] = __builtin_amdgcn_exp2f(s[u][i] - base + kShift<T>);
-                sum += w[4 * u + i];
-            }
-        l = fmaf(l, keep, sum);
-        if (__any(keep != 1.0f)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float f = __shfl(keep, 4 * g + i);  // of the output rows that this lane holds
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    o[e][i] *= f;
-            }
+        // join the waves
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (g == 0) {
+            stat_m[wave][c] = m;
+            stat_l[wave][c] = l;
         }
-        // the weights as a 16-bit pair, value and remainder: rounded once they
-        // would add an error of the output's own rounding's size
-        u32x4 hi, lo;
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hi[i] = pack2<T>(w[2 * i], w[2 * i + 1]);
-            lo[i] = pack2<T>(w[2 * i] - T::lo(hi[i]), w[2 * i + 1] - T::hi(hi[i]));
+            const int r = 4 * g + i;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                top = fmaxf(top, stat_m[w][r]);
+            const float f = __builtin_amdgcn_exp2f(stat_m[wave][r] - (top == -INFINITY ? 0.0f : top));
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                part[wave][r][c * E + e] = o[e][i] * f;
         }
-        if (seen[0] != 0xffffu || seen[1] != 0xffffu) {  // what is not visible may be NaN
+        __syncthreads();
+        const bool whole = steps == rounds;
+        const int64_t row0 = (2 * static_cast<int64_t>(wg) + (step0 == 0)) * 16;
+        for (int at = tid; at < rows * D; at += 64 * kWaves) {
+            const int r = at / D, d = at % D;
+            float top = -INFINITY, sum = 0.0f, y = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!((seen[i / 4] >> (4 * g + i % 4)) & 1))
-                    vf[i] = V{};
-        }
+            for (int w = 0; w < kWaves; ++w)
+                top = fmaxf(top, stat_m[w][r]);
+            const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            u32x4 f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = e % 2 ? high_halves(vf[2 * i][e / 2], vf[2 * i + 1][e / 2])
-                             : low_halves(vf[2 * i][e / 2], vf[2 * i + 1][e / 2]);
-            o[e] = Mma<T>::run(hi, f, o[e]);
-            o[e] = Mma<T>::run(lo, f, o[e]);
-        }
-    }
-
-    // join the waves
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (g == 0) {
-        stat_m[wave][c] = m;
-        stat_l[wave][c] = l;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * g + i;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            top = fmaxf(top, stat_m[w][r]);
-        const float f = __builtin_amdgcn_exp2f(stat_m[wave][r] - (top == -INFINITY ? 0.0f : top));
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            part[wave][r][c * E + e] = o[e][i] * f;
-    }
-    __syncthreads();
-    for (int at = static_cast<int>(threadIdx.x); at < rows * D; at += 64 * kWaves) {
-        const int r = at / D, d = at % D, h = h0 + r;
-        float top = -INFINITY, sum = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            top = fmaxf(top, stat_m[w][r]);
-        const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            sum = fmaf(stat_l[w][r], __builtin_amdgcn_exp2f(stat_m[w][r] - base), sum);
-            y += part[w][r][d];
-        }
-        if (sh.active == 1) {
-            p.out[b * p.o_b + h * p.o_h + d] = T::round(sum == 0.0f ? 0.0f : y / sum);
-            if (p.lse && d == 0)
-                p.lse[b * p.l_b + h * p.l_h] = sum == 0.0f ? -INFINITY : (base - kShift<T> + log2f(sum)) * kLn2Hi;
-        } else {
-            const int64_t row = (static_cast<int64_t>(b) * p.splits + split) * p.nq + h;
-            p.part[row * D + d] = y;
-            if (d == 0) {
-                p.stat[2 * row] = top;
-                p.stat[2 * row + 1] = sum;
+            for (int w = 0; w < kWaves; ++w) {
+                sum = fmaf(stat_l[w][r], __builtin_amdgcn_exp2f(stat_m[w][r] - base), sum);
+                y += part[w][r][d];
+            }
+            if (whole) {
+                write_row<T>(p, b, h0 + r, d, y, sum, base);
+            } else {
+                p.part[(row0 + r) * D + d] = y;
+                if (d == 0) {
+                    p.stat[2 * (row0 + r)] = top;
+                    p.stat[2 * (row0 + r) + 1] = sum;
+                }
             }
         }
+        if (!whole && step0 == 0 && tid == 0)
+            p.open[wg] = Open{b, unit, static_cast<int32_t>((pos + rounds - 1) / per), 0};
+
+        // the next unit
+        pos += steps;
+        if (pos >= stop)
+            return;
+        step0 = 0;
+        if (++unit == units) {
+            unit = 0;
+            do
+                n = visible(p, ++b);
+            while (n < 0);  // (pos < stop: there is one)
+            rounds = rounds_of(n, kRound);
+        }
+        __syncthreads();  // LDS is free again
     }
 }
 
-// One workgroup per (request, query head): the splits' partial sums joined.
+// A workgroup per unit that lies across several runs and kJoinRows of its rows:
+// the runs' partial sums joined, several of them on their way at once (it is
+// the latency of these reads that the kernel costs).
 template <typename T, int D>
-__global__ void __launch_bounds__(D) ssu_attn_join_kernel(const AttnParams p)
+__global__ void __launch_bounds__(64 * kJoinRows) ssu_attn_join_kernel(const AttnParams p)
 {
-    const int b = static_cast<int>(blockIdx.x) / p.nq, h = static_cast<int>(blockIdx.x) % p.nq;
-    const int d = static_cast<int>(threadIdx.x);
-    const Share sh = share_of(p, b, 0);
-    if (sh.n < 0 || sh.active == 1)
-        return;  // padding, or written already
-    const int64_t row0 = static_cast<int64_t>(b) * p.splits * p.nq + h;
-    float top = -INFINITY, sum = 0.0f, y = 0.0f;
-    for (int s = 0; s < sh.active; ++s)
-        top = fmaxf(top, p.stat[2 * (row0 + static_cast<int64_t>(s) * p.nq)]);
+    constexpr int E = D / 64;
+    const int wg = static_cast<int>(blockIdx.x) / (16 / kJoinRows);
+    const int r = static_cast<int>(blockIdx.x) % (16 / kJoinRows) * kJoinRows + (static_cast<int>(threadIdx.x) >> 6);
+    const Open u = p.open[wg];
+    if (u.b < 0)
+        return;
+    const int kh = u.unit / p.row_tiles, rt = u.unit - kh * p.row_tiles, lane = static_cast<int>(threadIdx.x) & 63;
+    if (r >= min(p.heads_per_kv - rt * 16, 16))
+        return;
+    // this workgroup's last unit, then the first ones of those up to u.last
+    auto row_of = [&](int w) { return (2 * static_cast<int64_t>(w) + (w == wg)) * 16 + r; };
+    float top = -INFINITY;
+    for (int w = wg + lane; w <= u.last; w += 64)
+        top = fmaxf(top, p.stat[2 * row_of(w)]);
+#pragma unroll
+    for (int m = 32; m >= 1; m /= 2)
+        top = fmaxf(top, __shfl_xor(top, m));
     const float base = top == -INFINITY ? 0.0f : top;
-    for (int s = 0; s < sh.active; ++s) {
-        const int64_t row = row0 + static_cast<int64_t>(s) * p.nq;
+    float sum = 0.0f, y[E] = {};
+#pragma unroll 8
+    for (int w = wg; w <= u.last; ++w) {
+        const int64_t row = row_of(w);
         const float f = __builtin_amdgcn_exp2f(p.stat[2 * row] - base);
         sum = fmaf(p.stat[2 * row + 1], f, sum);
-        y = fmaf(p.part[row * D + d], f, y);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            y[e] = fmaf(p.part[row * D + lane + 64 * e], f, y[e]);
     }
-    p.out[b * p.o_b + h * p.o_h + d] = T::round(sum == 0.0f ? 0.0f : y / sum);
-    if (p.lse && d == 0)
-        p.lse[b * p.l_b + h * p.l_h] = sum == 0.0f ? -INFINITY : (base - kShift<T> + log2f(sum)) * kLn2Hi;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        write_row<T>(p, u.b, kh * p.heads_per_kv + rt * 16 + r, lane + 64 * e, y[e], sum, base);
 }
 
 using AttnFn = void (*)(AttnParams);
@@ -365,7 +491,7 @@ ssu_status check_sizes(const ssu_attn_args &a, const char *who)
         return fail(SSU_ERR_INVALID_ARGUMENT, "%s: %d key heads do not divide %d query heads", who, a.nk, a.nq);
     if (a.headdim != 64 && a.headdim != 128 && a.headdim != 256)
         return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d is not 64, 128 or 256", who, a.headdim);
-    if (static_cast<int64_t>(a.batch) * a.nq > 0x7fffffff / kMaxSplits)
+    if (static_cast<int64_t>(a.batch) * a.nq > 0x7fffffff)
         return fail(SSU_ERR_UNSUPPORTED, "%s: batch * nq %lld too large", who, static_cast<long long>(a.batch) * a.nq);
     if (a.max_pages > INT64_MAX / a.page_size)
         return fail(SSU_ERR_INVALID_ARGUMENT, "%s: max_pages * page_size too large", who);
@@ -373,28 +499,29 @@ ssu_status check_sizes(const ssu_attn_args &a, const char *who)
 }
 
 struct Plan {
-    int row_tiles, splits, min_rounds;
-    int64_t stat_at, bytes;  // workspace: floats before the statistics, bytes in all
+    int row_tiles, groups;
+    int64_t part_at, stat_at, bytes;  // workspace
 };
 
-// How many splits each request's length may take: enough workgroups to fill
-// the chip several times over (lengths differ), no more than the table's room
-// needs.
+// One workgroup per CU at D = 128, where four waves' loads are enough to fill
+// the memory system and more only crowd it (64 requests up to 8192 tokens, 8
+// heads: 184 against 189 us with two; 3 of 100003 tokens, 4 heads: 118.5 against
+// 123), but two where the runs hold many units, each with its start and its
+// join (512 requests up to 600 tokens, 4 heads: 82 against 102 us); two at the
+// smaller steps of D = 64 (64 requests up to 8192 tokens: 106 against 121 us) and
+// at D = 256 (see waves_for). No more than there can be steps.
 Plan plan_of(const ssu_attn_args &a)
 {
     Plan p{};
     p.row_tiles = (a.nq / a.nk + 15) / 16;
     const int64_t units = static_cast<int64_t>(a.batch) * a.nk * p.row_tiles;
-    const int64_t rounds = (a.max_pages * a.page_size + kRound - 1) / kRound;
-    p.min_rounds = units >= kNumCUs ? 4 : 1;
-    const int64_t want = units > 0 ? (16 * kNumCUs + units - 1) / units : 1;
-    const int64_t most = (rounds + p.min_rounds - 1) / p.min_rounds;
-    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, kMaxSplits})));
-    if (p.splits > 1) {
-        const int64_t rows = static_cast<int64_t>(a.batch) * p.splits * a.nq;
-        p.stat_at = rows * a.headdim;
-        p.bytes = (p.stat_at + 2 * rows) * 4;
-    }
+    const int round = waves_for(a.headdim) * kTile;
+    const int64_t rounds = std::max<int64_t>((a.max_pages * a.page_size + round - 1) / round, 1);
+    const int64_t resident = a.headdim == 128 && units <= 4 * kNumCUs ? kNumCUs : 2 * kNumCUs;
+    p.groups = static_cast<int>(units > resident / rounds ? resident : std::max<int64_t>(units * rounds, 1));
+    p.part_at = static_cast<int64_t>(p.groups) * sizeof(Open);
+    p.stat_at = p.part_at + static_cast<int64_t>(p.groups) * 32 * a.headdim * 4;
+    p.bytes = p.stat_at + static_cast<int64_t>(p.groups) * 32 * 2 * 4;
     return p;
 }
 
@@ -457,13 +584,11 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     if (a.batch == 0)
         return SSU_OK;
     const Plan plan = plan_of(a);
-    if (plan.bytes > 0) {
-        if (!a.workspace || a.workspace_bytes < plan.bytes)
-            return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_paged_attention: workspace of %lld bytes, %lld needed",
-                        static_cast<long long>(a.workspace ? a.workspace_bytes : 0), static_cast<long long>(plan.bytes));
-        if (reinterpret_cast<uintptr_t>(a.workspace) % 16)
-            return fail(SSU_ERR_MISALIGNED, "ssu_paged_attention: workspace must be 16-byte aligned");
-    }
+    if (!a.workspace || a.workspace_bytes < plan.bytes)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_paged_attention: workspace of %lld bytes, %lld needed",
+                    static_cast<long long>(a.workspace ? a.workspace_bytes : 0), static_cast<long long>(plan.bytes));
+    if (reinterpret_cast<uintptr_t>(a.workspace) % 16)
+        return fail(SSU_ERR_MISALIGNED, "ssu_paged_attention: workspace must be 16-byte aligned");
     AttnParams p{};
     p.q = static_cast<const uint16_t *>(a.q.ptr);
     p.q_b = a.q.stride[0];
@@ -493,19 +618,19 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     p.heads_per_kv = a.nq / a.nk;
     p.page_size = a.page_size;
     p.row_tiles = plan.row_tiles;
-    p.splits = plan.splits;
-    p.min_rounds = plan.min_rounds;
+    p.groups = plan.groups;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-    p.part = static_cast<float *>(a.workspace);
-    p.stat = p.part + plan.stat_at;
-    p.total = a.batch * a.nk * plan.row_tiles * plan.splits;
+    char *const ws = static_cast<char *>(a.workspace);
+    p.open = reinterpret_cast<Open *>(ws);
+    p.part = reinterpret_cast<float *>(ws + plan.part_at);
+    p.stat = reinterpret_cast<float *>(ws + plan.stat_at);
     const bool page16 = a.page_size % 16 == 0;
     const AttnKernels k = a.q.dtype == SSU_BF16 ? attn_kernels<Bf16>(a.headdim, page16) : attn_kernels<F16>(a.headdim, page16);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
-    hipError_t e = launch_kernel(k.split, p, p.total, 64 * kWaves, 0, stream);
-    if (e == hipSuccess && plan.splits > 1)
-        e = launch_kernel(k.join, p, static_cast<int64_t>(a.batch) * a.nq, a.headdim, 0, stream);
+    hipError_t e = launch_kernel(k.split, p, plan.groups, 64 * waves_for(a.headdim), 0, stream);
+    if (e == hipSuccess && plan.groups > 1)
+        e = launch_kernel(k.join, p, plan.groups * (16 / kJoinRows), 64 * kJoinRows, 0, stream);
     if (e != hipSuccess)
         return fail(SSU_ERR_HIP, "launch of the paged attention kernels failed: %s", hipGetErrorString(e));
     return SSU_OK;

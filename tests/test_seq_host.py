@@ -186,7 +186,7 @@ ATTN_BAD = [
     ({"q.0": -1}, INVALID), ({"lse.reserved": 1}, INVALID),
     ({"q.2": 2}, UNSUPPORTED), ({"out.2": 2}, UNSUPPORTED), ({"k_cache.3": 0}, UNSUPPORTED), ({"table.1": 2}, UNSUPPORTED),
     ({"lens.0": 2}, UNSUPPORTED), ({"q.ptr": 0x10001}, MISALIGNED), ({"table.ptr": 0x10002}, MISALIGNED),
-    ({"lse.ptr": 0x10002}, MISALIGNED),
+    ({"lse.ptr": 0x10002}, MISALIGNED), (dict(ws=0), INVALID), (dict(ws_bytes=64), INVALID), (dict(ws=0x20008), MISALIGNED),
 ]
 
 
