@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -11,6 +12,18 @@
 #include "internal.h"
 #include "seq_common.h"
 
+#ifndef SEG_WANT
+#define SEG_WANT 2
+#endif
+#ifndef SEG_MAX
+#define SEG_MAX 32
+#endif
+#ifndef SEG_MIN
+#define SEG_MIN 4
+#endif
+#ifndef SEG_UNCUT
+#define SEG_UNCUT 4
+#endif
 namespace ssu {
 namespace {
 
@@ -119,6 +132,487 @@ __global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearPa
                 store4<true>(sp + (row0 + j * RPI) * p.s_row + 128 * e, s[j][e]);
 }
 
+// Prompts, 64 tokens (a chunk) at a time. With L_i the decays' logarithms summed
+// from the chunk's start, S the state before it:
+//
+//   out_i = scale * ( exp(L_i) S q_i + sum_{j <= i} exp(L_i - L_j) beta_j (k_j . q_i) v_j )
+//   S     = exp(L_63) S + sum_j exp(L_63 - L_j) beta_j v_j k_j^T
+//
+// One workgroup of four waves takes a segment of a sequence, one head and 64 NW
+// columns of v (rows p of the state); wave w owns columns 16 NW w .. of them,
+// whose state stays in its registers as the result tiles of the second line's
+// product (its n in tile m, row r is r * MT + m, MT = N/16). Places of a
+// contracted axis may stand for any value as long as both operands agree, which
+// is used throughout so that no operand needs a transposition across lanes:
+//
+//  - a lane's state values, r by r, are 8 consecutive n: they are the fragments
+//    of S q (as a bf16 pair, value and remainder), against 16-byte runs of q;
+//  - the scores k_j . q_i come out with 4 consecutive j per lane, and those of
+//    two 16-token tiles are a fragment of their product with v; wave w computes
+//    those of tokens 16 w .. 16 w + 15 and passes them on through LDS, also as a
+//    pair;
+//  - k is read for the update in runs of MT values of 8 tokens per lane and
+//    transposed inside the lane by byte permutes.
+//
+// The update's operand exp(L_63 - L_j) beta_j v_j is split into three bf16 (2^-24
+// relative): the state is fp32 and is handed on. L is summed in fp64 and in
+// units of log 2: a difference of two sums keeps its digits behind a reset.
+//
+// Long sequences are cut into segments: a first kernel (FULL = false) computes
+// every segment's own contribution to the state, and the second starts each
+// from the sum of those before it. The last segment's place in the workspace
+// holds the sequence's first state, which the last segment overwrites in the
+// pool while the first one may still start.
+constexpr int kChunk = 64;
+constexpr float kDecayFloor = -1.0e4f;  // exp is 0 far above it; sums of it stay finite
+
+struct ChunkParams {
+    LinearParams a;
+    float *states;  // [segments, nheads, headdim, dstate]
+    float *decays;  // [segments, nheads]: a segment's whole decay
+    int32_t seg_len, segments, slices, dstate, total, pad;
+};
+
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack2<Bf16>(x, y);
+    lo = pack2<Bf16>(x - Bf16::lo(hi), y - Bf16::hi(hi));
+}
+
+template <int N, int NW, bool FULL>
+__global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_kernel(const ChunkParams p)
+{
+    constexpr int MT = N / 16;        // state tiles along n
+    constexpr int KS = N / 32;        // products along n of a score
+    constexpr int PC = 64 * NW;       // columns of v
+    constexpr int ROW = N + 8;        // pitch of q and k in LDS (16 bytes more than a row: no bank twice)
+    constexpr int VROW = PC + 8;
+    constexpr int QU = N * kChunk / 8 / 256;   // 16-byte runs of q and of k per thread
+    constexpr int VU = PC * kChunk / 8 / 256;  // of v
+    using KW = uint32_t __attribute__((ext_vector_type(MT / 2)));
+    typedef KW KW_row __attribute__((aligned(MT < 8 ? 2 * MT : 16)));
+
+    __shared__ __attribute__((aligned(16))) uint16_t lq[FULL ? kChunk * ROW : 8];
+    __shared__ __attribute__((aligned(16))) uint16_t lk[kChunk * ROW];
+    __shared__ __attribute__((aligned(16))) uint16_t lv[kChunk * VROW];
+    __shared__ u32x4 lw[FULL ? 4 : 1][2][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
+    __shared__ double lsum[2][kChunk];            // L, in units of log 2
+    __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
+    __shared__ int bad[2], found;
+
+    const LinearParams &a = p.a;
+    int id = xcd_order(static_cast<int>(blockIdx.x), p.total);
+    const int slice = id % p.slices;
+    id /= p.slices;
+    const int h = id % a.nheads, f = id / a.nheads, grp = h / a.heads_per_group;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // segment f of all: sequence b's are cu[b] / seg_len + b and the following
+    // (distinct for ordered sequences)
+    if (tid == 0)
+        found = -1;
+    __syncthreads();
+    for (int b = tid; b < a.batch; b += 256) {
+        const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
+        const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
+        const int64_t s = f - (lo / p.seg_len + b);
+        if (s >= 0 && s * p.seg_len < hi - lo)
+            found = b;
+    }
+    __syncthreads();
+    const int b = __builtin_amdgcn_readfirstlane(found);
+    if (b < 0)
+        return;
+    const int64_t slot = load_index(a.idx, a.idx64, b);
+    if (slot < 0 || slot >= a.pool_slots)
+        return;  // padding
+    const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
+    const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
+    const int base = static_cast<int>(lo / p.seg_len) + b, seg = f - base;
+    const int segs = static_cast<int>((hi - lo + p.seg_len - 1) / p.seg_len);
+    const int64_t begin = lo + static_cast<int64_t>(seg) * p.seg_len, end = min(begin + p.seg_len, hi);
+    if (!FULL && segs == 1)
+        return;
+
+    const int p0 = slice * PC + wave * 16 * NW;  // this wave's first column
+    const bool live = p0 < a.headdim;
+    const int prow = p0 + c * NW;                // this lane's first
+    float *const pool = a.state + slot * a.s_slot + h * a.s_head;
+    const int64_t plane = static_cast<int64_t>(a.headdim) * p.dstate;
+    auto seg_state = [&](int s) { return p.states + (static_cast<int64_t>(base + s) * a.nheads + h) * plane; };
+
+    f32x4 st[MT][NW];
+    // the lane's state values n = (4g + r) MT + m of row `prow + w`
+    auto each_run = [&](auto &&fn) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (live && (4 * g + r) * MT < p.dstate)
+                    fn(w, r, (4 * g + r) * MT);
+    };
+    auto load_state = [&](const float *src, int64_t row, float keep, bool add) {
+        each_run([&](int w, int r, int n) {
+            const float *const at = src + (prow + w) * row + n;
+#pragma unroll
+            for (int m = 0; m < MT; m += (MT < 4 ? 2 : 4)) {
+                float x[4];
+                if constexpr (MT < 4) {
+                    x[0] = at[m];
+                    x[1] = at[m + 1];
+                } else {
+                    const f32x4 y = *reinterpret_cast<const f32x4 *>(at + m);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = y[e];
+                }
+#pragma unroll
+                for (int e = 0; e < (MT < 4 ? 2 : 4); ++e)
+                    st[m + e][w][r] = add ? fmaf(st[m + e][w][r], keep, x[e]) : x[e];
+            }
+        });
+    };
+    auto store_state = [&](float *dst, int64_t row) {
+        each_run([&](int w, int r, int n) {
+            float *const at = dst + (prow + w) * row + n;
+#pragma unroll
+            for (int m = 0; m < MT; m += (MT < 4 ? 2 : 4)) {
+                if constexpr (MT < 4) {
+                    at[m] = st[m][w][r];
+                    at[m + 1] = st[m + 1][w][r];
+                } else {
+                    *reinterpret_cast<f32x4 *>(at + m) = f32x4{st[m][w][r], st[m + 1][w][r], st[m + 2][w][r], st[m + 3][w][r]};
+                }
+            }
+        });
+    };
+
+    // requests of a chunk: rows behind the segment's end come from its last row
+    // and count as zeros
+    u32x4 rq[QU], rk[QU], rv[VU];
+    float rdecay = 0.0f, rbeta = 0.0f;
+    auto request = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < QU; ++i) {
+            const int u = tid + 256 * i, n = u % (N / 8) * 8;
+            const int64_t t = min(t0 + u / (N / 8), end - 1);
+            const int col = n < p.dstate ? n : 0;
+            if constexpr (FULL)
+                rq[i] = *reinterpret_cast<const u32x4_a2 *>(a.q + t * a.q_t + grp * a.q_g + col);
+            rk[i] = *reinterpret_cast<const u32x4_a2 *>(a.k + t * a.k_t + grp * a.k_g + col);
+        }
+#pragma unroll
+        for (int i = 0; i < VU; ++i) {
+            const int u = tid + 256 * i, col = slice * PC + u % (PC / 8) * 8;
+            const int64_t t = min(t0 + u / (PC / 8), end - 1);
+            rv[i] = *reinterpret_cast<const u32x4_a2 *>(a.v + t * a.v_t + h * a.v_h + (col < a.headdim ? col : 0));
+        }
+        if (wave == 0) {
+            const int64_t t = min(t0 + lane, end - 1);
+            rdecay = a.decay[t * a.d_t + h * a.d_h];
+            rbeta = a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f;
+        }
+    };
+    // L and what follows from it, by the first wave
+    double whole = 0.0;  // of the segment so far
+    auto sums = [&](int64_t t0, int buf) {
+        const bool in = t0 + lane < end;
+        const float d = rdecay < kDecayFloor ? kDecayFloor : rdecay;  // (NaN stays)
+        double sum = in ? static_cast<double>(d) * 1.4426950408889634 : 0.0;
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const double up = __shfl_up(sum, m);
+            sum += lane >= m ? up : 0.0;
+        }
+        const double all = __shfl(sum, 63);
+        const float gain = in ? rbeta : 0.0f;
+        whole += all;
+        lsum[buf][lane] = sum;
+        lbeta[buf][lane] = gain;
+        lgrow[buf][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum));
+        llate[buf][lane] = in ? gain * __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) : 0.0f;
+        if (lane == 0) {
+            lall[buf] = __builtin_amdgcn_exp2f(static_cast<float>(all));
+            bad[buf] = 0;
+        }
+    };
+    auto place = [&](int64_t t0, int buf) {
+        const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < QU; ++i) {
+            const int u = tid + 256 * i, t = u / (N / 8), n = u % (N / 8) * 8;
+            const bool in = t0 + t < end && n < p.dstate;
+            if constexpr (FULL)
+                *reinterpret_cast<u32x4 *>(lq + t * ROW + n) = in ? rq[i] : zero;
+            *reinterpret_cast<u32x4 *>(lk + t * ROW + n) = in ? rk[i] : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < VU; ++i) {
+            const int u = tid + 256 * i, t = u / (PC / 8), col = u % (PC / 8) * 8;
+            const bool in = t0 + t < end && slice * PC + col < a.headdim;
+            const u32x4 x = in ? rv[i] : zero;
+            *reinterpret_cast<u32x4 *>(lv + t * VROW + col) = x;
+            if constexpr (FULL) {
+                bool odd = false;  // an infinity or NaN
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    odd |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+                if (odd)
+                    bad[buf] = 1;
+            }
+        }
+    };
+
+    request(begin);
+    // the state before the segment
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            st[m][w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (FULL) {
+        if (segs == 1)
+            load_state(pool, a.s_row, 1.0f, false);
+        else if (seg == 0)
+            load_state(seg_state(segs - 1), p.dstate, 1.0f, false);
+        else
+            for (int s = 0; s < seg; ++s)
+                load_state(seg_state(s), p.dstate, p.decays[static_cast<int64_t>(base + s) * a.nheads + h], s > 0);
+    } else {
+        if (seg == 0 || seg == segs - 1)
+            load_state(pool, a.s_row, 1.0f, false);
+        if (seg == segs - 1) {
+            store_state(seg_state(seg), p.dstate);
+            return;
+        }
+    }
+    if (wave == 0)
+        sums(begin, 0);
+    __syncthreads();  // (bad is set by place)
+    place(begin, 0);
+    __syncthreads();
+
+    int buf = 0;
+    for (int64_t t0 = begin; t0 < end; t0 += kChunk, buf ^= 1) {
+        const int64_t next = t0 + kChunk;
+        const bool more = next < end;
+        if (more)
+            request(next);
+
+        // v of the wave's columns as fragments: 8 tokens of 32 per lane
+        u32x4 vf[2][NW];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint16_t *const at = lv + (32 * s + 16 * (i / 4) + 4 * g + i % 4) * VROW + wave * 16 * NW + c * NW;
+                if constexpr (NW == 1)
+                    x[i] = *at;
+                else
+                    x[i] = *reinterpret_cast<const uint32_t *>(at);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                vf[s][0][i] = low_halves(x[2 * i], x[2 * i + 1]);
+                if constexpr (NW == 2)
+                    vf[s][1][i] = high_halves(x[2 * i], x[2 * i + 1]);
+            }
+        }
+
+        if constexpr (FULL) {
+            // scores of tokens i = 16 wave + c against j <= i, weighted
+            {
+                u32x4 qf[KS];
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    qf[s] = *reinterpret_cast<const u32x4 *>(lq + (16 * wave + c) * ROW + g * (N / 4) + s * 8);
+                const double li = lsum[buf][16 * wave + c];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    u32x4 fh = {0, 0, 0, 0}, fl = {0, 0, 0, 0};
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int jt = 2 * s + u;
+                        if (jt > wave)
+                            continue;
+                        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int e = 0; e < KS; ++e) {
+                            const u32x4 kf = *reinterpret_cast<const u32x4 *>(lk + (16 * jt + c) * ROW + g * (N / 4) + e * 8);
+                            x = Mma<Bf16>::run(kf, qf[e], x);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int j = 16 * jt + 4 * g + r;
+                            const float w = lbeta[buf][j] * __builtin_amdgcn_exp2f(static_cast<float>(li - lsum[buf][j]));
+                            x[r] = j <= 16 * wave + c ? x[r] * w : 0.0f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t wh, wl;
+                            split_pair(x[2 * e], x[2 * e + 1], wh, wl);
+                            fh[2 * u + e] = wh;
+                            fl[2 * u + e] = wl;
+                        }
+                    }
+                    if (2 * s <= wave) {
+                        lw[wave][s][0][lane] = fh;
+                        lw[wave][s][1][lane] = fl;
+                    }
+                }
+            }
+
+            // S q, all tokens: result rows p, columns i
+            f32x4 o[NW][4];
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+                    o[w][it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                u32x4 fh[NW], fl[NW];
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int x = s * 8 + 2 * e, y = x + 1;
+                        uint32_t wh, wl;
+                        split_pair(st[x % MT][w][x / MT], st[y % MT][w][y / MT], wh, wl);
+                        fh[w][e] = wh;
+                        fl[w][e] = wl;
+                    }
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const u32x4 qf = *reinterpret_cast<const u32x4 *>(lq + (16 * it + c) * ROW + g * (N / 4) + s * 8);
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        o[w][it] = Mma<Bf16>::run(fh[w], qf, o[w][it]);
+                        o[w][it] = Mma<Bf16>::run(fl[w], qf, o[w][it]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const float grow = lgrow[buf][16 * it + c];
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+                    o[w][it] *= grow;
+            }
+            __syncthreads();  // the scores are there
+            if (!bad[buf]) {
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int s = 0; s <= it / 2; ++s) {
+                        const u32x4 fh = lw[it][s][0][lane], fl = lw[it][s][1][lane];
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            o[w][it] = Mma<Bf16>::run(vf[s][w], fh, o[w][it]);
+                            o[w][it] = Mma<Bf16>::run(vf[s][w], fl, o[w][it]);
+                        }
+                    }
+            } else {
+                // v holds infinities or NaN: a product would carry them, times the
+                // zeros of the scores, to the tokens before; sum token by token
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+                    for (int j = 0; j <= 16 * it + c; ++j) {
+                        const uint16_t *const at = reinterpret_cast<const uint16_t *>(&lw[it][j / 32][0][16 * (j % 16 / 4) + c]) +
+                                                   4 * (j % 32 / 16) + j % 4;
+                        const float x = Bf16::lo(at[0]) + Bf16::lo(at[64 * 8]);
+#pragma unroll
+                        for (int w = 0; w < NW; ++w)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                o[w][it][r] = fmaf(x, Bf16::lo(lv[j * VROW + wave * 16 * NW + (4 * g + r) * NW + w]), o[w][it][r]);
+                    }
+            }
+            if (live)
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int64_t t = t0 + 16 * it + c;
+                    if (t >= end)
+                        continue;
+                    uint16_t *const at = a.out + t * a.o_t + h * a.o_h + p0 + 4 * g * NW;
+                    uint32_t x[2 * NW];
+#pragma unroll
+                    for (int e = 0; e < 2 * NW; ++e)
+                        x[e] = NW == 1 ? pack2<Bf16>(a.scale * o[0][it][2 * e], a.scale * o[0][it][2 * e + 1])
+                                       : pack2<Bf16>(a.scale * o[0][it][e], a.scale * o[NW - 1][it][e]);
+                    if constexpr (NW == 1)
+                        *reinterpret_cast<u32x2_a2 *>(at) = u32x2{x[0], x[1]};
+                    else
+                        *reinterpret_cast<u32x4_a2 *>(at) = u32x4{x[0], x[1], x[2 % (2 * NW)], x[3 % (2 * NW)]};
+                }
+        }
+
+        // the state behind the chunk
+        const float all = lall[buf];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                st[m][w] *= all;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4 f1[NW], f2[NW], f3[NW];
+            const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 4 * g]);
+            const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 16 + 4 * g]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f32x4 &late = e < 2 ? late0 : late1;
+                    const float x = Bf16::lo(vf[s][w][e]) * late[2 * e % 4], y = Bf16::hi(vf[s][w][e]) * late[2 * e % 4 + 1];
+                    uint32_t h1, h2;
+                    h1 = pack2<Bf16>(x, y);
+                    const float x1 = x - Bf16::lo(h1), y1 = y - Bf16::hi(h1);
+                    h2 = pack2<Bf16>(x1, y1);
+                    f1[w][e] = h1;
+                    f2[w][e] = h2;
+                    f3[w][e] = pack2<Bf16>(x1 - Bf16::lo(h2), y1 - Bf16::hi(h2));
+                }
+            KW kr[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                kr[i] = *reinterpret_cast<const KW_row *>(lk + (32 * s + 16 * (i / 4) + 4 * g + i % 4) * ROW + c * MT);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                u32x4 kf;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    kf[i] = m % 2 ? high_halves(kr[2 * i][m / 2], kr[2 * i + 1][m / 2])
+                                  : low_halves(kr[2 * i][m / 2], kr[2 * i + 1][m / 2]);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    st[m][w] = Mma<Bf16>::run(kf, f1[w], st[m][w]);
+                    st[m][w] = Mma<Bf16>::run(kf, f2[w], st[m][w]);
+                    st[m][w] = Mma<Bf16>::run(kf, f3[w], st[m][w]);
+                }
+            }
+        }
+        if (more) {
+            if (wave == 0)
+                sums(next, buf ^ 1);
+            __syncthreads();  // LDS is free again
+            place(next, buf ^ 1);
+            __syncthreads();
+        }
+    }
+
+    if constexpr (FULL) {
+        if (seg == segs - 1)
+            store_state(pool, a.s_row);
+    } else {
+        store_state(seg_state(seg), p.dstate);
+        if (slice == 0 && tid == 0)
+            p.decays[static_cast<int64_t>(f) * a.nheads + h] = __builtin_amdgcn_exp2f(static_cast<float>(whole));
+    }
+}
+
 using LinearFn = void (*)(LinearParams);
 
 struct LinearKernel {
@@ -131,6 +625,30 @@ constexpr LinearKernel recurrent()
 {
     constexpr int VEC = N > 128 ? N / 128 : 1;
     return {&ssu_linear_recurrent_kernel<N, R>, 64 / (N / (4 * VEC)) * R};
+}
+
+using ChunkFn = void (*)(ChunkParams);
+
+struct ChunkKernels {
+    ChunkFn states, full;
+    int columns;  // of v per workgroup
+};
+
+template <int N, int NW>
+constexpr ChunkKernels chunk_kernels()
+{
+    return {&ssu_linear_chunk_kernel<N, NW, false>, &ssu_linear_chunk_kernel<N, NW, true>, 64 * NW};
+}
+
+ChunkKernels chunk_kernels(int N, int P)
+{
+    switch (N) {
+    case 16:
+    case 32: return chunk_kernels<32, 1>();
+    case 64: return chunk_kernels<64, 1>();
+    case 128: return P % 128 == 0 ? chunk_kernels<128, 2>() : chunk_kernels<128, 1>();
+    default: return chunk_kernels<256, 1>();
+    }
 }
 
 LinearKernel recurrent_kernel(int N)
@@ -159,9 +677,33 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
         return fail(SSU_ERR_UNSUPPORTED, "%s: dstate %d is not 16, 32, 64, 128 or 256", who, a.dstate);
     if (a.ntokens > 0x7fffffff)
         return fail(SSU_ERR_UNSUPPORTED, "%s: more than 2^31 tokens", who);
-    if (static_cast<int64_t>(a.batch) * a.nheads * (a.headdim / 16) > 0x7fffffff)
+    if ((a.ntokens / kChunk + a.batch) * a.nheads > 0x7fffffff / (a.headdim / 16))
         return fail(SSU_ERR_UNSUPPORTED, "%s: batch * nheads too large", who);
     return SSU_OK;
+}
+
+// Segments of a prompt call: enough workgroups to fill the chip.
+struct Plan {
+    int seg_len, segments, slices;
+    int64_t decays_at, bytes;  // workspace (0: one segment per sequence)
+};
+
+Plan plan_of(const ssu_linear_args &a)
+{
+    Plan p{};
+    const int columns = chunk_kernels(a.dstate, a.headdim).columns;
+    p.slices = (a.headdim + columns - 1) / columns;
+    const int64_t units = static_cast<int64_t>(a.nheads) * p.slices;
+    const int64_t chunks = (a.ntokens + kChunk - 1) / kChunk;
+    const int64_t per = std::max<int64_t>({(chunks * units + SEG_WANT * kNumCUs - 1) / (SEG_WANT * kNumCUs), (chunks + SEG_MAX - 1) / SEG_MAX, SEG_MIN});
+    const bool cut = per < chunks && a.batch * units < SEG_UNCUT * kNumCUs;
+    p.seg_len = cut ? static_cast<int>(per * kChunk) : std::max<int>(static_cast<int>(std::min<int64_t>(a.ntokens, INT32_MAX)), 1);
+    p.segments = static_cast<int>(a.ntokens / p.seg_len) + a.batch;
+    if (cut) {
+        p.decays_at = static_cast<int64_t>(p.segments) * a.nheads * a.headdim * a.dstate * 4;
+        p.bytes = p.decays_at + static_cast<int64_t>(p.segments) * a.nheads * 4;
+    }
+    return p;
 }
 
 ssu_status check_linear(const ssu_linear_args &a, const char *who, bool prompts)
@@ -261,6 +803,38 @@ ssu_status launch_recurrent(const ssu_linear_args &a, hipStream_t stream)
     return SSU_OK;
 }
 
+ssu_status launch_chunks(const ssu_linear_args &a, hipStream_t stream)
+{
+    const Plan plan = plan_of(a);
+    if (plan.bytes > 0) {
+        if (!a.workspace || a.workspace_bytes < plan.bytes)
+            return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_linear_attention: workspace of %lld bytes, %lld needed",
+                        static_cast<long long>(a.workspace ? a.workspace_bytes : 0), static_cast<long long>(plan.bytes));
+        if (reinterpret_cast<uintptr_t>(a.workspace) % 16)
+            return fail(SSU_ERR_MISALIGNED, "ssu_linear_attention: workspace must be 16-byte aligned");
+    }
+    const ChunkKernels k = chunk_kernels(a.dstate, a.headdim);
+    ChunkParams p{};
+    p.a = linear_params(a);
+    p.states = static_cast<float *>(a.workspace);
+    p.decays = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + plan.decays_at);
+    p.seg_len = plan.seg_len;
+    p.segments = plan.segments;
+    p.slices = plan.slices;
+    p.dstate = a.dstate;
+    p.total = plan.segments * a.nheads * plan.slices;
+    DeviceGuard guard;
+    SSU_TRY(guard.enter(a.device));
+    hipError_t e = hipSuccess;
+    if (plan.bytes > 0)
+        e = launch_kernel(k.states, p, p.total, 256, 0, stream);
+    if (e == hipSuccess)
+        e = launch_kernel(k.full, p, p.total, 256, 0, stream);
+    if (e != hipSuccess)
+        return fail(SSU_ERR_HIP, "launch of the chunked linear attention failed: %s", hipGetErrorString(e));
+    return SSU_OK;
+}
+
 }  // namespace
 }  // namespace ssu
 
@@ -271,7 +845,7 @@ int64_t ssu_linear_attention_workspace(const ssu_linear_args *a)
     using namespace ssu;
     if (!a || check_sizes(*a, "ssu_linear_attention_workspace") != SSU_OK)
         return -1;
-    return 0;
+    return plan_of(*a).bytes;
 }
 
 ssu_status ssu_linear_attention(const ssu_linear_args *a, hipStream_t stream)
@@ -282,7 +856,7 @@ ssu_status ssu_linear_attention(const ssu_linear_args *a, hipStream_t stream)
     SSU_TRY(check_linear(*a, "ssu_linear_attention", true));
     if (a->batch == 0 || a->ntokens == 0)
         return SSU_OK;
-    return launch_recurrent(*a, stream);
+    return launch_chunks(*a, stream);
 }
 
 ssu_status ssu_linear_attention_step(const ssu_linear_args *a, hipStream_t stream)
