@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
     __shared__ __attribute__((aligned(16))) uint16_t lk[kChunk * ROW];
     __shared__ __attribute__((aligned(16))) uint16_t lv[kChunk * VROW];
     __shared__ u32x4 lw[FULL ? 4 : 1][2][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
-    __shared__ double lsum[2][kChunk];            // L, in units of log 2
+    __shared__ float lsum[2][kChunk], lrest[2][kChunk];  // L in units of log 2: as fp32, and what that leaves
     __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
     __shared__ int bad[2], found;
 
@@ -293,23 +293,27 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
     u32x4 rq[QU], rk[QU], rv[VU];
     float rdecay = 0.0f, rbeta = 0.0f;
     auto request = [&](int64_t t0) {
+        const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
+        const uint16_t *const qt = a.q + t0 * a.q_t + grp * a.q_g, *const kt = a.k + t0 * a.k_t + grp * a.k_g;
+        const uint16_t *const vt = a.v + t0 * a.v_t + h * a.v_h;
+        // (rows times 32-bit strides: one multiplication)
+        auto row = [&](int t, int64_t stride) {
+            return static_cast<uint64_t>(static_cast<uint32_t>(min(t, last))) * static_cast<uint32_t>(stride);
+        };
 #pragma unroll
         for (int i = 0; i < QU; ++i) {
-            const int u = tid + 256 * i, n = u % (N / 8) * 8;
-            const int64_t t = min(t0 + u / (N / 8), end - 1);
-            const int col = n < p.dstate ? n : 0;
+            const int u = tid + 256 * i, n = u % (N / 8) * 8, t = u / (N / 8), col = n < p.dstate ? n : 0;
             if constexpr (FULL)
-                rq[i] = *reinterpret_cast<const u32x4_a2 *>(a.q + t * a.q_t + grp * a.q_g + col);
-            rk[i] = *reinterpret_cast<const u32x4_a2 *>(a.k + t * a.k_t + grp * a.k_g + col);
+                rq[i] = *reinterpret_cast<const u32x4_a2 *>(qt + row(t, a.q_t) + col);
+            rk[i] = *reinterpret_cast<const u32x4_a2 *>(kt + row(t, a.k_t) + col);
         }
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
             const int u = tid + 256 * i, col = slice * PC + u % (PC / 8) * 8;
-            const int64_t t = min(t0 + u / (PC / 8), end - 1);
-            rv[i] = *reinterpret_cast<const u32x4_a2 *>(a.v + t * a.v_t + h * a.v_h + (col < a.headdim ? col : 0));
+            rv[i] = *reinterpret_cast<const u32x4_a2 *>(vt + row(u / (PC / 8), a.v_t) + (col < a.headdim ? col : 0));
         }
         if (wave == 0) {
-            const int64_t t = min(t0 + lane, end - 1);
+            const int64_t t = t0 + min(lane, last);
             rdecay = a.decay[t * a.d_t + h * a.d_h];
             rbeta = a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f;
         }
@@ -328,7 +332,8 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
         const double all = __shfl(sum, 63);
         const float gain = in ? rbeta : 0.0f;
         whole += all;
-        lsum[buf][lane] = sum;
+        lsum[buf][lane] = static_cast<float>(sum);
+        lrest[buf][lane] = static_cast<float>(sum - static_cast<double>(static_cast<float>(sum)));
         lbeta[buf][lane] = gain;
         lgrow[buf][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum));
         llate[buf][lane] = in ? gain * __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) : 0.0f;
@@ -338,30 +343,46 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
         }
     };
     auto place = [&](int64_t t0, int buf) {
-        const u32x4 zero = {0, 0, 0, 0};
+        // zeros behind the segment's end, behind N (16 in a tile of 32) and behind P
+        const bool cut = t0 + kChunk > end || p.dstate < N || slice * PC + PC > a.headdim;
+        if (cut) {
 #pragma unroll
-        for (int i = 0; i < QU; ++i) {
-            const int u = tid + 256 * i, t = u / (N / 8), n = u % (N / 8) * 8;
-            const bool in = t0 + t < end && n < p.dstate;
-            if constexpr (FULL)
-                *reinterpret_cast<u32x4 *>(lq + t * ROW + n) = in ? rq[i] : zero;
-            *reinterpret_cast<u32x4 *>(lk + t * ROW + n) = in ? rk[i] : zero;
-        }
+            for (int i = 0; i < QU; ++i) {
+                const int u = tid + 256 * i;
+                if (t0 + u / (N / 8) >= end || u % (N / 8) * 8 >= p.dstate) {
+                    rk[i] = u32x4{0, 0, 0, 0};
+                    if constexpr (FULL)
+                        rq[i] = u32x4{0, 0, 0, 0};
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < VU; ++i) {
-            const int u = tid + 256 * i, t = u / (PC / 8), col = u % (PC / 8) * 8;
-            const bool in = t0 + t < end && slice * PC + col < a.headdim;
-            const u32x4 x = in ? rv[i] : zero;
-            *reinterpret_cast<u32x4 *>(lv + t * VROW + col) = x;
-            if constexpr (FULL) {
-                bool odd = false;  // an infinity or NaN
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    odd |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
-                if (odd)
-                    bad[buf] = 1;
+            for (int i = 0; i < VU; ++i) {
+                const int u = tid + 256 * i;
+                if (t0 + u / (PC / 8) >= end || slice * PC + u % (PC / 8) * 8 >= a.headdim)
+                    rv[i] = u32x4{0, 0, 0, 0};
             }
         }
+#pragma unroll
+        for (int i = 0; i < QU; ++i) {
+            const int u = tid + 256 * i, at = u / (N / 8) * ROW + u % (N / 8) * 8;
+            if constexpr (FULL)
+                *reinterpret_cast<u32x4 *>(lq + at) = rq[i];
+            *reinterpret_cast<u32x4 *>(lk + at) = rk[i];
+        }
+        using H2 = uint16_t __attribute__((ext_vector_type(2)));
+        H2 most = {0, 0};  // an infinity or NaN has the largest exponent
+#pragma unroll
+        for (int i = 0; i < VU; ++i) {
+            const int u = tid + 256 * i;
+            *reinterpret_cast<u32x4 *>(lv + u / (PC / 8) * VROW + u % (PC / 8) * 8) = rv[i];
+            if constexpr (FULL)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(H2, rv[i][e] & 0x7fff7fffu));
+        }
+        if constexpr (FULL)
+            if (most.x >= 0x7f80 || most.y >= 0x7f80)
+                bad[buf] = 1;
     };
 
     request(begin);
@@ -428,7 +449,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
                     qf[s] = *reinterpret_cast<const u32x4 *>(lq + (16 * wave + c) * ROW + g * (N / 4) + s * 8);
-                const double li = lsum[buf][16 * wave + c];
+                const float li = lsum[buf][16 * wave + c], ri = lrest[buf][16 * wave + c];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     u32x4 fh = {0, 0, 0, 0}, fl = {0, 0, 0, 0};
@@ -446,7 +467,8 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int j = 16 * jt + 4 * g + r;
-                            const float w = lbeta[buf][j] * __builtin_amdgcn_exp2f(static_cast<float>(li - lsum[buf][j]));
+                            const float d = (li - lsum[buf][j]) + (ri - lrest[buf][j]);
+                            const float w = lbeta[buf][j] * __builtin_amdgcn_exp2f(d);
                             x[r] = j <= 16 * wave + c ? x[r] * w : 0.0f;
                         }
 #pragma unroll
@@ -675,6 +697,9 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
         return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d is not a multiple of 16 in 16 .. 256", who, a.headdim);
     if (a.dstate != 16 && a.dstate != 32 && a.dstate != 64 && a.dstate != 128 && a.dstate != 256)
         return fail(SSU_ERR_UNSUPPORTED, "%s: dstate %d is not 16, 32, 64, 128 or 256", who, a.dstate);
+    for (const ssu_view *v : {&a.q, &a.k, &a.v})
+        if (v->stride[0] > 0x7fffffff)
+            return fail(SSU_ERR_UNSUPPORTED, "%s: a token stride of 2^31 elements or more", who);
     if (a.ntokens > 0x7fffffff)
         return fail(SSU_ERR_UNSUPPORTED, "%s: more than 2^31 tokens", who);
     if ((a.ntokens / kChunk + a.batch) * a.nheads > 0x7fffffff / (a.headdim / 16))

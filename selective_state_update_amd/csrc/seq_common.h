@@ -27,6 +27,7 @@ typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 // even from fp32 (the conversion is kept opaque to the compiler so that it is
 // never fused with the operation that produces its operand).
 struct Bf16 {
+    using Native = __bf16;
     static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
     static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
     static __device__ __forceinline__ uint16_t round(float f)
@@ -37,6 +38,7 @@ struct Bf16 {
 };
 
 struct F16 {
+    using Native = _Float16;
     static __device__ __forceinline__ float value(uint16_t b)
     {
         return static_cast<float>(__builtin_bit_cast(_Float16, b));
@@ -76,11 +78,14 @@ struct Mma<F16> {
     }
 };
 
-// Two fp32 values as a word of two 16-bit ones.
+// Two fp32 values as a word of two 16-bit ones, rounded to nearest even (one
+// instruction).
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
-    return static_cast<uint32_t>(T::round(lo)) | static_cast<uint32_t>(T::round(hi)) << 16;
+    using F = float __attribute__((ext_vector_type(2)));
+    using H = typename T::Native __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((F{lo, hi}), H));
 }
 
 // The 16-bit halves of two words side by side: the low ones, the high ones.
