@@ -405,13 +405,14 @@ int64_t ssu_linear_attention_workspace(const ssu_linear_args *args);
  * Errors (nothing is launched): SSU_ERR_INVALID_ARGUMENT (null pointers,
  * negative sizes or strides, wrong dtype tags, non-zero reserved fields, G not
  * dividing H, a scale that is not finite, a workspace too small),
- * SSU_ERR_UNSUPPORTED (P, N, inner strides, token strides of q, k and v of 2^31
+ * SSU_ERR_UNSUPPORTED (P, N, inner strides, token strides of q, k, v and out of 2^24
  * elements or more, more than 2^31 tokens or workgroups),
  * SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
 ssu_status ssu_linear_attention(const ssu_linear_args *args, hipStream_t stream);
 
 /* The same for one token per request: ntokens == batch, token b advances
- * request b; cu_seqlens.ptr and workspace are NULL. Same errors. */
+ * request b; cu_seqlens.ptr and workspace are NULL. Same errors, but token
+ * strides of any size. */
 ssu_status ssu_linear_attention_step(const ssu_linear_args *args, hipStream_t stream);
 
 /* ------------------------------------------ queries and keys of attention --

@@ -12,6 +12,9 @@
 #include "internal.h"
 #include "seq_common.h"
 
+#ifndef CHUNK_OCC
+#define CHUNK_OCC (W == 8 ? 2 : N == 256 ? 1 : 2)
+#endif
 #ifndef SEG_WANT
 #define SEG_WANT 2
 #endif
@@ -138,21 +141,19 @@ __global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearPa
 //   out_i = scale * ( exp(L_i) S q_i + sum_{j <= i} exp(L_i - L_j) beta_j (k_j . q_i) v_j )
 //   S     = exp(L_63) S + sum_j exp(L_63 - L_j) beta_j v_j k_j^T
 //
-// One workgroup of four waves takes a segment of a sequence, one head and 64 NW
-// columns of v (rows p of the state); wave w owns columns 16 NW w .. of them,
+// One workgroup of W waves takes a segment of a sequence, one head and 16 W
+// columns of v (rows p of the state); wave w owns columns 16 w .. 16 w + 15,
 // whose state stays in its registers as the result tiles of the second line's
-// product (its n in tile m, row r is r * MT + m, MT = N/16). Places of a
-// contracted axis may stand for any value as long as both operands agree, which
-// is used throughout so that no operand needs a transposition across lanes:
+// product. Places of a contracted axis may stand for any value as long as both
+// operands agree, which is used so that nothing is exchanged between lanes:
 //
-//  - a lane's state values, r by r, are 8 consecutive n: they are the fragments
-//    of S q (as a bf16 pair, value and remainder), against 16-byte runs of q;
+//  - a lane's state values of two tiles, 4 consecutive n each, are a fragment of
+//    S q (as a bf16 pair, value and remainder), against two 8-byte runs of q;
 //  - the scores k_j . q_i come out with 4 consecutive j per lane, and those of
-//    two 16-token tiles are a fragment of their product with v; wave w computes
-//    those of tokens 16 w .. 16 w + 15 and passes them on through LDS, also as a
-//    pair;
-//  - k is read for the update in runs of MT values of 8 tokens per lane and
-//    transposed inside the lane by byte permutes.
+//    two 16-token tiles are a fragment of their product with v; the waves share
+//    the tiles out and pass them on through LDS, also as a pair;
+//  - k for the update and v for both products are read from LDS transposed
+//    (ds_read_b64_tr_b16: 4 rows of 16 values become 4 values per lane).
 //
 // The update's operand exp(L_63 - L_j) beta_j v_j is split into three bf16 (2^-24
 // relative): the state is fp32 and is handed on. L is summed in fp64 and in
@@ -179,32 +180,62 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint3
     lo = pack2<Bf16>(x - Bf16::lo(hi), y - Bf16::hi(hi));
 }
 
-template <int N, int NW, bool FULL>
-__global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_kernel(const ChunkParams p)
+// A double from other lanes by DPP (zero where the lane has no source or its
+// row is not in MASK), and the last lane's in all.
+template <int CTRL, int MASK>
+__device__ __forceinline__ double lanes_up(double x)
 {
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, MASK, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, MASK, 0xf, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double last_lane(double x)
+{
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// 4 rows of 16 16-bit values in LDS, the lane's address being that of values
+// 4 (l % 4) .. of row (l % 16) / 4 of its 16 lanes' rows: the lane gets value
+// l % 16 of each.
+__device__ __forceinline__ u32x2 read_transposed(const uint16_t *p)
+{
+    using S4 = short __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) S4 *)(const_cast<uint16_t *>(p))));
+}
+
+template <int N, int W, bool FULL>
+__global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(const ChunkParams p)
+{
+    constexpr int THREADS = 64 * W;
     constexpr int MT = N / 16;        // state tiles along n
     constexpr int KS = N / 32;        // products along n of a score
-    constexpr int PC = 64 * NW;       // columns of v
-    constexpr int ROW = N + 8;        // pitch of q and k in LDS (16 bytes more than a row: no bank twice)
-    constexpr int VROW = PC + 8;
-    constexpr int QU = N * kChunk / 8 / 256;   // 16-byte runs of q and of k per thread
-    constexpr int VU = PC * kChunk / 8 / 256;  // of v
-    using KW = uint32_t __attribute__((ext_vector_type(MT / 2)));
-    typedef KW KW_row __attribute__((aligned(MT < 8 ? 2 * MT : 16)));
-
+    constexpr bool PART = N * kChunk / 8 < THREADS;  // not every thread has a run of q and k
+    constexpr int PC = 16 * W;        // columns of v
+    // pitches in LDS: 16 rows of 8 or 16 bytes, and 4 rows of 32, in banks of their own
+    constexpr int ROW = N == 32 ? 56 : N == 64 ? 72 : N + 24;
+    constexpr int VROW = W == 4 ? 72 : 152;
+    constexpr int QU = (N * kChunk / 8 + THREADS - 1) / THREADS;  // 16-byte runs of q and of k per thread
+    constexpr int VU = PC * kChunk / 8 / THREADS;                 // of v
     __shared__ __attribute__((aligned(16))) uint16_t lq[FULL ? kChunk * ROW : 8];
     __shared__ __attribute__((aligned(16))) uint16_t lk[kChunk * ROW];
     __shared__ __attribute__((aligned(16))) uint16_t lv[kChunk * VROW];
-    __shared__ u32x4 lw[FULL ? 4 : 1][2][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
+    __shared__ u32x4 lw[FULL ? 4 : 1][FULL ? 2 : 1][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
     __shared__ float lsum[2][kChunk], lrest[2][kChunk];  // L in units of log 2: as fp32, and what that leaves
     __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
     __shared__ int bad[2], found;
 
     const LinearParams &a = p.a;
-    int id = xcd_order(static_cast<int>(blockIdx.x), p.total);
-    const int slice = id % p.slices;
-    id /= p.slices;
-    const int h = id % a.nheads, f = id / a.nheads, grp = h / a.heads_per_group;
+    // workgroups go round the 8 XCDs: XCD x has segments x, x + 8, ..., all heads
+    // and slices of a segment (which share its q and k) beside each other
+    const int inner = a.nheads * p.slices, id = static_cast<int>(blockIdx.x) / 8;
+    const int f = id / inner * 8 + static_cast<int>(blockIdx.x) % 8;
+    const int h = id % inner / p.slices, slice = id % p.slices, grp = h / a.heads_per_group;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -213,7 +244,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
     if (tid == 0)
         found = -1;
     __syncthreads();
-    for (int b = tid; b < a.batch; b += 256) {
+    for (int b = tid; b < a.batch; b += THREADS) {
         const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
         const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
         const int64_t s = f - (lo / p.seg_len + b);
@@ -235,101 +266,96 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
     if (!FULL && segs == 1)
         return;
 
-    const int p0 = slice * PC + wave * 16 * NW;  // this wave's first column
+    const int p0 = slice * PC + wave * 16;  // this wave's first column
     const bool live = p0 < a.headdim;
-    const int prow = p0 + c * NW;                // this lane's first
+    const int prow = p0 + c;                // this lane's
     float *const pool = a.state + slot * a.s_slot + h * a.s_head;
     const int64_t plane = static_cast<int64_t>(a.headdim) * p.dstate;
     auto seg_state = [&](int s) { return p.states + (static_cast<int64_t>(base + s) * a.nheads + h) * plane; };
 
-    f32x4 st[MT][NW];
-    // the lane's state values n = (4g + r) MT + m of row `prow + w`
-    auto each_run = [&](auto &&fn) {
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (live && (4 * g + r) * MT < p.dstate)
-                    fn(w, r, (4 * g + r) * MT);
-    };
+    // the lane's values of row `prow`: n = 16 m + 4 g + 0 .. 3
+    f32x4 st[MT];
     auto load_state = [&](const float *src, int64_t row, float keep, bool add) {
-        each_run([&](int w, int r, int n) {
-            const float *const at = src + (prow + w) * row + n;
+        if (!live)
+            return;
+        src += prow * row + 4 * g;
 #pragma unroll
-            for (int m = 0; m < MT; m += (MT < 4 ? 2 : 4)) {
-                float x[4];
-                if constexpr (MT < 4) {
-                    x[0] = at[m];
-                    x[1] = at[m + 1];
-                } else {
-                    const f32x4 y = *reinterpret_cast<const f32x4 *>(at + m);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] = y[e];
-                }
-#pragma unroll
-                for (int e = 0; e < (MT < 4 ? 2 : 4); ++e)
-                    st[m + e][w][r] = add ? fmaf(st[m + e][w][r], keep, x[e]) : x[e];
+        for (int m = 0; m < MT; ++m)
+            if (16 * m < p.dstate) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(src + 16 * m);
+                st[m] = add ? st[m] * keep + x : x;
             }
-        });
     };
     auto store_state = [&](float *dst, int64_t row) {
-        each_run([&](int w, int r, int n) {
-            float *const at = dst + (prow + w) * row + n;
+        if (!live)
+            return;
+        dst += prow * row + 4 * g;
 #pragma unroll
-            for (int m = 0; m < MT; m += (MT < 4 ? 2 : 4)) {
-                if constexpr (MT < 4) {
-                    at[m] = st[m][w][r];
-                    at[m + 1] = st[m + 1][w][r];
-                } else {
-                    *reinterpret_cast<f32x4 *>(at + m) = f32x4{st[m][w][r], st[m + 1][w][r], st[m + 2][w][r], st[m + 3][w][r]};
-                }
-            }
-        });
+        for (int m = 0; m < MT; ++m)
+            if (16 * m < p.dstate)
+                *reinterpret_cast<f32x4 *>(dst + 16 * m) = st[m];
     };
 
     // requests of a chunk: rows behind the segment's end come from its last row
     // and count as zeros
     u32x4 rq[QU], rk[QU], rv[VU];
     float rdecay = 0.0f, rbeta = 0.0f;
-    auto request = [&](int64_t t0) {
-        const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
-        const uint16_t *const qt = a.q + t0 * a.q_t + grp * a.q_g, *const kt = a.k + t0 * a.k_t + grp * a.k_g;
-        const uint16_t *const vt = a.v + t0 * a.v_t + h * a.v_h;
-        // (rows times 32-bit strides: one multiplication)
-        auto row = [&](int t, int64_t stride) {
-            return static_cast<uint64_t>(static_cast<uint32_t>(min(t, last))) * static_cast<uint32_t>(stride);
-        };
+    uint32_t oo[4];  // of out: this lane's 4 values of token 16 it + c
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+        oo[it] = 2 * ((16 * it + c) * static_cast<uint32_t>(a.o_t) + 4 * g);
+    uint32_t oq[QU], ok[QU], ov[VU];  // byte offsets from a chunk's first row
+    auto offsets = [&](int last) {     // of a chunk with rows 0 .. last
 #pragma unroll
         for (int i = 0; i < QU; ++i) {
-            const int u = tid + 256 * i, n = u % (N / 8) * 8, t = u / (N / 8), col = n < p.dstate ? n : 0;
-            if constexpr (FULL)
-                rq[i] = *reinterpret_cast<const u32x4_a2 *>(qt + row(t, a.q_t) + col);
-            rk[i] = *reinterpret_cast<const u32x4_a2 *>(kt + row(t, a.k_t) + col);
+            const int u = tid + THREADS * i, n = u % (N / 8) * 8, col = n < p.dstate ? n : 0;
+            const uint32_t t = min(u / (N / 8), last);
+            oq[i] = 2 * (t * static_cast<uint32_t>(a.q_t) + col);
+            ok[i] = 2 * (t * static_cast<uint32_t>(a.k_t) + col);
         }
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
-            const int u = tid + 256 * i, col = slice * PC + u % (PC / 8) * 8;
-            rv[i] = *reinterpret_cast<const u32x4_a2 *>(vt + row(u / (PC / 8), a.v_t) + (col < a.headdim ? col : 0));
+            const int u = tid + THREADS * i, col = u % (PC / 8) * 8;
+            ov[i] = 2 * (min(u / (PC / 8), last) * static_cast<uint32_t>(a.v_t) + (slice * PC + col < a.headdim ? col : 0));
         }
-        if (wave == 0) {
+    };
+    auto at = [](const uint16_t *base, uint32_t off) {
+        return *reinterpret_cast<const u32x4_a2 *>(reinterpret_cast<const char *>(base) + off);
+    };
+    auto request = [&](int64_t t0) {
+        const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
+        if (last != kChunk - 1)
+            offsets(last);
+        const uint16_t *const qt = a.q + t0 * a.q_t + grp * a.q_g, *const kt = a.k + t0 * a.k_t + grp * a.k_g;
+        const uint16_t *const vt = a.v + t0 * a.v_t + h * a.v_h + slice * PC;
+#pragma unroll
+        for (int i = 0; i < QU; ++i) {
+            if constexpr (FULL)
+                rq[i] = at(qt, oq[i]);
+            rk[i] = at(kt, ok[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < VU; ++i)
+            rv[i] = at(vt, ov[i]);
+        if (wave == W - 1) {
             const int64_t t = t0 + min(lane, last);
             rdecay = a.decay[t * a.d_t + h * a.d_h];
             rbeta = a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f;
         }
     };
-    // L and what follows from it, by the first wave
+    // L and what follows from it, by the last wave (it has the fewest score tiles)
     double whole = 0.0;  // of the segment so far
     auto sums = [&](int64_t t0, int buf) {
         const bool in = t0 + lane < end;
         const float d = rdecay < kDecayFloor ? kDecayFloor : rdecay;  // (NaN stays)
         double sum = in ? static_cast<double>(d) * 1.4426950408889634 : 0.0;
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-            const double up = __shfl_up(sum, m);
-            sum += lane >= m ? up : 0.0;
-        }
-        const double all = __shfl(sum, 63);
+        sum += lanes_up<0x111, 0xf>(sum);  // lane - 1, - 2, - 4, - 8 of each 16
+        sum += lanes_up<0x112, 0xf>(sum);
+        sum += lanes_up<0x114, 0xf>(sum);
+        sum += lanes_up<0x118, 0xf>(sum);
+        sum += lanes_up<0x142, 0xa>(sum);  // the last of 16 to the next 16, of 32 to the next 32
+        sum += lanes_up<0x143, 0xc>(sum);
+        const double all = last_lane(sum);
         const float gain = in ? rbeta : 0.0f;
         whole += all;
         lsum[buf][lane] = static_cast<float>(sum);
@@ -348,7 +374,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
         if (cut) {
 #pragma unroll
             for (int i = 0; i < QU; ++i) {
-                const int u = tid + 256 * i;
+                const int u = tid + THREADS * i;
                 if (t0 + u / (N / 8) >= end || u % (N / 8) * 8 >= p.dstate) {
                     rk[i] = u32x4{0, 0, 0, 0};
                     if constexpr (FULL)
@@ -357,14 +383,16 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
             }
 #pragma unroll
             for (int i = 0; i < VU; ++i) {
-                const int u = tid + 256 * i;
+                const int u = tid + THREADS * i;
                 if (t0 + u / (PC / 8) >= end || slice * PC + u % (PC / 8) * 8 >= a.headdim)
                     rv[i] = u32x4{0, 0, 0, 0};
             }
         }
 #pragma unroll
         for (int i = 0; i < QU; ++i) {
-            const int u = tid + 256 * i, at = u / (N / 8) * ROW + u % (N / 8) * 8;
+            const int u = tid + THREADS * i, at = u / (N / 8) * ROW + u % (N / 8) * 8;
+            if (PART && u >= N * kChunk / 8)
+                break;
             if constexpr (FULL)
                 *reinterpret_cast<u32x4 *>(lq + at) = rq[i];
             *reinterpret_cast<u32x4 *>(lk + at) = rk[i];
@@ -373,7 +401,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
         H2 most = {0, 0};  // an infinity or NaN has the largest exponent
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
-            const int u = tid + 256 * i;
+            const int u = tid + THREADS * i;
             *reinterpret_cast<u32x4 *>(lv + u / (PC / 8) * VROW + u % (PC / 8) * 8) = rv[i];
             if constexpr (FULL)
 #pragma unroll
@@ -385,13 +413,15 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
                 bad[buf] = 1;
     };
 
+    offsets(kChunk - 1);
     request(begin);
     // the state before the segment
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-            st[m][w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        st[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (FULL)  // (the tiles above the diagonal stay zero)
+        for (int i = tid; i < 4 * 2 * 2 * 64; i += THREADS)
+            (&lw[0][0][0][0])[i] = u32x4{0, 0, 0, 0};
     if constexpr (FULL) {
         if (segs == 1)
             load_state(pool, a.s_row, 1.0f, false);
@@ -408,7 +438,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
             return;
         }
     }
-    if (wave == 0)
+    if (wave == W - 1)
         sums(begin, 0);
     __syncthreads();  // (bad is set by place)
     place(begin, 0);
@@ -422,119 +452,84 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
             request(next);
 
         // v of the wave's columns as fragments: 8 tokens of 32 per lane
-        u32x4 vf[2][NW];
+        const int tr = (4 * g + c / 4) * ROW + 4 * (c % 4), vtr = (4 * g + c / 4) * VROW + 4 * (c % 4) + wave * 16;
+        u32x4 vf[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            uint32_t x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint16_t *const at = lv + (32 * s + 16 * (i / 4) + 4 * g + i % 4) * VROW + wave * 16 * NW + c * NW;
-                if constexpr (NW == 1)
-                    x[i] = *at;
-                else
-                    x[i] = *reinterpret_cast<const uint32_t *>(at);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                vf[s][0][i] = low_halves(x[2 * i], x[2 * i + 1]);
-                if constexpr (NW == 2)
-                    vf[s][1][i] = high_halves(x[2 * i], x[2 * i + 1]);
-            }
+            const u32x2 x = read_transposed(lv + 32 * s * VROW + vtr), y = read_transposed(lv + (32 * s + 16) * VROW + vtr);
+            vf[s] = u32x4{x[0], x[1], y[0], y[1]};
         }
 
         if constexpr (FULL) {
-            // scores of tokens i = 16 wave + c against j <= i, weighted
-            {
-                u32x4 qf[KS];
+            // weighted scores of the ten pairs of 16-token tiles (it, jt <= it),
+            // dealt out to the waves; result rows j = 16 jt + 4g + r, columns
+            // i = 16 it + c
+            constexpr int PAIRS = (10 + W - 1) / W;
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    qf[s] = *reinterpret_cast<const u32x4 *>(lq + (16 * wave + c) * ROW + g * (N / 4) + s * 8);
-                const float li = lsum[buf][16 * wave + c], ri = lrest[buf][16 * wave + c];
+            for (int n = 0; n < PAIRS; ++n) {
+                const int pair = wave + W * n;
+                if (n == PAIRS - 1 && pair >= 10)
+                    break;
+                const int it = pair >= 6 ? 3 : pair >= 3 ? 2 : pair >= 1 ? 1 : 0, jt = pair - it * (it + 1) / 2;
+                f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    u32x4 fh = {0, 0, 0, 0}, fl = {0, 0, 0, 0};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int jt = 2 * s + u;
-                        if (jt > wave)
-                            continue;
-                        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int e = 0; e < KS; ++e) {
-                            const u32x4 kf = *reinterpret_cast<const u32x4 *>(lk + (16 * jt + c) * ROW + g * (N / 4) + e * 8);
-                            x = Mma<Bf16>::run(kf, qf[e], x);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int j = 16 * jt + 4 * g + r;
-                            const float d = (li - lsum[buf][j]) + (ri - lrest[buf][j]);
-                            const float w = lbeta[buf][j] * __builtin_amdgcn_exp2f(d);
-                            x[r] = j <= 16 * wave + c ? x[r] * w : 0.0f;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t wh, wl;
-                            split_pair(x[2 * e], x[2 * e + 1], wh, wl);
-                            fh[2 * u + e] = wh;
-                            fl[2 * u + e] = wl;
-                        }
-                    }
-                    if (2 * s <= wave) {
-                        lw[wave][s][0][lane] = fh;
-                        lw[wave][s][1][lane] = fl;
-                    }
+                for (int e = 0; e < KS; ++e) {
+                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(lk + (16 * jt + c) * ROW + 32 * e + 8 * g);
+                    const u32x4 qf = *reinterpret_cast<const u32x4 *>(lq + (16 * it + c) * ROW + 32 * e + 8 * g);
+                    x = Mma<Bf16>::run(kf, qf, x);
                 }
+                const float li = lsum[buf][16 * it + c], ri = lrest[buf][16 * it + c];
+                const f32x4 lj = *reinterpret_cast<const f32x4 *>(&lsum[buf][16 * jt + 4 * g]);
+                const f32x4 rj = *reinterpret_cast<const f32x4 *>(&lrest[buf][16 * jt + 4 * g]);
+                const f32x4 bj = *reinterpret_cast<const f32x4 *>(&lbeta[buf][16 * jt + 4 * g]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float y = x[r] * (bj[r] * __builtin_amdgcn_exp2f((li - lj[r]) + (ri - rj[r])));
+                    asm("" : "+v"(y));  // (a select, not a branch around the exponential)
+                    x[r] = 16 * jt + 4 * g + r <= 16 * it + c ? y : 0.0f;
+                }
+                uint32_t h0, h1, l0, l1;
+                split_pair(x[0], x[1], h0, l0);
+                split_pair(x[2], x[3], h1, l1);
+                *(reinterpret_cast<u32x2 *>(&lw[it][jt / 2][0][lane]) + jt % 2) = u32x2{h0, h1};
+                *(reinterpret_cast<u32x2 *>(&lw[it][jt / 2][1][lane]) + jt % 2) = u32x2{l0, l1};
             }
 
             // S q, all tokens: result rows p, columns i
-            f32x4 o[NW][4];
+            f32x4 o[4];
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-#pragma unroll
-                for (int it = 0; it < 4; ++it)
-                    o[w][it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int it = 0; it < 4; ++it)
+                o[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                u32x4 fh[NW], fl[NW];
+                u32x4 fh, fl;
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int x = s * 8 + 2 * e, y = x + 1;
-                        uint32_t wh, wl;
-                        split_pair(st[x % MT][w][x / MT], st[y % MT][w][y / MT], wh, wl);
-                        fh[w][e] = wh;
-                        fl[w][e] = wl;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t wh, wl;
+                    split_pair(st[2 * s + e / 2][2 * (e % 2)], st[2 * s + e / 2][2 * (e % 2) + 1], wh, wl);
+                    fh[e] = wh;
+                    fl[e] = wl;
+                }
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
-                    const u32x4 qf = *reinterpret_cast<const u32x4 *>(lq + (16 * it + c) * ROW + g * (N / 4) + s * 8);
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) {
-                        o[w][it] = Mma<Bf16>::run(fh[w], qf, o[w][it]);
-                        o[w][it] = Mma<Bf16>::run(fl[w], qf, o[w][it]);
-                    }
+                    const uint16_t *const qrow = lq + (16 * it + c) * ROW + 32 * s + 4 * g;
+                    const u32x2 x = *reinterpret_cast<const u32x2 *>(qrow), y = *reinterpret_cast<const u32x2 *>(qrow + 16);
+                    const u32x4 qf = {x[0], x[1], y[0], y[1]};
+                    o[it] = Mma<Bf16>::run(fh, qf, o[it]);
+                    o[it] = Mma<Bf16>::run(fl, qf, o[it]);
                 }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const float grow = lgrow[buf][16 * it + c];
-#pragma unroll
-                for (int w = 0; w < NW; ++w)
-                    o[w][it] *= grow;
-            }
+            for (int it = 0; it < 4; ++it)
+                o[it] *= lgrow[buf][16 * it + c];
             __syncthreads();  // the scores are there
-            if (!bad[buf]) {
+            if (!__builtin_amdgcn_readfirstlane(bad[buf])) {
 #pragma unroll
                 for (int it = 0; it < 4; ++it)
 #pragma unroll
                     for (int s = 0; s <= it / 2; ++s) {
-                        const u32x4 fh = lw[it][s][0][lane], fl = lw[it][s][1][lane];
-#pragma unroll
-                        for (int w = 0; w < NW; ++w) {
-                            o[w][it] = Mma<Bf16>::run(vf[s][w], fh, o[w][it]);
-                            o[w][it] = Mma<Bf16>::run(vf[s][w], fl, o[w][it]);
-                        }
+                        o[it] = Mma<Bf16>::run(vf[s], lw[it][s][0][lane], o[it]);
+                        o[it] = Mma<Bf16>::run(vf[s], lw[it][s][1][lane], o[it]);
                     }
             } else {
                 // v holds infinities or NaN: a product would carry them, times the
@@ -546,78 +541,55 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
                                                    4 * (j % 32 / 16) + j % 4;
                         const float x = Bf16::lo(at[0]) + Bf16::lo(at[64 * 8]);
 #pragma unroll
-                        for (int w = 0; w < NW; ++w)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                o[w][it][r] = fmaf(x, Bf16::lo(lv[j * VROW + wave * 16 * NW + (4 * g + r) * NW + w]), o[w][it][r]);
+                        for (int r = 0; r < 4; ++r)
+                            o[it][r] = fmaf(x, Bf16::lo(lv[j * VROW + wave * 16 + 4 * g + r]), o[it][r]);
                     }
             }
-            if (live)
+            if (live) {
+                char *const rows = reinterpret_cast<char *>(a.out + t0 * a.o_t + h * a.o_h + p0);
+                const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const int64_t t = t0 + 16 * it + c;
-                    if (t >= end)
-                        continue;
-                    uint16_t *const at = a.out + t * a.o_t + h * a.o_h + p0 + 4 * g * NW;
-                    uint32_t x[2 * NW];
-#pragma unroll
-                    for (int e = 0; e < 2 * NW; ++e)
-                        x[e] = NW == 1 ? pack2<Bf16>(a.scale * o[0][it][2 * e], a.scale * o[0][it][2 * e + 1])
-                                       : pack2<Bf16>(a.scale * o[0][it][e], a.scale * o[NW - 1][it][e]);
-                    if constexpr (NW == 1)
-                        *reinterpret_cast<u32x2_a2 *>(at) = u32x2{x[0], x[1]};
-                    else
-                        *reinterpret_cast<u32x4_a2 *>(at) = u32x4{x[0], x[1], x[2 % (2 * NW)], x[3 % (2 * NW)]};
-                }
+                for (int it = 0; it < 4; ++it)
+                    if (16 * it + c <= last)
+                        *reinterpret_cast<u32x2_a2 *>(rows + oo[it]) =
+                            u32x2{pack2<Bf16>(a.scale * o[it][0], a.scale * o[it][1]),
+                                  pack2<Bf16>(a.scale * o[it][2], a.scale * o[it][3])};
+            }
         }
 
         // the state behind the chunk
         const float all = lall[buf];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                st[m][w] *= all;
+            st[m] *= all;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            u32x4 f1[NW], f2[NW], f3[NW];
+            u32x4 f1, f2, f3;
             const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 4 * g]);
             const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 16 + 4 * g]);
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f32x4 &late = e < 2 ? late0 : late1;
-                    const float x = Bf16::lo(vf[s][w][e]) * late[2 * e % 4], y = Bf16::hi(vf[s][w][e]) * late[2 * e % 4 + 1];
-                    uint32_t h1, h2;
-                    h1 = pack2<Bf16>(x, y);
-                    const float x1 = x - Bf16::lo(h1), y1 = y - Bf16::hi(h1);
-                    h2 = pack2<Bf16>(x1, y1);
-                    f1[w][e] = h1;
-                    f2[w][e] = h2;
-                    f3[w][e] = pack2<Bf16>(x1 - Bf16::lo(h2), y1 - Bf16::hi(h2));
-                }
-            KW kr[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                kr[i] = *reinterpret_cast<const KW_row *>(lk + (32 * s + 16 * (i / 4) + 4 * g + i % 4) * ROW + c * MT);
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 &late = e < 2 ? late0 : late1;
+                const float x = Bf16::lo(vf[s][e]) * late[2 * e % 4], y = Bf16::hi(vf[s][e]) * late[2 * e % 4 + 1];
+                const uint32_t h1 = pack2<Bf16>(x, y);
+                const float x1 = x - Bf16::lo(h1), y1 = y - Bf16::hi(h1);
+                const uint32_t h2 = pack2<Bf16>(x1, y1);
+                f1[e] = h1;
+                f2[e] = h2;
+                f3[e] = pack2<Bf16>(x1 - Bf16::lo(h2), y1 - Bf16::hi(h2));
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                u32x4 kf;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    kf[i] = m % 2 ? high_halves(kr[2 * i][m / 2], kr[2 * i + 1][m / 2])
-                                  : low_halves(kr[2 * i][m / 2], kr[2 * i + 1][m / 2]);
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    st[m][w] = Mma<Bf16>::run(kf, f1[w], st[m][w]);
-                    st[m][w] = Mma<Bf16>::run(kf, f2[w], st[m][w]);
-                    st[m][w] = Mma<Bf16>::run(kf, f3[w], st[m][w]);
-                }
+                const u32x2 x = read_transposed(lk + 32 * s * ROW + tr + 16 * m);
+                const u32x2 y = read_transposed(lk + (32 * s + 16) * ROW + tr + 16 * m);
+                const u32x4 kf = {x[0], x[1], y[0], y[1]};
+                st[m] = Mma<Bf16>::run(kf, f1, st[m]);
+                st[m] = Mma<Bf16>::run(kf, f2, st[m]);
+                st[m] = Mma<Bf16>::run(kf, f3, st[m]);
             }
         }
         if (more) {
-            if (wave == 0)
+            if (wave == W - 1)
                 sums(next, buf ^ 1);
             __syncthreads();  // LDS is free again
             place(next, buf ^ 1);
@@ -630,7 +602,7 @@ __global__ void __launch_bounds__(256, N * NW <= 128 ? 2 : 1) ssu_linear_chunk_k
             store_state(pool, a.s_row);
     } else {
         store_state(seg_state(seg), p.dstate);
-        if (slice == 0 && tid == 0)
+        if (slice == 0 && tid == THREADS - 64)  // (of the wave that summed)
             p.decays[static_cast<int64_t>(f) * a.nheads + h] = __builtin_amdgcn_exp2f(static_cast<float>(whole));
     }
 }
@@ -656,21 +628,23 @@ struct ChunkKernels {
     int columns;  // of v per workgroup
 };
 
-template <int N, int NW>
+template <int N, int W>
 constexpr ChunkKernels chunk_kernels()
 {
-    return {&ssu_linear_chunk_kernel<N, NW, false>, &ssu_linear_chunk_kernel<N, NW, true>, 64 * NW};
+    return {&ssu_linear_chunk_kernel<N, W, false>, &ssu_linear_chunk_kernel<N, W, true>, 16 * W};
+}
+
+template <int W>
+ChunkKernels chunk_kernels(int N)
+{
+    return N <= 32 ? chunk_kernels<32, W>() : N == 64 ? chunk_kernels<64, W>() : N == 128 ? chunk_kernels<128, W>()
+                                                                                          : chunk_kernels<256, W>();
 }
 
 ChunkKernels chunk_kernels(int N, int P)
 {
-    switch (N) {
-    case 16:
-    case 32: return chunk_kernels<32, 1>();
-    case 64: return chunk_kernels<64, 1>();
-    case 128: return P % 128 == 0 ? chunk_kernels<128, 2>() : chunk_kernels<128, 1>();
-    default: return chunk_kernels<256, 1>();
-    }
+    // eight waves where the last 128 columns hold more than 64
+    return (P - 1) % 128 >= 64 ? chunk_kernels<8>(N) : chunk_kernels<4>(N);
 }
 
 LinearKernel recurrent_kernel(int N)
@@ -697,12 +671,9 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
         return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d is not a multiple of 16 in 16 .. 256", who, a.headdim);
     if (a.dstate != 16 && a.dstate != 32 && a.dstate != 64 && a.dstate != 128 && a.dstate != 256)
         return fail(SSU_ERR_UNSUPPORTED, "%s: dstate %d is not 16, 32, 64, 128 or 256", who, a.dstate);
-    for (const ssu_view *v : {&a.q, &a.k, &a.v})
-        if (v->stride[0] > 0x7fffffff)
-            return fail(SSU_ERR_UNSUPPORTED, "%s: a token stride of 2^31 elements or more", who);
     if (a.ntokens > 0x7fffffff)
         return fail(SSU_ERR_UNSUPPORTED, "%s: more than 2^31 tokens", who);
-    if ((a.ntokens / kChunk + a.batch) * a.nheads > 0x7fffffff / (a.headdim / 16))
+    if ((a.ntokens / kChunk + a.batch + 8) * a.nheads > 0x7fffffff / (a.headdim / 16))
         return fail(SSU_ERR_UNSUPPORTED, "%s: batch * nheads too large", who);
     return SSU_OK;
 }
@@ -722,7 +693,7 @@ Plan plan_of(const ssu_linear_args &a)
     const int64_t chunks = (a.ntokens + kChunk - 1) / kChunk;
     const int64_t per = std::max<int64_t>({(chunks * units + SEG_WANT * kNumCUs - 1) / (SEG_WANT * kNumCUs), (chunks + SEG_MAX - 1) / SEG_MAX, SEG_MIN});
     const bool cut = per < chunks && a.batch * units < SEG_UNCUT * kNumCUs;
-    p.seg_len = cut ? static_cast<int>(per * kChunk) : std::max<int>(static_cast<int>(std::min<int64_t>(a.ntokens, INT32_MAX)), 1);
+    p.seg_len = static_cast<int>(cut ? per * kChunk : std::min<int64_t>(a.ntokens + 1, INT32_MAX));
     p.segments = static_cast<int>(a.ntokens / p.seg_len) + a.batch;
     if (cut) {
         p.decays_at = static_cast<int64_t>(p.segments) * a.nheads * a.headdim * a.dstate * 4;
@@ -759,6 +730,10 @@ ssu_status check_linear(const ssu_linear_args &a, const char *who, bool prompts)
         return fail(SSU_ERR_UNSUPPORTED, "idx: stride must be 1");
     if (prompts && a.cu_seqlens.stride[0] != 1)
         return fail(SSU_ERR_UNSUPPORTED, "cu_seqlens: stride must be 1");
+    if (prompts)
+        for (const ssu_view *v : {&a.q, &a.k, &a.v, &a.out})
+            if (v->stride[0] >= int64_t(1) << 24)  // 64 rows lie within 2^31 bytes
+                return fail(SSU_ERR_UNSUPPORTED, "%s: a token stride of 2^24 elements or more", who);
     for (const ssu_view *v : {&a.q, &a.k, &a.v, &a.out})
         if (v->ptr && v->stride[2] != 1)
             return fail(SSU_ERR_UNSUPPORTED, "q/k/v/out: inner stride must be 1");
@@ -847,14 +822,14 @@ ssu_status launch_chunks(const ssu_linear_args &a, hipStream_t stream)
     p.segments = plan.segments;
     p.slices = plan.slices;
     p.dstate = a.dstate;
-    p.total = plan.segments * a.nheads * plan.slices;
+    p.total = (plan.segments + 7) / 8 * 8 * a.nheads * plan.slices;
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     hipError_t e = hipSuccess;
     if (plan.bytes > 0)
-        e = launch_kernel(k.states, p, p.total, 256, 0, stream);
+        e = launch_kernel(k.states, p, p.total, 4 * k.columns, 0, stream);
     if (e == hipSuccess)
-        e = launch_kernel(k.full, p, p.total, 256, 0, stream);
+        e = launch_kernel(k.full, p, p.total, 4 * k.columns, 0, stream);
     if (e != hipSuccess)
         return fail(SSU_ERR_HIP, "launch of the chunked linear attention failed: %s", hipGetErrorString(e));
     return SSU_OK;

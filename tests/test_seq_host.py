@@ -104,7 +104,7 @@ LINEAR_BAD = [
     ({"decay.dtype": BF16}, INVALID), ({"beta.dtype": I32}, INVALID), ({"out.dtype": F32}, INVALID),
     ({"q.reserved": 1}, INVALID), ({"v.0": -256}, INVALID), ({"decay.1": -1}, INVALID), ({"out.0": 0}, INVALID),
     ({"state.2": 0}, INVALID),
-    ({"v.0": 1 << 31}, UNSUPPORTED), ({"state.3": 2}, UNSUPPORTED), ({"q.2": 2}, UNSUPPORTED), ({"k.2": 0}, UNSUPPORTED), ({"v.2": 2}, UNSUPPORTED),
+    ({"state.3": 2}, UNSUPPORTED), ({"q.2": 2}, UNSUPPORTED), ({"k.2": 0}, UNSUPPORTED), ({"v.2": 2}, UNSUPPORTED),
     ({"out.2": 2}, UNSUPPORTED), ({"idx.0": 2}, UNSUPPORTED),
     ({"state.ptr": 0x10004}, MISALIGNED), ({"state.2": 130}, MISALIGNED), ({"q.ptr": 0x10001}, MISALIGNED),
     ({"beta.ptr": 0x10002}, MISALIGNED), ({"idx.ptr": 0x10004, "idx.dtype": I64}, MISALIGNED),
@@ -122,6 +122,7 @@ def test_linear_refusals(ssu, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [({"cu.ptr": 0}, INVALID), ({"cu.dtype": I64}, INVALID), ({"cu.0": 2}, UNSUPPORTED),
+                                     ({"v.0": 1 << 24}, UNSUPPORTED), ({"out.0": 1 << 24}, UNSUPPORTED),
                                      ({"cu.ptr": 0x10002}, MISALIGNED)])
 def test_linear_prompt_refusals(ssu, kw, code):
     assert ssu._lib.ssu_linear_attention(pack(ssu._LINEAR_ARGS, change(LINEAR, kw)), None) == code
