@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearPa
                 store4<true>(sp + (row0 + j * RPI) * p.s_row + 128 * e, s[j][e]);
 }
 
-// Prompts, 64 tokens (a chunk) at a time. With L_i the decays' logarithms summed
+// Prompts, 32 tokens (a chunk) at a time. With L_i the decays' logarithms summed
 // from the chunk's start, S the state before it:
 //
 //   out_i = scale * ( exp(L_i) S q_i + sum_{j <= i} exp(L_i - L_j) beta_j (k_j . q_i) v_j )
-//   S     = exp(L_63) S + sum_j exp(L_63 - L_j) beta_j v_j k_j^T
+//   S     = exp(L_31) S + sum_j exp(L_31 - L_j) beta_j v_j k_j^T
 //
 // One workgroup of W waves takes a segment of a sequence, one head and 16 W
 // columns of v (rows p of the state); wave w owns columns 16 w .. 16 w + 15,
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearPa
 //  - k for the update and v for both products are read from LDS transposed
 //    (ds_read_b64_tr_b16: 4 rows of 16 values become 4 values per lane).
 //
-// The update's operand exp(L_63 - L_j) beta_j v_j is split into three bf16 (2^-24
+// The update's operand exp(L_31 - L_j) beta_j v_j is split into three bf16 (2^-24
 // relative): the state is fp32 and is handed on. L is summed in fp64 and in
 // units of log 2: a difference of two sums keeps its digits behind a reset.
 //
@@ -164,7 +164,12 @@ __global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearPa
 // from the sum of those before it. The last segment's place in the workspace
 // holds the sequence's first state, which the last segment overwrites in the
 // pool while the first one may still start.
-constexpr int kChunk = 64;
+#ifndef CHUNK
+#define CHUNK 32
+#endif
+constexpr int kChunk = CHUNK;
+constexpr int kTiles = kChunk / 16;  // of tokens
+constexpr int kSteps = kChunk / 32;  // products along a chunk's tokens
 constexpr float kDecayFloor = -1.0e4f;  // exp is 0 far above it; sums of it stay finite
 
 struct ChunkParams {
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
     __shared__ __attribute__((aligned(16))) uint16_t lq[FULL ? kChunk * ROW : 8];
     __shared__ __attribute__((aligned(16))) uint16_t lk[kChunk * ROW];
     __shared__ __attribute__((aligned(16))) uint16_t lv[kChunk * VROW];
-    __shared__ u32x4 lw[FULL ? 4 : 1][FULL ? 2 : 1][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
+    __shared__ u32x4 lw[FULL ? kTiles : 1][FULL ? kSteps : 1][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
     __shared__ float lsum[2][kChunk], lrest[2][kChunk];  // L in units of log 2: as fp32, and what that leaves
     __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
     __shared__ int bad[2], found;
@@ -300,9 +305,9 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
     // and count as zeros
     u32x4 rq[QU], rk[QU], rv[VU];
     float rdecay = 0.0f, rbeta = 0.0f;
-    uint32_t oo[4];  // of out: this lane's 4 values of token 16 it + c
+    uint32_t oo[kTiles];  // of out: this lane's 4 values of token 16 it + c
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < kTiles; ++it)
         oo[it] = 2 * ((16 * it + c) * static_cast<uint32_t>(a.o_t) + 4 * g);
     uint32_t oq[QU], ok[QU], ov[VU];  // byte offsets from a chunk's first row
     auto offsets = [&](int last) {     // of a chunk with rows 0 .. last
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
     // L and what follows from it, by the last wave (it has the fewest score tiles)
     double whole = 0.0;  // of the segment so far
     auto sums = [&](int64_t t0, int buf) {
-        const bool in = t0 + lane < end;
+        const bool in = lane < kChunk && t0 + lane < end;
         const float d = rdecay < kDecayFloor ? kDecayFloor : rdecay;  // (NaN stays)
         double sum = in ? static_cast<double>(d) * 1.4426950408889634 : 0.0;
         sum += lanes_up<0x111, 0xf>(sum);  // lane - 1, - 2, - 4, - 8 of each 16
@@ -358,11 +363,13 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
         const double all = last_lane(sum);
         const float gain = in ? rbeta : 0.0f;
         whole += all;
-        lsum[buf][lane] = static_cast<float>(sum);
-        lrest[buf][lane] = static_cast<float>(sum - static_cast<double>(static_cast<float>(sum)));
-        lbeta[buf][lane] = gain;
-        lgrow[buf][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum));
-        llate[buf][lane] = in ? gain * __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) : 0.0f;
+        if (lane < kChunk) {
+            lsum[buf][lane] = static_cast<float>(sum);
+            lrest[buf][lane] = static_cast<float>(sum - static_cast<double>(static_cast<float>(sum)));
+            lbeta[buf][lane] = gain;
+            lgrow[buf][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum));
+            llate[buf][lane] = in ? gain * __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) : 0.0f;
+        }
         if (lane == 0) {
             lall[buf] = __builtin_amdgcn_exp2f(static_cast<float>(all));
             bad[buf] = 0;
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
     for (int m = 0; m < MT; ++m)
         st[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (FULL)  // (the tiles above the diagonal stay zero)
-        for (int i = tid; i < 4 * 2 * 2 * 64; i += THREADS)
+        for (int i = tid; i < kTiles * kSteps * 2 * 64; i += THREADS)
             (&lw[0][0][0][0])[i] = u32x4{0, 0, 0, 0};
     if constexpr (FULL) {
         if (segs == 1)
@@ -453,22 +460,22 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
 
         // v of the wave's columns as fragments: 8 tokens of 32 per lane
         const int tr = (4 * g + c / 4) * ROW + 4 * (c % 4), vtr = (4 * g + c / 4) * VROW + 4 * (c % 4) + wave * 16;
-        u32x4 vf[2];
+        u32x4 vf[kSteps];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kSteps; ++s) {
             const u32x2 x = read_transposed(lv + 32 * s * VROW + vtr), y = read_transposed(lv + (32 * s + 16) * VROW + vtr);
             vf[s] = u32x4{x[0], x[1], y[0], y[1]};
         }
 
         if constexpr (FULL) {
-            // weighted scores of the ten pairs of 16-token tiles (it, jt <= it),
-            // dealt out to the waves; result rows j = 16 jt + 4g + r, columns
+            // weighted scores of the pairs of 16-token tiles (it, jt <= it), dealt
+            // out to the waves; result rows j = 16 jt + 4g + r, columns
             // i = 16 it + c
-            constexpr int PAIRS = (10 + W - 1) / W;
+            constexpr int PAIRS = kTiles * (kTiles + 1) / 2;
 #pragma unroll
-            for (int n = 0; n < PAIRS; ++n) {
+            for (int n = 0; n < (PAIRS + W - 1) / W; ++n) {
                 const int pair = wave + W * n;
-                if (n == PAIRS - 1 && pair >= 10)
+                if (pair >= PAIRS)
                     break;
                 const int it = pair >= 6 ? 3 : pair >= 3 ? 2 : pair >= 1 ? 1 : 0, jt = pair - it * (it + 1) / 2;
                 f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -496,9 +503,9 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
             }
 
             // S q, all tokens: result rows p, columns i
-            f32x4 o[4];
+            f32x4 o[kTiles];
 #pragma unroll
-            for (int it = 0; it < 4; ++it)
+            for (int it = 0; it < kTiles; ++it)
                 o[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
                     fl[e] = wl;
                 }
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
+                for (int it = 0; it < kTiles; ++it) {
                     const uint16_t *const qrow = lq + (16 * it + c) * ROW + 32 * s + 4 * g;
                     const u32x2 x = *reinterpret_cast<const u32x2 *>(qrow), y = *reinterpret_cast<const u32x2 *>(qrow + 16);
                     const u32x4 qf = {x[0], x[1], y[0], y[1]};
@@ -520,12 +527,12 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
                 }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it)
+            for (int it = 0; it < kTiles; ++it)
                 o[it] *= lgrow[buf][16 * it + c];
             __syncthreads();  // the scores are there
             if (!__builtin_amdgcn_readfirstlane(bad[buf])) {
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
+                for (int it = 0; it < kTiles; ++it)
 #pragma unroll
                     for (int s = 0; s <= it / 2; ++s) {
                         o[it] = Mma<Bf16>::run(vf[s], lw[it][s][0][lane], o[it]);
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
                 // v holds infinities or NaN: a product would carry them, times the
                 // zeros of the scores, to the tokens before; sum token by token
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
+                for (int it = 0; it < kTiles; ++it)
                     for (int j = 0; j <= 16 * it + c; ++j) {
                         const uint16_t *const at = reinterpret_cast<const uint16_t *>(&lw[it][j / 32][0][16 * (j % 16 / 4) + c]) +
                                                    4 * (j % 32 / 16) + j % 4;
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
                 char *const rows = reinterpret_cast<char *>(a.out + t0 * a.o_t + h * a.o_h + p0);
                 const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
+                for (int it = 0; it < kTiles; ++it)
                     if (16 * it + c <= last)
                         *reinterpret_cast<u32x2_a2 *>(rows + oo[it]) =
                             u32x2{pack2<Bf16>(a.scale * o[it][0], a.scale * o[it][1]),
@@ -563,7 +570,7 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
         for (int m = 0; m < MT; ++m)
             st[m] *= all;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kSteps; ++s) {
             u32x4 f1, f2, f3;
             const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 4 * g]);
             const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 16 + 4 * g]);
