@@ -12,21 +12,6 @@
 #include "internal.h"
 #include "seq_common.h"
 
-#ifndef CHUNK_OCC
-#define CHUNK_OCC (W == 8 ? 2 : N == 256 ? 1 : 2)
-#endif
-#ifndef SEG_WANT
-#define SEG_WANT 2
-#endif
-#ifndef SEG_MAX
-#define SEG_MAX 32
-#endif
-#ifndef SEG_MIN
-#define SEG_MIN 4
-#endif
-#ifndef SEG_UNCUT
-#define SEG_UNCUT 4
-#endif
 namespace ssu {
 namespace {
 
@@ -160,14 +145,9 @@ __global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearPa
 // units of log 2: a difference of two sums keeps its digits behind a reset.
 //
 // Long sequences are cut into segments: a first kernel (FULL = false) computes
-// every segment's own contribution to the state, and the second starts each
-// from the sum of those before it. The last segment's place in the workspace
-// holds the sequence's first state, which the last segment overwrites in the
-// pool while the first one may still start.
-#ifndef CHUNK
-#define CHUNK 32
-#endif
-constexpr int kChunk = CHUNK;
+// every segment's own contribution to the state, a second the states in front
+// of the segments from them, and the third starts every segment there.
+constexpr int kChunk = 32;
 constexpr int kTiles = kChunk / 16;  // of tokens
 constexpr int kSteps = kChunk / 32;  // products along a chunk's tokens
 constexpr float kDecayFloor = -1.0e4f;  // exp is 0 far above it; sums of it stay finite
@@ -215,7 +195,7 @@ __device__ __forceinline__ u32x2 read_transposed(const uint16_t *p)
 }
 
 template <int N, int W, bool FULL>
-__global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(const ChunkParams p)
+__global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_kernel(const ChunkParams p)
 {
     constexpr int THREADS = 64 * W;
     constexpr int MT = N / 16;        // state tiles along n
@@ -268,28 +248,25 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
     const int base = static_cast<int>(lo / p.seg_len) + b, seg = f - base;
     const int segs = static_cast<int>((hi - lo + p.seg_len - 1) / p.seg_len);
     const int64_t begin = lo + static_cast<int64_t>(seg) * p.seg_len, end = min(begin + p.seg_len, hi);
-    if (!FULL && segs == 1)
-        return;
+    if (!FULL && seg == segs - 1)
+        return;  // nothing comes behind it
 
     const int p0 = slice * PC + wave * 16;  // this wave's first column
     const bool live = p0 < a.headdim;
     const int prow = p0 + c;                // this lane's
     float *const pool = a.state + slot * a.s_slot + h * a.s_head;
     const int64_t plane = static_cast<int64_t>(a.headdim) * p.dstate;
-    auto seg_state = [&](int s) { return p.states + (static_cast<int64_t>(base + s) * a.nheads + h) * plane; };
 
     // the lane's values of row `prow`: n = 16 m + 4 g + 0 .. 3
     f32x4 st[MT];
-    auto load_state = [&](const float *src, int64_t row, float keep, bool add) {
+    auto load_state = [&](const float *src, int64_t row) {
         if (!live)
             return;
         src += prow * row + 4 * g;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            if (16 * m < p.dstate) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(src + 16 * m);
-                st[m] = add ? st[m] * keep + x : x;
-            }
+            if (16 * m < p.dstate)
+                st[m] = *reinterpret_cast<const f32x4 *>(src + 16 * m);
     };
     auto store_state = [&](float *dst, int64_t row) {
         if (!live)
@@ -431,19 +408,9 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
             (&lw[0][0][0][0])[i] = u32x4{0, 0, 0, 0};
     if constexpr (FULL) {
         if (segs == 1)
-            load_state(pool, a.s_row, 1.0f, false);
-        else if (seg == 0)
-            load_state(seg_state(segs - 1), p.dstate, 1.0f, false);
+            load_state(pool, a.s_row);
         else
-            for (int s = 0; s < seg; ++s)
-                load_state(seg_state(s), p.dstate, p.decays[static_cast<int64_t>(base + s) * a.nheads + h], s > 0);
-    } else {
-        if (seg == 0 || seg == segs - 1)
-            load_state(pool, a.s_row, 1.0f, false);
-        if (seg == segs - 1) {
-            store_state(seg_state(seg), p.dstate);
-            return;
-        }
+            load_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
     }
     if (wave == W - 1)
         sums(begin, 0);
@@ -608,9 +575,48 @@ __global__ void __launch_bounds__(64 * W, CHUNK_OCC) ssu_linear_chunk_kernel(con
         if (seg == segs - 1)
             store_state(pool, a.s_row);
     } else {
-        store_state(seg_state(seg), p.dstate);
+        store_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
         if (slice == 0 && tid == THREADS - 64)  // (of the wave that summed)
             p.decays[static_cast<int64_t>(f) * a.nheads + h] = __builtin_amdgcn_exp2f(static_cast<float>(whole));
+    }
+}
+
+// The states in front of a sequence's segments, in place of the segments' own
+// contributions: four consecutive values of one head per thread.
+__global__ void __launch_bounds__(256) ssu_linear_segments_kernel(const ChunkParams p)
+{
+    const LinearParams &a = p.a;
+    const int plane = a.headdim * p.dstate, blocks = (plane + 1023) / 1024;
+    const int id = static_cast<int>(blockIdx.x), h = id / blocks % a.nheads, b = id / blocks / a.nheads;
+    const int i = (id % blocks * 256 + static_cast<int>(threadIdx.x)) * 4;
+    const int64_t slot = load_index(a.idx, a.idx64, b);
+    const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
+    const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
+    const int segs = static_cast<int>((hi - lo + p.seg_len - 1) / p.seg_len);
+    if (slot < 0 || slot >= a.pool_slots || segs <= 1 || i >= plane)
+        return;
+    const int64_t first = (lo / p.seg_len + b) * a.nheads + h, step = static_cast<int64_t>(a.nheads) * plane;
+    f32x4 s = *reinterpret_cast<const f32x4 *>(a.state + slot * a.s_slot + h * a.s_head + i / p.dstate * a.s_row + i % p.dstate);
+    float *at = p.states + first * plane + i;
+    const float *decay = p.decays + first;
+    constexpr int U = 8;  // segments on their way at once
+    for (int t = 0; t < segs; t += U) {
+        f32x4 x[U];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < segs - 1) {
+                x[u] = *reinterpret_cast<const f32x4 *>(at + u * step);
+                d[u] = decay[static_cast<int64_t>(t + u) * a.nheads];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u < segs)
+                *reinterpret_cast<f32x4 *>(at + u * step) = s;
+            if (t + u < segs - 1)
+                s = s * d[u] + x[u];
+        }
+        at += U * step;
     }
 }
 
@@ -685,21 +691,28 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
     return SSU_OK;
 }
 
-// Segments of a prompt call: enough workgroups to fill the chip.
+// Segments of a prompt call.
 struct Plan {
     int seg_len, segments, slices;
     int64_t decays_at, bytes;  // workspace (0: one segment per sequence)
 };
 
+// Sequences are cut where whole ones would leave most of the chip idle: at most
+// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 87 us
+// cut, 153 uncut; with twice the waves and equal lengths uncut is faster, 89
+// against 110 us). Then segments are as long as fills the chip once, 4096 waves
+// (N = 256: 2048), but of 128 tokens at least and a 64th of all at most: one
+// prompt of 4096 tokens takes 40 us in segments of 128, 47 in segments of 256.
 Plan plan_of(const ssu_linear_args &a)
 {
     Plan p{};
-    const int columns = chunk_kernels(a.dstate, a.headdim).columns;
+    const int columns = chunk_kernels(a.dstate, a.headdim).columns, waves = columns / 16;
     p.slices = (a.headdim + columns - 1) / columns;
-    const int64_t units = static_cast<int64_t>(a.nheads) * p.slices;
+    const int64_t units = static_cast<int64_t>(a.nheads) * p.slices * waves;
     const int64_t chunks = (a.ntokens + kChunk - 1) / kChunk;
-    const int64_t per = std::max<int64_t>({(chunks * units + SEG_WANT * kNumCUs - 1) / (SEG_WANT * kNumCUs), (chunks + SEG_MAX - 1) / SEG_MAX, SEG_MIN});
-    const bool cut = per < chunks && a.batch * units < SEG_UNCUT * kNumCUs;
+    const int64_t room = (a.dstate == 256 ? 8 : 16) * kNumCUs;
+    const int64_t per = std::max<int64_t>({(chunks * units + room - 1) / room, (chunks + 63) / 64, 4});
+    const bool cut = per < chunks && a.batch * units <= 4 * kNumCUs;
     p.seg_len = static_cast<int>(cut ? per * kChunk : std::min<int64_t>(a.ntokens + 1, INT32_MAX));
     p.segments = static_cast<int>(a.ntokens / p.seg_len) + a.batch;
     if (cut) {
@@ -833,8 +846,12 @@ ssu_status launch_chunks(const ssu_linear_args &a, hipStream_t stream)
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     hipError_t e = hipSuccess;
-    if (plan.bytes > 0)
+    if (plan.bytes > 0) {
         e = launch_kernel(k.states, p, p.total, 4 * k.columns, 0, stream);
+        const int64_t blocks = (static_cast<int64_t>(a.headdim) * a.dstate + 1023) / 1024;
+        if (e == hipSuccess)
+            e = launch_kernel(&ssu_linear_segments_kernel, p, blocks * a.nheads * a.batch, 256, 0, stream);
+    }
     if (e == hipSuccess)
         e = launch_kernel(k.full, p, p.total, 4 * k.columns, 0, stream);
     if (e != hipSuccess)
