@@ -597,105 +597,129 @@ _NO_VIEW = (0, 0, 0, 0, 0, 0, 0)
 _PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
 _TAGS = {torch.float32: SSU_F32, torch.bfloat16: SSU_BF16, torch.int32: SSU_I32, torch.int64: SSU_I64,
          torch.float16: SSU_F16}
-_HALF = (torch.bfloat16, torch.float16)
+_F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
 _INTS = (torch.int32, torch.int64)
+_HALF = {torch.bfloat16: ((torch.bfloat16,), (torch.bfloat16, torch.float32)),
+         torch.float16: ((torch.float16,), (torch.float16, torch.float32))}
 
 
-def _take(t, name, shape, dtypes, device):
-    """The view fields of tensor ``t`` after checking its shape, dtype and device."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _take(t, name, shape, dtypes, gpu):
+    """The view fields of tensor ``t`` after checking its shape, dtype and device
+    (the index of a GPU)."""
     dtype = t.dtype
-    if dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {dtype} not supported here")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape or dtype not in dtypes or t.get_device() != gpu or t.requires_grad:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {dtype} not supported here")
+        if t.get_device() != gpu:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{gpu}")
+        if torch.is_grad_enabled():
+            raise ValueError(f"inference only: no gradient is recorded for {name}; call under torch.no_grad() or detach it")
     s = t.stride()
     return (t.data_ptr(), _TAGS[dtype], 0) + s + _PAD[len(s)]
 
 
-def _inference_only(*tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("inference only: no gradient is recorded; call under torch.no_grad() or detach the inputs")
-
-
 def _gpu_of(t, name):
-    device = t.device
-    if device.type != "cuda":
+    gpu = t.get_device()
+    if gpu < 0:
         raise ValueError(f"{name} must be on a GPU")
-    return device
+    return gpu
 
 
-class _On:
-    """Where a call runs: its stream's handle, and memory for it that the
-    caching allocator hands out for that stream."""
+def _raw_stream(gpu):
+    return torch.cuda.current_stream(gpu).cuda_stream
 
-    def __init__(self, stream, device):
-        self.device = device
-        self.stream = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.stream = (stream if hasattr(stream, "cuda_stream")
-                           else torch.cuda.ExternalStream(int(stream), device=device))
-            self.handle = self.stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+# The current stream's handle without building a Stream object for it (several
+# times faster, and small calls take little longer than this); the public call
+# where torch does not have it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+class _Own:
+    """A caller's stream: its handle, and memory that the caching allocator hands
+    out for it."""
+
+    def __init__(self, stream, gpu):
+        self.stream = (stream if hasattr(stream, "cuda_stream")
+                       else torch.cuda.ExternalStream(int(stream), device=f"cuda:{gpu}"))
+        self.handle = self.stream.cuda_stream
+
+    def empty(self, shape, dtype, device):
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace(given, need, on):
+class _Current:
+    """The current stream's memory."""
+
+    @staticmethod
+    def empty(shape, dtype, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _on(stream, gpu):
+    """(allocator, handle) of the stream that a call runs on."""
+    if stream is None:
+        return _Current, _raw_stream(gpu)
+    own = _Own(stream, gpu)
+    return own, own.handle
+
+
+def _workspace(given, need, memory, device, gpu):
     """(tensor, pointer, bytes) of a call's workspace: the caller's, or a new one."""
     if given is not None:
-        if given.device != on.device or not given.is_contiguous():
-            raise ValueError(f"workspace must be contiguous, on {on.device}")
+        if given.get_device() != gpu or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous, on cuda:{gpu}")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need <= 0:
         return None, 0, 0
-    ws = on.empty((need,), torch.uint8)
+    ws = memory.empty(need, torch.uint8, device)
     return ws, ws.data_ptr(), need
 
 
-def _check(status, where):
+_TAIL = struct.Struct("Qq")  # workspace, workspace_bytes: the last fields of the structs that have them
+_LINEAR_BUF, _ATTN_BUF = ctypes.c_char * _LINEAR_ARGS.size, ctypes.c_char * _ATTN_ARGS.size
+
+
+def _linear(state, q, k, v, log_decay, cu_seqlens, idx, beta, scale, out, workspace, stream):
+    gpu = _gpu_of(state, "state")
+    try:
+        pool, H, P, N = state.shape
+        T, G, _ = q.shape
+        batch, = idx.shape
+    except ValueError:
+        raise ValueError("state must be [pool, H, P, N], q and k [tokens, G, N], v [tokens, H, P], "
+                         "state_batch_indices [batch]") from None
+    memory, handle = _on(stream, gpu)
+    if out is None:
+        out = memory.empty((T, H, P), torch.bfloat16, state.device)
+    if log_decay.dim() == 1 and log_decay.shape[0] == H:  # one rate for each head
+        decay = _take(log_decay, "log_decay", (H,), _F32, gpu)
+        decay = decay[:3] + (0, decay[3], 0, 0)
+    else:
+        decay = _take(log_decay, "log_decay", (T, H), _F32, gpu)
+    args = _LINEAR_BUF()
+    _LINEAR_ARGS.pack_into(
+        args, 0, batch, H, P, N, G, gpu, T, pool, scale, 0, *_take(state, "state", (pool, H, P, N), _F32, gpu),
+        *_take(idx, "state_batch_indices", (batch,), _INTS, gpu),
+        *(_NO_VIEW if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", (batch + 1,), _I32, gpu)),
+        *_take(q, "q", (T, G, N), _BF16, gpu), *_take(k, "k", (T, G, N), _BF16, gpu),
+        *_take(v, "v", (T, H, P), _BF16, gpu), *decay,
+        *(_NO_VIEW if beta is None else _take(beta, "beta", (T, H), _F32, gpu)),
+        *_take(out, "out", (T, H, P), _BF16, gpu), 0, 0)
+    if cu_seqlens is None:
+        status, where = _lib.ssu_linear_attention_step(args, handle), "ssu_linear_attention_step"
+    else:
+        ws = None
+        need = _lib.ssu_linear_attention_workspace(args)
+        if need > 0:
+            ws, ptr, size = _workspace(workspace, need, memory, state.device, gpu)
+            _TAIL.pack_into(args, _LINEAR_ARGS.size - 16, ptr, size)
+        status, where = _lib.ssu_linear_attention(args, handle), "ssu_linear_attention"
     if status != SSU_OK:
         raise SSUError(status, where)
-
-
-def _linear(state, q, k, v, log_decay, cu_seqlens, idx, beta, scale, out, workspace, stream, where):
-    device = _gpu_of(state, "state")
-    _inference_only(state, q, k, v, log_decay, beta, out)
-    if state.dim() != 4 or q.dim() != 3 or v.dim() != 3:
-        raise ValueError("state must be [pool, H, P, N], q and k [tokens, G, N], v [tokens, H, P]")
-    pool, H, P, N = state.shape
-    T, G = q.shape[0], q.shape[1]
-    if idx.dim() != 1:
-        raise ValueError("state_batch_indices must be [batch]")
-    batch = idx.shape[0]
-    on = _On(stream, device)
-    if out is None:
-        out = on.empty((T, H, P), torch.bfloat16)
-    f32, bf16 = (torch.float32,), (torch.bfloat16,)
-    if log_decay.dim() == 1:  # one rate for each head
-        log_decay = log_decay.expand(T, H) if log_decay.shape[0] == H else log_decay
-    views = (_take(state, "state", (pool, H, P, N), f32, device)
-             + _take(idx, "state_batch_indices", (batch,), _INTS, device)
-             + (_NO_VIEW if cu_seqlens is None
-                else _take(cu_seqlens, "cu_seqlens", (batch + 1,), (torch.int32,), device))
-             + _take(q, "q", (T, G, N), bf16, device) + _take(k, "k", (T, G, N), bf16, device)
-             + _take(v, "v", (T, H, P), bf16, device) + _take(log_decay, "log_decay", (T, H), f32, device)
-             + (_NO_VIEW if beta is None else _take(beta, "beta", (T, H), f32, device))
-             + _take(out, "out", (T, H, P), bf16, device))
-    sizes = (batch, H, P, N, G, device.index, T, pool, scale, 0)
-    ws, ptr, size = None, 0, 0
-    if cu_seqlens is not None:
-        need = _lib.ssu_linear_attention_workspace(_LINEAR_ARGS.pack(*sizes, *views, 0, 0))
-        ws, ptr, size = _workspace(workspace, need, on)
-    args = _LINEAR_ARGS.pack(*sizes, *views, ptr, size)
-    fn = _lib.ssu_linear_attention_step if cu_seqlens is None else _lib.ssu_linear_attention
-    _check(fn(args, on.handle), where)
     return out
 
 
@@ -714,8 +738,7 @@ def linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices,
     used by another call at the same time. Inference only: no gradient."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
-    return _linear(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace, stream,
-                   "ssu_linear_attention")
+    return _linear(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace, stream)
 
 
 def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=None, scale=1.0, out=None, stream=None):
@@ -724,8 +747,7 @@ def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=N
     None. Returns out [batch, H, P] bf16."""
     if q.shape[0] != state_batch_indices.shape[0]:
         raise ValueError(f"q has {q.shape[0]} tokens for {state_batch_indices.shape[0]} requests")
-    return _linear(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None, stream,
-                   "ssu_linear_attention_step")
+    return _linear(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None, stream)
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -741,43 +763,45 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
     (int32/int64, outside the cache: skipped; in-range slots distinct), keys and
     values go into the cache, and k_out is None unless it is given. Inference
     only: no gradient."""
-    device = _gpu_of(q, "q")
-    _inference_only(q, k, q_weight, k_weight, cos_sin, v, k_cache, v_cache, q_out, k_out)
-    if q.dim() != 3 or k.dim() != 3 or cos_sin.dim() != 2:
-        raise ValueError("q must be [tokens, Hq, D], k [tokens, Hk, D], cos_sin [max_pos, rot]")
-    if q.dtype not in _HALF:
-        raise TypeError(f"q: dtype {q.dtype} not supported here")
-    T, nq, D = q.shape
-    nk = k.shape[1]
-    half, weight = (q.dtype,), (torch.float32, q.dtype)
-    max_pos, rot = cos_sin.shape
-    on = _On(stream, device)
-    with_cache = k_cache is not None
-    if (v_cache is not None) != with_cache or (v is not None) != with_cache or (slots is not None) != with_cache:
-        raise ValueError("v, k_cache, v_cache and slots go together")
-    if q_out is None:
-        q_out = on.empty((T, nq, D), q.dtype)
-    if k_out is None and not with_cache:
-        k_out = on.empty((T, nk, D), q.dtype)
+    gpu = _gpu_of(q, "q")
+    try:
+        T, nq, D = q.shape
+        _, nk, _ = k.shape
+        max_pos, rot = cos_sin.shape
+        half, weight = _HALF[q.dtype]
+    except ValueError:
+        raise ValueError("q must be [tokens, Hq, D], k [tokens, Hk, D], cos_sin [max_pos, rot]") from None
+    except KeyError:
+        raise TypeError(f"q: dtype {q.dtype} not supported here") from None
+    memory, handle = _on(stream, gpu)
     pages = page_size = 0
     cache = _NO_VIEW * 4
-    if with_cache:
+    if k_cache is not None:
+        if v is None or v_cache is None or slots is None:
+            raise ValueError("v, k_cache, v_cache and slots go together")
         if k_cache.dim() != 4:
             raise ValueError("k_cache must be [pages, page_size, Hk, D]")
-        pages, page_size = k_cache.shape[0], k_cache.shape[1]
+        pages, page_size = k_cache.shape[:2]
         shape = (pages, page_size, nk, D)
-        cache = (_take(v, "v", (T, nk, D), half, device) + _take(k_cache, "k_cache", shape, half, device)
-                 + _take(v_cache, "v_cache", shape, half, device) + _take(slots, "slots", (T,), _INTS, device))
+        cache = (_take(v, "v", (T, nk, D), half, gpu) + _take(k_cache, "k_cache", shape, half, gpu)
+                 + _take(v_cache, "v_cache", shape, half, gpu) + _take(slots, "slots", (T,), _INTS, gpu))
+    elif v is not None or v_cache is not None or slots is not None:
+        raise ValueError("v, k_cache, v_cache and slots go together")
+    elif k_out is None:
+        k_out = memory.empty((T, nk, D), q.dtype, q.device)
+    if q_out is None:
+        q_out = memory.empty((T, nq, D), q.dtype, q.device)
     args = _QK_ARGS.pack(
-        T, nq, nk, D, rot, 1 if interleaved else 0, device.index, eps, page_size, max_pos, pages,
-        *_take(q, "q", (T, nq, D), half, device), *_take(k, "k", (T, nk, D), half, device),
-        *(_NO_VIEW if q_weight is None else _take(q_weight, "q_weight", (D,), weight, device)),
-        *(_NO_VIEW if k_weight is None else _take(k_weight, "k_weight", (D,), weight, device)),
-        *_take(positions, "positions", (T,), _INTS, device),
-        *_take(cos_sin, "cos_sin", (max_pos, rot), (torch.float32,), device),
-        *_take(q_out, "q_out", (T, nq, D), half, device),
-        *(_NO_VIEW if k_out is None else _take(k_out, "k_out", (T, nk, D), half, device)), *cache)
-    _check(_lib.ssu_qk_norm_rope(args, on.handle), "ssu_qk_norm_rope")
+        T, nq, nk, D, rot, 1 if interleaved else 0, gpu, eps, page_size, max_pos, pages,
+        *_take(q, "q", (T, nq, D), half, gpu), *_take(k, "k", (T, nk, D), half, gpu),
+        *(_NO_VIEW if q_weight is None else _take(q_weight, "q_weight", (D,), weight, gpu)),
+        *(_NO_VIEW if k_weight is None else _take(k_weight, "k_weight", (D,), weight, gpu)),
+        *_take(positions, "positions", (T,), _INTS, gpu), *_take(cos_sin, "cos_sin", (max_pos, rot), _F32, gpu),
+        *_take(q_out, "q_out", (T, nq, D), half, gpu),
+        *(_NO_VIEW if k_out is None else _take(k_out, "k_out", (T, nk, D), half, gpu)), *cache)
+    status = _lib.ssu_qk_norm_rope(args, handle)
+    if status != SSU_OK:
+        raise SSUError(status, "ssu_qk_norm_rope")
     return q_out, k_out
 
 
@@ -793,28 +817,34 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=
     [batch, Hq, D], with return_lse also the logarithms of the softmax sums
     [batch, Hq] fp32. ``workspace`` as in linear_attention. Inference only: no
     gradient."""
-    device = _gpu_of(q, "q")
-    _inference_only(q, k_cache, v_cache, out)
-    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q must be [batch, Hq, D], k_cache [pages, page_size, Hk, D], block_table [batch, max_pages]")
-    if q.dtype not in _HALF:
-        raise TypeError(f"q: dtype {q.dtype} not supported here")
-    batch, nq, D = q.shape
-    pages, page_size, nk, _ = k_cache.shape
-    half, i32 = (q.dtype,), (torch.int32,)
-    on = _On(stream, device)
+    gpu = _gpu_of(q, "q")
+    try:
+        batch, nq, D = q.shape
+        pages, page_size, nk, _ = k_cache.shape
+        _, max_pages = block_table.shape
+        half, _ = _HALF[q.dtype]
+    except ValueError:
+        raise ValueError("q must be [batch, Hq, D], k_cache [pages, page_size, Hk, D], block_table [batch, max_pages]") from None
+    except KeyError:
+        raise TypeError(f"q: dtype {q.dtype} not supported here") from None
+    memory, handle = _on(stream, gpu)
+    device = q.device
     if out is None:
-        out = on.empty((batch, nq, D), q.dtype)
-    lse = on.empty((batch, nq), torch.float32) if return_lse else None
-    sizes = (batch, nq, nk, D, page_size, device.index, pages, block_table.shape[1],
-             D ** -0.5 if scale is None else scale, 0)
+        out = memory.empty((batch, nq, D), q.dtype, device)
+    lse = memory.empty((batch, nq), torch.float32, device) if return_lse else None
     cache = (pages, page_size, nk, D)
-    views = (_take(q, "q", (batch, nq, D), half, device) + _take(k_cache, "k_cache", cache, half, device)
-             + _take(v_cache, "v_cache", cache, half, device)
-             + _take(block_table, "block_table", (batch, block_table.shape[1]), i32, device)
-             + _take(seq_lens, "seq_lens", (batch,), i32, device) + _take(out, "out", (batch, nq, D), half, device)
-             + (_NO_VIEW if lse is None else _take(lse, "lse", (batch, nq), (torch.float32,), device)))
-    need = _lib.ssu_paged_attention_workspace(_ATTN_ARGS.pack(*sizes, *views, 0, 0))
-    ws, ptr, size = _workspace(workspace, need, on)
-    _check(_lib.ssu_paged_attention(_ATTN_ARGS.pack(*sizes, *views, ptr, size), on.handle), "ssu_paged_attention")
+    args = _ATTN_BUF()
+    _ATTN_ARGS.pack_into(
+        args, 0, batch, nq, nk, D, page_size, gpu, pages, max_pages, D ** -0.5 if scale is None else scale, 0,
+        *_take(q, "q", (batch, nq, D), half, gpu), *_take(k_cache, "k_cache", cache, half, gpu),
+        *_take(v_cache, "v_cache", cache, half, gpu), *_take(block_table, "block_table", (batch, max_pages), _I32, gpu),
+        *_take(seq_lens, "seq_lens", (batch,), _I32, gpu), *_take(out, "out", (batch, nq, D), half, gpu),
+        *(_NO_VIEW if lse is None else _take(lse, "lse", (batch, nq), _F32, gpu)), 0, 0)
+    need = _lib.ssu_paged_attention_workspace(args)
+    if need > 0:
+        ws, ptr, size = _workspace(workspace, need, memory, device, gpu)
+        _TAIL.pack_into(args, _ATTN_ARGS.size - 16, ptr, size)
+    status = _lib.ssu_paged_attention(args, handle)
+    if status != SSU_OK:
+        raise SSUError(status, "ssu_paged_attention")
     return (out, lse) if return_lse else out

@@ -22,6 +22,7 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 // 16-bit floating types: the fp32 value of bits, and bits rounded to nearest
 // even from fp32 (the conversion is kept opaque to the compiler so that it is
@@ -96,6 +97,32 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return
 __device__ __forceinline__ int64_t load_index(const void *p, int is64, int64_t i)
 {
     return is64 ? static_cast<const int64_t *>(p)[i] : static_cast<int64_t>(static_cast<const int32_t *>(p)[i]);
+}
+
+// The sum over aligned groups of LANES lanes, in every lane of a group: within 16
+// lanes by DPP (quad permutes, half-row and row mirror), beyond by exchange.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x)
+{
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
+template <int LANES>
+__device__ __forceinline__ float sum_lanes(float x)
+{
+    if constexpr (LANES >= 2)
+        x = dpp_add<0xB1>(x);
+    if constexpr (LANES >= 4)
+        x = dpp_add<0x4E>(x);
+    if constexpr (LANES >= 8)
+        x = dpp_add<0x141>(x);
+    if constexpr (LANES >= 16)
+        x = dpp_add<0x140>(x);
+    if constexpr (LANES >= 32)
+        x += __shfl_xor(x, 16);
+    if constexpr (LANES >= 64)
+        x += __shfl_xor(x, 32);
+    return x;
 }
 
 // Launch a kernel and return its own status (a call that fails leaves no
