@@ -20,7 +20,7 @@ struct LinearParams {
     int64_t s_slot, s_head, s_row;
     const void *idx;
     int64_t pool_slots;
-    const int32_t *cu;  // NULL: token b is request b's
+    const int32_t *cu;  // (prompts)
     const uint16_t *q, *k, *v;
     int64_t q_t, q_g, k_t, k_g, v_t, v_h;
     const float *decay, *beta;
@@ -32,92 +32,82 @@ struct LinearParams {
     float scale;
 };
 
-// The recurrence, token after token, the state in registers. One wave owns
-// RPI * R rows p of one (request, head): a row's N values are split over LPR =
-// N / 4 lanes (N = 256: 32 lanes with two chunks), one dwordx4 each, so that
-// one instruction moves 1 KiB of contiguous state.
+// One token per request. One wave owns RPI * R rows p of one (request, head): a
+// row's N values are split over LPR = N / 4 lanes (N = 256: 32 lanes with two
+// chunks), one dwordx4 each, so that one instruction moves 1 KiB of contiguous
+// state. Memory-bound by the state, read and written once: what does not
+// depend on the slot is requested first (vector loads return in order, so
+// nothing may wait behind the state), the slot and the head's decay and gain go
+// through the scalar cache, and the state goes past the caches.
 template <int N, int R>
-__global__ void __launch_bounds__(64) ssu_linear_recurrent_kernel(const LinearParams p)
+__global__ void __launch_bounds__(64) ssu_linear_step_kernel(const LinearParams p)
 {
     constexpr int VEC = N > 128 ? N / 128 : 1;
     constexpr int LPR = N / (4 * VEC);
     constexpr int RPI = 64 / LPR;
     static_assert(R <= LPR, "one writer lane per row");
-    const int g = xcd_order(static_cast<int>(blockIdx.x), p.total);
-    const int tile = g % p.tiles, bh = g / p.tiles;
-    const int h = bh % p.nheads, b = bh / p.nheads, grp = h / p.heads_per_group;
+    const int id = xcd_order(static_cast<int>(blockIdx.x), p.total);
+    const int tile = id % p.tiles, bh = id / p.tiles;
+    const int h = __builtin_amdgcn_readfirstlane(bh % p.nheads), b = __builtin_amdgcn_readfirstlane(bh / p.nheads);
+    const int grp = __builtin_amdgcn_readfirstlane(h / p.heads_per_group);
     const int lane = static_cast<int>(threadIdx.x), c = lane % LPR, sub = lane / LPR;
-    const int64_t slot = load_index(p.idx, p.idx64, b);
+    const int row0 = __builtin_amdgcn_readfirstlane(tile * RPI * R) + sub;
+
+    const uint16_t *const qt = p.q + b * p.q_t + grp * p.q_g, *const kt = p.k + b * p.k_t + grp * p.k_g;
+    const uint16_t *const vt = p.v + b * p.v_t + h * p.v_h;
+    u32x2 qw[VEC], kw[VEC];
+    uint16_t vw[R];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        qw[e] = *reinterpret_cast<const u32x2_a2 *>(qt + 4 * c + 128 * e);
+        kw[e] = *reinterpret_cast<const u32x2_a2 *>(kt + 4 * c + 128 * e);
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        vw[j] = vt[min(row0 + j * RPI, p.headdim - 1)];
+
+    const int64_t slot = p.idx64 ? load_ro(static_cast<const int64_t *>(p.idx) + b)
+                                 : static_cast<int64_t>(load_ro(static_cast<const int32_t *>(p.idx) + b));
     if (slot < 0 || slot >= p.pool_slots)
         return;  // padding
-    int64_t t = b, end = b + 1;
-    if (p.cu) {
-        t = max(static_cast<int64_t>(p.cu[b]), int64_t(0));
-        end = min(static_cast<int64_t>(p.cu[b + 1]), p.ntokens);
-    }
-    if (t >= end)
-        return;
-
-    const int row0 = tile * RPI * R + sub;
-    float *const sp = p.state + slot * p.s_slot + h * p.s_head + 4 * c;
+    float *const sp = p.state + slot * p.s_slot + h * p.s_head + row0 * p.s_row + 4 * c;
     f32x4 s[R][VEC];
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            if (row0 + j * RPI < p.headdim)
-                s[j][e] = load4<true>(sp + (row0 + j * RPI) * p.s_row + 128 * e);
-            else
-                s[j][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            s[j][e] = row0 + j * RPI < p.headdim ? load4<true>(sp + j * RPI * p.s_row + 128 * e) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (; t < end; ++t) {
-        const uint16_t *const qt = p.q + t * p.q_t + grp * p.q_g, *const kt = p.k + t * p.k_t + grp * p.k_g;
-        const uint16_t *const vt = p.v + t * p.v_t + h * p.v_h;
-        const float a = exp_f32(p.decay[t * p.d_t + h * p.d_h]);
-        const float beta = p.beta ? p.beta[t * p.b_t + h * p.b_h] : 1.0f;
-        float q[VEC][4], k[VEC][4];
+    const float a = exp_f32(load_ro(p.decay + (b * p.d_t + h * p.d_h)));
+    const float beta = p.beta ? load_ro(p.beta + (b * p.b_t + h * p.b_h)) : 1.0f;
+    float y[R];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const u32x2 qw = *reinterpret_cast<const u32x2_a2 *>(qt + 4 * c + 128 * e);
-            const u32x2 kw = *reinterpret_cast<const u32x2_a2 *>(kt + 4 * c + 128 * e);
+    for (int j = 0; j < R; ++j) {
+        const float v = beta * Bf16::lo(vw[j]);
+        float acc = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                q[e][2 * i] = Bf16::lo(qw[i]);
-                q[e][2 * i + 1] = Bf16::hi(qw[i]);
-                k[e][2 * i] = Bf16::lo(kw[i]);
-                k[e][2 * i + 1] = Bf16::hi(kw[i]);
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float k = i % 2 ? Bf16::hi(kw[e][i / 2]) : Bf16::lo(kw[e][i / 2]);
+                const float q = i % 2 ? Bf16::hi(qw[e][i / 2]) : Bf16::lo(qw[e][i / 2]);
+                s[j][e][i] = fmaf(s[j][e][i], a, v * k);
+                acc = fmaf(s[j][e][i], q, acc);
             }
-        }
-        float y[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const int row = row0 + j * RPI;
-            const float v = beta * (row < p.headdim ? Bf16::lo(vt[row]) : 0.0f);
-            float acc = 0.0f;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[j][e][i] = fmaf(s[j][e][i], a, v * k[e][i]);
-                    acc = fmaf(s[j][e][i], q[e][i], acc);
-                }
-#pragma unroll
-            for (int m = LPR / 2; m >= 1; m /= 2)
-                acc += __shfl_xor(acc, m);
-            y[j] = acc;
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (c == j && row0 + j * RPI < p.headdim)
-                p.out[t * p.o_t + h * p.o_h + row0 + j * RPI] = Bf16::round(p.scale * y[j]);
-    }
-
-#pragma unroll
-    for (int j = 0; j < R; ++j)
+        y[j] = acc;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             if (row0 + j * RPI < p.headdim)
-                store4<true>(sp + (row0 + j * RPI) * p.s_row + 128 * e, s[j][e]);
+                store4<true>(sp + j * RPI * p.s_row + 128 * e, s[j][e]);
+    }
+    float mine = 0.0f;  // row c of this lane's R
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const float sum = sum_lanes<LPR>(y[j]);
+        mine = c == j ? sum : mine;
+    }
+    if (c < R && row0 + c * RPI < p.headdim)
+        p.out[b * p.o_t + h * p.o_h + row0 + c * RPI] = Bf16::round(p.scale * mine);
 }
 
 // Prompts, 32 tokens (a chunk) at a time. With L_i the decays' logarithms summed
@@ -622,16 +612,29 @@ __global__ void __launch_bounds__(256) ssu_linear_segments_kernel(const ChunkPar
 
 using LinearFn = void (*)(LinearParams);
 
-struct LinearKernel {
+struct StepKernel {
     LinearFn fn;
     int rows;  // of the state per workgroup
 };
 
-template <int N, int R>
-constexpr LinearKernel recurrent()
+// LOADS dwordx4 of state per lane.
+template <int N, int LOADS>
+constexpr StepKernel step_kernel()
 {
     constexpr int VEC = N > 128 ? N / 128 : 1;
-    return {&ssu_linear_recurrent_kernel<N, R>, 64 / (N / (4 * VEC)) * R};
+    return {&ssu_linear_step_kernel<N, LOADS / VEC>, 64 / (N / (4 * VEC)) * LOADS / VEC};
+}
+
+template <int LOADS>
+StepKernel step_kernel(int N)
+{
+    switch (N) {
+    case 16: return step_kernel<16, LOADS>();
+    case 32: return step_kernel<32, LOADS>();
+    case 64: return step_kernel<64, LOADS>();
+    case 128: return step_kernel<128, LOADS>();
+    default: return step_kernel<256, LOADS>();
+    }
 }
 
 using ChunkFn = void (*)(ChunkParams);
@@ -658,17 +661,6 @@ ChunkKernels chunk_kernels(int N, int P)
 {
     // eight waves where the last 128 columns hold more than 64
     return (P - 1) % 128 >= 64 ? chunk_kernels<8>(N) : chunk_kernels<4>(N);
-}
-
-LinearKernel recurrent_kernel(int N)
-{
-    switch (N) {
-    case 16: return recurrent<16, 4>();
-    case 32: return recurrent<32, 4>();
-    case 64: return recurrent<64, 4>();
-    case 128: return recurrent<128, 4>();
-    default: return recurrent<256, 4>();
-    }
 }
 
 // ------------------------------------------------------------------ host --
@@ -809,17 +801,32 @@ LinearParams linear_params(const ssu_linear_args &a)
     return p;
 }
 
-ssu_status launch_recurrent(const ssu_linear_args &a, hipStream_t stream)
+// Launch of a step by the bytes of state that it moves one way (H16 P64 N128 and
+// others): two dwordx4 per lane below 8 MiB (more waves for the latency: one
+// request 2.9 us), four above; residency capped (by unused LDS) at 16 workgroups per
+// CU from 40 MiB and 14 from 128 MiB, since more state in flight only crowds
+// the memory system (256 MiB: 88.5 us, 6.1 TB/s, at 14;
+// 96.0 uncapped, 91.9 at 12, 89.0 at 16; 32 MiB: 13.5 us uncapped, 14.0 at 16).
+ssu_status launch_step(const ssu_linear_args &a, hipStream_t stream)
 {
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
-    const LinearKernel k = recurrent_kernel(a.dstate);
+    const int64_t mib = static_cast<int64_t>(a.batch) * a.nheads * a.headdim * a.dstate >> 18;
+    const StepKernel k = mib < 8 ? step_kernel<2>(a.dstate) : step_kernel<4>(a.dstate);
     LinearParams p = linear_params(a);
     p.tiles = (a.headdim + k.rows - 1) / k.rows;
     p.total = a.batch * a.nheads * p.tiles;
-    const hipError_t e = launch_kernel(k.fn, p, p.total, 64, 0, stream);
+    size_t lds = 0;
+    if (mib >= 40) {
+        int dev = 0;
+        if (hipGetDevice(&dev) != hipSuccess)
+            return fail(SSU_ERR_HIP, "hipGetDevice failed");
+        const DeviceLimits lim = device_limits(dev);
+        lds = lds_for_cap(mib < 128 ? 16 : 14, lim.lds_cu, lim.lds_block);
+    }
+    const hipError_t e = launch_kernel(k.fn, p, p.total, 64, lds, stream);
     if (e != hipSuccess)
-        return fail(SSU_ERR_HIP, "launch of the linear attention kernel failed: %s", hipGetErrorString(e));
+        return fail(SSU_ERR_HIP, "launch of the linear attention step failed: %s", hipGetErrorString(e));
     return SSU_OK;
 }
 
@@ -891,7 +898,7 @@ ssu_status ssu_linear_attention_step(const ssu_linear_args *a, hipStream_t strea
     SSU_TRY(check_linear(*a, "ssu_linear_attention_step", false));
     if (a->batch == 0)
         return SSU_OK;
-    return launch_recurrent(*a, stream);
+    return launch_step(*a, stream);
 }
 
 }  // extern "C"
