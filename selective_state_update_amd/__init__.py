@@ -29,7 +29,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 __all__ = [
@@ -164,12 +163,6 @@ _lib.ssu_scan_tile_name.argtypes = [_i32]
 _lib.ssu_scan_tile_name.restype = ctypes.c_char_p
 _lib.ssu_scan_select_tile.argtypes = [ctypes.POINTER(ScanArgs), _i64]
 _lib.ssu_scan_select_tile.restype = _i32
-for _name in ("ssu_linear_attention", "ssu_linear_attention_step", "ssu_qk_norm_rope", "ssu_paged_attention"):
-    getattr(_lib, _name).argtypes = [_vp, _vp]
-    getattr(_lib, _name).restype = _i32
-for _name in ("ssu_linear_attention_workspace", "ssu_paged_attention_workspace"):
-    getattr(_lib, _name).argtypes = [_vp]
-    getattr(_lib, _name).restype = _i64
 _lib.ssu_abi_version.argtypes = []
 _lib.ssu_abi_version.restype = _i32
 
@@ -587,140 +580,20 @@ def selective_scan(u, delta, A, B, C, state, D=None, delta_bias=None, delta_soft
 # Sequence operators of hybrid models: ssu_linear_attention(_step),
 # ssu_qk_norm_rope, ssu_paged_attention
 # --------------------------------------------------------------------------- #
-# The arguments' structs as include/ssu.h declares them, packed in one go (a
-# struct field at a time, ctypes takes longer than the smallest calls run).
-_VIEW = "Qii4q"  # ptr, dtype, reserved, strides
-_LINEAR_ARGS = struct.Struct("6i2qfi" + _VIEW * 9 + "Qq")
-_QK_ARGS = struct.Struct("q6ifi2q" + _VIEW * 12)
-_ATTN_ARGS = struct.Struct("6i2qfi" + _VIEW * 7 + "Qq")
-_NO_VIEW = (0, 0, 0, 0, 0, 0, 0)
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
-_TAGS = {torch.float32: SSU_F32, torch.bfloat16: SSU_BF16, torch.int32: SSU_I32, torch.int64: SSU_I64,
-         torch.float16: SSU_F16}
-_F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
-_INTS = (torch.int32, torch.int64)
-_HALF = {torch.bfloat16: ((torch.bfloat16,), (torch.bfloat16, torch.float32)),
-         torch.float16: ((torch.float16,), (torch.float16, torch.float32))}
+# Checked, packed and launched by a native module (csrc/binding.cpp): the
+# smallest of these calls run for a few microseconds.
+from . import _native  # noqa: E402
+
+_native.errors(SSUError)
 
 
-def _take(t, name, shape, dtypes, gpu):
-    """The view fields of tensor ``t`` after checking its shape, dtype and device
-    (the index of a GPU)."""
-    dtype = t.dtype
-    if t.shape != shape or dtype not in dtypes or t.get_device() != gpu or t.requires_grad:
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if dtype not in dtypes:
-            raise TypeError(f"{name}: dtype {dtype} not supported here")
-        if t.get_device() != gpu:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{gpu}")
-        if torch.is_grad_enabled():
-            raise ValueError(f"inference only: no gradient is recorded for {name}; call under torch.no_grad() or detach it")
-    s = t.stride()
-    return (t.data_ptr(), _TAGS[dtype], 0) + s + _PAD[len(s)]
-
-
-def _gpu_of(t, name):
-    gpu = t.get_device()
-    if gpu < 0:
-        raise ValueError(f"{name} must be on a GPU")
-    return gpu
-
-
-def _raw_stream(gpu):
-    return torch.cuda.current_stream(gpu).cuda_stream
-
-
-# The current stream's handle without building a Stream object for it (several
-# times faster, and small calls take little longer than this); the public call
-# where torch does not have it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-
-
-class _Own:
-    """A caller's stream: its handle, and memory that the caching allocator hands
-    out for it."""
-
-    def __init__(self, stream, gpu):
-        self.stream = (stream if hasattr(stream, "cuda_stream")
-                       else torch.cuda.ExternalStream(int(stream), device=f"cuda:{gpu}"))
-        self.handle = self.stream.cuda_stream
-
-    def empty(self, shape, dtype, device):
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-
-
-class _Current:
-    """The current stream's memory."""
-
-    @staticmethod
-    def empty(shape, dtype, device):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _on(stream, gpu):
-    """(allocator, handle) of the stream that a call runs on."""
-    if stream is None:
-        return _Current, _raw_stream(gpu)
-    own = _Own(stream, gpu)
-    return own, own.handle
-
-
-def _workspace(given, need, memory, device, gpu):
-    """(tensor, pointer, bytes) of a call's workspace: the caller's, or a new one."""
-    if given is not None:
-        if given.get_device() != gpu or not given.is_contiguous():
-            raise ValueError(f"workspace must be contiguous, on cuda:{gpu}")
-        return given, given.data_ptr(), given.numel() * given.element_size()
-    if need <= 0:
-        return None, 0, 0
-    ws = memory.empty(need, torch.uint8, device)
-    return ws, ws.data_ptr(), need
-
-
-_TAIL = struct.Struct("Qq")  # workspace, workspace_bytes: the last fields of the structs that have them
-_LINEAR_BUF, _ATTN_BUF = ctypes.c_char * _LINEAR_ARGS.size, ctypes.c_char * _ATTN_ARGS.size
-
-
-def _linear(state, q, k, v, log_decay, cu_seqlens, idx, beta, scale, out, workspace, stream):
-    gpu = _gpu_of(state, "state")
-    try:
-        pool, H, P, N = state.shape
-        T, G, _ = q.shape
-        batch, = idx.shape
-    except ValueError:
-        raise ValueError("state must be [pool, H, P, N], q and k [tokens, G, N], v [tokens, H, P], "
-                         "state_batch_indices [batch]") from None
-    memory, handle = _on(stream, gpu)
-    if out is None:
-        out = memory.empty((T, H, P), torch.bfloat16, state.device)
-    if log_decay.dim() == 1 and log_decay.shape[0] == H:  # one rate for each head
-        decay = _take(log_decay, "log_decay", (H,), _F32, gpu)
-        decay = decay[:3] + (0, decay[3], 0, 0)
-    else:
-        decay = _take(log_decay, "log_decay", (T, H), _F32, gpu)
-    args = _LINEAR_BUF()
-    _LINEAR_ARGS.pack_into(
-        args, 0, batch, H, P, N, G, gpu, T, pool, scale, 0, *_take(state, "state", (pool, H, P, N), _F32, gpu),
-        *_take(idx, "state_batch_indices", (batch,), _INTS, gpu),
-        *(_NO_VIEW if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", (batch + 1,), _I32, gpu)),
-        *_take(q, "q", (T, G, N), _BF16, gpu), *_take(k, "k", (T, G, N), _BF16, gpu),
-        *_take(v, "v", (T, H, P), _BF16, gpu), *decay,
-        *(_NO_VIEW if beta is None else _take(beta, "beta", (T, H), _F32, gpu)),
-        *_take(out, "out", (T, H, P), _BF16, gpu), 0, 0)
-    if cu_seqlens is None:
-        status, where = _lib.ssu_linear_attention_step(args, handle), "ssu_linear_attention_step"
-    else:
-        ws = None
-        need = _lib.ssu_linear_attention_workspace(args)
-        if need > 0:
-            ws, ptr, size = _workspace(workspace, need, memory, state.device, gpu)
-            _TAIL.pack_into(args, _LINEAR_ARGS.size - 16, ptr, size)
-        status, where = _lib.ssu_linear_attention(args, handle), "ssu_linear_attention"
-    if status != SSU_OK:
-        raise SSUError(status, where)
-    return out
+def _on(stream, t):
+    """A context in which ``stream`` (a torch stream or a raw handle) is the
+    current stream, so that it runs the call and its memory is allocated for it."""
+    torch = _torch()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta=None, scale=1.0, out=None,
@@ -738,16 +611,20 @@ def linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices,
     used by another call at the same time. Inference only: no gradient."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
-    return _linear(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace, stream)
+    if stream is not None:
+        with _on(stream, state):
+            return linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace)
+    return _native.linear(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace)
 
 
 def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=None, scale=1.0, out=None, stream=None):
     """The same for one token per request (ssu_linear_attention_step): q, k
     [batch, G, N], v [batch, H, P], log_decay [batch, H] or [H], beta [batch, H] or
     None. Returns out [batch, H, P] bf16."""
-    if q.shape[0] != state_batch_indices.shape[0]:
-        raise ValueError(f"q has {q.shape[0]} tokens for {state_batch_indices.shape[0]} requests")
-    return _linear(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None, stream)
+    if stream is not None:
+        with _on(stream, state):
+            return linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta, scale, out)
+    return _native.linear(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None)
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -763,46 +640,12 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
     (int32/int64, outside the cache: skipped; in-range slots distinct), keys and
     values go into the cache, and k_out is None unless it is given. Inference
     only: no gradient."""
-    gpu = _gpu_of(q, "q")
-    try:
-        T, nq, D = q.shape
-        _, nk, _ = k.shape
-        max_pos, rot = cos_sin.shape
-        half, weight = _HALF[q.dtype]
-    except ValueError:
-        raise ValueError("q must be [tokens, Hq, D], k [tokens, Hk, D], cos_sin [max_pos, rot]") from None
-    except KeyError:
-        raise TypeError(f"q: dtype {q.dtype} not supported here") from None
-    memory, handle = _on(stream, gpu)
-    pages = page_size = 0
-    cache = _NO_VIEW * 4
-    if k_cache is not None:
-        if v is None or v_cache is None or slots is None:
-            raise ValueError("v, k_cache, v_cache and slots go together")
-        if k_cache.dim() != 4:
-            raise ValueError("k_cache must be [pages, page_size, Hk, D]")
-        pages, page_size = k_cache.shape[:2]
-        shape = (pages, page_size, nk, D)
-        cache = (_take(v, "v", (T, nk, D), half, gpu) + _take(k_cache, "k_cache", shape, half, gpu)
-                 + _take(v_cache, "v_cache", shape, half, gpu) + _take(slots, "slots", (T,), _INTS, gpu))
-    elif v is not None or v_cache is not None or slots is not None:
-        raise ValueError("v, k_cache, v_cache and slots go together")
-    elif k_out is None:
-        k_out = memory.empty((T, nk, D), q.dtype, q.device)
-    if q_out is None:
-        q_out = memory.empty((T, nq, D), q.dtype, q.device)
-    args = _QK_ARGS.pack(
-        T, nq, nk, D, rot, 1 if interleaved else 0, gpu, eps, page_size, max_pos, pages,
-        *_take(q, "q", (T, nq, D), half, gpu), *_take(k, "k", (T, nk, D), half, gpu),
-        *(_NO_VIEW if q_weight is None else _take(q_weight, "q_weight", (D,), weight, gpu)),
-        *(_NO_VIEW if k_weight is None else _take(k_weight, "k_weight", (D,), weight, gpu)),
-        *_take(positions, "positions", (T,), _INTS, gpu), *_take(cos_sin, "cos_sin", (max_pos, rot), _F32, gpu),
-        *_take(q_out, "q_out", (T, nq, D), half, gpu),
-        *(_NO_VIEW if k_out is None else _take(k_out, "k_out", (T, nk, D), half, gpu)), *cache)
-    status = _lib.ssu_qk_norm_rope(args, handle)
-    if status != SSU_OK:
-        raise SSUError(status, "ssu_qk_norm_rope")
-    return q_out, k_out
+    if stream is not None:
+        with _on(stream, q):
+            return qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, v, k_cache,
+                                v_cache, slots)
+    return _native.qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, v, k_cache, v_cache,
+                      slots)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, return_lse=False, workspace=None,
@@ -817,34 +660,7 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=
     [batch, Hq, D], with return_lse also the logarithms of the softmax sums
     [batch, Hq] fp32. ``workspace`` as in linear_attention. Inference only: no
     gradient."""
-    gpu = _gpu_of(q, "q")
-    try:
-        batch, nq, D = q.shape
-        pages, page_size, nk, _ = k_cache.shape
-        _, max_pages = block_table.shape
-        half, _ = _HALF[q.dtype]
-    except ValueError:
-        raise ValueError("q must be [batch, Hq, D], k_cache [pages, page_size, Hk, D], block_table [batch, max_pages]") from None
-    except KeyError:
-        raise TypeError(f"q: dtype {q.dtype} not supported here") from None
-    memory, handle = _on(stream, gpu)
-    device = q.device
-    if out is None:
-        out = memory.empty((batch, nq, D), q.dtype, device)
-    lse = memory.empty((batch, nq), torch.float32, device) if return_lse else None
-    cache = (pages, page_size, nk, D)
-    args = _ATTN_BUF()
-    _ATTN_ARGS.pack_into(
-        args, 0, batch, nq, nk, D, page_size, gpu, pages, max_pages, D ** -0.5 if scale is None else scale, 0,
-        *_take(q, "q", (batch, nq, D), half, gpu), *_take(k_cache, "k_cache", cache, half, gpu),
-        *_take(v_cache, "v_cache", cache, half, gpu), *_take(block_table, "block_table", (batch, max_pages), _I32, gpu),
-        *_take(seq_lens, "seq_lens", (batch,), _I32, gpu), *_take(out, "out", (batch, nq, D), half, gpu),
-        *(_NO_VIEW if lse is None else _take(lse, "lse", (batch, nq), _F32, gpu)), 0, 0)
-    need = _lib.ssu_paged_attention_workspace(args)
-    if need > 0:
-        ws, ptr, size = _workspace(workspace, need, memory, device, gpu)
-        _TAIL.pack_into(args, _ATTN_ARGS.size - 16, ptr, size)
-    status = _lib.ssu_paged_attention(args, handle)
-    if status != SSU_OK:
-        raise SSUError(status, "ssu_paged_attention")
-    return (out, lse) if return_lse else out
+    if stream is not None:
+        with _on(stream, q):
+            return paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, return_lse, workspace)
+    return _native.attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, return_lse, workspace)

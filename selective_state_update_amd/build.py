@@ -1,4 +1,5 @@
-"""Build libssu.so (HIP, gfx950) in-tree with hipcc.
+"""Build libssu.so (HIP, gfx950) in-tree with hipcc, and the native Python module
+of its sequence operators (_native.so, g++).
 
     python selective_state_update_amd/build.py
 
@@ -63,6 +64,31 @@ def build(extra=(), out: str = LIB, verbose: bool = False) -> str:
     return out
 
 
+BINDING_SRC = os.path.join(HERE, "csrc", "binding.cpp")
+BINDING = os.path.join(HERE, "_native.so")
+
+
+def build_binding(lib: str = LIB, out: str = BINDING, verbose: bool = False) -> str:
+    """The native Python module of the sequence operators (host code: torch's
+    C++ headers, linked to libssu.so beside it)."""
+    import sysconfig
+
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(ROOT, "include"), "-o", out + ".tmp", BINDING_SRC,
+           "-L", os.path.dirname(lib), "-l:" + os.path.basename(lib), "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    _run(cmd, "binding build", verbose)
+    os.replace(out + ".tmp", out)
+    return out
+
+
 PROBE_SRC = os.path.join(HERE, "csrc", "valu_rate_probe.hip")
 PROBE = os.path.join(HERE, "valu_rate_probe")
 MATH_PROBE_SRC = os.path.join(HERE, "csrc", "math_probe.hip")
@@ -89,4 +115,5 @@ def build_probe(out: str = PROBE) -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_binding(verbose=True))
     print(build_probe())

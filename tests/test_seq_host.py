@@ -1,10 +1,12 @@
-"""The sequence operators' C ABI on the host: the binding packs the structs that
-include/ssu.h declares, and bad arguments are refused before the GPU is touched.
+"""The sequence operators' C ABI on the host: bad arguments are refused before the
+GPU is touched. The structs are packed here as include/ssu.h declares them.
 
 No test here launches a kernel: every call carries an invalid field or nothing
 to do. The pointer values are never dereferenced on the host."""
+import ctypes
 import os
 import re
+import struct
 import subprocess
 
 import pytest
@@ -14,11 +16,28 @@ OK, INVALID, UNSUPPORTED, MISALIGNED = 0, 1, 2, 3
 F32, BF16, I32, I64, F16 = range(5)
 
 
+VIEW = "Qii4q"  # ptr, dtype, reserved, strides
+LAYOUTS = {"linear": struct.Struct("6i2qfi" + VIEW * 9 + "Qq"), "qk": struct.Struct("q6ifi2q" + VIEW * 12),
+           "attn": struct.Struct("6i2qfi" + VIEW * 7 + "Qq")}
+
+
 @pytest.fixture(scope="module")
 def ssu():
     import selective_state_update_amd as m
 
     return m
+
+
+@pytest.fixture(scope="module")
+def lib(ssu):
+    lib = ctypes.CDLL(ssu.library_path())
+    for name in ("ssu_linear_attention", "ssu_linear_attention_step", "ssu_qk_norm_rope", "ssu_paged_attention"):
+        getattr(lib, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    for name in ("ssu_linear_attention_workspace", "ssu_paged_attention_workspace"):
+        getattr(lib, name).argtypes = [ctypes.c_void_p]
+        getattr(lib, name).restype = ctypes.c_int64
+    lib.ssu_last_error.restype = ctypes.c_char_p
+    return lib
 
 
 def view(dtype, *strides, ptr=0x10000, reserved=0):
@@ -65,10 +84,10 @@ def pack(layout, d):
     out = []
     for v in d.values():
         out.extend(flat(v) if isinstance(v, dict) else (v,))
-    return layout.pack(*out)
+    return LAYOUTS[layout].pack(*out)
 
 
-def test_struct_layouts_match_the_header(ssu, tmp_path):
+def test_struct_layouts_match_the_header(tmp_path):
     src = tmp_path / "sizes.c"
     src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "ssu.h"\nint main(void) { printf("%zu %zu %zu %zu %zu %zu\\n", '
                    "sizeof(ssu_linear_args), sizeof(ssu_qk_args), sizeof(ssu_attn_args), offsetof(ssu_linear_args, state), "
@@ -78,7 +97,7 @@ def test_struct_layouts_match_the_header(ssu, tmp_path):
     subprocess.run(["gcc", "-std=c11", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"),
                     "-I", os.path.join(rocm, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
-    assert got == [ssu._LINEAR_ARGS.size, ssu._QK_ARGS.size, ssu._ATTN_ARGS.size, 48, 56, ssu._ATTN_ARGS.size - 16]
+    assert got == [LAYOUTS["linear"].size, LAYOUTS["qk"].size, LAYOUTS["attn"].size, 48, 56, LAYOUTS["attn"].size - 16]
 
 
 def test_field_order_matches_the_header():
@@ -112,38 +131,38 @@ LINEAR_BAD = [
 
 
 @pytest.mark.parametrize("kw,code", LINEAR_BAD)
-def test_linear_refusals(ssu, kw, code):
+def test_linear_refusals(lib, kw, code):
     prompt = change(LINEAR, kw)
-    assert ssu._lib.ssu_linear_attention(pack(ssu._LINEAR_ARGS, prompt), None) == code, ssu._lib.ssu_last_error()
-    assert ssu._lib.ssu_last_error()
+    assert lib.ssu_linear_attention(pack("linear", prompt), None) == code, lib.ssu_last_error()
+    assert lib.ssu_last_error()
     step = change(LINEAR, {"cu": NONE, "ws": 0, "ws_bytes": 0, "batch": 10, **kw})
     if "batch" not in kw and "ntokens" not in kw:
-        assert ssu._lib.ssu_linear_attention_step(pack(ssu._LINEAR_ARGS, step), None) == code
+        assert lib.ssu_linear_attention_step(pack("linear", step), None) == code
 
 
 @pytest.mark.parametrize("kw,code", [({"cu.ptr": 0}, INVALID), ({"cu.dtype": I64}, INVALID), ({"cu.0": 2}, UNSUPPORTED),
                                      ({"v.0": 1 << 24}, UNSUPPORTED), ({"out.0": 1 << 24}, UNSUPPORTED),
                                      ({"cu.ptr": 0x10002}, MISALIGNED)])
-def test_linear_prompt_refusals(ssu, kw, code):
-    assert ssu._lib.ssu_linear_attention(pack(ssu._LINEAR_ARGS, change(LINEAR, kw)), None) == code
+def test_linear_prompt_refusals(lib, kw, code):
+    assert lib.ssu_linear_attention(pack("linear", change(LINEAR, kw)), None) == code
 
 
 @pytest.mark.parametrize("kw", [dict(batch=9), dict(cu=view(I32, 1)), dict(ws=0x20000)])
-def test_linear_step_refusals(ssu, kw):
+def test_linear_step_refusals(lib, kw):
     d = change(LINEAR, {"cu": NONE, "ws": 0, "ws_bytes": 0, "batch": 10, **kw})
-    assert ssu._lib.ssu_linear_attention_step(pack(ssu._LINEAR_ARGS, d), None) == INVALID
+    assert lib.ssu_linear_attention_step(pack("linear", d), None) == INVALID
 
 
-def test_linear_nothing_to_do(ssu):
-    assert ssu._lib.ssu_linear_attention(pack(ssu._LINEAR_ARGS, change(LINEAR, dict(batch=0))), None) == OK
+def test_linear_nothing_to_do(lib):
+    assert lib.ssu_linear_attention(pack("linear", change(LINEAR, dict(batch=0))), None) == OK
     empty = {k: 0 for k in ("q.ptr", "k.ptr", "v.ptr", "decay.ptr", "out.ptr")}
-    assert ssu._lib.ssu_linear_attention(pack(ssu._LINEAR_ARGS, change(LINEAR, dict(ntokens=0, **empty))), None) == OK
+    assert lib.ssu_linear_attention(pack("linear", change(LINEAR, dict(ntokens=0, **empty))), None) == OK
     step = change(LINEAR, {"cu": NONE, "ws": 0, "ws_bytes": 0, "batch": 0, "ntokens": 0})
-    assert ssu._lib.ssu_linear_attention_step(pack(ssu._LINEAR_ARGS, step), None) == OK
-    for fn in (ssu._lib.ssu_linear_attention, ssu._lib.ssu_linear_attention_step, ssu._lib.ssu_qk_norm_rope,
-               ssu._lib.ssu_paged_attention):
+    assert lib.ssu_linear_attention_step(pack("linear", step), None) == OK
+    for fn in (lib.ssu_linear_attention, lib.ssu_linear_attention_step, lib.ssu_qk_norm_rope,
+               lib.ssu_paged_attention):
         assert fn(None, None) == INVALID
-    assert ssu._lib.ssu_linear_attention_workspace(None) == ssu._lib.ssu_paged_attention_workspace(None) == -1
+    assert lib.ssu_linear_attention_workspace(None) == lib.ssu_paged_attention_workspace(None) == -1
 
 
 QK_BAD = [
@@ -166,13 +185,13 @@ QK_BAD = [
 
 
 @pytest.mark.parametrize("kw,code", QK_BAD)
-def test_qk_refusals(ssu, kw, code):
-    assert ssu._lib.ssu_qk_norm_rope(pack(ssu._QK_ARGS, change(QK, kw)), None) == code, ssu._lib.ssu_last_error()
+def test_qk_refusals(lib, kw, code):
+    assert lib.ssu_qk_norm_rope(pack("qk", change(QK, kw)), None) == code, lib.ssu_last_error()
 
 
-def test_qk_nothing_to_do(ssu):
+def test_qk_nothing_to_do(lib):
     for kw in (dict(ntokens=0), dict(nq=0, nk=0), dict(max_pos=0)):
-        assert ssu._lib.ssu_qk_norm_rope(pack(ssu._QK_ARGS, change(QK, kw)), None) == OK
+        assert lib.ssu_qk_norm_rope(pack("qk", change(QK, kw)), None) == OK
 
 
 ATTN_BAD = [
@@ -192,12 +211,12 @@ ATTN_BAD = [
 
 
 @pytest.mark.parametrize("kw,code", ATTN_BAD)
-def test_attention_refusals(ssu, kw, code):
-    assert ssu._lib.ssu_paged_attention(pack(ssu._ATTN_ARGS, change(ATTN, kw)), None) == code, ssu._lib.ssu_last_error()
+def test_attention_refusals(lib, kw, code):
+    assert lib.ssu_paged_attention(pack("attn", change(ATTN, kw)), None) == code, lib.ssu_last_error()
 
 
-def test_attention_nothing_to_do(ssu):
-    assert ssu._lib.ssu_paged_attention(pack(ssu._ATTN_ARGS, change(ATTN, dict(batch=0))), None) == OK
+def test_attention_nothing_to_do(lib):
+    assert lib.ssu_paged_attention(pack("attn", change(ATTN, dict(batch=0))), None) == OK
 
 
 def test_python_wants_the_gpu(ssu):
