@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     __shared__ u32x4 lw[FULL ? kTiles : 1][FULL ? kSteps : 1][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
     __shared__ float lsum[2][kChunk], lrest[2][kChunk];  // L in units of log 2: as fp32, and what that leaves
     __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
-    __shared__ int bad[2], found;
+    __shared__ int bad[2];
+    __shared__ int64_t found[4];  // this segment's sequence, its slot and rows
 
     const LinearParams &a = p.a;
     // workgroups go round the 8 XCDs: XCD x has segments x, x + 8, ..., all heads
@@ -217,24 +218,25 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     // segment f of all: sequence b's are cu[b] / seg_len + b and the following
     // (distinct for ordered sequences)
     if (tid == 0)
-        found = -1;
+        found[0] = -1;
     __syncthreads();
     for (int b = tid; b < a.batch; b += THREADS) {
+        const int64_t slot = load_index(a.idx, a.idx64, b);
         const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
         const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
         const int64_t s = f - (lo / p.seg_len + b);
-        if (s >= 0 && s * p.seg_len < hi - lo)
-            found = b;
+        if (s >= 0 && s * p.seg_len < hi - lo && slot >= 0 && slot < a.pool_slots) {  // (padding: none)
+            found[0] = b;
+            found[1] = slot;
+            found[2] = lo;
+            found[3] = hi;
+        }
     }
     __syncthreads();
-    const int b = __builtin_amdgcn_readfirstlane(found);
+    const int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
     if (b < 0)
         return;
-    const int64_t slot = load_index(a.idx, a.idx64, b);
-    if (slot < 0 || slot >= a.pool_slots)
-        return;  // padding
-    const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
-    const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
+    const int64_t slot = found[1], lo = found[2], hi = found[3];
     const int base = static_cast<int>(lo / p.seg_len) + b, seg = f - base;
     const int segs = static_cast<int>((hi - lo + p.seg_len - 1) / p.seg_len);
     const int64_t begin = lo + static_cast<int64_t>(seg) * p.seg_len, end = min(begin + p.seg_len, hi);

@@ -122,62 +122,81 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int units = p.nk * p.row_tiles;  // of a request
 
-    // this workgroup's run of the line, and the request that it begins in
-    // (up to 256 requests their lengths are read once)
-    const int64_t first_n = tid < p.batch ? visible(p, tid) : -1;
-    int64_t total = rounds_of(first_n, kRound);
-    for (int b = tid + 64 * kWaves; b < p.batch; b += 64 * kWaves)
-        total += rounds_of(visible(p, b), kRound);
-#pragma unroll
-    for (int m = 32; m >= 1; m /= 2)
-        total += __shfl_xor(total, m);
-    if (lane == 0)
-        scan[wave] = total;
+    // this workgroup's run of the line, and the request that it begins in: the
+    // steps of one unit of every request, summed over them
     if (tid == 0)
         p.open[wg] = Open{-1, 0, 0, 0};
-    __syncthreads();
-    total = 0;
+    int64_t per, pos, stop, n, before;  // (before: a unit's steps of all earlier requests)
+    int b;
+    auto run_of = [&](int64_t steps) {
+        const int64_t total = steps * units;
+        per = (total + p.groups - 1) / p.groups;
+        pos = wg * per;
+        stop = min(pos + per, total);
+    };
+    if (p.batch <= 64) {  // every wave for itself: a request per lane (at most 2^25 steps each)
+        const int64_t own_n = lane < p.batch ? visible(p, lane) : -1;
+        const uint32_t own = static_cast<uint32_t>(rounds_of(own_n, kRound)), sum = scan_lanes(static_cast<int>(own));
+        run_of(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(sum), 63)));
+        if (pos >= stop)
+            return;
+        const uint64_t mine = __ballot(static_cast<int64_t>(sum - own) * units <= pos && pos < static_cast<int64_t>(sum) * units);
+        b = static_cast<int>(__builtin_ctzll(mine));
+        n = __builtin_amdgcn_readlane(static_cast<int>(own_n), b);
+        before = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(sum - own), b));
+    } else {
+        int64_t total = 0;
+        for (int i = tid; i < p.batch; i += 64 * kWaves)
+            total += rounds_of(visible(p, i), kRound);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-        total += scan[w] * units;
-    const int64_t per = (total + p.groups - 1) / p.groups;
-    int64_t pos = wg * per;
-    const int64_t stop = min(pos + per, total);
-    if (pos >= stop)
-        return;
-    int64_t before = 0;  // steps of a unit of every earlier request
-    for (int b0 = 0; b0 < p.batch; b0 += 64 * kWaves) {
-        const int b = b0 + tid;
-        const int64_t n = b0 == 0 ? first_n : b < p.batch ? visible(p, b) : -1, own = rounds_of(n, kRound);
-        int64_t sum = own;
+        for (int m = 32; m >= 1; m /= 2)
+            total += __shfl_xor(total, m);
+        if (lane == 0)
+            scan[wave] = total;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-            const int64_t up = __shfl_up(sum, m);
-            sum += lane >= m ? up : 0;
+        for (int w = 0; w < kWaves; ++w)
+            total += scan[w];
+        run_of(total);
+        if (pos >= stop)
+            return;
+        before = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 64 * kWaves) {
+            const int i = b0 + tid;
+            const int64_t own_n = i < p.batch ? visible(p, i) : -1, own = rounds_of(own_n, kRound);
+            int64_t sum = own;
+#pragma unroll
+            for (int m = 1; m < 64; m *= 2) {
+                const int64_t up = __shfl_up(sum, m);
+                sum += lane >= m ? up : 0;
+            }
+            __syncthreads();
+            if (lane == 63)
+                scan[wave] = sum;
+            __syncthreads();
+            int64_t first = before + sum - own;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                first += w < wave ? scan[w] : 0;
+                before += scan[w];
+            }
+            if (first * units <= pos && pos < (first + own) * units) {
+                found[0] = i;
+                found[1] = first;
+                found[2] = own_n;
+            }
+            if (before * units > pos)
+                break;
         }
         __syncthreads();
-        if (lane == 63)
-            scan[wave] = sum;
-        __syncthreads();
-        int64_t first = before + sum - own;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            first += w < wave ? scan[w] : 0;
-            before += scan[w];
-        }
-        if (first * units <= pos && pos < (first + own) * units) {
-            found[0] = b;
-            found[1] = first;
-            found[2] = n;
-        }
-        if (before * units > pos)
-            break;
+        b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
+        before = found[1];
+        n = found[2];
     }
-    __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
-    int64_t n = found[2], rounds = rounds_of(n, kRound);
-    int unit = static_cast<int>((pos - found[1] * units) / rounds);
-    int64_t step0 = pos - found[1] * units - unit * rounds;  // of the unit, where this workgroup begins
+    int64_t rounds = rounds_of(n, kRound);
+    int unit = static_cast<int>((pos - before * units) / rounds);
+    int64_t step0 = pos - before * units - unit * rounds;  // of the unit, where this workgroup begins
 
     for (;;) {
         const int64_t steps = min(rounds - step0, stop - pos);

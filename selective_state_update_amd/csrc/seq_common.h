@@ -125,6 +125,24 @@ __device__ __forceinline__ float sum_lanes(float x)
     return x;
 }
 
+// Inclusive sums over the wave's lanes, by DPP: within 16 lanes (lane - 1, - 2,
+// - 4, - 8), then the last of 16 to the next 16 and of 32 to the next 32.
+template <int CTRL, int MASK>
+__device__ __forceinline__ int dpp_up(int x)
+{
+    return x + __builtin_amdgcn_update_dpp(0, x, CTRL, MASK, 0xf, true);
+}
+
+__device__ __forceinline__ int scan_lanes(int x)
+{
+    x = dpp_up<0x111, 0xf>(x);
+    x = dpp_up<0x112, 0xf>(x);
+    x = dpp_up<0x114, 0xf>(x);
+    x = dpp_up<0x118, 0xf>(x);
+    x = dpp_up<0x142, 0xa>(x);
+    return dpp_up<0x143, 0xc>(x);
+}
+
 // Launch a kernel and return its own status (a call that fails leaves no
 // error behind for the caller's next runtime call).
 template <typename P>
