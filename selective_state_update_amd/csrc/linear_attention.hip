@@ -174,6 +174,13 @@ __device__ __forceinline__ double last_lane(double x)
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // 4 rows of 16 16-bit values in LDS, the lane's address being that of values
 // 4 (l % 4) .. of row (l % 16) / 4 of its 16 lanes' rows: the lane gets value
 // l % 16 of each.
@@ -236,10 +243,11 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     const int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
     if (b < 0)
         return;
-    const int64_t slot = found[1], lo = found[2], hi = found[3];
+    const int64_t slot = uniform(found[1]), lo = uniform(found[2]), hi = uniform(found[3]);
     const int base = static_cast<int>(lo / p.seg_len) + b, seg = f - base;
     const int segs = static_cast<int>((hi - lo + p.seg_len - 1) / p.seg_len);
-    const int64_t begin = lo + static_cast<int64_t>(seg) * p.seg_len, end = min(begin + p.seg_len, hi);
+    const int64_t begin = lo + static_cast<int64_t>(seg) * p.seg_len;
+    const int rows = __builtin_amdgcn_readfirstlane(static_cast<int>(min(hi - begin, static_cast<int64_t>(p.seg_len))));
     if (!FULL && seg == segs - 1)
         return;  // nothing comes behind it
 
@@ -274,10 +282,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     // and count as zeros
     u32x4 rq[QU], rk[QU], rv[VU];
     float rdecay = 0.0f, rbeta = 0.0f;
-    uint32_t oo[kTiles];  // of out: this lane's 4 values of token 16 it + c
-#pragma unroll
-    for (int it = 0; it < kTiles; ++it)
-        oo[it] = 2 * ((16 * it + c) * static_cast<uint32_t>(a.o_t) + 4 * g);
+    const uint32_t oo = 2 * (c * static_cast<uint32_t>(a.o_t) + 4 * g);  // of out: this lane's 4 values of token c
     uint32_t oq[QU], ok[QU], ov[VU];  // byte offsets from a chunk's first row
     auto offsets = [&](int last) {     // of a chunk with rows 0 .. last
 #pragma unroll
@@ -296,12 +301,11 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     auto at = [](const uint16_t *base, uint32_t off) {
         return *reinterpret_cast<const u32x4_a2 *>(reinterpret_cast<const char *>(base) + off);
     };
-    auto request = [&](int64_t t0) {
-        const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
-        if (last != kChunk - 1)
-            offsets(last);
-        const uint16_t *const qt = a.q + t0 * a.q_t + grp * a.q_g, *const kt = a.k + t0 * a.k_t + grp * a.k_g;
-        const uint16_t *const vt = a.v + t0 * a.v_t + h * a.v_h + slice * PC;
+    const uint16_t *qt = a.q + begin * a.q_t + grp * a.q_g, *kt = a.k + begin * a.k_t + grp * a.k_g;  // of the next request
+    const uint16_t *vt = a.v + begin * a.v_t + h * a.v_h + slice * PC;
+    auto request = [&](int t0) {
+        if (rows - t0 < kChunk)
+            offsets(rows - t0 - 1);
 #pragma unroll
         for (int i = 0; i < QU; ++i) {
             if constexpr (FULL)
@@ -311,16 +315,20 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
 #pragma unroll
         for (int i = 0; i < VU; ++i)
             rv[i] = at(vt, ov[i]);
-        if (wave == W - 1) {
-            const int64_t t = t0 + min(lane, last);
-            rdecay = a.decay[t * a.d_t + h * a.d_h];
-            rbeta = a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f;
-        }
+        qt += kChunk * a.q_t;
+        kt += kChunk * a.k_t;
+        vt += kChunk * a.v_t;
     };
-    // L and what follows from it, by the last wave (it has the fewest score tiles)
+    auto request_sums = [&](int t0) {  // (behind the segment's end: of its last token)
+        const int64_t t = begin + min(t0 + lane, rows - 1);
+        rdecay = a.decay[t * a.d_t + h * a.d_h];
+        rbeta = a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f;
+    };
+    // L and what follows from it, by the last wave (which has no score tile), a
+    // chunk ahead of the others
     double whole = 0.0;  // of the segment so far
-    auto sums = [&](int64_t t0, int buf) {
-        const bool in = lane < kChunk && t0 + lane < end;
+    auto sums = [&](int t0, int buf) {
+        const bool in = lane < kChunk && t0 + lane < rows;
         const float d = rdecay < kDecayFloor ? kDecayFloor : rdecay;  // (NaN stays)
         double sum = in ? static_cast<double>(d) * 1.4426950408889634 : 0.0;
         sum += lanes_up<0x111, 0xf>(sum);  // lane - 1, - 2, - 4, - 8 of each 16
@@ -344,14 +352,14 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
             bad[buf] = 0;
         }
     };
-    auto place = [&](int64_t t0, int buf) {
+    auto place = [&](int t0, int buf) {
         // zeros behind the segment's end, behind N (16 in a tile of 32) and behind P
-        const bool cut = t0 + kChunk > end || p.dstate < N || slice * PC + PC > a.headdim;
+        const bool cut = t0 + kChunk > rows || p.dstate < N || slice * PC + PC > a.headdim;
         if (cut) {
 #pragma unroll
             for (int i = 0; i < QU; ++i) {
                 const int u = tid + THREADS * i;
-                if (t0 + u / (N / 8) >= end || u % (N / 8) * 8 >= p.dstate) {
+                if (t0 + u / (N / 8) >= rows || u % (N / 8) * 8 >= p.dstate) {
                     rk[i] = u32x4{0, 0, 0, 0};
                     if constexpr (FULL)
                         rq[i] = u32x4{0, 0, 0, 0};
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
 #pragma unroll
             for (int i = 0; i < VU; ++i) {
                 const int u = tid + THREADS * i;
-                if (t0 + u / (PC / 8) >= end || slice * PC + u % (PC / 8) * 8 >= a.headdim)
+                if (t0 + u / (PC / 8) >= rows || slice * PC + u % (PC / 8) * 8 >= a.headdim)
                     rv[i] = u32x4{0, 0, 0, 0};
             }
         }
@@ -390,7 +398,9 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     };
 
     offsets(kChunk - 1);
-    request(begin);
+    if (wave == W - 1)
+        request_sums(0);
+    request(0);
     // the state before the segment
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -404,18 +414,26 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
         else
             load_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
     }
-    if (wave == W - 1)
-        sums(begin, 0);
+    if (wave == W - 1) {
+        sums(0, 0);
+        request_sums(kChunk);
+    }
     __syncthreads();  // (bad is set by place)
-    place(begin, 0);
+    place(0, 0);
     __syncthreads();
 
     int buf = 0;
-    for (int64_t t0 = begin; t0 < end; t0 += kChunk, buf ^= 1) {
-        const int64_t next = t0 + kChunk;
-        const bool more = next < end;
-        if (more)
+    uint16_t *out = a.out + begin * a.o_t + h * a.o_h + p0;
+    for (int t0 = 0; t0 < rows; t0 += kChunk, buf ^= 1) {
+        const int next = t0 + kChunk;
+        const bool more = next < rows;
+        if (more) {
             request(next);
+            if (wave == W - 1) {
+                sums(next, buf ^ 1);
+                request_sums(next + kChunk);
+            }
+        }
 
         // v of the wave's columns as fragments: 8 tokens of 32 per lane
         const int tr = (4 * g + c / 4) * ROW + 4 * (c % 4), vtr = (4 * g + c / 4) * VROW + 4 * (c % 4) + wave * 16;
@@ -468,7 +486,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
                 o[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                u32x4 fh, fl;
+                u32x4 fh, fl, qf[kTiles];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t wh, wl;
@@ -480,10 +498,12 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
                 for (int it = 0; it < kTiles; ++it) {
                     const uint16_t *const qrow = lq + (16 * it + c) * ROW + 32 * s + 4 * g;
                     const u32x2 x = *reinterpret_cast<const u32x2 *>(qrow), y = *reinterpret_cast<const u32x2 *>(qrow + 16);
-                    const u32x4 qf = {x[0], x[1], y[0], y[1]};
-                    o[it] = Mma<Bf16>::run(fh, qf, o[it]);
-                    o[it] = Mma<Bf16>::run(fl, qf, o[it]);
+                    qf[it] = u32x4{x[0], x[1], y[0], y[1]};
+                    o[it] = Mma<Bf16>::run(fh, qf[it], o[it]);
                 }
+#pragma unroll
+                for (int it = 0; it < kTiles; ++it)
+                    o[it] = Mma<Bf16>::run(fl, qf[it], o[it]);
             }
 #pragma unroll
             for (int it = 0; it < kTiles; ++it)
@@ -512,14 +532,13 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
                     }
             }
             if (live) {
-                char *const rows = reinterpret_cast<char *>(a.out + t0 * a.o_t + h * a.o_h + p0);
-                const int last = static_cast<int>(min(end - t0, int64_t(kChunk))) - 1;
 #pragma unroll
                 for (int it = 0; it < kTiles; ++it)
-                    if (16 * it + c <= last)
-                        *reinterpret_cast<u32x2_a2 *>(rows + oo[it]) =
+                    if (t0 + 16 * it + c < rows)
+                        *reinterpret_cast<u32x2_a2 *>(reinterpret_cast<char *>(out + it * 16 * a.o_t) + oo) =
                             u32x2{pack2<Bf16>(a.scale * o[it][0], a.scale * o[it][1]),
                                   pack2<Bf16>(a.scale * o[it][2], a.scale * o[it][3])};
+                out += kChunk * a.o_t;
             }
         }
 
@@ -555,8 +574,6 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
             }
         }
         if (more) {
-            if (wave == W - 1)
-                sums(next, buf ^ 1);
             __syncthreads();  // LDS is free again
             place(next, buf ^ 1);
             __syncthreads();
@@ -652,17 +669,18 @@ constexpr ChunkKernels chunk_kernels()
     return {&ssu_linear_chunk_kernel<N, W, false>, &ssu_linear_chunk_kernel<N, W, true>, 16 * W};
 }
 
-template <int W>
-ChunkKernels chunk_kernels(int N)
-{
-    return N <= 32 ? chunk_kernels<32, W>() : N == 64 ? chunk_kernels<64, W>() : N == 128 ? chunk_kernels<128, W>()
-                                                                                          : chunk_kernels<256, W>();
-}
-
+// Eight waves where they share the products of q and k of whole heads and their
+// states fit four waves per SIMD: N = 128, P in 80 .. 128 (one prompt of 16384
+// tokens, 32 heads of 128 x 128: 228 us, 245 with four waves; a head of 64 x 128
+// has columns for four only). Four elsewhere: more workgroups to hide each other's
+// waits (4 prompts of 3000, 8 heads of 128 x 64: 35.9 us against 36.9; of
+// 128 x 256: 79.5 against 92.2; of 224 x 128: 71.5 against 77.6).
 ChunkKernels chunk_kernels(int N, int P)
 {
-    // eight waves where the last 128 columns hold more than 64
-    return (P - 1) % 128 >= 64 ? chunk_kernels<8>(N) : chunk_kernels<4>(N);
+    if (N == 128 && P > 64 && P <= 128)
+        return chunk_kernels<128, 8>();
+    return N <= 32 ? chunk_kernels<32, 4>() : N == 64 ? chunk_kernels<64, 4>() : N == 128 ? chunk_kernels<128, 4>()
+                                                                                        : chunk_kernels<256, 4>();
 }
 
 // ------------------------------------------------------------------ host --
@@ -678,7 +696,7 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
         return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d is not a multiple of 16 in 16 .. 256", who, a.headdim);
     if (a.dstate != 16 && a.dstate != 32 && a.dstate != 64 && a.dstate != 128 && a.dstate != 256)
         return fail(SSU_ERR_UNSUPPORTED, "%s: dstate %d is not 16, 32, 64, 128 or 256", who, a.dstate);
-    if (a.ntokens > 0x7fffffff)
+    if (a.ntokens > 0x7fffffbf)  // (a segment and two chunks count in 32 bits)
         return fail(SSU_ERR_UNSUPPORTED, "%s: more than 2^31 tokens", who);
     if ((a.ntokens / kChunk + a.batch + 8) * a.nheads > 0x7fffffff / (a.headdim / 16))
         return fail(SSU_ERR_UNSUPPORTED, "%s: batch * nheads too large", who);
