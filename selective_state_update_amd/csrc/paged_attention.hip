@@ -21,8 +21,8 @@ constexpr int kJoinRows = 4;  // rows that a workgroup of the join takes
 // Waves of a workgroup. D = 256 needs half the register file per wave: two
 // waves and two workgroups per CU instead of four and one keep one of them
 // loading while the other joins (64 requests up to 4096 tokens, 8 heads of 256:
-// 185 against 208 us).
-constexpr int waves_for(int D) { return D == 256 ? 2 : 4; }
+// 185 against 208 us). Twice as many where a workgroup has one whole unit.
+constexpr int waves_for(int D, bool whole) { return (D == 256 ? 2 : 4) * (whole ? 2 : 1); }
 
 struct AttnParams {
     const uint16_t *q, *k, *v;
@@ -101,11 +101,12 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 // reads half a cache line of each row and the next the other half. Each wave
 // takes every fourth step of 32 tokens with statistics of its own. PAGE16:
 // pages are a multiple of 16 tokens, a tile lies in one page and its address
-// is uniform; otherwise every lane looks its own token up.
-template <typename T, int D, bool PAGE16>
-__global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
+// is uniform; otherwise every lane looks its own token up. WHOLE (short caches,
+// see plan_of): no line, a workgroup per unit, nothing to join behind it.
+template <typename T, int D, bool PAGE16, bool WHOLE>
+__global__ void __launch_bounds__(64 * waves_for(D, WHOLE), D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
 {
-    constexpr int kWaves = waves_for(D);
+    constexpr int kWaves = waves_for(D, WHOLE);
     constexpr int kRound = kWaves * kTile;  // tokens of one workgroup's step
     constexpr int KS = D / 32;      // products along D of a score
     constexpr int E = D / 16;       // values of a V row per lane, products of an output row
@@ -117,14 +118,14 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
     __shared__ int64_t scan[kWaves];
     __shared__ int64_t found[3];  // its request, the steps before it, its tokens
 
-    const int wg = xcd_order(static_cast<int>(blockIdx.x), p.groups);
+    const int wg = WHOLE ? static_cast<int>(blockIdx.x) : xcd_order(static_cast<int>(blockIdx.x), p.groups);
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int units = p.nk * p.row_tiles;  // of a request
 
     // this workgroup's run of the line, and the request that it begins in: the
     // steps of one unit of every request, summed over them
-    if (tid == 0)
+    if (!WHOLE && tid == 0)
         p.open[wg] = Open{-1, 0, 0, 0};
     int64_t per, pos, stop, n, before;  // (before: a unit's steps of all earlier requests)
     int b;
@@ -134,7 +135,15 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
         pos = wg * per;
         stop = min(pos + per, total);
     };
-    if (p.batch <= 64) {  // every wave for itself: a request per lane (at most 2^25 steps each)
+    if constexpr (WHOLE) {
+        b = wg / units;
+        n = visible(p, b);
+        if (n < 0)
+            return;
+        before = 0;
+        per = stop = rounds_of(n, kRound);
+        pos = 0;
+    } else if (p.batch <= 64) {  // every wave for itself: a request per lane (at most 2^25 steps each)
         const int64_t own_n = lane < p.batch ? visible(p, lane) : -1;
         const uint32_t own = static_cast<uint32_t>(rounds_of(own_n, kRound)), sum = scan_lanes(static_cast<int>(own));
         run_of(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(sum), 63)));
@@ -195,8 +204,8 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
         n = found[2];
     }
     int64_t rounds = rounds_of(n, kRound);
-    int unit = static_cast<int>((pos - before * units) / rounds);
-    int64_t step0 = pos - before * units - unit * rounds;  // of the unit, where this workgroup begins
+    int unit = WHOLE ? wg % units : static_cast<int>((pos - before * units) / rounds);
+    int64_t step0 = WHOLE ? 0 : pos - before * units - unit * rounds;  // of the unit, where this workgroup begins
 
     for (;;) {
         const int64_t steps = min(rounds - step0, stop - pos);
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
                 part[wave][r][c * E + e] = o[e][i] * f;
         }
         __syncthreads();
-        const bool whole = steps == rounds;
+        const bool whole = WHOLE || steps == rounds;
         const int64_t row0 = (2 * static_cast<int64_t>(wg) + (step0 == 0)) * 16;
         for (int at = tid; at < rows * D; at += 64 * kWaves) {
             const int r = at / D, d = at % D;
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
 
         // the next unit
         pos += steps;
-        if (pos >= stop)
+        if (WHOLE || pos >= stop)
             return;
         step0 = 0;
         if (++unit == units) {
@@ -484,13 +493,15 @@ __global__ void __launch_bounds__(64 * kJoinRows) ssu_attn_join_kernel(const Att
 using AttnFn = void (*)(AttnParams);
 
 struct AttnKernels {
-    AttnFn split, join;
+    AttnFn split, join, whole;
 };
 
 template <typename T, int D>
 AttnKernels attn_kernels(bool page16)
 {
-    return {page16 ? &ssu_attn_split_kernel<T, D, true> : &ssu_attn_split_kernel<T, D, false>, &ssu_attn_join_kernel<T, D>};
+    return {page16 ? &ssu_attn_split_kernel<T, D, true, false> : &ssu_attn_split_kernel<T, D, false, false>,
+            &ssu_attn_join_kernel<T, D>,
+            page16 ? &ssu_attn_split_kernel<T, D, true, true> : &ssu_attn_split_kernel<T, D, false, true>};
 }
 
 template <typename T>
@@ -519,11 +530,19 @@ ssu_status check_sizes(const ssu_attn_args &a, const char *who)
 
 struct Plan {
     int row_tiles, groups;
+    bool whole;  // a workgroup per unit, no workspace
     int64_t part_at, stat_at, bytes;  // workspace
 };
 
-// One workgroup per CU at D = 128, where four waves' loads are enough to fill
-// the memory system and more only crowd it (64 requests up to 8192 tokens, 8
+// A workgroup of its own per unit where no unit has more than two steps (512
+// tokens, 256 at D = 256) and the chip holds all of them: no line to lay out, no
+// partial sums, one launch (one request, 2 heads of 128: 100 tokens 6.4 against
+// 9.2 us, 512 tokens 10.7 against 11.1, 777 tokens 13.3 against 12.2; 32 requests
+// of 1 to 512 tokens, 8 heads: 14.2 against 22.5 us; 64 requests: 25.2 against
+// 32.4; 256 of 300 tokens 87 against 70).
+//
+// Otherwise one workgroup per CU at D = 128, where four waves' loads are enough to
+// fill the memory system and more only crowd it (64 requests up to 8192 tokens, 8
 // heads: 184 against 189 us with two; 3 of 100003 tokens, 4 heads: 118.5 against
 // 123), but two where the runs hold many units, each with its start and its
 // join (512 requests up to 600 tokens, 4 heads: 82 against 102 us); two at the
@@ -534,7 +553,12 @@ Plan plan_of(const ssu_attn_args &a)
     Plan p{};
     p.row_tiles = (a.nq / a.nk + 15) / 16;
     const int64_t units = static_cast<int64_t>(a.batch) * a.nk * p.row_tiles;
-    const int round = waves_for(a.headdim) * kTile;
+    p.whole = units <= 2 * kNumCUs && a.max_pages * a.page_size <= 2 * waves_for(a.headdim, true) * kTile;
+    if (p.whole) {
+        p.groups = static_cast<int>(units);
+        return p;
+    }
+    const int round = waves_for(a.headdim, false) * kTile;
     const int64_t rounds = std::max<int64_t>((a.max_pages * a.page_size + round - 1) / round, 1);
     const int64_t resident = a.headdim == 128 && units <= 4 * kNumCUs ? kNumCUs : 2 * kNumCUs;
     p.groups = static_cast<int>(units > resident / rounds ? resident : std::max<int64_t>(units * rounds, 1));
@@ -603,7 +627,7 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     if (a.batch == 0)
         return SSU_OK;
     const Plan plan = plan_of(a);
-    if (!a.workspace || a.workspace_bytes < plan.bytes)
+    if (plan.bytes > 0 && (!a.workspace || a.workspace_bytes < plan.bytes))
         return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_paged_attention: workspace of %lld bytes, %lld needed",
                     static_cast<long long>(a.workspace ? a.workspace_bytes : 0), static_cast<long long>(plan.bytes));
     if (reinterpret_cast<uintptr_t>(a.workspace) % 16)
@@ -647,8 +671,8 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     const AttnKernels k = a.q.dtype == SSU_BF16 ? attn_kernels<Bf16>(a.headdim, page16) : attn_kernels<F16>(a.headdim, page16);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
-    hipError_t e = launch_kernel(k.split, p, plan.groups, 64 * waves_for(a.headdim), 0, stream);
-    if (e == hipSuccess && plan.groups > 1)
+    hipError_t e = launch_kernel(plan.whole ? k.whole : k.split, p, plan.groups, 64 * waves_for(a.headdim, plan.whole), 0, stream);
+    if (e == hipSuccess && !plan.whole && plan.groups > 1)
         e = launch_kernel(k.join, p, plan.groups * (16 / kJoinRows), 64 * kJoinRows, 0, stream);
     if (e != hipSuccess)
         return fail(SSU_ERR_HIP, "launch of the paged attention kernels failed: %s", hipGetErrorString(e));

@@ -18,8 +18,16 @@ def ssu():
     return m
 
 
+@pytest.fixture(params=[0, 1500], ids=["narrow", "wide"], autouse=True)
+def width(request, monkeypatch):
+    """Tables as wide as the requests need, and wider by that many tokens: short caches have a kernel of their own."""
+    monkeypatch.setattr(Case, "wider", request.param)
+
+
 class Case:
     """Scattered pages; every cache row that no request sees is NaN."""
+
+    wider = 0
 
     def __init__(self, lens, nq, nk, D, page, dtype=BF16, seed=0, spare=1, gain=1.0, scale=None):
         g = torch.Generator().manual_seed(seed)
@@ -28,7 +36,7 @@ class Case:
         used = [-(-max(n, 0) // page) for n in lens]
         pages = sum(used) + 2
         order = torch.randperm(pages, generator=g).tolist()
-        self.table = torch.full((B, max(used + [0]) + spare), -7, dtype=torch.int32)
+        self.table = torch.full((B, max(used + [0]) + spare + self.wider // page), -7, dtype=torch.int32)
         kc, vc = (torch.randn(pages, page, nk, D, generator=g).to(dtype) for _ in range(2))
         seen = torch.zeros(pages, page, dtype=torch.bool)
         for b, n in enumerate(lens):
@@ -204,6 +212,34 @@ def test_graph_replays(ssu):
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+def test_short_graph_replays(ssu):
+    """Lengths that change between replays of one graph, up to what the table holds."""
+    c = Case([500, 400, 450], 8, 2, 128, 16, seed=25)
+    out, lens = torch.zeros_like(c.q), c.lens.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(ssu, out=out)
+    for n in (0, 1, 17, 256, 257, 400):
+        c.lens.fill_(n)
+        out.fill_(9.0)
+        g.replay()
+        assert torch.equal(out, c.run(ssu)[0])
+    c.lens.copy_(lens)
+    g.replay()
+    want = c.ref()
+    seq_ref.assert_close(out, want["out"], want["out_tol"], "out")
+
+
+@pytest.mark.parametrize("D,tokens", [(64, 512), (128, 512), (256, 256)])
+@pytest.mark.parametrize("page", [1, 16])
+def test_short_limits(ssu, D, tokens, page):
+    """On both sides of the longest cache that a workgroup takes alone, and of the most units."""
+    for n in (tokens - 1, tokens, tokens + 1):
+        Case([n, 3, 0, n // 2 + 1], 6, 3, D, page, seed=n, spare=0).check(ssu)
+    for batch in (256, 257):
+        Case([1 + 37 * i % 40 for i in range(batch)], 2, 2, D, page, seed=batch, spare=0).check(ssu)
+
+
 def test_two_streams(ssu):
     cases = [Case([4000, 60], 8, 2, 128, 16, seed=18 + i) for i in range(2)]
     want = [c.ref() for c in cases]
@@ -219,7 +255,8 @@ def test_two_streams(ssu):
 def test_no_requests(ssu):
     c = Case([], 4, 2, 64, 16, seed=20)
     assert c.run(ssu)[0].shape == (0, 4, 64)
-    c = Case([0, 0], 4, 2, 64, 16, seed=21, spare=0)  # a table without columns
+    c = Case([0, 0], 4, 2, 64, 16, seed=21, spare=0)
+    c.table = c.table[:, :0]
     out, _ = c.check(ssu)
     assert (out == 0).all()
 
