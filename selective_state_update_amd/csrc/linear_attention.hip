@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     __shared__ float lsum[2][kChunk], lrest[2][kChunk];  // L in units of log 2: as fp32, and what that leaves
     __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
     __shared__ int bad[2];
-    __shared__ int64_t found[4];  // this segment's sequence, its slot and rows
+    __shared__ int owner;         // this segment's sequence
+    __shared__ int64_t found[3];  // its slot and rows
 
     const LinearParams &a = p.a;
     // workgroups go round the 8 XCDs: XCD x has segments x, x + 8, ..., all heads
@@ -223,27 +224,26 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // segment f of all: sequence b's are cu[b] / seg_len + b and the following
-    // (distinct for ordered sequences)
+    // (distinct for ordered sequences; otherwise the first to come has it)
     if (tid == 0)
-        found[0] = -1;
+        owner = -1;
     __syncthreads();
     for (int b = tid; b < a.batch; b += THREADS) {
         const int64_t slot = load_index(a.idx, a.idx64, b);
         const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
         const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
         const int64_t s = f - (lo / p.seg_len + b);
-        if (s >= 0 && s * p.seg_len < hi - lo && slot >= 0 && slot < a.pool_slots) {  // (padding: none)
-            found[0] = b;
-            found[1] = slot;
-            found[2] = lo;
-            found[3] = hi;
+        if (s >= 0 && s * p.seg_len < hi - lo && slot >= 0 && slot < a.pool_slots && atomicCAS(&owner, -1, b) == -1) {  // (padding: none)
+            found[0] = slot;
+            found[1] = lo;
+            found[2] = hi;
         }
     }
     __syncthreads();
-    const int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
+    const int b = __builtin_amdgcn_readfirstlane(owner);
     if (b < 0)
         return;
-    const int64_t slot = uniform(found[1]), lo = uniform(found[2]), hi = uniform(found[3]);
+    const int64_t slot = uniform(found[0]), lo = uniform(found[1]), hi = uniform(found[2]);
     const int base = static_cast<int>(lo / p.seg_len) + b, seg = f - base;
     const int segs = static_cast<int>((hi - lo + p.seg_len - 1) / p.seg_len);
     const int64_t begin = lo + static_cast<int64_t>(seg) * p.seg_len;
@@ -710,9 +710,10 @@ struct Plan {
 };
 
 // Sequences are cut where whole ones would leave most of the chip idle: at most
-// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 87 us
-// cut, 153 uncut; with twice the waves and equal lengths uncut is faster, 89
-// against 110 us). Then segments are as long as fills the chip once, 4096 waves
+// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 84 us
+// cut, 128 uncut; 16 of 1024 tokens 89 and 70, but the host cannot tell them apart;
+// with twice the waves uncut is faster for both, 147 against 177 us and 89
+// against 110). Then segments are as long as fills the chip once, 4096 waves
 // (N = 256: 2048), but of 128 tokens at least and a 64th of all at most: one
 // prompt of 4096 tokens takes 40 us in segments of 128, 47 in segments of 256.
 Plan plan_of(const ssu_linear_args &a)

@@ -146,6 +146,19 @@ def test_prompt_scattered_starts(ssu):
     seq_ref.assert_close(c.out, want["out"], want["out_tol"], "out")
 
 
+def test_prompt_unordered_sequences(ssu):
+    """Sequences out of order may share a segment: their values are unspecified, all others are as they were."""
+    c = Case([1200, 0, 0, 0], 2, 64, 64, 1, seed=25)
+    c.cu = torch.tensor([512, 900, 0, 400, 300], dtype=torch.int32, device="cuda")  # 512 .. 899, none, 0 .. 399, none
+    before = c.state.clone()
+    for _ in range(3):
+        c.run(ssu)
+    torch.cuda.synchronize()
+    rest = [i for i in range(before.shape[0]) if i not in (c.idx[0].item(), c.idx[2].item())]
+    assert torch.equal(c.state[rest], before[rest])
+    assert (c.out[400:512] == 7.0).all() and (c.out[900:] == 7.0).all()
+
+
 @pytest.mark.parametrize("rate", [0.0, 20.0, 300.0])
 def test_prompt_decays(ssu, rate):
     """No decay, and decays that leave nothing of the token before."""
