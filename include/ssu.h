@@ -352,10 +352,10 @@ int32_t ssu_scan_select_tile(const ssu_scan_args *args, int64_t chunk);
  *
  * Numerics: state, decays, sums and the recurrence in fp32 (the decays'
  * running sums in fp64, where a sum over many tokens would lose digits). Over
- * prompts the products run on bf16 matrix instructions with fp32 sums; fp32
- * operands (the state, decayed v) enter as a bf16 pair (value and remainder,
- * 2^-17 relative), the scores of a chunk as well, so only the output's own
- * rounding to bf16 is seen. log_decay below -10000 counts as -10000 (exp is 0
+ * prompts the products run on bf16 matrix instructions with fp32 sums; the
+ * state and a chunk's scores enter the output's as a bf16 pair (value and
+ * remainder, 2^-17 relative), so that only the output's own rounding to bf16 is
+ * seen, and decayed v enters the state's as three (2^-24). log_decay below -10000 counts as -10000 (exp is 0
  * from -104 on), so -inf is a reset of the state; NaN and infinite v reach
  * their own and later tokens of their channel p only, NaN and infinite k
  * their own and later tokens, NaN and infinite q their own token.
@@ -387,7 +387,7 @@ typedef struct ssu_linear_args {
     ssu_view beta;       /* [T, H] F32, any strides >= 0; ptr NULL: 1 */
     ssu_view out;        /* [T, H, P] BF16, written, stride[2] == 1 */
     void *workspace;     /* device memory, 16-byte aligned; its contents do not matter
-                            before and after the call */
+                            before and after the call; NULL where none is needed */
     int64_t workspace_bytes;
 } ssu_linear_args;
 
@@ -472,14 +472,14 @@ ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stream);
  *   out[b,h] = sum_j w_j V_j / sum_j w_j
  *   lse[b,h] = m + log(sum_j w_j)
  *
- * No visible token, or only scores of -inf: out 0, lse -inf. A negative seq_lens[b] marks a padding
- * request, whose out and lse are left untouched. Tokens of a page id outside
- * [0, num_pages) are not visible. fp32 scores, statistics and sums; the
+ * No visible token, or only scores of -inf: out 0, lse -inf. A negative
+ * seq_lens[b] marks a padding request, whose out and lse are left untouched.
+ * Tokens of a page id outside [0, num_pages) are not visible. fp32 scores, statistics and sums; the
  * weights w_j enter the product with V as a 16-bit pair (value and
  * remainder), so that only the output's own rounding is seen. What the cache
  * holds in rows that no request sees, NaN and infinities too, does not matter.
- * Results do not depend on other requests of the batch, but on its size and
- * on max_pages within rounding (they set the split).
+ * The batch's other lengths and max_pages set where a request is split, and so
+ * change its result within rounding; the same call gives the same bits.
  */
 typedef struct ssu_attn_args {
     int32_t batch;       /* >= 0 (0: no-op) */
@@ -489,7 +489,7 @@ typedef struct ssu_attn_args {
     int32_t device;      /* as in ssu_linear_args */
     int64_t num_pages;   /* pages of the caches, >= 0 */
     int64_t max_pages;   /* columns of block_table, >= 0 */
-    float scale;         /* finite */
+    float scale;         /* finite, also times log2(e) */
     int32_t reserved;    /* must be 0 */
     ssu_view q;          /* [batch, nq, D] BF16 or F16, stride[2] == 1 */
     ssu_view k_cache, v_cache; /* [num_pages, page_size, nk, D], q's type, stride[3] == 1 */
@@ -497,7 +497,8 @@ typedef struct ssu_attn_args {
     ssu_view seq_lens;   /* [batch] I32, stride[0] == 1 */
     ssu_view out;        /* [batch, nq, D] q's type, written, stride[2] == 1 */
     ssu_view lse;        /* [batch, nq] F32, written; ptr NULL: not wanted */
-    void *workspace;     /* device memory, 16-byte aligned; contents do not matter */
+    void *workspace;     /* device memory, 16-byte aligned; contents do not matter;
+                            NULL where none is needed */
     int64_t workspace_bytes;
 } ssu_attn_args;
 
@@ -506,9 +507,10 @@ typedef struct ssu_attn_args {
 int64_t ssu_paged_attention_workspace(const ssu_attn_args *args);
 
 /* Enqueue it on `stream`. Rows of 16-byte multiples (pointers and strides) are
- * read fastest; elements aligned to their size are enough. out, lse and workspace must not overlap each other or any input; calls that
- * may run at the same time need workspaces of their own. Asynchronous,
- * allocation-free, graph-capturable. Errors (nothing is launched):
+ * read fastest; elements aligned to their size are enough. out, lse and
+ * workspace must not overlap each other or any input; calls that may run at the
+ * same time need workspaces of their own. Asynchronous, allocation-free,
+ * graph-capturable. Errors (nothing is launched):
  * SSU_ERR_INVALID_ARGUMENT (null pointers, sizes, strides, dtype tags, a
  * workspace too small), SSU_ERR_UNSUPPORTED (D, inner strides, more than 2^31
  * workgroups), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */

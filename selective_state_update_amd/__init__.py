@@ -593,6 +593,8 @@ def _on(stream, t):
     torch = _torch()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the operands on {t.device}")
     return torch.cuda.stream(stream)
 
 

@@ -568,12 +568,14 @@ Plan plan_of(const ssu_attn_args &a)
     return p;
 }
 
+float log2_scale(const ssu_attn_args &a) { return static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634); }
+
 ssu_status check_attn(const ssu_attn_args &a)
 {
     const char *const who = "ssu_paged_attention";
     if (a.reserved != 0)
         return fail(SSU_ERR_INVALID_ARGUMENT, "%s: reserved field must be 0", who);
-    if (!std::isfinite(a.scale))
+    if (!std::isfinite(log2_scale(a)))
         return fail(SSU_ERR_INVALID_ARGUMENT, "%s: scale is not finite", who);
     SSU_TRY(check_sizes(a, who));
     if (a.batch == 0)
@@ -662,7 +664,7 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     p.page_size = a.page_size;
     p.row_tiles = plan.row_tiles;
     p.groups = plan.groups;
-    p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    p.scale_log2 = log2_scale(a);
     char *const ws = static_cast<char *>(a.workspace);
     p.open = reinterpret_cast<Open *>(ws);
     p.part = reinterpret_cast<float *>(ws + plan.part_at);

@@ -75,7 +75,7 @@ QK = dict(ntokens=3, nq=4, nk=2, headdim=64, rot=64, interleaved=0, device=-1, e
           q=view(BF16, 256, 64, 1), k=view(BF16, 128, 64, 1), q_weight=view(BF16, 1), k_weight=view(F32, 1),
           positions=view(I64, 1), cos_sin=view(F32, 64, 1), q_out=view(BF16, 256, 64, 1), k_out=view(BF16, 128, 64, 1),
           v=view(BF16, 128, 64, 1), k_cache=view(BF16, 2048, 128, 64, 1), v_cache=view(BF16, 2048, 128, 64, 1), slots=view(I64, 1))
-ATTN = dict(batch=2, nq=4, nk=2, headdim=64, page_size=16, device=-1, num_pages=8, max_pages=4, scale=0.1, reserved=0,
+ATTN = dict(batch=2, nq=4, nk=2, headdim=64, page_size=16, device=-1, num_pages=8, max_pages=100, scale=0.1, reserved=0,
             q=view(BF16, 256, 64, 1), k_cache=view(BF16, 2048, 128, 64, 1), v_cache=view(BF16, 2048, 128, 64, 1),
             table=view(I32, 4, 1), lens=view(I32, 1), out=view(BF16, 256, 64, 1), lse=view(F32, 4, 1), ws=0x20000, ws_bytes=1 << 40)
 
@@ -197,7 +197,7 @@ def test_qk_nothing_to_do(lib):
 ATTN_BAD = [
     (dict(batch=-1), INVALID), (dict(num_pages=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(page_size=0), INVALID),
     (dict(nk=0), INVALID), (dict(nq=3), INVALID), (dict(nq=0), INVALID), (dict(reserved=1), INVALID),
-    (dict(scale=float("inf")), INVALID), (dict(headdim=96), UNSUPPORTED), (dict(headdim=512), UNSUPPORTED),
+    (dict(scale=float("inf")), INVALID), (dict(scale=3e38), INVALID), (dict(headdim=96), UNSUPPORTED), (dict(headdim=512), UNSUPPORTED),
     (dict(batch=1 << 30), UNSUPPORTED),
     ({"q.ptr": 0}, INVALID), ({"k_cache.ptr": 0}, INVALID), ({"v_cache.ptr": 0}, INVALID), ({"table.ptr": 0}, INVALID),
     ({"lens.ptr": 0}, INVALID), ({"out.ptr": 0}, INVALID), ({"q.dtype": F32}, INVALID), ({"k_cache.dtype": F16}, INVALID),
@@ -217,6 +217,31 @@ def test_attention_refusals(lib, kw, code):
 
 def test_attention_nothing_to_do(lib):
     assert lib.ssu_paged_attention(pack("attn", change(ATTN, dict(batch=0))), None) == OK
+
+
+def test_attention_workspace(lib):
+    """None for short caches of few units: a workgroup takes each."""
+    def need(**kw):
+        return lib.ssu_paged_attention_workspace(pack("attn", change(ATTN, kw)))
+
+    assert need(max_pages=32) == 0 and need(max_pages=33) > 0
+    assert need(max_pages=16, headdim=256) == 0 and need(max_pages=17, headdim=256) > 0
+    assert need(max_pages=32, batch=256) == 0 and need(max_pages=32, batch=257) > 0
+    assert need(max_pages=0) == 0 and need(nk=0) == -1
+
+
+def test_stream_of_another_device():
+    """Refused: the call would run on the operands' own current stream instead."""
+    import types
+
+    import torch
+
+    import selective_state_update_amd as ssu
+
+    operand = types.SimpleNamespace(device=torch.device("cuda", 0))
+    stream = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="cuda:1"):
+        ssu._on(stream, operand)
 
 
 def test_python_wants_the_gpu(ssu):
