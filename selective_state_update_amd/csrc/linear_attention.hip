@@ -191,12 +191,19 @@ __device__ __forceinline__ u32x2 read_transposed(const uint16_t *p)
                                          (__attribute__((address_space(3))) S4 *)(const_cast<uint16_t *>(p))));
 }
 
+// Waves per SIMD: four with eight-wave workgroups, whose instructions are enough for
+// each other's waits. Four-wave ones run with three and read the operands of several
+// products ahead instead (a prompt of 37 tokens 9.0 against 9.7 us, 16 of 1 to 2048
+// tokens 82 against 84, one of 16384 tokens 77 against 81; a 128 x 128 head's eight
+// waves 252 us that way against 228).
 template <int N, int W, bool FULL>
-__global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_kernel(const ChunkParams p)
+__global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && W == 4 ? 3 : 4) ssu_linear_chunk_kernel(const ChunkParams p)
 {
     constexpr int THREADS = 64 * W;
     constexpr int MT = N / 16;        // state tiles along n
     constexpr int KS = N / 32;        // products along n of a score
+    constexpr int AHEAD = W == 8 ? 1 : KS < 4 ? KS : 4;  // of them, read ahead
+    constexpr int MAHEAD = W == 8 ? 1 : MT < 8 ? MT : 8;  // the same of state tiles
     constexpr bool PART = N * kChunk / 8 < THREADS;  // not every thread has a run of q and k
     constexpr int PC = 16 * W;        // columns of v
     // pitches in LDS: 16 rows of 8 or 16 bytes, and 4 rows of 32, in banks of their own
@@ -457,10 +464,16 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
                 const int it = pair >= 6 ? 3 : pair >= 3 ? 2 : pair >= 1 ? 1 : 0, jt = pair - it * (it + 1) / 2;
                 f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int e = 0; e < KS; ++e) {
-                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(lk + (16 * jt + c) * ROW + 32 * e + 8 * g);
-                    const u32x4 qf = *reinterpret_cast<const u32x4 *>(lq + (16 * it + c) * ROW + 32 * e + 8 * g);
-                    x = Mma<Bf16>::run(kf, qf, x);
+                for (int e0 = 0; e0 < KS; e0 += AHEAD) {
+                    u32x4 kf[AHEAD], qf[AHEAD];
+#pragma unroll
+                    for (int e = 0; e < AHEAD; ++e) {
+                        kf[e] = *reinterpret_cast<const u32x4 *>(lk + (16 * jt + c) * ROW + 32 * (e0 + e) + 8 * g);
+                        qf[e] = *reinterpret_cast<const u32x4 *>(lq + (16 * it + c) * ROW + 32 * (e0 + e) + 8 * g);
+                    }
+#pragma unroll
+                    for (int e = 0; e < AHEAD; ++e)
+                        x = Mma<Bf16>::run(kf[e], qf[e], x);
                 }
                 const float li = lsum[buf][16 * it + c], ri = lrest[buf][16 * it + c];
                 const f32x4 lj = *reinterpret_cast<const f32x4 *>(&lsum[buf][16 * jt + 4 * g]);
@@ -484,9 +497,19 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
 #pragma unroll
             for (int it = 0; it < kTiles; ++it)
                 o[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            u32x4 qf[AHEAD][kTiles];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                u32x4 fh, fl, qf[kTiles];
+                if (s % AHEAD == 0)
+#pragma unroll
+                    for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+                        for (int it = 0; it < kTiles; ++it) {
+                            const uint16_t *const qrow = lq + (16 * it + c) * ROW + 32 * (s + e) + 4 * g;
+                            const u32x2 x = *reinterpret_cast<const u32x2 *>(qrow), y = *reinterpret_cast<const u32x2 *>(qrow + 16);
+                            qf[e][it] = u32x4{x[0], x[1], y[0], y[1]};
+                        }
+                u32x4 fh, fl;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t wh, wl;
@@ -495,15 +518,11 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
                     fl[e] = wl;
                 }
 #pragma unroll
-                for (int it = 0; it < kTiles; ++it) {
-                    const uint16_t *const qrow = lq + (16 * it + c) * ROW + 32 * s + 4 * g;
-                    const u32x2 x = *reinterpret_cast<const u32x2 *>(qrow), y = *reinterpret_cast<const u32x2 *>(qrow + 16);
-                    qf[it] = u32x4{x[0], x[1], y[0], y[1]};
-                    o[it] = Mma<Bf16>::run(fh, qf[it], o[it]);
-                }
+                for (int it = 0; it < kTiles; ++it)
+                    o[it] = Mma<Bf16>::run(fh, qf[s % AHEAD][it], o[it]);
 #pragma unroll
                 for (int it = 0; it < kTiles; ++it)
-                    o[it] = Mma<Bf16>::run(fl, qf[it], o[it]);
+                    o[it] = Mma<Bf16>::run(fl, qf[s % AHEAD][it], o[it]);
             }
 #pragma unroll
             for (int it = 0; it < kTiles; ++it)
@@ -564,13 +583,19 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : 4) ssu_linear_chunk_ker
                 f3[e] = pack2<Bf16>(x1 - Bf16::lo(h2), y1 - Bf16::hi(h2));
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const u32x2 x = read_transposed(lk + 32 * s * ROW + tr + 16 * m);
-                const u32x2 y = read_transposed(lk + (32 * s + 16) * ROW + tr + 16 * m);
-                const u32x4 kf = {x[0], x[1], y[0], y[1]};
-                st[m] = Mma<Bf16>::run(kf, f1, st[m]);
-                st[m] = Mma<Bf16>::run(kf, f2, st[m]);
-                st[m] = Mma<Bf16>::run(kf, f3, st[m]);
+            for (int m0 = 0; m0 < MT; m0 += MAHEAD) {
+                u32x4 kf[MAHEAD];
+#pragma unroll
+                for (int m = 0; m < MAHEAD; ++m) {
+                    const u32x2 x = read_transposed(lk + 32 * s * ROW + tr + 16 * (m0 + m));
+                    const u32x2 y = read_transposed(lk + (32 * s + 16) * ROW + tr + 16 * (m0 + m));
+                    kf[m] = u32x4{x[0], x[1], y[0], y[1]};
+                }
+#pragma unroll
+                for (const u32x4 &f : {f1, f2, f3})
+#pragma unroll
+                    for (int m = 0; m < MAHEAD; ++m)
+                        st[m0 + m] = Mma<Bf16>::run(kf[m], f, st[m0 + m]);
             }
         }
         if (more) {
@@ -710,12 +735,14 @@ struct Plan {
 };
 
 // Sequences are cut where whole ones would leave most of the chip idle: at most
-// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 84 us
-// cut, 128 uncut; 16 of 1024 tokens 89 and 70, but the host cannot tell them apart;
-// with twice the waves uncut is faster for both, 147 against 177 us and 89
-// against 110). Then segments are as long as fills the chip once, 4096 waves
-// (N = 256: 2048), but of 128 tokens at least and a 64th of all at most: one
-// prompt of 4096 tokens takes 40 us in segments of 128, 47 in segments of 256.
+// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 82 us
+// cut, 129 uncut; 16 of 1024 tokens 90 and 70, but the host cannot tell them
+// apart; with twice the waves uncut is faster for both, 145 against 155 us and 86
+// against 126), and more than 256 tokens (256 tokens of one prompt: 23 us cut, 20
+// uncut). Then segments are as long as fills the chip once, 3072 waves (4096 in
+// workgroups of eight, 2048 at N = 256), half a segment of every sequence but one lost,
+// but of 128 tokens at least and a 64th of all at most: one prompt of 4096 tokens
+// takes 38 us in segments of 128, 44 in segments of 256.
 Plan plan_of(const ssu_linear_args &a)
 {
     Plan p{};
@@ -723,9 +750,10 @@ Plan plan_of(const ssu_linear_args &a)
     p.slices = (a.headdim + columns - 1) / columns;
     const int64_t units = static_cast<int64_t>(a.nheads) * p.slices * waves;
     const int64_t chunks = (a.ntokens + kChunk - 1) / kChunk;
-    const int64_t room = (a.dstate == 256 ? 8 : 16) * kNumCUs;
+    const bool cuts = chunks > 8 && a.batch * units <= 4 * kNumCUs;
+    const int64_t room = (a.dstate == 256 ? 8 : waves == 4 ? 12 : 16) * kNumCUs - (cuts ? (a.batch - 1) * units / 2 : 0);
     const int64_t per = std::max<int64_t>({(chunks * units + room - 1) / room, (chunks + 63) / 64, 4});
-    const bool cut = per < chunks && a.batch * units <= 4 * kNumCUs;
+    const bool cut = cuts && per < chunks;
     p.seg_len = static_cast<int>(cut ? per * kChunk : std::min<int64_t>(a.ntokens + 1, INT32_MAX));
     p.segments = static_cast<int>(a.ntokens / p.seg_len) + a.batch;
     if (cut) {
