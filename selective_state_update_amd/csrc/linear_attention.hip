@@ -191,19 +191,17 @@ __device__ __forceinline__ u32x2 read_transposed(const uint16_t *p)
                                          (__attribute__((address_space(3))) S4 *)(const_cast<uint16_t *>(p))));
 }
 
-// Waves per SIMD: four with eight-wave workgroups, whose instructions are enough for
-// each other's waits. Four-wave ones run with three and read the operands of several
-// products ahead instead (a prompt of 37 tokens 9.0 against 9.7 us, 16 of 1 to 2048
-// tokens 82 against 84, one of 16384 tokens 77 against 81; a 128 x 128 head's eight
-// waves 252 us that way against 228).
-template <int N, int W, bool FULL>
-__global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && W == 4 ? 3 : 4) ssu_linear_chunk_kernel(const ChunkParams p)
+// DENSE: four waves per SIMD, whose instructions are enough for each other's waits;
+// otherwise three (N = 128), which read the operands of several products ahead
+// (chunk_kernels says which).
+template <int N, int W, bool FULL, bool DENSE>
+__global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4) ssu_linear_chunk_kernel(const ChunkParams p)
 {
     constexpr int THREADS = 64 * W;
     constexpr int MT = N / 16;        // state tiles along n
     constexpr int KS = N / 32;        // products along n of a score
-    constexpr int AHEAD = W == 8 ? 1 : KS < 4 ? KS : 4;  // of them, read ahead
-    constexpr int MAHEAD = W == 8 ? 1 : MT < 8 ? MT : 8;  // the same of state tiles
+    constexpr int AHEAD = DENSE ? 1 : KS < 4 ? KS : 4;  // of them, read ahead
+    constexpr int MAHEAD = DENSE ? 1 : MT < 8 ? MT : 8;  // the same of state tiles
     constexpr bool PART = N * kChunk / 8 < THREADS;  // not every thread has a run of q and k
     constexpr int PC = 16 * W;        // columns of v
     // pitches in LDS: 16 rows of 8 or 16 bytes, and 4 rows of 32, in banks of their own
@@ -688,24 +686,31 @@ struct ChunkKernels {
     int columns;  // of v per workgroup
 };
 
-template <int N, int W>
+template <int N, int W, bool DENSE>
 constexpr ChunkKernels chunk_kernels()
 {
-    return {&ssu_linear_chunk_kernel<N, W, false>, &ssu_linear_chunk_kernel<N, W, true>, 16 * W};
+    return {&ssu_linear_chunk_kernel<N, W, false, W == 8>, &ssu_linear_chunk_kernel<N, W, true, DENSE>, 16 * W};
 }
 
 // Eight waves where they share the products of q and k of whole heads and their
 // states fit four waves per SIMD: N = 128, P in 80 .. 128 (one prompt of 16384
-// tokens, 32 heads of 128 x 128: 228 us, 245 with four waves; a head of 64 x 128
+// tokens, 32 heads of 128 x 128: 226 us, 270 with four waves; a head of 64 x 128
 // has columns for four only). Four elsewhere: more workgroups to hide each other's
-// waits (4 prompts of 3000, 8 heads of 128 x 64: 35.9 us against 36.9; of
-// 128 x 256: 79.5 against 92.2; of 224 x 128: 71.5 against 77.6).
-ChunkKernels chunk_kernels(int N, int P)
+// waits (4 prompts of 3000, 8 heads of 128 x 64: 34.5 us against 36.9; of
+// 128 x 256: 68.7 against 92.2; of 224 x 128: 62.5 against 77.6).
+//
+// Those of four read ahead (a prompt of 37 tokens 9.1 us against 9.7 dense, 16 of 1
+// to 2048 tokens 82 against 84.5), unless there are more of N = 128 than three waves
+// per SIMD hold (32 prompts of 700 tokens, 16 heads of 224 x 128: 144 against 129);
+// eight always are dense (the prompt of 16384 tokens 252 us otherwise).
+ChunkKernels chunk_kernels(int N, int P, int64_t waves)
 {
     if (N == 128 && P > 64 && P <= 128)
-        return chunk_kernels<128, 8>();
-    return N <= 32 ? chunk_kernels<32, 4>() : N == 64 ? chunk_kernels<64, 4>() : N == 128 ? chunk_kernels<128, 4>()
-                                                                                        : chunk_kernels<256, 4>();
+        return chunk_kernels<128, 8, true>();
+    if (N == 128 && waves > 12 * kNumCUs)
+        return chunk_kernels<128, 4, true>();
+    return N <= 32 ? chunk_kernels<32, 4, false>() : N == 64 ? chunk_kernels<64, 4, false>()
+         : N == 128 ? chunk_kernels<128, 4, false>() : chunk_kernels<256, 4, false>();
 }
 
 // ------------------------------------------------------------------ host --
@@ -731,13 +736,14 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
 // Segments of a prompt call.
 struct Plan {
     int seg_len, segments, slices;
+    int64_t waves;             // of all sequences, uncut
     int64_t decays_at, bytes;  // workspace (0: one segment per sequence)
 };
 
 // Sequences are cut where whole ones would leave most of the chip idle: at most
 // one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 82 us
 // cut, 129 uncut; 16 of 1024 tokens 90 and 70, but the host cannot tell them
-// apart; with twice the waves uncut is faster for both, 145 against 155 us and 86
+// apart; with twice the waves uncut is faster for both, 131 against 155 us and 86
 // against 126), and more than 256 tokens (256 tokens of one prompt: 23 us cut, 20
 // uncut). Then segments are as long as fills the chip once, 3072 waves (4096 in
 // workgroups of eight, 2048 at N = 256), half a segment of every sequence but one lost,
@@ -746,11 +752,12 @@ struct Plan {
 Plan plan_of(const ssu_linear_args &a)
 {
     Plan p{};
-    const int columns = chunk_kernels(a.dstate, a.headdim).columns, waves = columns / 16;
+    const int columns = chunk_kernels(a.dstate, a.headdim, 0).columns, waves = columns / 16;
     p.slices = (a.headdim + columns - 1) / columns;
     const int64_t units = static_cast<int64_t>(a.nheads) * p.slices * waves;
     const int64_t chunks = (a.ntokens + kChunk - 1) / kChunk;
-    const bool cuts = chunks > 8 && a.batch * units <= 4 * kNumCUs;
+    p.waves = a.batch * units;
+    const bool cuts = chunks > 8 && p.waves <= 4 * kNumCUs;
     const int64_t room = (a.dstate == 256 ? 8 : waves == 4 ? 12 : 16) * kNumCUs - (cuts ? (a.batch - 1) * units / 2 : 0);
     const int64_t per = std::max<int64_t>({(chunks * units + room - 1) / room, (chunks + 63) / 64, 4});
     const bool cut = cuts && per < chunks;
@@ -889,7 +896,7 @@ ssu_status launch_chunks(const ssu_linear_args &a, hipStream_t stream)
         if (reinterpret_cast<uintptr_t>(a.workspace) % 16)
             return fail(SSU_ERR_MISALIGNED, "ssu_linear_attention: workspace must be 16-byte aligned");
     }
-    const ChunkKernels k = chunk_kernels(a.dstate, a.headdim);
+    const ChunkKernels k = chunk_kernels(a.dstate, a.headdim, plan.bytes > 0 ? 0 : plan.waves);
     ChunkParams p{};
     p.a = linear_params(a);
     p.states = static_cast<float *>(a.workspace);
