@@ -21,8 +21,8 @@ constexpr int kJoinRows = 4;  // rows that a workgroup of the join takes
 // Waves of a workgroup. D = 256 needs half the register file per wave: two
 // waves and two workgroups per CU instead of four and one keep one of them
 // loading while the other joins (64 requests up to 4096 tokens, 8 heads of 256:
-// 185 against 208 us). Twice as many where a workgroup has one whole unit.
-constexpr int waves_for(int D, bool whole) { return (D == 256 ? 2 : 4) * (whole ? 2 : 1); }
+// 185 against 208 us).
+constexpr int waves_for(int D) { return D == 256 ? 2 : 4; }
 
 struct AttnParams {
     const uint16_t *q, *k, *v;
@@ -104,9 +104,9 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 // is uniform; otherwise every lane looks its own token up. WHOLE (short caches,
 // see plan_of): no line, a workgroup per unit, nothing to join behind it.
 template <typename T, int D, bool PAGE16, bool WHOLE>
-__global__ void __launch_bounds__(64 * waves_for(D, WHOLE), D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
+__global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
 {
-    constexpr int kWaves = waves_for(D, WHOLE);
+    constexpr int kWaves = waves_for(D);
     constexpr int kRound = kWaves * kTile;  // tokens of one workgroup's step
     constexpr int KS = D / 32;      // products along D of a score
     constexpr int E = D / 16;       // values of a V row per lane, products of an output row
@@ -118,22 +118,28 @@ __global__ void __launch_bounds__(64 * waves_for(D, WHOLE), D <= 128 ? 2 : 1) ss
     __shared__ int64_t scan[kWaves];
     __shared__ int64_t found[3];  // its request, the steps before it, its tokens
 
-    const int wg = WHOLE ? static_cast<int>(blockIdx.x) : xcd_order(static_cast<int>(blockIdx.x), p.groups);
+    int wg = static_cast<int>(blockIdx.x);
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int units = p.nk * p.row_tiles;  // of a request
 
     // this workgroup's run of the line, and the request that it begins in: the
     // steps of one unit of every request, summed over them
-    if (!WHOLE && tid == 0)
-        p.open[wg] = Open{-1, 0, 0, 0};
     int64_t per, pos, stop, n, before;  // (before: a unit's steps of all earlier requests)
     int b;
     auto run_of = [&](int64_t steps) {
         const int64_t total = steps * units;
-        per = (total + p.groups - 1) / p.groups;
+        const int64_t all = static_cast<int64_t>(p.batch) * units;  // of the batch
+        const bool half = D == 128 && p.groups > kNumCUs && (all <= kNumCUs / 8 || total >= 16 * (kNumCUs + all));
+        // (no more than steps: those with work are spread over all XCDs)
+        const int groups = static_cast<int>(min(static_cast<int64_t>(half ? kNumCUs : p.groups), max(total, int64_t(1))));
+        per = (total + groups - 1) / groups;
+        if (wg < groups)
+            wg = xcd_order(wg, groups);
         pos = wg * per;
-        stop = min(pos + per, total);
+        stop = wg < groups ? min(pos + per, total) : 0;
+        if (tid == 0)
+            p.open[wg] = Open{-1, 0, 0, 0};
     };
     if constexpr (WHOLE) {
         b = wg / units;
@@ -534,33 +540,34 @@ struct Plan {
     int64_t part_at, stat_at, bytes;  // workspace
 };
 
-// A workgroup of its own per unit where no unit has more than two steps (512
-// tokens, 256 at D = 256) and the chip holds all of them: no line to lay out, no
-// partial sums, one launch (one request, 2 heads of 128: 100 tokens 6.4 against
-// 9.2 us, 512 tokens 10.7 against 11.1, 777 tokens 13.3 against 12.2; 32 requests
-// of 1 to 512 tokens, 8 heads: 14.2 against 22.5 us; 64 requests: 25.2 against
-// 32.4; 256 of 300 tokens 87 against 70).
+// A workgroup of its own per unit where no unit has more than four steps (512
+// tokens, 256 at D = 256), or no more than 16 and there is at least one unit for
+// every CU: no line to lay out, no partial sums, one launch, and as many workgroups
+// per CU as fit, which load while others start and join (one request, 2 heads of
+// 128: 100 tokens 6.1 against 9.2 us, 400 tokens 9.0 against 10.3, 800 tokens 13.1
+// against 11.1; 32 requests of 1 to 1600 tokens, 8 heads: 26 against 34 us; 64
+// of 1 to 1600: 48 against 50; 64 of 1 to 8192: 218 against 184).
 //
-// Otherwise one workgroup per CU at D = 128, where four waves' loads are enough to
-// fill the memory system and more only crowd it (64 requests up to 8192 tokens, 8
-// heads: 184 against 189 us with two; 3 of 100003 tokens, 4 heads: 118.5 against
-// 123), but two where the runs hold many units, each with its start and its
-// join (512 requests up to 600 tokens, 4 heads: 82 against 102 us); two at the
-// smaller steps of D = 64 (64 requests up to 8192 tokens: 106 against 121 us) and
-// at D = 256 (see waves_for). No more than there can be steps.
+// Otherwise a line with two workgroups per CU; at D = 128 every second one leaves
+// (the kernel knows the lengths) where the runs' pieces of units have 16 steps or
+// more or are few: four waves' loads are enough then to fill the memory system, and
+// more only crowd it (64 requests up to 8192 tokens, 8 heads: 184 against 193 us with
+// two; 3 of 100003 tokens, 4 heads: 118 against 124; but 32 up to 6000 tokens, 8 heads:
+// 92 against 83, 64 up to 800 tokens in a wide table 44 against 34; D = 64, 64
+// requests up to 8192 tokens: 121 against 105). No more than there can be steps.
 Plan plan_of(const ssu_attn_args &a)
 {
     Plan p{};
     p.row_tiles = (a.nq / a.nk + 15) / 16;
     const int64_t units = static_cast<int64_t>(a.batch) * a.nk * p.row_tiles;
-    p.whole = units <= 2 * kNumCUs && a.max_pages * a.page_size <= 2 * waves_for(a.headdim, true) * kTile;
+    const int round = waves_for(a.headdim) * kTile;
+    const int64_t rounds = std::max<int64_t>((a.max_pages * a.page_size + round - 1) / round, 1);
+    p.whole = rounds <= (units < kNumCUs ? 4 : 16);
     if (p.whole) {
         p.groups = static_cast<int>(units);
         return p;
     }
-    const int round = waves_for(a.headdim, false) * kTile;
-    const int64_t rounds = std::max<int64_t>((a.max_pages * a.page_size + round - 1) / round, 1);
-    const int64_t resident = a.headdim == 128 && units <= 4 * kNumCUs ? kNumCUs : 2 * kNumCUs;
+    const int64_t resident = 2 * kNumCUs;
     p.groups = static_cast<int>(units > resident / rounds ? resident : std::max<int64_t>(units * rounds, 1));
     p.part_at = static_cast<int64_t>(p.groups) * sizeof(Open);
     p.stat_at = p.part_at + static_cast<int64_t>(p.groups) * 32 * a.headdim * 4;
@@ -673,7 +680,7 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     const AttnKernels k = a.q.dtype == SSU_BF16 ? attn_kernels<Bf16>(a.headdim, page16) : attn_kernels<F16>(a.headdim, page16);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
-    hipError_t e = launch_kernel(plan.whole ? k.whole : k.split, p, plan.groups, 64 * waves_for(a.headdim, plan.whole), 0, stream);
+    hipError_t e = launch_kernel(plan.whole ? k.whole : k.split, p, plan.groups, 64 * waves_for(a.headdim), 0, stream);
     if (e == hipSuccess && !plan.whole && plan.groups > 1)
         e = launch_kernel(k.join, p, plan.groups * (16 / kJoinRows), 64 * kJoinRows, 0, stream);
     if (e != hipSuccess)

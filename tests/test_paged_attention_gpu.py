@@ -233,11 +233,17 @@ def test_short_graph_replays(ssu):
 @pytest.mark.parametrize("D,tokens", [(64, 512), (128, 512), (256, 256)])
 @pytest.mark.parametrize("page", [1, 16])
 def test_short_limits(ssu, D, tokens, page):
-    """On both sides of the longest cache that a workgroup takes alone, and of the most units."""
+    """On both sides of the longest cache that a workgroup takes alone, with few units and with many."""
     for n in (tokens - 1, tokens, tokens + 1):
         Case([n, 3, 0, n // 2 + 1], 6, 3, D, page, seed=n, spare=0).check(ssu)
-    for batch in (256, 257):
-        Case([1 + 37 * i % 40 for i in range(batch)], 2, 2, D, page, seed=batch, spare=0).check(ssu)
+    for batch, n in ((127, tokens + 1), (128, tokens + 1), (128, 4 * tokens), (128, 4 * tokens + 1)):
+        Case([n] + [1 + 37 * i % 40 for i in range(1, batch)], 2, 2, D, page, seed=batch, spare=0).check(ssu)
+
+
+@pytest.mark.parametrize("lens,nk", [([9000] * 3, 11), ([9000] * 2, 16), ([7000, 9000, 8000, 9500, 100], 8)])
+def test_runs_of_one_and_two_workgroups(ssu, lens, nk):
+    """Lines that every second workgroup leaves (few units, long pieces) and that all share."""
+    Case(lens, nk, nk, 128, 64, seed=nk).check(ssu)
 
 
 def test_two_streams(ssu):

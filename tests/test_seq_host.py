@@ -220,13 +220,15 @@ def test_attention_nothing_to_do(lib):
 
 
 def test_attention_workspace(lib):
-    """None for short caches of few units: a workgroup takes each."""
+    """None for short caches: a workgroup takes each unit."""
     def need(**kw):
         return lib.ssu_paged_attention_workspace(pack("attn", change(ATTN, kw)))
 
     assert need(max_pages=32) == 0 and need(max_pages=33) > 0
     assert need(max_pages=16, headdim=256) == 0 and need(max_pages=17, headdim=256) > 0
-    assert need(max_pages=32, batch=256) == 0 and need(max_pages=32, batch=257) > 0
+    assert need(max_pages=33, batch=127) > 0 and need(max_pages=33, batch=128) == 0  # two units a request
+    assert need(max_pages=128, batch=128) == 0 and need(max_pages=129, batch=128) > 0
+    assert need(max_pages=64, batch=128, headdim=256) == 0 and need(max_pages=65, batch=128, headdim=256) > 0
     assert need(max_pages=0) == 0 and need(nk=0) == -1
 
 
