@@ -69,11 +69,10 @@ template <>
 constexpr float kShift<F16> = 14.0f;
 
 template <typename T>
-__device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int d, float y, float sum, float base)
+__device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, float sum, float top)
 {
-    p.out[b * p.o_b + h * p.o_h + d] = T::round(sum == 0.0f ? 0.0f : y / sum);
-    if (p.lse && d == 0)
-        p.lse[b * p.l_b + h * p.l_h] = sum == 0.0f ? -INFINITY : (base - kShift<T> + log2f(sum)) * kLn2Hi;
+    if (p.lse)
+        p.lse[b * p.l_b + h * p.l_h] = sum == 0.0f ? -INFINITY : (top - kShift<T> + log2f(sum)) * kLn2Hi;
 }
 
 // The steps of all units stand in one line (requests in order, a request's
@@ -113,8 +112,8 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
     constexpr int EW = E / 2;       // the same in words
     using V = uint32_t __attribute__((ext_vector_type(EW)));
     typedef V V_a2 __attribute__((aligned(2)));
-    __shared__ float part[kWaves][16][D];
-    __shared__ float stat_m[kWaves][16], stat_l[kWaves][16];
+    __shared__ __attribute__((aligned(16))) float part[kWaves][16][D];
+    __shared__ __attribute__((aligned(16))) float stat_m[kWaves][16], stat_l[kWaves][16], row_top[16], row_sum[16];
     __shared__ int64_t scan[kWaves];
     __shared__ int64_t found[3];  // its request, the steps before it, its tokens
 
@@ -401,39 +400,52 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
             stat_l[wave][c] = l;
         }
         __syncthreads();
+        f32x4 top = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, base, own;  // of rows 4g .. 4g+3
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            top = __builtin_elementwise_max(top, *reinterpret_cast<const f32x4 *>(&stat_m[w][4 * g]));
+        own = *reinterpret_cast<const f32x4 *>(&stat_m[wave][4 * g]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = 4 * g + i;
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                top = fmaxf(top, stat_m[w][r]);
-            const float f = __builtin_amdgcn_exp2f(stat_m[wave][r] - (top == -INFINITY ? 0.0f : top));
+            base[i] = top[i] == -INFINITY ? 0.0f : top[i];
+            const float f = __builtin_amdgcn_exp2f(own[i] - base[i]);
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                part[wave][r][c * E + e] = o[e][i] * f;
+                part[wave][4 * g + i][c * E + e] = o[e][i] * f;
+        }
+        if (wave == 0 && c == 0) {
+            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(&stat_m[w][4 * g]);
+                const f32x4 y = *reinterpret_cast<const f32x4 *>(&stat_l[w][4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[i] = fmaf(y[i], __builtin_amdgcn_exp2f(x[i] - base[i]), sum[i]);
+            }
+            *reinterpret_cast<f32x4 *>(&row_top[4 * g]) = top;
+            *reinterpret_cast<f32x4 *>(&row_sum[4 * g]) = sum;
         }
         __syncthreads();
         const bool whole = WHOLE || steps == rounds;
         const int64_t row0 = (2 * static_cast<int64_t>(wg) + (step0 == 0)) * 16;
-        for (int at = tid; at < rows * D; at += 64 * kWaves) {
+        for (int at = 4 * tid; at < rows * D; at += 4 * 64 * kWaves) {
             const int r = at / D, d = at % D;
-            float top = -INFINITY, sum = 0.0f, y = 0.0f;
+            f32x4 y = *reinterpret_cast<const f32x4 *>(&part[0][r][d]);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                top = fmaxf(top, stat_m[w][r]);
-            const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                sum = fmaf(stat_l[w][r], __builtin_amdgcn_exp2f(stat_m[w][r] - base), sum);
-                y += part[w][r][d];
-            }
+            for (int w = 1; w < kWaves; ++w)
+                y += *reinterpret_cast<const f32x4 *>(&part[w][r][d]);
+            const float most = row_top[r], sum = row_sum[r];
             if (whole) {
-                write_row<T>(p, b, h0 + r, d, y, sum, base);
+                y *= sum == 0.0f ? 0.0f : 1.0f / sum;
+                *reinterpret_cast<u32x2_a2 *>(p.out + b * p.o_b + (h0 + r) * p.o_h + d) =
+                    u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+                if (d == 0)
+                    write_lse<T>(p, b, h0 + r, sum, most);
             } else {
-                p.part[(row0 + r) * D + d] = y;
+                *reinterpret_cast<f32x4 *>(p.part + (row0 + r) * D + d) = y;
                 if (d == 0) {
-                    p.stat[2 * (row0 + r)] = top;
+                    p.stat[2 * (row0 + r)] = most;
                     p.stat[2 * (row0 + r) + 1] = sum;
                 }
             }
@@ -509,9 +521,12 @@ __global__ void __launch_bounds__(64 * kJoinWaves) ssu_attn_join_kernel(const At
         for (int e = 0; e < E; ++e)
             y[e] += part[k][lane + 64 * e];
     }
+    const int h = kh * p.heads_per_kv + rt * 16 + r;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        write_row<T>(p, u.b, kh * p.heads_per_kv + rt * 16 + r, lane + 64 * e, y[e], sum, base);
+        p.out[u.b * p.o_b + h * p.o_h + lane + 64 * e] = T::round(sum == 0.0f ? 0.0f : y[e] / sum);
+    if (lane == 0)
+        write_lse<T>(p, u.b, h, sum, top);
 }
 
 using AttnFn = void (*)(AttnParams);
