@@ -744,8 +744,9 @@ struct Plan {
 // one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 82 us
 // cut, 129 uncut; 16 of 1024 tokens 90 and 70, but the host cannot tell them
 // apart; with twice the waves uncut is faster for both, 131 against 155 us and 86
-// against 126), and more than 256 tokens (256 tokens of one prompt: 23 us cut, 20
-// uncut). Then segments are as long as fills the chip once, 3072 waves (4096 in
+// against 126), and more than 256 tokens, or 64 of every sequence up to 1024 in
+// all (256 tokens of one prompt: 23 us cut, 20 uncut; 19 prompts of 1 to 86, 8
+// heads of 16 x 16: 11.0 and 7.0). Then segments are as long as fills the chip once, 3072 waves (4096 in
 // workgroups of eight, 2048 at N = 256), half a segment of every sequence but one lost,
 // but of 128 tokens at least and a 64th of all at most: one prompt of 4096 tokens
 // takes 38 us in segments of 128, 44 in segments of 256.
@@ -757,7 +758,7 @@ Plan plan_of(const ssu_linear_args &a)
     const int64_t units = static_cast<int64_t>(a.nheads) * p.slices * waves;
     const int64_t chunks = (a.ntokens + kChunk - 1) / kChunk;
     p.waves = a.batch * units;
-    const bool cuts = chunks > 8 && p.waves <= 4 * kNumCUs;
+    const bool cuts = chunks > std::max(8, std::min(a.batch, 16) * 2) && p.waves <= 4 * kNumCUs;
     const int64_t room = (a.dstate == 256 ? 8 : waves == 4 ? 12 : 16) * kNumCUs - (cuts ? (a.batch - 1) * units / 2 : 0);
     const int64_t per = std::max<int64_t>({(chunks * units + room - 1) / room, (chunks + 63) / 64, 4});
     const bool cut = cuts && per < chunks;
