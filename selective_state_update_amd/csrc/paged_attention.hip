@@ -21,7 +21,7 @@ constexpr int kJoinWaves = 4;  // of a workgroup of the join
 // Waves of a workgroup. D = 256 needs half the register file per wave: two
 // waves and two workgroups per CU instead of four and one keep one of them
 // loading while the other joins (64 requests up to 4096 tokens, 8 heads of 256:
-// 185 against 208 us).
+// 178 against 195 us).
 constexpr int waves_for(int D) { return D == 256 ? 2 : 4; }
 
 struct AttnParams {
@@ -85,8 +85,10 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, flo
 // Memory-bound: every visible K and V row is read once per 16 query heads, so
 // the loads decide, and the products are arranged for them:
 //
-//  - S^T = K Q^T with K's rows as they lie in memory: lane l reads 16 bytes of
-//    token l % 16, which is a fragment of the product; no LDS.
+//  - S^T = K Q^T. Whole rows of K are read, 1 KiB per load, and turned into the
+//    product's fragments (lane l: 16 bytes of token l % 16) through LDS, runs
+//    of a row swapped so that neither side has bank conflicts. Read as fragments, 64
+//    bytes of each of 16 rows per load, they came at 6.1 to 6.3 TB/s at best.
 //  - The result has one query head per lane column, so a row's statistics are
 //    one value per lane (plus two exchanges for the maximum), and the weights
 //    lie exactly as the second product's fragment wants them: the lane's 4
@@ -96,8 +98,8 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, flo
 //    for value c * D/16 + m, so a product's fragment is a transposition inside
 //    the lane (byte permutes), and the output comes back in runs of D/16.
 //
-// V is read past the caches (non-temporal); K is not, because one instruction
-// reads half a cache line of each row and the next the other half. Each wave
+// K and V are read past the caches (non-temporal; 64 requests of 1 to 1600 tokens 45.6
+// against 46.3 us, 3 of 100003 tokens 113 against 115, and 116 without LDS). Each wave
 // takes every fourth step of 32 tokens with statistics of its own. PAGE16:
 // pages are a multiple of 16 tokens, a tile lies in one page and its address
 // is uniform; otherwise every lane looks its own token up. WHOLE (short caches,
@@ -110,6 +112,9 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
     constexpr int KS = D / 32;      // products along D of a score
     constexpr int E = D / 16;       // values of a V row per lane, products of an output row
     constexpr int EW = E / 2;       // the same in words
+    constexpr int CH = D / 8;       // 16-byte runs of a K row
+    constexpr int RPI = 64 / CH;    // K rows that one load reads
+    constexpr int SW = CH < 16 ? CH - 1 : 15;
     using V = uint32_t __attribute__((ext_vector_type(EW)));
     typedef V V_a2 __attribute__((aligned(2)));
     __shared__ __attribute__((aligned(16))) float part[kWaves][16][D];
@@ -121,6 +126,8 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int units = p.nk * p.row_tiles;  // of a request
+    const int ch = lane % CH, ksub = lane / CH;
+    u32x4 *const kbuf = reinterpret_cast<u32x4 *>(&part[wave][0][0]);  // a step's K; sums only behind the last step
 
     // this workgroup's run of the line, and the request that it begins in: the
     // steps of one unit of every request, summed over them
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
             qf[i] = c < rows ? *reinterpret_cast<const u32x4_a2 *>(p.q + b * p.q_b + (h0 + c) * p.q_h + (i * 4 + g) * 8)
                              : u32x4{0, 0, 0, 0};
         const int32_t *const table = p.table + b * p.t_b;
-        const uint16_t *const kbase = p.k + kh * p.k_h + g * 8, *const vbase = p.v + kh * p.v_h + c * E;
+        const uint16_t *const kbase = p.k + kh * p.k_h + ch * 8, *const vbase = p.v + kh * p.v_h + c * E;
 
         // A tile of 16 tokens: its page id as the table has it (requested a step
         // before it is needed), then where it is and which of its tokens are
@@ -272,11 +279,13 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
             }
             return t;
         };
-        const uint16_t *const klane = kbase + (PAGE16 ? c * p.k_row : 0), *const vlane = vbase + (PAGE16 ? 4 * g * p.v_row : 0);
+        const uint16_t *const klane = kbase + (PAGE16 ? ksub * p.k_row : 0), *const vlane = vbase + (PAGE16 ? 4 * g * p.v_row : 0);
         auto load_k = [&](const Tile &t, u32x4 (&f)[KS]) {
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
-                f[i] = *reinterpret_cast<const u32x4_a2 *>(klane + t.k + i * 32);
+            for (int i = 0; i < KS; ++i) {
+                const int64_t row = PAGE16 ? t.k + i * RPI * p.k_row : __shfl(t.k, RPI * i + ksub);
+                f[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2 *>(klane + row));
+            }
         };
         auto load_v = [&](const Tile &t, V *f) {  // tokens 4g .. 4g+3
 #pragma unroll
@@ -318,6 +327,16 @@ __global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 s[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    kbuf[(u * 16 + RPI * i + ksub) * CH + (ch ^ ((RPI * i + ksub) & SW))] = kf[u][i];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // (the buffer is this wave's own)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    kf[u][i] = kbuf[(u * 16 + c) * CH + ((4 * i + g) ^ (c & SW))];
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
                     s[u] = Mma<T>::run(kf[u][i], qf[i], s[u]);
@@ -579,15 +598,15 @@ struct Plan {
 // per CU as fit, which load while others start and join (one request, 2 heads of
 // 128: 100 tokens 6.1 against 9.2 us, 400 tokens 9.0 against 10.3, 800 tokens 13.1
 // against 11.1; 32 requests of 1 to 1600 tokens, 8 heads: 26 against 34 us; 64
-// of 1 to 1600: 48 against 50; 64 of 1 to 8192: 218 against 184).
+// of 1 to 1600: 46 against 50; 64 of 1 to 8192: 218 against 184).
 //
 // Otherwise a line with two workgroups per CU; at D = 128 every second one leaves
 // (the kernel knows the lengths) where the runs' pieces of units have 16 steps or
 // more or are few: four waves' loads are enough then to fill the memory system, and
-// more only crowd it (64 requests up to 8192 tokens, 8 heads: 184 against 193 us with
-// two; 3 of 100003 tokens, 4 heads: 118 against 124; but 32 up to 6000 tokens, 8 heads:
-// 92 against 83, 64 up to 800 tokens in a wide table 44 against 34; D = 64, 64
-// requests up to 8192 tokens: 121 against 105). No more than there can be steps.
+// more only crowd it (3 requests of 100003 tokens, 4 heads: 113 against 115 us with
+// two; one of 100000, 8 heads: 75 against 78; 64 up to 8192: 179 against 181; but 32
+// up to 6000 tokens: 87 against 78, 64 up to 4500: 117 against 110; D = 64, 64 up to
+// 8192: 121 against 101). No more than there can be steps.
 Plan plan_of(const ssu_attn_args &a)
 {
     Plan p{};
