@@ -156,7 +156,7 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint3
 }
 
 // A double from other lanes by DPP (zero where the lane has no source or its
-// row is not in MASK), and the last lane's in all.
+// row is not in MASK), and one lane's in all.
 template <int CTRL, int MASK>
 __device__ __forceinline__ double lanes_up(double x)
 {
@@ -166,11 +166,11 @@ __device__ __forceinline__ double lanes_up(double x)
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-__device__ __forceinline__ double last_lane(double x)
+__device__ __forceinline__ double lane_of(double x, int lane)
 {
     const uint64_t v = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), 63);
-    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), 63);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane);
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
@@ -213,8 +213,10 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
     __shared__ __attribute__((aligned(16))) uint16_t lk[kChunk * ROW];
     __shared__ __attribute__((aligned(16))) uint16_t lv[kChunk * VROW];
     __shared__ u32x4 lw[FULL ? kTiles : 1][FULL ? kSteps : 1][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
-    __shared__ float lsum[2][kChunk], lrest[2][kChunk];  // L in units of log 2: as fp32, and what that leaves
-    __shared__ float lbeta[2][kChunk], lgrow[2][kChunk], llate[2][kChunk], lall[2];
+    // of THREADS tokens: L in units of log 2, as fp32 and what that leaves, and what follows from it
+    __shared__ __attribute__((aligned(16))) float lsum[THREADS], lrest[THREADS], lbeta[THREADS], lgrow[THREADS], llate[THREADS];
+    __shared__ float lall[THREADS / kChunk];
+    __shared__ double whole[W];  // the segment's log decay so far, of every wave's tokens
     __shared__ int bad[2];
     __shared__ int owner;         // this segment's sequence
     __shared__ int64_t found[3];  // its slot and rows
@@ -324,38 +326,33 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
         kt += kChunk * a.k_t;
         vt += kChunk * a.v_t;
     };
+    // L and what follows from it for as many tokens as the workgroup has threads:
+    // a wave has two chunks, and a chunk waits for its sums once in 2 W
     auto request_sums = [&](int t0) {  // (behind the segment's end: of its last token)
-        const int64_t t = begin + min(t0 + lane, rows - 1);
+        const int64_t t = begin + min(t0 + tid, rows - 1);
         rdecay = a.decay[t * a.d_t + h * a.d_h];
         rbeta = a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f;
     };
-    // L and what follows from it, by the last wave (which has no score tile), a
-    // chunk ahead of the others
-    double whole = 0.0;  // of the segment so far
-    auto sums = [&](int t0, int buf) {
-        const bool in = lane < kChunk && t0 + lane < rows;
+    auto sums = [&](int t0) {
+        const bool in = t0 + tid < rows;
         const float d = rdecay < kDecayFloor ? kDecayFloor : rdecay;  // (NaN stays)
         double sum = in ? static_cast<double>(d) * 1.4426950408889634 : 0.0;
         sum += lanes_up<0x111, 0xf>(sum);  // lane - 1, - 2, - 4, - 8 of each 16
         sum += lanes_up<0x112, 0xf>(sum);
         sum += lanes_up<0x114, 0xf>(sum);
         sum += lanes_up<0x118, 0xf>(sum);
-        sum += lanes_up<0x142, 0xa>(sum);  // the last of 16 to the next 16, of 32 to the next 32
-        sum += lanes_up<0x143, 0xc>(sum);
-        const double all = last_lane(sum);
+        sum += lanes_up<0x142, 0xa>(sum);  // the last of 16 to the next 16
+        const double first = lane_of(sum, 31), second = lane_of(sum, 63), all = lane < kChunk ? first : second;
         const float gain = in ? rbeta : 0.0f;
-        whole += all;
-        if (lane < kChunk) {
-            lsum[buf][lane] = static_cast<float>(sum);
-            lrest[buf][lane] = static_cast<float>(sum - static_cast<double>(static_cast<float>(sum)));
-            lbeta[buf][lane] = gain;
-            lgrow[buf][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum));
-            llate[buf][lane] = in ? gain * __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) : 0.0f;
-        }
-        if (lane == 0) {
-            lall[buf] = __builtin_amdgcn_exp2f(static_cast<float>(all));
-            bad[buf] = 0;
-        }
+        lsum[tid] = static_cast<float>(sum);
+        lrest[tid] = static_cast<float>(sum - static_cast<double>(static_cast<float>(sum)));
+        lbeta[tid] = gain;
+        lgrow[tid] = __builtin_amdgcn_exp2f(static_cast<float>(sum));
+        llate[tid] = in ? gain * __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) : 0.0f;
+        if (lane % kChunk == 0)
+            lall[tid / kChunk] = __builtin_amdgcn_exp2f(static_cast<float>(all));
+        if (!FULL && lane == 0)
+            whole[wave] = t0 == 0 ? first + second : whole[wave] + (first + second);
     };
     auto place = [&](int t0, int buf) {
         // zeros behind the segment's end, behind N (16 in a tile of 32) and behind P
@@ -403,8 +400,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
     };
 
     offsets(kChunk - 1);
-    if (wave == W - 1)
-        request_sums(0);
+    request_sums(0);
     request(0);
     // the state before the segment
 #pragma unroll
@@ -419,10 +415,10 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
         else
             load_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
     }
-    if (wave == W - 1) {
-        sums(0, 0);
-        request_sums(kChunk);
-    }
+    sums(0);
+    request_sums(THREADS);
+    if (tid == 0)
+        bad[0] = 0;
     __syncthreads();  // (bad is set by place)
     place(0, 0);
     __syncthreads();
@@ -432,13 +428,11 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
     for (int t0 = 0; t0 < rows; t0 += kChunk, buf ^= 1) {
         const int next = t0 + kChunk;
         const bool more = next < rows;
-        if (more) {
+        const int at0 = t0 % THREADS;  // of the chunk's sums
+        if (more)
             request(next);
-            if (wave == W - 1) {
-                sums(next, buf ^ 1);
-                request_sums(next + kChunk);
-            }
-        }
+        if (tid == 0)
+            bad[buf ^ 1] = 0;
 
         // v of the wave's columns as fragments: 8 tokens of 32 per lane
         const int tr = (4 * g + c / 4) * ROW + 4 * (c % 4), vtr = (4 * g + c / 4) * VROW + 4 * (c % 4) + wave * 16;
@@ -473,10 +467,10 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
                     for (int e = 0; e < AHEAD; ++e)
                         x = Mma<Bf16>::run(kf[e], qf[e], x);
                 }
-                const float li = lsum[buf][16 * it + c], ri = lrest[buf][16 * it + c];
-                const f32x4 lj = *reinterpret_cast<const f32x4 *>(&lsum[buf][16 * jt + 4 * g]);
-                const f32x4 rj = *reinterpret_cast<const f32x4 *>(&lrest[buf][16 * jt + 4 * g]);
-                const f32x4 bj = *reinterpret_cast<const f32x4 *>(&lbeta[buf][16 * jt + 4 * g]);
+                const float li = lsum[at0 + 16 * it + c], ri = lrest[at0 + 16 * it + c];
+                const f32x4 lj = *reinterpret_cast<const f32x4 *>(&lsum[at0 + 16 * jt + 4 * g]);
+                const f32x4 rj = *reinterpret_cast<const f32x4 *>(&lrest[at0 + 16 * jt + 4 * g]);
+                const f32x4 bj = *reinterpret_cast<const f32x4 *>(&lbeta[at0 + 16 * jt + 4 * g]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float y = x[r] * (bj[r] * __builtin_amdgcn_exp2f((li - lj[r]) + (ri - rj[r])));
@@ -524,7 +518,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
             }
 #pragma unroll
             for (int it = 0; it < kTiles; ++it)
-                o[it] *= lgrow[buf][16 * it + c];
+                o[it] *= lgrow[at0 + 16 * it + c];
             __syncthreads();  // the scores are there
             if (!__builtin_amdgcn_readfirstlane(bad[buf])) {
 #pragma unroll
@@ -560,15 +554,15 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
         }
 
         // the state behind the chunk
-        const float all = lall[buf];
+        const float all = lall[at0 / kChunk];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             st[m] *= all;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             u32x4 f1, f2, f3;
-            const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 4 * g]);
-            const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[buf][32 * s + 16 + 4 * g]);
+            const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[at0 + 32 * s + 4 * g]);
+            const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[at0 + 32 * s + 16 + 4 * g]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const f32x4 &late = e < 2 ? late0 : late1;
@@ -598,6 +592,10 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
         }
         if (more) {
             __syncthreads();  // LDS is free again
+            if (next % THREADS == 0) {
+                sums(next);
+                request_sums(next + THREADS);
+            }
             place(next, buf ^ 1);
             __syncthreads();
         }
@@ -608,8 +606,13 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
             store_state(pool, a.s_row);
     } else {
         store_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
-        if (slice == 0 && tid == THREADS - 64)  // (of the wave that summed)
-            p.decays[static_cast<int64_t>(f) * a.nheads + h] = __builtin_amdgcn_exp2f(static_cast<float>(whole));
+        if (slice == 0 && tid == 0) {
+            double log_decay = whole[0];
+#pragma unroll
+            for (int w = 1; w < W; ++w)
+                log_decay += whole[w];
+            p.decays[static_cast<int64_t>(f) * a.nheads + h] = __builtin_amdgcn_exp2f(static_cast<float>(log_decay));
+        }
     }
 }
 
@@ -726,7 +729,7 @@ ssu_status check_sizes(const ssu_linear_args &a, const char *who)
         return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d is not a multiple of 16 in 16 .. 256", who, a.headdim);
     if (a.dstate != 16 && a.dstate != 32 && a.dstate != 64 && a.dstate != 128 && a.dstate != 256)
         return fail(SSU_ERR_UNSUPPORTED, "%s: dstate %d is not 16, 32, 64, 128 or 256", who, a.dstate);
-    if (a.ntokens > 0x7fffffbf)  // (a segment and two chunks count in 32 bits)
+    if (a.ntokens > 0x7ffff000)  // (a segment and two workgroups' tokens count in 32 bits)
         return fail(SSU_ERR_UNSUPPORTED, "%s: more than 2^31 tokens", who);
     if ((a.ntokens / kChunk + a.batch + 8) * a.nheads > 0x7fffffff / (a.headdim / 16))
         return fail(SSU_ERR_UNSUPPORTED, "%s: batch * nheads too large", who);
