@@ -43,9 +43,10 @@ __device__ __forceinline__ float weight_at(const void *w, int is32, int i)
 
 // One wave per head row (a token's query, key and, with a cache, value heads),
 // lane l holding elements l, l + 64, ... and, for the rotation, their pairs'
-// other elements. Any headdim and rotation width: it takes those that the kernel
-// below does not (4096 tokens of 32 + 8 heads of 128, rot 34: 75 us, four times
-// that kernel's time).
+// other elements. Any headdim and rotation width: it takes the headdims that the
+// kernel below does not, and few rows of a width that is no multiple of 8 (16 tokens
+// of 32 + 8 heads of 128 into a cache, rot 94: 4.2 against 5.2 us; 128 tokens 5.8
+// against 5.5, 4096 tokens 119 against 41).
 template <typename T>
 __global__ void __launch_bounds__(256) ssu_qk_rows_kernel(const QkParams p)
 {
@@ -124,54 +125,109 @@ __global__ void __launch_bounds__(256) ssu_qk_rows_kernel(const QkParams p)
 
 constexpr int kRows = 4;  // heads of a token per group of lanes
 
-// Four weights from element i on.
-template <typename T>
-__device__ __forceinline__ f32x4 weights_at(const void *w, int is32, int i)
+// Which elements of a row a lane has, as two runs of up to four.
+enum class Runs {
+    halves,       // both elements of pairs (i, i + rot/2); rot a multiple of 8
+    halves_edge,  // the same, any rot
+    inter,        // pairs (2i, 2i + 1); rot a multiple of 8
+    inter_edge,   // the same, any rot
+};
+
+// n elements of a row of d from `at` on, zeros behind them. EDGE: n < 4 or none;
+// the four elements read lie in the row.
+template <bool EDGE, bool STREAM>
+__device__ __forceinline__ u32x2 load_run(const uint16_t *row, int at, int n, int d)
 {
-    if (!w)
-        return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
-    if (is32)
-        return *reinterpret_cast<const f32x4_a4 *>(static_cast<const float *>(w) + i);
-    const u32x2 x = *reinterpret_cast<const u32x2_a2 *>(static_cast<const uint16_t *>(w) + i);
-    return f32x4{T::lo(x[0]), T::hi(x[0]), T::lo(x[1]), T::hi(x[1])};
+    const int from = EDGE ? min(at, d - 4) : at;
+    const u32x2_a2 *const p = reinterpret_cast<const u32x2_a2 *>(row + from);
+    u32x2 x;
+    if constexpr (STREAM)
+        x = __builtin_nontemporal_load(p);
+    else
+        x = *p;
+    if constexpr (EDGE) {
+        const uint64_t y = (static_cast<uint64_t>(x[1]) << 32 | x[0]) >> 16 * min(at - from, 3);
+        const uint64_t kept = n <= 0 ? 0 : ~uint64_t(0) >> 16 * (4 - min(n, 4));
+        x = u32x2{static_cast<uint32_t>(y & kept), static_cast<uint32_t>((y & kept) >> 32)};
+    }
+    return x;
 }
 
-// A lane's two runs of four elements of a row, at p + at and p + at2.
-template <bool SIDE>
-__device__ __forceinline__ u32x4 load_runs(const uint16_t *p, int at, int at2)
+template <bool EDGE>
+__device__ __forceinline__ void store_run(uint16_t *p, int n, uint32_t x, uint32_t y)
 {
-    if constexpr (SIDE) {
+    if (!EDGE || n == 4) {
+        __builtin_nontemporal_store(u32x2{x, y}, reinterpret_cast<u32x2_a2 *>(p));
+        return;
+    }
+    if (n > 0)
+        p[0] = static_cast<uint16_t>(x);
+    if (n > 1)
+        p[1] = static_cast<uint16_t>(x >> 16);
+    if (n > 2)
+        p[2] = static_cast<uint16_t>(y);
+}
+
+// A lane's two runs of a row.
+template <Runs RUNS>
+__device__ __forceinline__ u32x4 load_runs(const uint16_t *p, int at, int n, int at2, int n2, int d)
+{
+    if constexpr (RUNS == Runs::inter || RUNS == Runs::inter_edge) {
         return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2 *>(p + at));
     } else {
-        const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a2 *>(p + at));
-        const u32x2 y = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a2 *>(p + at2));
+        constexpr bool EDGE = RUNS == Runs::halves_edge;
+        const u32x2 x = load_run<EDGE, true>(p, at, n, d), y = load_run<EDGE, true>(p, at2, n2, d);
         return u32x4{x[0], x[1], y[0], y[1]};
     }
 }
 
-template <bool SIDE>
-__device__ __forceinline__ void store_runs(uint16_t *p, int at, int at2, u32x4 v)
+template <Runs RUNS>
+__device__ __forceinline__ void store_runs(uint16_t *p, int at, int n, int at2, int n2, u32x4 v)
 {
-    if constexpr (SIDE) {
+    if constexpr (RUNS == Runs::inter || RUNS == Runs::inter_edge) {
         __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2 *>(p + at));
     } else {
-        __builtin_nontemporal_store(u32x2{v[0], v[1]}, reinterpret_cast<u32x2_a2 *>(p + at));
-        __builtin_nontemporal_store(u32x2{v[2], v[3]}, reinterpret_cast<u32x2_a2 *>(p + at2));
+        store_run<RUNS == Runs::halves_edge>(p + at, n, v[0], v[1]);
+        store_run<RUNS == Runs::halves_edge>(p + at2, n2, v[2], v[3]);
     }
 }
 
-// Rows of 16-byte runs: headdim and rot multiples of 8. LANES lanes take one
-// head row, a lane 8 of its elements as two runs of 4: both elements of 4 pairs
-// (runs at 4 l and rot / 2 + 4 l, or 8 consecutive elements when interleaved),
-// or 8 elements behind the rotated part. So nothing is exchanged but the sum
-// of squares. A group of lanes takes kRows heads of one token, all q, all k or
-// all v, with the weights and the token's cosines and sines read once and the
-// rows' loads on their way together: memory-bound, each element is read and
-// written once, past the caches (16384 tokens of 32 + 8 heads of 128: 60 us, 5.6
-// TB/s; with cached accesses 69 us).
-template <typename T, bool INTER, int LANES>
+// Four values from element i on; PART: the last of `count` for what lies behind it.
+template <bool PART>
+__device__ __forceinline__ f32x4 load_floats(const float *p, int i, int count)
+{
+    if constexpr (PART)
+        return f32x4{p[min(i, count - 1)], p[min(i + 1, count - 1)], p[min(i + 2, count - 1)], p[min(i + 3, count - 1)]};
+    else
+        return *reinterpret_cast<const f32x4_a4 *>(p + i);
+}
+
+// The weights of a run.
+template <typename T, bool EDGE>
+__device__ __forceinline__ f32x4 weights_at(const void *w, int is32, int i, int n, int d)
+{
+    if (!w)
+        return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+    if (is32)
+        return load_floats<EDGE>(static_cast<const float *>(w), i, d);
+    const u32x2 x = load_run<EDGE, false>(static_cast<const uint16_t *>(w), i, n, d);
+    return f32x4{T::lo(x[0]), T::hi(x[0]), T::lo(x[1]), T::hi(x[1])};
+}
+
+// Rows of 16-byte runs: headdim a multiple of 8. LANES lanes take one head row, a
+// lane 8 of its elements as two runs of 4: both elements of 4 pairs (runs at 4 l and
+// rot / 2 + 4 l, or 8 consecutive elements when interleaved), or 8 elements behind the
+// rotated part; at the end of either part fewer (halves_edge). So nothing is
+// exchanged but the sum of squares. A group of lanes takes kRows heads of one token,
+// all q, all k or all v, with the weights and the token's cosines and sines read once
+// and the rows' loads on their way together: memory-bound, each element is read and
+// written once, past the caches (16384 tokens of 32 + 8 heads of 128: 60 us, 5.6 TB/s;
+// with cached accesses 69 us).
+template <typename T, Runs RUNS, int LANES>
 __global__ void __launch_bounds__(256) ssu_qk_groups_kernel(const QkParams p)
 {
+    constexpr bool INTER = RUNS == Runs::inter || RUNS == Runs::inter_edge, EDGE = RUNS == Runs::halves_edge;
+    constexpr bool PART = EDGE || RUNS == Runs::inter_edge;  // a lane may have fewer than four pairs
     const uint32_t group = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
     const int l = static_cast<int>(threadIdx.x) % LANES;
     const uint32_t t = group / static_cast<uint32_t>(p.groups_per_token);
@@ -187,13 +243,16 @@ __global__ void __launch_bounds__(256) ssu_qk_groups_kernel(const QkParams p)
     const uint16_t *x = is_q ? p.q + t * p.q_t + h0 * p.q_h : is_v ? p.v + t * p.v_t + h0 * p.v_h : p.k + t * p.k_t + h0 * p.k_h;
     const int64_t x_h = is_q ? p.q_h : is_v ? p.v_h : p.k_h;
 
-    const int half = p.rot / 2;
-    const bool in = 8 * l < p.headdim, turned = 8 * l < p.rot;
-    const int at = INTER || !turned ? 8 * l : 4 * l, at2 = INTER || !turned ? 8 * l + 4 : half + 4 * l;
+    const int half = p.rot / 2, pairs = (half + 3) / 4;  // lanes with pairs in halves
+    const bool turned = EDGE ? l < pairs : 8 * l < p.rot;
+    const int at = INTER || (!EDGE && !turned) ? 8 * l : turned ? 4 * l : p.rot + 8 * (l - pairs);
+    const int at2 = !INTER && turned ? half + 4 * l : at + 4;
+    const int n = EDGE && turned ? min(half - at, 4) : min(p.headdim - at, 4), n2 = EDGE && turned ? n : min(p.headdim - at2, 4);
+    const bool in = EDGE ? n > 0 : 8 * l < p.headdim;
     u32x4 v[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        v[i] = in && i < heads ? load_runs<INTER>(x + i * x_h, at, at2) : u32x4{0, 0, 0, 0};
+        v[i] = in && i < heads ? load_runs<RUNS>(x + i * x_h, at, n, at2, n2, p.headdim) : u32x4{0, 0, 0, 0};
 
     uint16_t *cache = nullptr;
     int64_t c_h = 0;
@@ -211,15 +270,16 @@ __global__ void __launch_bounds__(256) ssu_qk_groups_kernel(const QkParams p)
     if (!is_v) {
         const void *const w = is_q ? p.q_weight : p.k_weight;
         const int w32 = is_q ? p.qw32 : p.kw32;
-        f32x4 wa = {0.0f, 0.0f, 0.0f, 0.0f}, wb = wa, c = {1.0f, 1.0f, 1.0f, 1.0f}, s = wa;
+        f32x4 wa = {0.0f, 0.0f, 0.0f, 0.0f}, wb = wa, c = wa, s = wa;
         if (in) {
-            wa = weights_at<T>(w, w32, at);
-            wb = weights_at<T>(w, w32, at2);
+            wa = weights_at<T, EDGE>(w, w32, at, n, p.headdim);
+            wb = weights_at<T, EDGE>(w, w32, at2, n2, p.headdim);
         }
+        const int m = half - 4 * l;  // this lane's pairs, from 4 l on, or more
         if (turned) {
-            const float *const cs = p.cos_sin + pos * p.cs_row + 4 * l;
-            c = *reinterpret_cast<const f32x4_a4 *>(cs);
-            s = *reinterpret_cast<const f32x4_a4 *>(cs + half);
+            const float *const cs = p.cos_sin + pos * p.cs_row;
+            c = load_floats<PART>(cs, 4 * l, half);
+            s = load_floats<PART>(cs + half, 4 * l, half);
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -242,14 +302,17 @@ __global__ void __launch_bounds__(256) ssu_qk_groups_kernel(const QkParams p)
                 a[e] *= wa[e] * scale;
                 b[e] *= wb[e] * scale;
             }
-            // the pairs: (a[e], b[e]), or neighbours when interleaved
+            // the pairs: (a[e], b[e]), or neighbours when interleaved; the others are
+            // left out, since a zero sine would carry infinities over
+            if (turned) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float &first = INTER ? (e < 2 ? a[2 * e % 4] : b[2 * e % 4]) : a[e];
-                float &second = INTER ? (e < 2 ? a[2 * e % 4 + 1] : b[2 * e % 4 + 1]) : b[e];
-                const float u = first * c[e] - second * s[e];
-                second = second * c[e] + first * s[e];
-                first = u;
+                for (int e = 0; e < 4; ++e) {
+                    float &first = INTER ? (e < 2 ? a[2 * e % 4] : b[2 * e % 4]) : a[e];
+                    float &second = INTER ? (e < 2 ? a[2 * e % 4 + 1] : b[2 * e % 4 + 1]) : b[e];
+                    const float u = first * c[e] - second * s[e], w = second * c[e] + first * s[e];
+                    first = !PART || e < m ? u : first;
+                    second = !PART || e < m ? w : second;
+                }
             }
             v[i] = u32x4{pack2<T>(a[0], a[1]), pack2<T>(a[2], a[3]), pack2<T>(b[0], b[1]), pack2<T>(b[2], b[3])};
         }
@@ -258,32 +321,34 @@ __global__ void __launch_bounds__(256) ssu_qk_groups_kernel(const QkParams p)
     for (int i = 0; i < kRows; ++i)
         if (in && i < heads) {
             if (out)
-                store_runs<INTER>(out + i * o_h, at, at2, v[i]);
+                store_runs<RUNS>(out + i * o_h, at, n, at2, n2, v[i]);
             if (cache)
-                store_runs<INTER>(cache + i * c_h, at, at2, v[i]);
+                store_runs<RUNS>(cache + i * c_h, at, n, at2, n2, v[i]);
         }
 }
 
 using QkFn = void (*)(QkParams);
 
-template <typename T, bool INTER>
+template <typename T, Runs RUNS>
 QkFn groups_kernel(int lanes)
 {
     switch (lanes) {
-    case 1: return &ssu_qk_groups_kernel<T, INTER, 1>;
-    case 2: return &ssu_qk_groups_kernel<T, INTER, 2>;
-    case 4: return &ssu_qk_groups_kernel<T, INTER, 4>;
-    case 8: return &ssu_qk_groups_kernel<T, INTER, 8>;
-    case 16: return &ssu_qk_groups_kernel<T, INTER, 16>;
-    case 32: return &ssu_qk_groups_kernel<T, INTER, 32>;
-    default: return &ssu_qk_groups_kernel<T, INTER, 64>;
+    case 1: return &ssu_qk_groups_kernel<T, RUNS, 1>;
+    case 2: return &ssu_qk_groups_kernel<T, RUNS, 2>;
+    case 4: return &ssu_qk_groups_kernel<T, RUNS, 4>;
+    case 8: return &ssu_qk_groups_kernel<T, RUNS, 8>;
+    case 16: return &ssu_qk_groups_kernel<T, RUNS, 16>;
+    case 32: return &ssu_qk_groups_kernel<T, RUNS, 32>;
+    default: return &ssu_qk_groups_kernel<T, RUNS, 64>;
     }
 }
 
-QkFn groups_kernel(bool bf16, bool inter, int lanes)
+template <typename T>
+QkFn groups_kernel(Runs runs, int lanes)
 {
-    return bf16 ? (inter ? groups_kernel<Bf16, true>(lanes) : groups_kernel<Bf16, false>(lanes))
-                : (inter ? groups_kernel<F16, true>(lanes) : groups_kernel<F16, false>(lanes));
+    return runs == Runs::inter ? groups_kernel<T, Runs::inter>(lanes)
+         : runs == Runs::inter_edge ? groups_kernel<T, Runs::inter_edge>(lanes)
+         : runs == Runs::halves ? groups_kernel<T, Runs::halves>(lanes) : groups_kernel<T, Runs::halves_edge>(lanes);
 }
 
 // ------------------------------------------------------------------ host --
@@ -428,11 +493,15 @@ extern "C" ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stre
     p.groups_per_token = p.q_groups + p.k_groups * (p.k_cache ? 2 : 1);
     const int64_t groups = a.ntokens * p.groups_per_token;
     hipError_t e;
-    if (a.headdim % 8 == 0 && a.rot % 8 == 0 && groups <= 0x7fffffff) {
-        int lanes = 1;
-        while (lanes * 8 < a.headdim)
-            lanes *= 2;
-        e = launch_kernel(groups_kernel(bf16, a.interleaved, lanes), p, (groups * lanes + 255) / 256, 256, 0, stream);
+    const Runs runs = a.rot % 8 == 0 ? (a.interleaved ? Runs::inter : Runs::halves) : a.interleaved ? Runs::inter_edge : Runs::halves_edge;
+    const int need = runs == Runs::halves_edge ? (a.rot / 2 + 3) / 4 + (a.headdim - a.rot + 7) / 8 : (a.headdim + 7) / 8;
+    int lanes = 1;
+    while (lanes < need)
+        lanes *= 2;
+    const bool few = a.rot % 8 != 0 && p.total <= 2048;  // (the kernel of single rows starts sooner)
+    if (a.headdim % 8 == 0 && lanes <= 64 && groups <= 0x7fffffff && !few) {
+        e = launch_kernel(bf16 ? groups_kernel<Bf16>(runs, lanes) : groups_kernel<F16>(runs, lanes), p,
+                          (groups * lanes + 255) / 256, 256, 0, stream);
     } else {
         e = launch_kernel(bf16 ? &ssu_qk_rows_kernel<Bf16> : &ssu_qk_rows_kernel<F16>, p, (p.total + 3) / 4, 256, 0, stream);
     }

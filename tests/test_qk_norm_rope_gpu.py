@@ -81,6 +81,33 @@ def test_shapes(ssu, dtype, inter, D, rot):
     Case(5, 6, 2, D, rot, dtype, inter, seed=D + rot).check(ssu)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,D", [(3, 64), (45, 8), (45, 16), (45, 64), (45, 80), (45, 128), (45, 256), (45, 512)])
+def test_rotation_widths(ssu, T, D, inter):
+    """Every width's last pairs and what lies behind them; nothing beside the rows is written."""
+    for rot in sorted({2, 4, 6, 10, 22, 50, D // 2 - 2, D // 2 + 2, D - 6, D - 4, D - 2}):
+        if not 0 < rot <= D:
+            continue
+        c = Case(T, 40, 4, D, rot, BF16, inter, page=2, seed=D + rot, gap=1, weights="fp32" if rot % 4 else "same")
+        wide = torch.full((T, 40, D + 3), 9.0, dtype=BF16, device="cuda")
+        c.check(ssu, q_out=wide[..., 1:D + 1])
+        assert (wide[..., 0] == 9.0).all() and (wide[..., D + 1:] == 9.0).all(), rot
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 22), (64, 32), (66, 30)])
+def test_infinity_behind_the_rotated_part(ssu, D, rot, inter):
+    """It makes its own row's norm infinite: every other element is 0, its own NaN."""
+    c = Case(80, 24, 4, D, rot, inter=inter, seed=3)
+    c.q[1, 1, D - 2] = float("inf")
+    q, _ = c.run(ssu)
+    want = torch.zeros(D, device="cuda")
+    want[D - 2] = float("nan")
+    assert torch.equal(q[1, 1].isnan(), want.isnan()) and (q[1, 1].nan_to_num() == 0).all()
+    q[1, 1] = 0
+    assert q.isfinite().all()
+
+
 @pytest.mark.parametrize("page", [1, 16, 17])
 @pytest.mark.parametrize("T", [1, 2, 33, 257])
 def test_cache(ssu, T, page):
