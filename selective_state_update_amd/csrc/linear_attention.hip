@@ -744,15 +744,16 @@ struct Plan {
 };
 
 // Sequences are cut where whole ones would leave most of the chip idle: at most
-// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 82 us
-// cut, 129 uncut; 16 of 1024 tokens 90 and 70, but the host cannot tell them
-// apart; with twice the waves uncut is faster for both, 131 against 155 us and 86
+// one wave per SIMD (16 prompts of 1 to 2048 tokens, 16 heads of 64 x 128: 81 us
+// cut, 129 uncut; 16 of 1024 tokens 89 and 70, but the host cannot tell them
+// apart; with twice the waves uncut is faster for both, 131 against 155 us and 85
 // against 126), and more than 256 tokens, or 64 of every sequence up to 1024 in
 // all (256 tokens of one prompt: 23 us cut, 20 uncut; 19 prompts of 1 to 86, 8
-// heads of 16 x 16: 11.0 and 7.0). Then segments are as long as fills the chip once, 3072 waves (4096 in
-// workgroups of eight, 2048 at N = 256), half a segment of every sequence but one lost,
-// but of 128 tokens at least and a 64th of all at most: one prompt of 4096 tokens
-// takes 38 us in segments of 128, 44 in segments of 256.
+// heads of 16 x 16: 11.0 and 7.0). Then segments are as long as fills the chip
+// once, with three waves per SIMD (four in workgroups of eight, two at N = 256),
+// half a segment of every sequence but one lost, but of 128 tokens at least and a
+// 64th of all at most: one prompt of 4096 tokens takes 38 us in segments of 128,
+// 44 in segments of 256.
 Plan plan_of(const ssu_linear_args &a)
 {
     Plan p{};
