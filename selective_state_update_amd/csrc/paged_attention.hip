@@ -24,6 +24,9 @@ constexpr int kJoinWaves = 4;  // of a workgroup of the join
 // 178 against 195 us).
 constexpr int waves_for(int D) { return D == 256 ? 2 : 4; }
 
+// Tokens of a step of a workgroup of so many waves.
+constexpr int round_of(int waves) { return waves * kTile; }
+
 struct AttnParams {
     const uint16_t *q, *k, *v;
     int64_t q_b, q_h, k_page, k_row, k_h, v_page, v_row, v_h;
@@ -104,11 +107,11 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, flo
 // pages are a multiple of 16 tokens, a tile lies in one page and its address
 // is uniform; otherwise every lane looks its own token up. WHOLE (short caches,
 // see plan_of): no line, a workgroup per unit, nothing to join behind it.
-template <typename T, int D, bool PAGE16, bool WHOLE>
-__global__ void __launch_bounds__(64 * waves_for(D), D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
+template <typename T, int D, bool PAGE16, bool WHOLE, int W>
+__global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kernel(const AttnParams p)
 {
-    constexpr int kWaves = waves_for(D);
-    constexpr int kRound = kWaves * kTile;  // tokens of one workgroup's step
+    constexpr int kWaves = W;
+    constexpr int kRound = round_of(W);
     constexpr int KS = D / 32;      // products along D of a score
     constexpr int E = D / 16;       // values of a V row per lane, products of an output row
     constexpr int EW = E / 2;       // the same in words
@@ -551,21 +554,25 @@ __global__ void __launch_bounds__(64 * kJoinWaves) ssu_attn_join_kernel(const At
 using AttnFn = void (*)(AttnParams);
 
 struct AttnKernels {
-    AttnFn split, join, whole;
+    AttnFn split, join;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool WHOLE, int W>
 AttnKernels attn_kernels(bool page16)
 {
-    return {page16 ? &ssu_attn_split_kernel<T, D, true, false> : &ssu_attn_split_kernel<T, D, false, false>,
-            &ssu_attn_join_kernel<T, D>,
-            page16 ? &ssu_attn_split_kernel<T, D, true, true> : &ssu_attn_split_kernel<T, D, false, true>};
+    return {page16 ? &ssu_attn_split_kernel<T, D, true, WHOLE, W> : &ssu_attn_split_kernel<T, D, false, WHOLE, W>,
+            &ssu_attn_join_kernel<T, D>};
 }
 
 template <typename T>
-AttnKernels attn_kernels(int D, bool page16)
+AttnKernels attn_kernels(int D, bool page16, bool whole, int waves)
 {
-    return D == 64 ? attn_kernels<T, 64>(page16) : D == 128 ? attn_kernels<T, 128>(page16) : attn_kernels<T, 256>(page16);
+    if (!whole)
+        return D == 64 ? attn_kernels<T, 64, false, waves_for(64)>(page16)
+             : D == 128 ? attn_kernels<T, 128, false, waves_for(128)>(page16) : attn_kernels<T, 256, false, waves_for(256)>(page16);
+    return D == 64 ? attn_kernels<T, 64, true, 4>(page16)
+         : D == 128 ? attn_kernels<T, 128, true, 4>(page16)
+         : waves == 4 ? attn_kernels<T, 256, true, 4>(page16) : attn_kernels<T, 256, true, 2>(page16);
 }
 
 // ------------------------------------------------------------------ host --
@@ -581,24 +588,26 @@ ssu_status check_sizes(const ssu_attn_args &a, const char *who)
         return fail(SSU_ERR_UNSUPPORTED, "%s: headdim %d is not 64, 128 or 256", who, a.headdim);
     if (static_cast<int64_t>(a.batch) * a.nq > 0x7fffffff)
         return fail(SSU_ERR_UNSUPPORTED, "%s: batch * nq %lld too large", who, static_cast<long long>(a.batch) * a.nq);
-    if (a.max_pages > INT64_MAX / a.page_size)
+    if (a.max_pages > (INT64_MAX >> 1) / a.page_size)
         return fail(SSU_ERR_INVALID_ARGUMENT, "%s: max_pages * page_size too large", who);
     return SSU_OK;
 }
 
 struct Plan {
-    int row_tiles, groups;
+    int row_tiles, groups, waves;
     bool whole;  // a workgroup per unit, no workspace
     int64_t part_at, stat_at, bytes;  // workspace
 };
 
-// A workgroup of its own per unit where no unit has more than four steps (512
-// tokens, 256 at D = 256), or no more than 16 and there is at least one unit for
-// every CU: no line to lay out, no partial sums, one launch, and as many workgroups
-// per CU as fit, which load while others start and join (one request, 2 heads of
-// 128: 100 tokens 6.1 against 9.2 us, 400 tokens 9.0 against 10.3, 800 tokens 13.1
-// against 11.1; 32 requests of 1 to 1600 tokens, 8 heads: 26 against 34 us; 64
-// of 1 to 1600: 46 against 50; 64 of 1 to 8192: 218 against 184).
+// A workgroup of its own per unit where no unit has more than 512 tokens (256 at D =
+// 256), or no more than 16 steps and there is at least one unit for every CU: no line
+// to lay out, no partial sums, one launch, and as many workgroups per CU as fit,
+// which load while others start and join (one request, 2 heads of 128: 100 tokens 6.1
+// against 9.2 us, 400 tokens 9.0 against 10.3, 800 tokens 13.1 against 11.1; 32
+// requests of 1 to 1600 tokens, 8 heads: 26 against 34 us; 64 of 1 to 1600: 46
+// against 50; 64 of 1 to 8192: 218 against 184). At D = 256 with four waves while
+// each has a CU to itself (32 requests of 1 to 1600 tokens, 8 heads: 52 us, 62 in a line;
+// 64 of 1 to 200: 23 us with four waves, 18 with two).
 //
 // Otherwise a line with two workgroups per CU; at D = 128 every second one leaves
 // (the kernel knows the lengths) where the runs' pieces of units have 16 steps or
@@ -612,13 +621,15 @@ Plan plan_of(const ssu_attn_args &a)
     Plan p{};
     p.row_tiles = (a.nq / a.nk + 15) / 16;
     const int64_t units = static_cast<int64_t>(a.batch) * a.nk * p.row_tiles;
-    const int round = waves_for(a.headdim) * kTile;
-    const int64_t rounds = std::max<int64_t>((a.max_pages * a.page_size + round - 1) / round, 1);
-    p.whole = rounds <= (units < kNumCUs ? 4 : 16);
+    const int64_t tokens = a.max_pages * a.page_size;
+    p.waves = a.headdim == 256 && units > kNumCUs ? 2 : 4;
+    p.whole = tokens <= (units < kNumCUs ? (a.headdim == 256 ? 256 : 512) : 16 * round_of(p.waves));
     if (p.whole) {
         p.groups = static_cast<int>(units);
         return p;
     }
+    p.waves = waves_for(a.headdim);
+    const int64_t rounds = (tokens + round_of(p.waves) - 1) / round_of(p.waves);
     const int64_t resident = 2 * kNumCUs;
     p.groups = static_cast<int>(units > resident / rounds ? resident : std::max<int64_t>(units * rounds, 1));
     p.part_at = static_cast<int64_t>(p.groups) * sizeof(Open);
@@ -729,10 +740,11 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     p.part = reinterpret_cast<float *>(ws + plan.part_at);
     p.stat = reinterpret_cast<float *>(ws + plan.stat_at);
     const bool page16 = a.page_size % 16 == 0;
-    const AttnKernels k = a.q.dtype == SSU_BF16 ? attn_kernels<Bf16>(a.headdim, page16) : attn_kernels<F16>(a.headdim, page16);
+    const AttnKernels k = a.q.dtype == SSU_BF16 ? attn_kernels<Bf16>(a.headdim, page16, plan.whole, plan.waves)
+                                                : attn_kernels<F16>(a.headdim, page16, plan.whole, plan.waves);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
-    hipError_t e = launch_kernel(plan.whole ? k.whole : k.split, p, plan.groups, 64 * waves_for(a.headdim), 0, stream);
+    hipError_t e = launch_kernel(k.split, p, plan.groups, 64 * plan.waves, 0, stream);
     if (e == hipSuccess && !plan.whole && plan.groups > 1)
         e = launch_kernel(k.join, p, plan.groups * std::min(p.heads_per_kv, 16), 64 * kJoinWaves, 0, stream);
     if (e != hipSuccess)

@@ -236,7 +236,7 @@ def test_short_limits(ssu, D, tokens, page):
     """On both sides of the longest cache that a workgroup takes alone, with few units and with many."""
     for n in (tokens - 1, tokens, tokens + 1):
         Case([n, 3, 0, n // 2 + 1], 6, 3, D, page, seed=n, spare=0).check(ssu)
-    for batch, n in ((127, tokens + 1), (128, tokens + 1), (128, 4 * tokens), (128, 4 * tokens + 1)):
+    for batch, n in ((127, tokens + 1), (128, tokens + 1), (128, 2048), (128, 2049), (129, 1024), (129, 1025)):
         Case([n] + [1 + 37 * i % 40 for i in range(1, batch)], 2, 2, D, page, seed=batch, spare=0).check(ssu)
 
 

@@ -228,7 +228,8 @@ def test_attention_workspace(lib):
     assert need(max_pages=16, headdim=256) == 0 and need(max_pages=17, headdim=256) > 0
     assert need(max_pages=33, batch=127) > 0 and need(max_pages=33, batch=128) == 0  # two units a request
     assert need(max_pages=128, batch=128) == 0 and need(max_pages=129, batch=128) > 0
-    assert need(max_pages=64, batch=128, headdim=256) == 0 and need(max_pages=65, batch=128, headdim=256) > 0
+    assert need(max_pages=128, batch=128, headdim=256) == 0 and need(max_pages=129, batch=128, headdim=256) > 0
+    assert need(max_pages=64, batch=129, headdim=256) == 0 and need(max_pages=65, batch=129, headdim=256) > 0
     assert need(max_pages=0) == 0 and need(nk=0) == -1
 
 
