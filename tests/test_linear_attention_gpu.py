@@ -100,6 +100,15 @@ def test_prompt_long(ssu):
     Case([5000], 1, 64, 128, 1, seed=12, rate=0.05, beta=False).check(ssu)
 
 
+@pytest.mark.parametrize("lens,H,P,N", [
+    ([700, 300] + [5] * 10, 32, 16, 32),       # whole sequences past the tokens that one round of decay sums covers
+    ([600, 40, 1, 0, 3], 32, 128, 128),        # the same in workgroups of eight waves
+    ([3 + 7 * i % 40 for i in range(130)], 6, 64, 128),  # more workgroups than three waves per SIMD hold
+    ([1500], 2, 128, 128), ([1500, 100], 3, 96, 256), ([1200], 2, 48, 16)])  # cut into segments
+def test_prompt_launch_shapes(ssu, lens, H, P, N):
+    Case(lens, H, P, N, 1, seed=len(lens) + N).check(ssu)
+
+
 def test_prompt_unaligned_views(ssu):
     """Odd row pitches and offsets: elements aligned to their size alone."""
     c = Case([50, 81], 3, 32, 64, 1, seed=21, gap=3)

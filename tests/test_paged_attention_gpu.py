@@ -258,6 +258,18 @@ def test_two_streams(ssu):
         seq_ref.assert_close(lse, w["lse"], w["lse_tol"], "lse")
 
 
+@pytest.mark.parametrize("batch", [3, 70])
+def test_only_padding(ssu, batch):
+    c = Case([20] * batch, 4, 2, 64, 16, seed=26)
+    c.lens.fill_(-1)
+    out = torch.full(c.q.shape, 7.0, dtype=BF16, device="cuda")
+    c.run(ssu, out=out)
+    assert (out == 7.0).all()
+    c.lens[batch - 1] = 20  # one request behind all the padding
+    c.check(ssu, out=out)
+    assert (out[:batch - 1] == 7.0).all()
+
+
 def test_no_requests(ssu):
     c = Case([], 4, 2, 64, 16, seed=20)
     assert c.run(ssu)[0].shape == (0, 4, 64)
