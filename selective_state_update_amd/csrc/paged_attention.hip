@@ -42,13 +42,14 @@ struct AttnParams {
     struct Open *open;
     float *part, *stat;
     int32_t batch, nq, nk, heads_per_kv, row_tiles, page_size, groups;
+    int32_t cuts, cuts_half;  // runs of a unit's line, with all workgroups or one per CU; 0: too many would be left over
     float scale_log2;  // scale * log2(e): weights are powers of 2
 };
 
 // A unit (request, key/value head, 16 query heads) whose first steps a
 // workgroup did and whose last ones workgroup `last` does; b < 0: none.
 struct Open {
-    int32_t b, unit, last, reserved;
+    int32_t b, unit, last, stride;  // (every stride-th workgroup up to `last`)
 };
 
 // The visible tokens of a request (negative: padding) and its steps; a request
@@ -84,6 +85,12 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, flo
 // short ones all fill the chip with one set of resident workgroups. A unit
 // that lies across two or more runs is joined by the second kernel; a
 // workgroup leaves at most two of its units unfinished, its first and its last.
+//
+// With four steps or more for a workgroup (D of 128 and 256), and where hardly one is
+// left over, there is a line for each unit of a request instead, all cut alike: the
+// workgroups of a run read the same tokens' heads, which lie beside each other, at
+// about the same time (64 requests up to 8192 tokens, 8 heads of 128: 175 against 181
+// us; one of 100000: 71 against 76; D = 64, 64 up to 8192: 105 against 100).
 //
 // Memory-bound: every visible K and V row is read once per 16 query heads, so
 // the loads decide, and the products are arranged for them:
@@ -135,18 +142,32 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
     // this workgroup's run of the line, and the request that it begins in: the
     // steps of one unit of every request, summed over them
     int64_t per, pos, stop, n, before;  // (before: a unit's steps of all earlier requests)
-    int b;
+    int b, lanes = 1, line = units, unit = -1, run = wg;  // lines; units of a request in one; the line's unit
     auto run_of = [&](int64_t steps) {
         const int64_t total = steps * units;
         const int64_t all = static_cast<int64_t>(p.batch) * units;  // of the batch
         const bool half = D == 128 && p.groups > kNumCUs && (all <= kNumCUs / 8 || total >= 16 * (kNumCUs + all));
         // (no more than steps: those with work are spread over all XCDs)
         const int groups = static_cast<int>(min(static_cast<int64_t>(half ? kNumCUs : p.groups), max(total, int64_t(1))));
-        per = (total + groups - 1) / groups;
-        if (wg < groups)
-            wg = xcd_order(wg, groups);
-        pos = wg * per;
-        stop = wg < groups ? min(pos + per, total) : 0;
+        int runs = groups;
+        int64_t length = total;
+        bool in = wg < groups;
+        const int cuts = half ? p.cuts_half : p.cuts;
+        if (D > 64 && cuts > 0 && total >= 4 * groups) {
+            asm volatile("");  // (a branch, not its divisions ahead of it)
+            lanes = units;
+            line = 1;
+            length = steps;
+            runs = cuts;
+            run = wg / units;
+            unit = wg - run * units;
+            in = run < runs;
+        } else if (in) {
+            run = wg = xcd_order(wg, groups);
+        }
+        per = (length + runs - 1) / runs;
+        pos = run * per;
+        stop = in ? min(pos + per, length) : 0;
         if (tid == 0)
             p.open[wg] = Open{-1, 0, 0, 0};
     };
@@ -164,7 +185,7 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
         run_of(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(sum), 63)));
         if (pos >= stop)
             return;
-        const uint64_t mine = __ballot(static_cast<int64_t>(sum - own) * units <= pos && pos < static_cast<int64_t>(sum) * units);
+        const uint64_t mine = __ballot(static_cast<int64_t>(sum - own) * line <= pos && pos < static_cast<int64_t>(sum) * line);
         b = static_cast<int>(__builtin_ctzll(mine));
         n = __builtin_amdgcn_readlane(static_cast<int>(own_n), b);
         before = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(sum - own), b));
@@ -205,12 +226,12 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
                 first += w < wave ? scan[w] : 0;
                 before += scan[w];
             }
-            if (first * units <= pos && pos < (first + own) * units) {
+            if (first * line <= pos && pos < (first + own) * line) {
                 found[0] = i;
                 found[1] = first;
                 found[2] = own_n;
             }
-            if (before * units > pos)
+            if (before * line > pos)
                 break;
         }
         __syncthreads();
@@ -219,8 +240,15 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
         n = found[2];
     }
     int64_t rounds = rounds_of(n, kRound);
-    int unit = WHOLE ? wg % units : static_cast<int>((pos - before * units) / rounds);
-    int64_t step0 = WHOLE ? 0 : pos - before * units - unit * rounds;  // of the unit, where this workgroup begins
+    int64_t step0 = 0;  // of the unit, where this workgroup begins
+    if constexpr (WHOLE) {
+        unit = wg % units;
+    } else if (unit < 0) {
+        unit = static_cast<int>((pos - before * units) / rounds);
+        step0 = pos - before * units - unit * rounds;
+    } else {
+        step0 = pos - before;
+    }
 
     for (;;) {
         const int64_t steps = min(rounds - step0, stop - pos);
@@ -473,15 +501,15 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
             }
         }
         if (!whole && step0 == 0 && tid == 0)
-            p.open[wg] = Open{b, unit, static_cast<int32_t>((pos + rounds - 1) / per), 0};
+            p.open[wg] = Open{b, unit, wg + (static_cast<int32_t>((pos + rounds - 1) / per) - run) * lanes, lanes};
 
         // the next unit
         pos += steps;
         if (WHOLE || pos >= stop)
             return;
         step0 = 0;
-        if (++unit == units) {
-            unit = 0;
+        if (lanes > 1 || ++unit == units) {
+            unit = lanes > 1 ? unit : 0;
             do
                 n = visible(p, ++b);
             while (n < 0);  // (pos < stop: there is one)
@@ -512,7 +540,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) ssu_attn_join_kernel(const At
     // this workgroup's last unit, then the first ones of those up to u.last
     auto row_of = [&](int w) { return (2 * static_cast<int64_t>(w) + (w == wg)) * 16 + r; };
     float top = -INFINITY;
-    for (int w = wg + lane; w <= u.last; w += 64)
+    for (int w = wg + lane * u.stride; w <= u.last; w += 64 * u.stride)
         top = fmaxf(top, p.stat[2 * row_of(w)]);
 #pragma unroll
     for (int m = 32; m >= 1; m /= 2)
@@ -520,7 +548,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) ssu_attn_join_kernel(const At
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, y[E] = {};
 #pragma unroll 8
-    for (int w = wg + wave; w <= u.last; w += kJoinWaves) {
+    for (int w = wg + wave * u.stride; w <= u.last; w += kJoinWaves * u.stride) {
         const int64_t row = row_of(w);
         const float f = __builtin_amdgcn_exp2f(p.stat[2 * row] - base);
         sum = fmaf(p.stat[2 * row + 1], f, sum);
@@ -734,6 +762,9 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     p.page_size = a.page_size;
     p.row_tiles = plan.row_tiles;
     p.groups = plan.groups;
+    const auto cuts = [units = a.nk * plan.row_tiles](int groups) { return groups % units * 16 <= groups ? groups / units : 0; };
+    p.cuts = cuts(plan.groups);
+    p.cuts_half = cuts(kNumCUs);
     p.scale_log2 = log2_scale(a);
     char *const ws = static_cast<char *>(a.workspace);
     p.open = reinterpret_cast<Open *>(ws);
