@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
     auto run_of = [&](int64_t steps) {
         const int64_t total = steps * units;
         const int64_t all = static_cast<int64_t>(p.batch) * units;  // of the batch
-        const bool half = D == 128 && p.groups > kNumCUs && (all <= kNumCUs / 8 || total >= 16 * (kNumCUs + all));
+        const bool half = D == 128 && p.groups > kNumCUs && (all <= kNumCUs / 8 || total >= 6 * (kNumCUs + all));
         // (no more than steps: those with work are spread over all XCDs)
         const int groups = static_cast<int>(min(static_cast<int64_t>(half ? kNumCUs : p.groups), max(total, int64_t(1))));
         int runs = groups;
@@ -638,12 +638,12 @@ struct Plan {
 // 64 of 1 to 200: 23 us with four waves, 18 with two).
 //
 // Otherwise a line with two workgroups per CU; at D = 128 every second one leaves
-// (the kernel knows the lengths) where the runs' pieces of units have 16 steps or
-// more or are few: four waves' loads are enough then to fill the memory system, and
-// more only crowd it (3 requests of 100003 tokens, 4 heads: 113 against 115 us with
-// two; one of 100000, 8 heads: 75 against 78; 64 up to 8192: 179 against 181; but 32
-// up to 6000 tokens: 87 against 78, 64 up to 4500: 117 against 110; D = 64, 64 up to
-// 8192: 121 against 101). No more than there can be steps.
+// (the kernel knows the lengths) where the runs' pieces of units have 6 steps or more
+// or are few: four waves' loads are enough then to fill the memory system, and more
+// only crowd it (64 requests up to 8192 tokens, 8 heads: 174 against 180 us with two;
+// 64 up to 4500: 104 against 110; one of 100000: 71 against 76; but in a table for 16384
+// tokens 64 up to 800: 36 against 34, 256 up to 400: 76 against 67; D = 64, 64 up to
+// 8192: 121 against 100). No more than there can be steps.
 Plan plan_of(const ssu_attn_args &a)
 {
     Plan p{};
