@@ -240,10 +240,13 @@ def test_short_limits(ssu, D, tokens, page):
         Case([n] + [1 + 37 * i % 40 for i in range(1, batch)], 2, 2, D, page, seed=batch, spare=0).check(ssu)
 
 
-@pytest.mark.parametrize("lens,nk", [([9000] * 3, 11), ([9000] * 2, 16), ([7000, 9000, 8000, 9500, 100], 8)])
-def test_runs_of_one_and_two_workgroups(ssu, lens, nk):
-    """Lines that every second workgroup leaves (few units, long pieces) and that all share."""
-    Case(lens, nk, nk, 128, 64, seed=nk).check(ssu)
+@pytest.mark.parametrize("lens,nk,D", [
+    ([9000] * 3, 11, 128), ([9000] * 2, 16, 128), ([7000, 9000, 8000, 9500, 100], 8, 128),
+    ([1000 + i % 7 for i in range(66)], 2, 256),  # a line per head, more requests than a wave has lanes
+    ([2900], 100, 128)])                          # too many heads for that
+def test_long_lines(ssu, lens, nk, D):
+    """Lines that every second workgroup leaves and that all share, of all heads and of each."""
+    Case(lens, nk, nk, D, 64, seed=nk).check(ssu)
 
 
 def test_two_streams(ssu):
