@@ -110,7 +110,7 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, flo
 //
 // K and V are read past the caches (non-temporal; 64 requests of 1 to 1600 tokens 45.6
 // against 46.3 us, 3 of 100003 tokens 113 against 115, and 116 without LDS). Each wave
-// takes every fourth step of 32 tokens with statistics of its own. PAGE16:
+// takes every W-th step of 32 tokens with statistics of its own. PAGE16:
 // pages are a multiple of 16 tokens, a tile lies in one page and its address
 // is uniform; otherwise every lane looks its own token up. WHOLE (short caches,
 // see plan_of): no line, a workgroup per unit, nothing to join behind it.

@@ -332,8 +332,10 @@ using QkFn = void (*)(QkParams);
 template <typename T, Runs RUNS>
 QkFn groups_kernel(int lanes)
 {
+    if constexpr (RUNS != Runs::halves_edge)  // (a lane for each part at least)
+        if (lanes == 1)
+            return &ssu_qk_groups_kernel<T, RUNS, 1>;
     switch (lanes) {
-    case 1: return &ssu_qk_groups_kernel<T, RUNS, 1>;
     case 2: return &ssu_qk_groups_kernel<T, RUNS, 2>;
     case 4: return &ssu_qk_groups_kernel<T, RUNS, 4>;
     case 8: return &ssu_qk_groups_kernel<T, RUNS, 8>;
