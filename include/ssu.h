@@ -477,7 +477,10 @@ ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stream);
  * Tokens of a page id outside [0, num_pages) are not visible. fp32 scores, statistics and sums; the
  * weights w_j enter the product with V as a 16-bit pair (value and
  * remainder), so that only the output's own rounding is seen. What the cache
- * holds in rows that no request sees, NaN and infinities too, does not matter.
+ * holds in rows that no request sees, NaN and infinities too, does not matter;
+ * infinities in rows of V that one sees give what the formula gives: an infinity,
+ * or NaN where both signs meet or the score is -inf (a weight of 0). A wave that
+ * meets one, or a NaN, reads its tokens again one by one, which takes longer.
  * The batch's other lengths and max_pages set where a request is split, and so
  * change its result within rounding; the same call gives the same bits.
  */

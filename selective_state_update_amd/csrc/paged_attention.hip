@@ -72,6 +72,14 @@ constexpr float kShift = 0.0f;
 template <>
 constexpr float kShift<F16> = 14.0f;
 
+// What a partial sum with maximum `own` is multiplied by under the maximum `top`:
+// positive wherever the sum's weights are, so that infinities in it stay (2^-126 of
+// a finite sum is nothing beside the largest weight's).
+__device__ __forceinline__ float rescale(float own, float top)
+{
+    return __builtin_amdgcn_exp2f(fmaxf(own - (top == -INFINITY ? 0.0f : top), own == -INFINITY ? own : -126.0f));
+}
+
 template <typename T>
 __device__ __forceinline__ void write_lse(const AttnParams &p, int b, int h, float sum, float top)
 {
@@ -442,6 +450,52 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
             load_v(tile[1], vf + 4);
         }
 
+        // An infinity in V, times a weight's remainder or a weight that 16 bits round to
+        // 0, is not what the formula has: such a wave's sums are taken again with whole
+        // weights, token by token (the check costs a call 0.2 to 1 us).
+        f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                zero[i] = fmaf(o[e][i], 0.0f, zero[i]);
+        if (__any((zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+            for (int64_t j = sh.begin + wave * kTile; j < sh.end; j += (j + 1) % kTile ? 1 : 1 + kRound - kTile) {
+                const int at = static_cast<int>(j), col = at / p.page_size, off = at - col * p.page_size;
+                const int64_t page = table[col];
+                if (page < 0 || page >= p.num_pages)
+                    continue;
+                const uint16_t *const kr = p.k + page * p.k_page + off * p.k_row + kh * p.k_h;
+                const uint16_t *const qr = p.q + b * p.q_b + (h0 + min(c, rows - 1)) * p.q_h;
+                float s = 0.0f;  // of query head c, this lane's quarter of D
+#pragma unroll 1
+                for (int d = g * (D / 4); d < (g + 1) * (D / 4); d += 8) {
+                    const u32x4 kw = *reinterpret_cast<const u32x4_a2 *>(kr + d), qw = *reinterpret_cast<const u32x4_a2 *>(qr + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s = fmaf(T::hi(kw[i]), T::hi(qw[i]), fmaf(T::lo(kw[i]), T::lo(qw[i]), s));
+                }
+                s += __shfl_xor(s, 16);
+                s += __shfl_xor(s, 32);
+                s *= p.scale_log2;
+                float w = __builtin_amdgcn_exp2f(s - base + kShift<T>);
+                w = s > -INFINITY && w == 0.0f ? 0x1p-126f : w;
+                const V x = *reinterpret_cast<const V_a2 *>(p.v + page * p.v_page + off * p.v_row + kh * p.v_h + c * E);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float wi = __shfl(w, 4 * g + i);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        o[e][i] = fmaf(wi, e % 2 ? T::hi(x[e / 2]) : T::lo(x[e / 2]), o[e][i]);
+                }
+            }
+        }
+
         // join the waves
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
@@ -450,15 +504,14 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
             stat_l[wave][c] = l;
         }
         __syncthreads();
-        f32x4 top = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, base, own;  // of rows 4g .. 4g+3
+        f32x4 top = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, own;  // of rows 4g .. 4g+3
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
             top = __builtin_elementwise_max(top, *reinterpret_cast<const f32x4 *>(&stat_m[w][4 * g]));
         own = *reinterpret_cast<const f32x4 *>(&stat_m[wave][4 * g]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            base[i] = top[i] == -INFINITY ? 0.0f : top[i];
-            const float f = __builtin_amdgcn_exp2f(own[i] - base[i]);
+            const float f = rescale(own[i], top[i]);
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 part[wave][4 * g + i][c * E + e] = o[e][i] * f;
@@ -471,7 +524,7 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
                 const f32x4 y = *reinterpret_cast<const f32x4 *>(&stat_l[w][4 * g]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[i] = fmaf(y[i], __builtin_amdgcn_exp2f(x[i] - base[i]), sum[i]);
+                    sum[i] = fmaf(y[i], rescale(x[i], top[i]), sum[i]);
             }
             *reinterpret_cast<f32x4 *>(&row_top[4 * g]) = top;
             *reinterpret_cast<f32x4 *>(&row_sum[4 * g]) = sum;
@@ -545,12 +598,11 @@ __global__ void __launch_bounds__(64 * kJoinWaves) ssu_attn_join_kernel(const At
 #pragma unroll
     for (int m = 32; m >= 1; m /= 2)
         top = fmaxf(top, __shfl_xor(top, m));
-    const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, y[E] = {};
 #pragma unroll 8
     for (int w = wg + wave * u.stride; w <= u.last; w += kJoinWaves * u.stride) {
         const int64_t row = row_of(w);
-        const float f = __builtin_amdgcn_exp2f(p.stat[2 * row] - base);
+        const float f = rescale(p.stat[2 * row], top);
         sum = fmaf(p.stat[2 * row + 1], f, sum);
 #pragma unroll
         for (int e = 0; e < E; ++e)
