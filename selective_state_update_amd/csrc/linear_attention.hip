@@ -145,7 +145,7 @@ constexpr float kDecayFloor = -1.0e4f;  // exp is 0 far above it; sums of it sta
 struct ChunkParams {
     LinearParams a;
     float *states;  // [segments, nheads, headdim, dstate]
-    float *decays;  // [segments, nheads]: a segment's whole decay
+    float *decays;  // [segments, nheads]: a segment's whole decay, log2 of it
     int32_t seg_len, segments, slices, dstate, total, pad;
 };
 
@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
     __shared__ __attribute__((aligned(16))) float lsum[THREADS], lrest[THREADS], lbeta[THREADS], lgrow[THREADS], llate[THREADS];
     __shared__ float lall[THREADS / kChunk];
     __shared__ double whole[W];  // the segment's log decay so far, of every wave's tokens
-    __shared__ int bad[2];
     __shared__ int owner;         // this segment's sequence
     __shared__ int64_t found[3];  // its slot and rows
 
@@ -354,7 +353,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
         if (!FULL && lane == 0)
             whole[wave] = t0 == 0 ? first + second : whole[wave] + (first + second);
     };
-    auto place = [&](int t0, int buf) {
+    auto place = [&](int t0) {
         // zeros behind the segment's end, behind N (16 in a tile of 32) and behind P
         const bool cut = t0 + kChunk > rows || p.dstate < N || slice * PC + PC > a.headdim;
         if (cut) {
@@ -383,56 +382,44 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
                 *reinterpret_cast<u32x4 *>(lq + at) = rq[i];
             *reinterpret_cast<u32x4 *>(lk + at) = rk[i];
         }
-        using H2 = uint16_t __attribute__((ext_vector_type(2)));
-        H2 most = {0, 0};  // an infinity or NaN has the largest exponent
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
             const int u = tid + THREADS * i;
             *reinterpret_cast<u32x4 *>(lv + u / (PC / 8) * VROW + u % (PC / 8) * 8) = rv[i];
-            if constexpr (FULL)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    most = __builtin_elementwise_max(most, __builtin_bit_cast(H2, rv[i][e] & 0x7fff7fffu));
         }
-        if constexpr (FULL)
-            if (most.x >= 0x7f80 || most.y >= 0x7f80)
-                bad[buf] = 1;
     };
 
     offsets(kChunk - 1);
     request_sums(0);
     request(0);
-    // the state before the segment
+    auto start = [&] {  // the state before the segment
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-        st[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int m = 0; m < MT; ++m)
+            st[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (FULL) {
+            if (segs == 1)
+                load_state(pool, a.s_row);
+            else
+                load_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
+        }
+    };
+    start();
     if constexpr (FULL)  // (the tiles above the diagonal stay zero)
         for (int i = tid; i < kTiles * kSteps * 2 * 64; i += THREADS)
             (&lw[0][0][0][0])[i] = u32x4{0, 0, 0, 0};
-    if constexpr (FULL) {
-        if (segs == 1)
-            load_state(pool, a.s_row);
-        else
-            load_state(p.states + (static_cast<int64_t>(f) * a.nheads + h) * plane, p.dstate);
-    }
     sums(0);
     request_sums(THREADS);
-    if (tid == 0)
-        bad[0] = 0;
-    __syncthreads();  // (bad is set by place)
-    place(0, 0);
+    place(0);
     __syncthreads();
 
-    int buf = 0;
+    float zero = 0.0f;  // or NaN: an output was not finite
     uint16_t *out = a.out + begin * a.o_t + h * a.o_h + p0;
-    for (int t0 = 0; t0 < rows; t0 += kChunk, buf ^= 1) {
+    for (int t0 = 0; t0 < rows; t0 += kChunk) {
         const int next = t0 + kChunk;
         const bool more = next < rows;
         const int at0 = t0 % THREADS;  // of the chunk's sums
         if (more)
             request(next);
-        if (tid == 0)
-            bad[buf ^ 1] = 0;
 
         // v of the wave's columns as fragments: 8 tokens of 32 per lane
         const int tr = (4 * g + c / 4) * ROW + 4 * (c % 4), vtr = (4 * g + c / 4) * VROW + 4 * (c % 4) + wave * 16;
@@ -520,28 +507,18 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
             for (int it = 0; it < kTiles; ++it)
                 o[it] *= lgrow[at0 + 16 * it + c];
             __syncthreads();  // the scores are there
-            if (!__builtin_amdgcn_readfirstlane(bad[buf])) {
 #pragma unroll
-                for (int it = 0; it < kTiles; ++it)
+            for (int it = 0; it < kTiles; ++it)
 #pragma unroll
-                    for (int s = 0; s <= it / 2; ++s) {
-                        o[it] = Mma<Bf16>::run(vf[s], lw[it][s][0][lane], o[it]);
-                        o[it] = Mma<Bf16>::run(vf[s], lw[it][s][1][lane], o[it]);
-                    }
-            } else {
-                // v holds infinities or NaN: a product would carry them, times the
-                // zeros of the scores, to the tokens before; sum token by token
+                for (int s = 0; s <= it / 2; ++s) {
+                    o[it] = Mma<Bf16>::run(vf[s], lw[it][s][0][lane], o[it]);
+                    o[it] = Mma<Bf16>::run(vf[s], lw[it][s][1][lane], o[it]);
+                }
 #pragma unroll
-                for (int it = 0; it < kTiles; ++it)
-                    for (int j = 0; j <= 16 * it + c; ++j) {
-                        const uint16_t *const at = reinterpret_cast<const uint16_t *>(&lw[it][j / 32][0][16 * (j % 16 / 4) + c]) +
-                                                   4 * (j % 32 / 16) + j % 4;
-                        const float x = Bf16::lo(at[0]) + Bf16::lo(at[64 * 8]);
+            for (int it = 0; it < kTiles; ++it)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            o[it][r] = fmaf(x, Bf16::lo(lv[j * VROW + wave * 16 + 4 * g + r]), o[it][r]);
-                    }
-            }
+                for (int r = 0; r < 4; ++r)
+                    zero = fmaf(o[it][r], 0.0f, zero);
             if (live) {
 #pragma unroll
                 for (int it = 0; it < kTiles; ++it)
@@ -596,8 +573,46 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
                 sums(next);
                 request_sums(next + THREADS);
             }
-            place(next, buf ^ 1);
+            place(next);
             __syncthreads();
+        }
+    }
+
+    // Not finite: the pieces in 16 bits make NaN of infinities, a zero times the growth
+    // of a chunk that fp32 does not hold is one too, and NaN stays. Then the segment
+    // goes through the recurrence again, token by token, as in the kernel of steps
+    // (finite data pays for the checks less than a measurement shows; a NaN in one of 16
+    // prompts of 1 to 2048 tokens makes 81 us 1.5 ms).
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            zero = fmaf(st[m][e], 0.0f, zero);
+    if (live && __any(zero != 0.0f)) {
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "agent");  // (behind this wave's own outputs)
+        start();
+#pragma unroll 1
+        for (int64_t t = begin; t < begin + rows; ++t) {
+            const float keep = exp_f32(a.decay[t * a.d_t + h * a.d_h]);
+            const float x = (a.beta ? a.beta[t * a.b_t + h * a.b_h] : 1.0f) * Bf16::lo(a.v[t * a.v_t + h * a.v_h + prow]);
+            const uint16_t *const kr = a.k + t * a.k_t + grp * a.k_g + 4 * g, *const qr = a.q + t * a.q_t + grp * a.q_g + 4 * g;
+            float y = 0.0f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                if (16 * m < p.dstate) {
+                    const u32x2 kw = *reinterpret_cast<const u32x2_a2 *>(kr + 16 * m), qw = *reinterpret_cast<const u32x2_a2 *>(qr + 16 * m);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        st[m][e] = fmaf(st[m][e], keep, x * (e % 2 ? Bf16::hi(kw[e / 2]) : Bf16::lo(kw[e / 2])));
+                        y = fmaf(st[m][e], e % 2 ? Bf16::hi(qw[e / 2]) : Bf16::lo(qw[e / 2]), y);
+                    }
+                }
+            if constexpr (FULL) {
+                y += __shfl_xor(y, 16);
+                y += __shfl_xor(y, 32);
+                if (g == 0)
+                    a.out[t * a.o_t + h * a.o_h + prow] = Bf16::round(a.scale * y);
+            }
         }
     }
 
@@ -611,7 +626,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
 #pragma unroll
             for (int w = 1; w < W; ++w)
                 log_decay += whole[w];
-            p.decays[static_cast<int64_t>(f) * a.nheads + h] = __builtin_amdgcn_exp2f(static_cast<float>(log_decay));
+            p.decays[static_cast<int64_t>(f) * a.nheads + h] = static_cast<float>(log_decay);
         }
     }
 }
@@ -644,12 +659,36 @@ __global__ void __launch_bounds__(256) ssu_linear_segments_kernel(const ChunkPar
                 x[u] = *reinterpret_cast<const f32x4 *>(at + u * step);
                 d[u] = decay[static_cast<int64_t>(t + u) * a.nheads];
             }
+        const f32x4 s0 = s;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u < segs)
                 *reinterpret_cast<f32x4 *>(at + u * step) = s;
             if (t + u < segs - 1)
-                s = s * d[u] + x[u];
+                s = s * __builtin_amdgcn_exp2f(d[u]) + x[u];
+        }
+        // Not finite (and so it stays): a decay over a whole segment may have left fp32
+        // where the tokens' own, one after the other, leave an infinity infinite, a zero
+        // 0 and a tiny value finite.
+        if (__builtin_expect(!__builtin_isfinite((s[0] + s[1]) + (s[2] + s[3])), 0)) {
+            s = s0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u < segs)
+                    *reinterpret_cast<f32x4 *>(at + u * step) = s;
+                if (t + u < segs - 1) {
+                    bool reset = false;  // (a token's own decay is 0)
+                    const int64_t r0 = lo + static_cast<int64_t>(t + u) * p.seg_len;
+                    for (int r = 0; r < p.seg_len; ++r)
+                        reset |= exp_f32(a.decay[(r0 + r) * a.d_t + h * a.d_h]) == 0.0f;
+                    const float whole = __builtin_amdgcn_exp2f(d[u]), half = __builtin_amdgcn_exp2f(0.5f * d[u]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float kept = __builtin_isinf(s[e]) ? s[e] * (reset ? 0.0f : 1.0f) : whole < INFINITY ? s[e] * whole : s[e] * half * half;
+                        s[e] = s[e] == 0.0f ? x[u][e] : kept + x[u][e];
+                    }
+                }
+            }
         }
         at += U * step;
     }
