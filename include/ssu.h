@@ -410,7 +410,7 @@ int64_t ssu_linear_attention_workspace(const ssu_linear_args *args);
  * negative sizes or strides, wrong dtype tags, non-zero reserved fields, G not
  * dividing H, a scale that is not finite, a workspace too small),
  * SSU_ERR_UNSUPPORTED (P, N, inner strides, token strides of q, k, v and out of 2^24
- * elements or more, more than 2^31 tokens or workgroups),
+ * elements or more, more than 2^31 tokens, 2^32 threads of a launch or more),
  * SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
 ssu_status ssu_linear_attention(const ssu_linear_args *args, hipStream_t stream);
 
@@ -462,7 +462,7 @@ typedef struct ssu_qk_args {
  * q_out may be q and k_out may be k (same pointer and strides). Asynchronous,
  * allocation-free, graph-capturable. Errors (nothing is launched):
  * SSU_ERR_INVALID_ARGUMENT (null pointers, sizes, strides, dtype tags),
- * SSU_ERR_UNSUPPORTED (D > 512, inner strides, more than 2^31 workgroups),
+ * SSU_ERR_UNSUPPORTED (D > 512, inner strides, 2^32 threads of a launch or more),
  * SSU_ERR_MISALIGNED (elements not aligned to their size), SSU_ERR_HIP. */
 ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stream);
 
@@ -519,8 +519,8 @@ int64_t ssu_paged_attention_workspace(const ssu_attn_args *args);
  * same time need workspaces of their own. Asynchronous, allocation-free,
  * graph-capturable. Errors (nothing is launched):
  * SSU_ERR_INVALID_ARGUMENT (null pointers, sizes, strides, dtype tags, a
- * workspace too small), SSU_ERR_UNSUPPORTED (D, inner strides, more than 2^31
- * workgroups), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
+ * workspace too small), SSU_ERR_UNSUPPORTED (D, inner strides, 2^32 threads
+ * of a launch or more), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
 ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream);
 
 /* SSU_ABI_VERSION of the built library. */

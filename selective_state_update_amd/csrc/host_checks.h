@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cstdint>
 #include <initializer_list>
 
 #include "internal.h"
@@ -45,6 +46,15 @@ inline ssu_status check_written(const ssu_view &v, const char *name, std::initia
             return fail(SSU_ERR_INVALID_ARGUMENT, "%s: written with stride[%d] = 0", name, i);
         ++i;
     }
+    return SSU_OK;
+}
+
+// A launch counts its threads in 32 bits.
+inline ssu_status check_launch(int64_t groups, int threads, const char *who)
+{
+    if (groups > UINT32_MAX / threads)
+        return fail(SSU_ERR_UNSUPPORTED, "%s: %lld workgroups of %d threads, 2^32 threads or more", who,
+                    static_cast<long long>(groups), threads);
     return SSU_OK;
 }
 

@@ -909,13 +909,15 @@ LinearParams linear_params(const ssu_linear_args &a)
 // 96.0 uncapped, 91.9 at 12, 89.0 at 16; 32 MiB: 13.5 us uncapped, 14.0 at 16).
 ssu_status launch_step(const ssu_linear_args &a, hipStream_t stream)
 {
-    DeviceGuard guard;
-    SSU_TRY(guard.enter(a.device));
     const int64_t mib = static_cast<int64_t>(a.batch) * a.nheads * a.headdim * a.dstate >> 18;
     const StepKernel k = mib < 8 ? step_kernel<2>(a.dstate) : step_kernel<4>(a.dstate);
     LinearParams p = linear_params(a);
     p.tiles = (a.headdim + k.rows - 1) / k.rows;
-    p.total = a.batch * a.nheads * p.tiles;
+    const int64_t groups = static_cast<int64_t>(a.batch) * a.nheads * p.tiles;
+    SSU_TRY(check_launch(groups, 64, "ssu_linear_attention_step"));
+    p.total = static_cast<int>(groups);
+    DeviceGuard guard;
+    SSU_TRY(guard.enter(a.device));
     size_t lds = 0;
     if (mib >= 40) {
         int dev = 0;
@@ -949,7 +951,9 @@ ssu_status launch_chunks(const ssu_linear_args &a, hipStream_t stream)
     p.segments = plan.segments;
     p.slices = plan.slices;
     p.dstate = a.dstate;
-    p.total = (plan.segments + 7) / 8 * 8 * a.nheads * plan.slices;
+    const int64_t groups = (static_cast<int64_t>(plan.segments) + 7) / 8 * 8 * a.nheads * plan.slices;
+    SSU_TRY(check_launch(groups, 4 * k.columns, "ssu_linear_attention"));
+    p.total = static_cast<int>(groups);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     hipError_t e = hipSuccess;

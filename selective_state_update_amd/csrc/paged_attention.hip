@@ -825,6 +825,7 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     const bool page16 = a.page_size % 16 == 0;
     const AttnKernels k = a.q.dtype == SSU_BF16 ? attn_kernels<Bf16>(a.headdim, page16, plan.whole, plan.waves)
                                                 : attn_kernels<F16>(a.headdim, page16, plan.whole, plan.waves);
+    SSU_TRY(check_launch(plan.groups, 64 * plan.waves, "ssu_paged_attention"));
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     hipError_t e = launch_kernel(k.split, p, plan.groups, 64 * plan.waves, 0, stream);

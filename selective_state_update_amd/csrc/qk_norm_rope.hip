@@ -478,35 +478,35 @@ extern "C" ssu_status ssu_qk_norm_rope(const ssu_qk_args *args, hipStream_t stre
     p.num_slots = p.k_cache ? a.num_pages * a.page_size : 0;
     p.nq = a.nq;
     p.nk = a.nk;
-    p.rows_per_token = a.nq + a.nk + (p.k_cache ? a.nk : 0);
+    const int64_t rows = static_cast<int64_t>(a.nq) + static_cast<int64_t>(a.nk) * (p.k_cache ? 2 : 1);
+    if (rows > INT32_MAX - kRows || a.ntokens > INT64_MAX / rows)
+        return fail(SSU_ERR_UNSUPPORTED, "ssu_qk_norm_rope: 2^31 heads or 2^63 head rows");
+    p.rows_per_token = static_cast<int32_t>(rows);
     p.headdim = a.headdim;
     p.rot = a.rot;
     p.interleaved = a.interleaved;
     p.page_size = a.page_size;
     p.eps = a.eps;
-    if (a.ntokens > INT64_MAX / p.rows_per_token || a.ntokens * p.rows_per_token > int64_t(4) * 0x7fffffff)
-        return fail(SSU_ERR_UNSUPPORTED, "ssu_qk_norm_rope: more than 2^31 workgroups");
     p.total = a.ntokens * p.rows_per_token;
-    DeviceGuard guard;
-    SSU_TRY(guard.enter(a.device));
     const bool bf16 = (a.nq > 0 ? a.q.dtype : a.k.dtype) == SSU_BF16;
     p.q_groups = (a.nq + kRows - 1) / kRows;
     p.k_groups = (a.nk + kRows - 1) / kRows;
     p.groups_per_token = p.q_groups + p.k_groups * (p.k_cache ? 2 : 1);
     const int64_t groups = a.ntokens * p.groups_per_token;
-    hipError_t e;
     const Runs runs = a.rot % 8 == 0 ? (a.interleaved ? Runs::inter : Runs::halves) : a.interleaved ? Runs::inter_edge : Runs::halves_edge;
     const int need = runs == Runs::halves_edge ? (a.rot / 2 + 3) / 4 + (a.headdim - a.rot + 7) / 8 : (a.headdim + 7) / 8;
     int lanes = 1;
     while (lanes < need)
         lanes *= 2;
     const bool few = a.rot % 8 != 0 && p.total <= 2048;  // (the kernel of single rows starts sooner)
-    if (a.headdim % 8 == 0 && lanes <= 64 && groups <= 0x7fffffff && !few) {
-        e = launch_kernel(bf16 ? groups_kernel<Bf16>(runs, lanes) : groups_kernel<F16>(runs, lanes), p,
-                          (groups * lanes + 255) / 256, 256, 0, stream);
-    } else {
-        e = launch_kernel(bf16 ? &ssu_qk_rows_kernel<Bf16> : &ssu_qk_rows_kernel<F16>, p, (p.total + 3) / 4, 256, 0, stream);
-    }
+    const bool grouped = a.headdim % 8 == 0 && lanes <= 64 && !few;
+    const int64_t workgroups = grouped ? groups / (256 / lanes) + (groups % (256 / lanes) != 0) : p.total / 4 + (p.total % 4 != 0);
+    SSU_TRY(check_launch(workgroups, 256, "ssu_qk_norm_rope"));
+    DeviceGuard guard;
+    SSU_TRY(guard.enter(a.device));
+    const QkFn fn = !grouped ? (bf16 ? &ssu_qk_rows_kernel<Bf16> : &ssu_qk_rows_kernel<F16>)
+                             : bf16 ? groups_kernel<Bf16>(runs, lanes) : groups_kernel<F16>(runs, lanes);
+    const hipError_t e = launch_kernel(fn, p, workgroups, 256, 0, stream);
     if (e != hipSuccess)
         return fail(SSU_ERR_HIP, "launch of the norm and rotation kernel failed: %s", hipGetErrorString(e));
     return SSU_OK;
