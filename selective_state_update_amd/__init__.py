@@ -46,8 +46,10 @@ __all__ = [
     "scan_tiles",
     "linear_attention",
     "linear_attention_step",
+    "linear_attention_workspace",
     "qk_norm_rope",
     "paged_attention",
+    "paged_attention_workspace",
     "tile_fits",
     "tiles",
     "library_path",
@@ -609,7 +611,7 @@ def linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices,
     cu_seqlens[b + 1]; state_batch_indices [batch] int32/int64 (ids outside the
     pool are padding); beta [T, H] fp32 or None for 1. Returns out [T, H, P]
     bf16 (rows of no sequence are left as they were). ``workspace`` (optional): a
-    contiguous GPU tensor of at least ssu_linear_attention_workspace bytes, not
+    contiguous GPU tensor of at least linear_attention_workspace bytes, not
     used by another call at the same time. Inference only: no gradient."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
@@ -617,6 +619,12 @@ def linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices,
         with _on(stream, state):
             return linear_attention(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace)
     return _native.linear(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace)
+
+
+def linear_attention_workspace(batch, ntokens, nheads, headdim, dstate, ngroups=1):
+    """Bytes of workspace that linear_attention needs for ``batch`` sequences of
+    ``ntokens`` tokens in all (H, P, N and G as there); 0 where none is needed."""
+    return _native.linear_workspace(batch, ntokens, nheads, headdim, dstate, ngroups)
 
 
 def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=None, scale=1.0, out=None, stream=None):
@@ -660,9 +668,16 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=
     tokens each request sees (its new one among them; 0: out is 0; negative:
     padding, out is left as it was); scale: 1 / sqrt(D) by default. Returns out
     [batch, Hq, D], with return_lse also the logarithms of the softmax sums
-    [batch, Hq] fp32. ``workspace`` as in linear_attention. Inference only: no
-    gradient."""
+    [batch, Hq] fp32. ``workspace`` as in linear_attention, of
+    paged_attention_workspace bytes. Inference only: no gradient."""
     if stream is not None:
         with _on(stream, q):
             return paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, return_lse, workspace)
     return _native.attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, return_lse, workspace)
+
+
+def paged_attention_workspace(batch, nq, nk, headdim, page_size, max_pages):
+    """Bytes of workspace that paged_attention needs for q [batch, nq, headdim], caches
+    of nk heads in pages of page_size and a table [batch, max_pages]; 0 where none
+    is needed."""
+    return _native.attention_workspace(batch, nq, nk, headdim, page_size, max_pages)

@@ -101,7 +101,7 @@ ssu_view view_or_none(PyObject *o, const char *name, at::IntArrayRef shape, Type
 
 int32_t i32(int64_t n, const char *name)
 {
-    if (n > INT32_MAX)
+    if (n > INT32_MAX || n < INT32_MIN)
         refuse(PyExc_ValueError, std::string(name) + " is too large: " + std::to_string(n));
     return static_cast<int32_t>(n);
 }
@@ -343,6 +343,53 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+int64_t integer(PyObject *o)
+{
+    const long long n = PyLong_AsLongLong(o);
+    if (n == -1 && PyErr_Occurred())
+        throw python_error();
+    return n;
+}
+
+PyObject *bytes_of(int64_t n)
+{
+    if (n < 0)
+        refuse(PyExc_ValueError, ssu_last_error());
+    return PyLong_FromLongLong(n);
+}
+
+// linear_workspace(batch, ntokens, H, P, N, G)
+PyObject *linear_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    ssu_linear_args a{};
+    a.batch = i32(integer(o[0]), "batch");
+    a.ntokens = integer(o[1]);
+    a.nheads = i32(integer(o[2]), "H");
+    a.headdim = i32(integer(o[3]), "P");
+    a.dstate = i32(integer(o[4]), "N");
+    a.ngroups = i32(integer(o[5]), "G");
+    return bytes_of(ssu_linear_attention_workspace(&a));
+    END_HANDLE_TH_ERRORS
+}
+
+// attention_workspace(batch, Hq, Hk, D, page_size, max_pages)
+PyObject *attention_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    ssu_attn_args a{};
+    a.batch = i32(integer(o[0]), "batch");
+    a.nq = i32(integer(o[1]), "Hq");
+    a.nk = i32(integer(o[2]), "Hk");
+    a.headdim = i32(integer(o[3]), "D");
+    a.page_size = i32(integer(o[4]), "page_size");
+    a.max_pages = integer(o[5]);
+    return bytes_of(ssu_paged_attention_workspace(&a));
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *errors(PyObject *, PyObject *cls)
 {
     Py_INCREF(cls);
@@ -360,6 +407,8 @@ PyMethodDef methods[] = {
     {"linear", fast<linear>(), METH_FASTCALL, nullptr},
     {"qk", fast<qk>(), METH_FASTCALL, nullptr},
     {"attention", fast<attention>(), METH_FASTCALL, nullptr},
+    {"linear_workspace", fast<linear_workspace>(), METH_FASTCALL, nullptr},
+    {"attention_workspace", fast<attention_workspace>(), METH_FASTCALL, nullptr},
     {"errors", errors, METH_O, "Set the class that a failed call raises: cls(status, where)."},
     {nullptr, nullptr, 0, nullptr},
 };
