@@ -59,11 +59,12 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libssu.so")
 
-if not os.path.exists(_LIB_PATH):
-    raise ImportError(
-        f"{_LIB_PATH} is not built; run `python selective_state_update_amd/build.py` "
-        "(there is no fallback implementation)"
-    )
+for _path in (_LIB_PATH, os.path.join(_HERE, "_native.so")):
+    if not os.path.exists(_path):
+        raise ImportError(
+            f"{_path} is not built; run `python selective_state_update_amd/build.py` "
+            "(there is no fallback implementation)"
+        )
 
 # libssu must bind to the HIP runtime torch has loaded. torch ships its own
 # libamdhip64 (soname libamdhip64.so.7) and its libraries ask for it by file
