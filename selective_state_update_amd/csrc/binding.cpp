@@ -81,6 +81,8 @@ ssu_view view(const at::Tensor &t, const char *name, at::IntArrayRef shape, Type
     if (t.requires_grad() && c10::GradMode::is_enabled())
         refuse(PyExc_ValueError, std::string("inference only: no gradient is recorded for ") + name +
                                      "; call under torch.no_grad() or detach it");
+    if (t._fw_grad(0).defined())
+        refuse(PyExc_ValueError, std::string("inference only: no tangent is carried for ") + name + "; unpack the dual tensor");
     ssu_view v{};
     v.ptr = t.data_ptr();
     v.dtype = tag_of(t.scalar_type());
