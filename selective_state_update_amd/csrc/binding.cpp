@@ -83,6 +83,8 @@ ssu_view view(const at::Tensor &t, const char *name, at::IntArrayRef shape, Type
                                      "; call under torch.no_grad() or detach it");
     if (t._fw_grad(0).defined())
         refuse(PyExc_ValueError, std::string("inference only: no tangent is carried for ") + name + "; unpack the dual tensor");
+    if (t.is_neg())  // (as the imaginary part of a conjugate is)
+        refuse(PyExc_ValueError, std::string(name) + " is a view of negated memory; call resolve_neg() on it");
     ssu_view v{};
     v.ptr = t.data_ptr();
     v.dtype = tag_of(t.scalar_type());

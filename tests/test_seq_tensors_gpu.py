@@ -60,3 +60,14 @@ def test_dual_tensors(ssu, f, make, name):
             getattr(ssu, f)(**a)
         a[name] = fwd.unpack_dual(a[name]).primal
         getattr(ssu, f)(**a)
+
+
+@pytest.mark.parametrize("f,make,name", FLOATS)
+def test_negated_views(ssu, f, make, name):
+    """Their memory holds the values' negatives (a conjugate's imaginary part is one)."""
+    a = make()
+    a[name] = torch._neg_view(a[name])
+    with pytest.raises(ValueError, match=f"{name} is a view of negated memory"):
+        getattr(ssu, f)(**a)
+    a[name] = a[name].resolve_neg()
+    getattr(ssu, f)(**a)
