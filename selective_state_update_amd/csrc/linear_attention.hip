@@ -138,15 +138,14 @@ __global__ void __launch_bounds__(64) ssu_linear_step_kernel(const LinearParams 
 // every segment's own contribution to the state, a second the states in front
 // of the segments from them, and the third starts every segment there.
 constexpr int kChunk = 32;
-constexpr int kTiles = kChunk / 16;  // of tokens
-constexpr int kSteps = kChunk / 32;  // products along a chunk's tokens
+constexpr int kTiles = kChunk / 16;  // of tokens: a product's 32 places hold both
 constexpr float kDecayFloor = -1.0e4f;  // exp is 0 far above it; sums of it stay finite
 
 struct ChunkParams {
     LinearParams a;
     float *states;  // [segments, nheads, headdim, dstate]
     float *decays;  // [segments, nheads]: a segment's whole decay, log2 of it
-    int32_t seg_len, segments, slices, dstate, total, pad;
+    int32_t seg_len, slices, dstate;
 };
 
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo)
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
     __shared__ __attribute__((aligned(16))) uint16_t lq[FULL ? kChunk * ROW : 8];
     __shared__ __attribute__((aligned(16))) uint16_t lk[kChunk * ROW];
     __shared__ __attribute__((aligned(16))) uint16_t lv[kChunk * VROW];
-    __shared__ u32x4 lw[FULL ? kTiles : 1][FULL ? kSteps : 1][2][64];  // scores: token tile, 32 tokens j, value / remainder, lane
+    __shared__ u32x4 lw[FULL ? kTiles : 1][2][64];  // scores: token tile, value / remainder, lane
     // of THREADS tokens: L in units of log 2, as fp32 and what that leaves, and what follows from it
     __shared__ __attribute__((aligned(16))) float lsum[THREADS], lrest[THREADS], lbeta[THREADS], lgrow[THREADS], llate[THREADS];
     __shared__ float lall[THREADS / kChunk];
@@ -405,8 +404,8 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
     };
     start();
     if constexpr (FULL)  // (the tiles above the diagonal stay zero)
-        for (int i = tid; i < kTiles * kSteps * 2 * 64; i += THREADS)
-            (&lw[0][0][0][0])[i] = u32x4{0, 0, 0, 0};
+        for (int i = tid; i < kTiles * 2 * 64; i += THREADS)
+            (&lw[0][0][0])[i] = u32x4{0, 0, 0, 0};
     sums(0);
     request_sums(THREADS);
     place(0);
@@ -423,24 +422,16 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
 
         // v of the wave's columns as fragments: 8 tokens of 32 per lane
         const int tr = (4 * g + c / 4) * ROW + 4 * (c % 4), vtr = (4 * g + c / 4) * VROW + 4 * (c % 4) + wave * 16;
-        u32x4 vf[kSteps];
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const u32x2 x = read_transposed(lv + 32 * s * VROW + vtr), y = read_transposed(lv + (32 * s + 16) * VROW + vtr);
-            vf[s] = u32x4{x[0], x[1], y[0], y[1]};
-        }
+        const u32x2 v0 = read_transposed(lv + vtr), v1 = read_transposed(lv + 16 * VROW + vtr);
+        const u32x4 vf = {v0[0], v0[1], v1[0], v1[1]};
 
         if constexpr (FULL) {
             // weighted scores of the pairs of 16-token tiles (it, jt <= it), dealt
             // out to the waves; result rows j = 16 jt + 4g + r, columns
             // i = 16 it + c
-            constexpr int PAIRS = kTiles * (kTiles + 1) / 2;
-#pragma unroll
-            for (int n = 0; n < (PAIRS + W - 1) / W; ++n) {
-                const int pair = wave + W * n;
-                if (pair >= PAIRS)
-                    break;
-                const int it = pair >= 6 ? 3 : pair >= 3 ? 2 : pair >= 1 ? 1 : 0, jt = pair - it * (it + 1) / 2;
+            static_assert(kTiles == 2 && W >= 3, "three pairs, one for a wave");
+            if (const int pair = wave; pair < 3) {
+                const int it = pair >= 1 ? 1 : 0, jt = pair >= 2 ? 1 : 0;
                 f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int e0 = 0; e0 < KS; e0 += AHEAD) {
@@ -467,8 +458,8 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
                 uint32_t h0, h1, l0, l1;
                 split_pair(x[0], x[1], h0, l0);
                 split_pair(x[2], x[3], h1, l1);
-                *(reinterpret_cast<u32x2 *>(&lw[it][jt / 2][0][lane]) + jt % 2) = u32x2{h0, h1};
-                *(reinterpret_cast<u32x2 *>(&lw[it][jt / 2][1][lane]) + jt % 2) = u32x2{l0, l1};
+                *(reinterpret_cast<u32x2 *>(&lw[it][0][lane]) + jt) = u32x2{h0, h1};
+                *(reinterpret_cast<u32x2 *>(&lw[it][1][lane]) + jt) = u32x2{l0, l1};
             }
 
             // S q, all tokens: result rows p, columns i
@@ -508,12 +499,10 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
                 o[it] *= lgrow[at0 + 16 * it + c];
             __syncthreads();  // the scores are there
 #pragma unroll
-            for (int it = 0; it < kTiles; ++it)
-#pragma unroll
-                for (int s = 0; s <= it / 2; ++s) {
-                    o[it] = Mma<Bf16>::run(vf[s], lw[it][s][0][lane], o[it]);
-                    o[it] = Mma<Bf16>::run(vf[s], lw[it][s][1][lane], o[it]);
-                }
+            for (int it = 0; it < kTiles; ++it) {
+                o[it] = Mma<Bf16>::run(vf, lw[it][0][lane], o[it]);
+                o[it] = Mma<Bf16>::run(vf, lw[it][1][lane], o[it]);
+            }
 #pragma unroll
             for (int it = 0; it < kTiles; ++it)
 #pragma unroll
@@ -535,37 +524,33 @@ __global__ void __launch_bounds__(64 * W, N == 256 ? 2 : FULL && !DENSE ? 3 : 4)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             st[m] *= all;
+        u32x4 f1, f2, f3;
+        const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[at0 + 4 * g]);
+        const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[at0 + 16 + 4 * g]);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            u32x4 f1, f2, f3;
-            const f32x4 late0 = *reinterpret_cast<const f32x4 *>(&llate[at0 + 32 * s + 4 * g]);
-            const f32x4 late1 = *reinterpret_cast<const f32x4 *>(&llate[at0 + 32 * s + 16 + 4 * g]);
+        for (int e = 0; e < 4; ++e) {
+            const f32x4 &late = e < 2 ? late0 : late1;
+            const float x = Bf16::lo(vf[e]) * late[2 * e % 4], y = Bf16::hi(vf[e]) * late[2 * e % 4 + 1];
+            const uint32_t h1 = pack2<Bf16>(x, y);
+            const float x1 = x - Bf16::lo(h1), y1 = y - Bf16::hi(h1);
+            const uint32_t h2 = pack2<Bf16>(x1, y1);
+            f1[e] = h1;
+            f2[e] = h2;
+            f3[e] = pack2<Bf16>(x1 - Bf16::lo(h2), y1 - Bf16::hi(h2));
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x4 &late = e < 2 ? late0 : late1;
-                const float x = Bf16::lo(vf[s][e]) * late[2 * e % 4], y = Bf16::hi(vf[s][e]) * late[2 * e % 4 + 1];
-                const uint32_t h1 = pack2<Bf16>(x, y);
-                const float x1 = x - Bf16::lo(h1), y1 = y - Bf16::hi(h1);
-                const uint32_t h2 = pack2<Bf16>(x1, y1);
-                f1[e] = h1;
-                f2[e] = h2;
-                f3[e] = pack2<Bf16>(x1 - Bf16::lo(h2), y1 - Bf16::hi(h2));
+        for (int m0 = 0; m0 < MT; m0 += MAHEAD) {
+            u32x4 kf[MAHEAD];
+#pragma unroll
+            for (int m = 0; m < MAHEAD; ++m) {
+                const u32x2 x = read_transposed(lk + tr + 16 * (m0 + m)), y = read_transposed(lk + 16 * ROW + tr + 16 * (m0 + m));
+                kf[m] = u32x4{x[0], x[1], y[0], y[1]};
             }
 #pragma unroll
-            for (int m0 = 0; m0 < MT; m0 += MAHEAD) {
-                u32x4 kf[MAHEAD];
+            for (const u32x4 &f : {f1, f2, f3})
 #pragma unroll
-                for (int m = 0; m < MAHEAD; ++m) {
-                    const u32x2 x = read_transposed(lk + 32 * s * ROW + tr + 16 * (m0 + m));
-                    const u32x2 y = read_transposed(lk + (32 * s + 16) * ROW + tr + 16 * (m0 + m));
-                    kf[m] = u32x4{x[0], x[1], y[0], y[1]};
-                }
-#pragma unroll
-                for (const u32x4 &f : {f1, f2, f3})
-#pragma unroll
-                    for (int m = 0; m < MAHEAD; ++m)
-                        st[m0 + m] = Mma<Bf16>::run(kf[m], f, st[m0 + m]);
-            }
+                for (int m = 0; m < MAHEAD; ++m)
+                    st[m0 + m] = Mma<Bf16>::run(kf[m], f, st[m0 + m]);
         }
         if (more) {
             __syncthreads();  // LDS is free again
@@ -948,23 +933,21 @@ ssu_status launch_chunks(const ssu_linear_args &a, hipStream_t stream)
     p.states = static_cast<float *>(a.workspace);
     p.decays = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + plan.decays_at);
     p.seg_len = plan.seg_len;
-    p.segments = plan.segments;
     p.slices = plan.slices;
     p.dstate = a.dstate;
     const int64_t groups = (static_cast<int64_t>(plan.segments) + 7) / 8 * 8 * a.nheads * plan.slices;
     SSU_TRY(check_launch(groups, 4 * k.columns, "ssu_linear_attention"));
-    p.total = static_cast<int>(groups);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     hipError_t e = hipSuccess;
     if (plan.bytes > 0) {
-        e = launch_kernel(k.states, p, p.total, 4 * k.columns, 0, stream);
+        e = launch_kernel(k.states, p, groups, 4 * k.columns, 0, stream);
         const int64_t blocks = (static_cast<int64_t>(a.headdim) * a.dstate + 1023) / 1024;
         if (e == hipSuccess)
             e = launch_kernel(&ssu_linear_segments_kernel, p, blocks * a.nheads * a.batch, 256, 0, stream);
     }
     if (e == hipSuccess)
-        e = launch_kernel(k.full, p, p.total, 4 * k.columns, 0, stream);
+        e = launch_kernel(k.full, p, groups, 4 * k.columns, 0, stream);
     if (e != hipSuccess)
         return fail(SSU_ERR_HIP, "launch of the chunked linear attention failed: %s", hipGetErrorString(e));
     return SSU_OK;

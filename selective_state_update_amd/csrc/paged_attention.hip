@@ -41,7 +41,7 @@ struct AttnParams {
     // (maximum, sum).
     struct Open *open;
     float *part, *stat;
-    int32_t batch, nq, nk, heads_per_kv, row_tiles, page_size, groups;
+    int32_t batch, nk, heads_per_kv, row_tiles, page_size, groups;
     int32_t cuts, cuts_half;  // runs of a unit's line, with all workgroups or one per CU; 0: too many would be left over
     float scale_log2;  // scale * log2(e): weights are powers of 2
 };
@@ -808,7 +808,6 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream)
     p.l_b = a.lse.stride[0];
     p.l_h = a.lse.stride[1];
     p.batch = a.batch;
-    p.nq = a.nq;
     p.nk = a.nk;
     p.heads_per_kv = a.nq / a.nk;
     p.page_size = a.page_size;
