@@ -347,8 +347,9 @@ int32_t ssu_scan_select_tile(const ssu_scan_args *args, int64_t chunk);
  * S starts from state[idx[b], h] and is written back there after the
  * sequence's last token. With q = C, k = B, v = x, beta = delta and
  * log_decay = A * delta this is the recurrence of ssu_update (without D), so a
- * prompt's state can be advanced by either step afterwards; with
- * log_decay constant in t (stride 0) it is attention with fixed decay rates.
+ * prompt's state can be advanced by either step afterwards (by ssu_update for
+ * Mamba2, which has softplus and D in the same pass); with log_decay constant in
+ * t (stride 0) it is attention with fixed decay rates.
  *
  * Numerics: state, decays, sums and the recurrence in fp32 (the decays'
  * running sums in fp64, where a sum over many tokens would lose digits). Over
@@ -362,7 +363,8 @@ int32_t ssu_scan_select_tile(const ssu_scan_args *args, int64_t chunk);
  * through the recurrence as written, in fp32 (0 times one is NaN): a prompt
  * leaves the infinities and NaN in state and out that single steps leave. Where
  * a sequence's results are not finite they are computed again token by token,
- * 10 to 30 times as long.
+ * 10 to 30 times as long. The sizes of a call set where its sequences are cut, and
+ * so change its results within rounding; the same call gives the same bits.
  */
 typedef struct ssu_linear_args {
     int32_t batch;      /* sequences, >= 0 (0: no-op) */
@@ -428,11 +430,15 @@ ssu_status ssu_linear_attention_step(const ssu_linear_args *args, hipStream_t st
  *
  * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved, and c_i, s_i
  * columns i and rot/2 + i of row positions[t] of cos_sin; values from rot on
- * are only normed. fp32 throughout, one rounding (to nearest even) at the end.
+ * are only normed. fp32 throughout, one rounding (to nearest even) at the end
+ * (rows whose squares add up beyond fp32 become 0). Where rot is no multiple of 8,
+ * calls of up to 2048 head rows and longer ones run in kernels of their own, whose
+ * results differ within fp32's rounding before it.
  * With k_cache and v_cache, token t's keys and values also go into row
  * slots[t] of a paged cache (page slots[t] / page_size, row slots[t] %
  * page_size); slots outside the cache are skipped. A token whose position is
  * outside [0, max_pos) is padding: nothing of it is read or written.
+ * (ssu_paged_attention reads caches of D = 64, 128 and 256.)
  */
 typedef struct ssu_qk_args {
     int64_t ntokens;     /* T >= 0 (0: no-op) */

@@ -629,7 +629,8 @@ def linear_attention_workspace(batch, ntokens, nheads, headdim, dstate, ngroups=
 
 
 def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=None, scale=1.0, out=None, stream=None):
-    """The same for one token per request (ssu_linear_attention_step): q, k
+    """The same for one token per request (ssu_linear_attention_step; a Mamba2
+    layer's: selective_state_update, with softplus and D in the same pass): q, k
     [batch, G, N], v [batch, H, P], log_decay [batch, H] or [H], beta [batch, H] or
     None. Returns out [batch, H, P] bf16."""
     if stream is not None:

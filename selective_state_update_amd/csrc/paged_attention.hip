@@ -687,7 +687,8 @@ struct Plan {
 // requests of 1 to 1600 tokens, 8 heads: 26 against 34 us; 64 of 1 to 1600: 46
 // against 50; 64 of 1 to 8192: 218 against 184). At D = 256 with four waves while
 // each has a CU to itself (32 requests of 1 to 1600 tokens, 8 heads: 52 us, 62 in a line;
-// 64 of 1 to 200: 23 us with four waves, 18 with two).
+// 64 of 1 to 200: 23 us with four waves, 18 with two). (All of these, and those below,
+// from before the check for infinities, which costs either side 0.2 to 1 us.)
 //
 // Otherwise a line with two workgroups per CU; at D = 128 every second one leaves
 // (the kernel knows the lengths) where the runs' pieces of units have 6 steps or more
