@@ -66,7 +66,8 @@ typedef enum ssu_dtype {
     SSU_BF16 = 1,
     SSU_I32 = 2,
     SSU_I64 = 3,
-    SSU_F16 = 4 /* IEEE binary16 (ssu_scan activations) */
+    SSU_F16 = 4, /* IEEE binary16 (ssu_scan activations) */
+    SSU_E4M3 = 5 /* 8 bits, 4 of exponent, no infinities (ssu_add_rms_norm) */
 } ssu_dtype;
 
 /* Problem shape and options, fixed for the life of a handle. */
@@ -421,6 +422,68 @@ ssu_status ssu_linear_attention(const ssu_linear_args *args, hipStream_t stream)
  * strides of any size. */
 ssu_status ssu_linear_attention_step(const ssu_linear_args *args, hipStream_t stream);
 
+/* ------------------------------------------------------- gated delta rule --
+ * The gated delta rule over whole prompts and for single tokens, on state slots
+ * as ssu_linear_attention's: what a key already recalls is taken out of the
+ * value before it is written. For every sequence, head h (group
+ * g = h / (nheads / ngroups)) and token t in order:
+ *
+ *   S[p,n]   = S[p,n] * exp(log_decay[t,h])
+ *   u[p]     = beta[t,h] * (v[t,h,p] - sum_n S[p,n] * k[t,g,n])
+ *   S[p,n]   = S[p,n] + u[p] * k[t,g,n]
+ *   out[t,p] = bf16( scale * sum_n S[p,n] * q[t,g,n] )
+ *
+ * With normalize, k and q stand for k / sqrt(sum_n k^2 + 1e-6) and
+ * q / sqrt(sum_n q^2 + 1e-6). log_decay 0 (one zero, strides 0) is the delta rule
+ * without a gate. The recurrence does not grow while beta |k|^2 <= 2 and
+ * log_decay <= 0.
+ *
+ * Numerics as in ssu_linear_attention: state, decays, sums and the recurrence in
+ * fp32; over prompts the products run on bf16 matrix instructions, fp32 operands
+ * as three bf16 pieces where they enter the state (2^-24 relative), as two where
+ * they enter only the output (2^-17). log_decay below -10000 counts as -10000. A chunk of tokens
+ * with a value that is not finite goes through the recurrence token by token, so
+ * that prompts leave the infinities and NaN that single steps leave: NaN and
+ * infinite v reach their own and later tokens of their channel p only, NaN and
+ * infinite k and beta their own and later tokens, NaN and infinite q their own
+ * token. Such chunks take 20 to 100 times as long. The same call gives the same bits.
+ */
+typedef struct ssu_delta_args {
+    int32_t batch;      /* sequences, >= 0 (0: no-op) */
+    int32_t nheads;     /* H >= 1 */
+    int32_t headdim;    /* P: a multiple of 16, 16 <= P <= 256 */
+    int32_t dstate;     /* N: 16, 32, 64, 128 or 256 */
+    int32_t ngroups;    /* G >= 1, divides H */
+    int32_t device;     /* as in ssu_linear_args */
+    int64_t ntokens;    /* T >= 0: rows of q, k, v, log_decay, beta and out */
+    int64_t pool_slots; /* slots in the state pool, >= 0 */
+    float scale;        /* finite */
+    int32_t normalize;  /* 1 or 0 */
+    ssu_view state;      /* [pool_slots, H, P, N] F32, this and the other views as in ssu_linear_args */
+    ssu_view idx;        /* [batch] I32 or I64 */
+    ssu_view cu_seqlens; /* [batch + 1] I32; ssu_gated_delta_rule_step: ptr NULL */
+    ssu_view q, k;       /* [T, G, N] BF16 */
+    ssu_view v;          /* [T, H, P] BF16 */
+    ssu_view log_decay;  /* [T, H] F32, any strides >= 0 */
+    ssu_view beta;       /* [T, H] F32, any strides >= 0; ptr NULL: 1 */
+    ssu_view out;        /* [T, H, P] BF16, written */
+    void *workspace;     /* as in ssu_linear_args */
+    int64_t workspace_bytes;
+} ssu_delta_args;
+
+/* Bytes of workspace that ssu_gated_delta_rule needs for `args` (only its sizes
+ * are read; -1 for sizes that it refuses): 10.5 KiB for each head and 32 tokens. */
+int64_t ssu_gated_delta_rule_workspace(const ssu_delta_args *args);
+
+/* Enqueue `args`' prompts on `stream`: conditions and errors of
+ * ssu_linear_attention, and SSU_ERR_INVALID_ARGUMENT for another value of normalize. */
+ssu_status ssu_gated_delta_rule(const ssu_delta_args *args, hipStream_t stream);
+
+/* The same for one token per request: ntokens == batch, token b advances
+ * request b; cu_seqlens.ptr and workspace are NULL. Same errors, but token
+ * strides of any size. */
+ssu_status ssu_gated_delta_rule_step(const ssu_delta_args *args, hipStream_t stream);
+
 /* ------------------------------------------ queries and keys of attention --
  * Norms of queries and keys for each head with the position rotation, for the
  * attention layers of hybrid models. Each head row x of q and k [D] becomes
@@ -528,6 +591,43 @@ int64_t ssu_paged_attention_workspace(const ssu_attn_args *args);
  * workspace too small), SSU_ERR_UNSUPPORTED (D, inner strides, 2^32 threads
  * of a launch or more), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
 ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream);
+
+/* ------------------------------------------ norm with the residual added --
+ * What stands between the layers: the residual stream takes a layer's output and
+ * the next layer's input is its norm, in 16 bits or in 8 with scales. For every
+ * row t of width D:
+ *
+ *   s = x[t] + residual[t]                      (no residual: s = x[t])
+ *   residual[t] = s                             (rounded to its type)
+ *   y = s / sqrt(mean(s^2) + eps) * weight      (no weight: factor 1)
+ *   out[t] = y, or, in E4M3, for each `group` of consecutive values (0: all D)
+ *   scales[t,i] = max(max|y| / 448, 2^-126),  out[t] = y / scales[t,i]
+ *
+ * fp32 throughout (the norm takes s before it is rounded into the residual),
+ * each output rounded once, to nearest even. Rows whose squares add up beyond
+ * fp32 become 0. A NaN in a row's s makes its y NaN, a NaN in y its group's scale and values.
+ */
+typedef struct ssu_norm_args {
+    int64_t ntokens;    /* T >= 0 (0: no-op) */
+    int32_t width;      /* D, 1 <= D <= 32768 */
+    int32_t group;      /* E4M3: 0, or 32, 64, 128 or 256 dividing D; otherwise 0 */
+    int32_t device;     /* as in ssu_linear_args */
+    float eps;          /* >= 0, finite */
+    ssu_view x;         /* [T, D] BF16 or F16, stride[1] == 1 */
+    ssu_view residual;  /* [T, D] x's type or F32, read and written, stride[1] == 1; ptr NULL: none */
+    ssu_view weight;    /* [D] x's type or F32, stride[0] == 1; ptr NULL: 1 */
+    ssu_view out;       /* [T, D] x's type or E4M3, written, stride[1] == 1; may be x itself */
+    ssu_view scales;    /* [T, group ? D / group : 1] F32, written (with E4M3; otherwise ptr NULL) */
+} ssu_norm_args;
+
+/* Enqueue it on `stream`. Outputs must not overlap inputs or each other, but out
+ * may be x (same pointer and strides). Asynchronous, allocation-free,
+ * graph-capturable, without workspace. Errors (nothing is launched):
+ * SSU_ERR_INVALID_ARGUMENT (null pointers, sizes, strides, dtype tags, a group that
+ * does not divide D, scales without E4M3), SSU_ERR_UNSUPPORTED (D > 32768, other
+ * groups, inner strides, 2^32 threads of a launch or more), SSU_ERR_MISALIGNED
+ * (elements not aligned to their size), SSU_ERR_HIP. */
+ssu_status ssu_add_rms_norm(const ssu_norm_args *args, hipStream_t stream);
 
 /* SSU_ABI_VERSION of the built library. */
 int32_t ssu_abi_version(void);

@@ -581,7 +581,8 @@ def selective_scan(u, delta, A, B, C, state, D=None, delta_bias=None, delta_soft
 
 # --------------------------------------------------------------------------- #
 # Sequence operators of hybrid models: ssu_linear_attention(_step),
-# ssu_qk_norm_rope, ssu_paged_attention
+# ssu_gated_delta_rule(_step), ssu_qk_norm_rope, ssu_add_rms_norm,
+# ssu_paged_attention
 # --------------------------------------------------------------------------- #
 # Checked, packed and launched by a native module (csrc/binding.cpp): the
 # smallest of these calls run for a few microseconds.
@@ -639,6 +640,45 @@ def linear_attention_step(state, q, k, v, log_decay, state_batch_indices, beta=N
     return _native.linear(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None)
 
 
+def gated_delta_rule(state, q, k, v, log_decay, beta, cu_seqlens, state_batch_indices, scale=1.0, normalize=False, out=None,
+                     workspace=None, stream=None):
+    """The gated delta rule over packed prompts (see include/ssu.h,
+    ssu_gated_delta_rule); ``state`` advances in place.
+
+    Operands as in linear_attention: state [pool, H, P, N] fp32; q, k [T, G, N]
+    bf16; v [T, H, P] bf16; log_decay [T, H] fp32, or [H] for fixed rates (zeros:
+    no gate); beta [T, H] fp32 or None for 1; cu_seqlens [batch + 1] int32;
+    state_batch_indices [batch] int32/int64 (ids outside the pool are padding).
+    normalize: q and k are divided by their lengths. Returns out [T, H, P] bf16
+    (rows of no sequence are left as they were). ``workspace`` as in
+    linear_attention, of gated_delta_rule_workspace bytes. Inference only: no
+    gradient."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    if stream is not None:
+        with _on(stream, state):
+            return gated_delta_rule(state, q, k, v, log_decay, beta, cu_seqlens, state_batch_indices, scale, normalize, out,
+                                    workspace)
+    return _native.delta(state, q, k, v, log_decay, cu_seqlens, state_batch_indices, beta, scale, out, workspace, normalize)
+
+
+def gated_delta_rule_workspace(batch, ntokens, nheads, headdim, dstate, ngroups=1):
+    """Bytes of workspace that gated_delta_rule needs for ``batch`` sequences of
+    ``ntokens`` tokens in all (H, P, N and G as there)."""
+    return _native.delta_workspace(batch, ntokens, nheads, headdim, dstate, ngroups)
+
+
+def gated_delta_rule_step(state, q, k, v, log_decay, beta, state_batch_indices, scale=1.0, normalize=False, out=None,
+                          stream=None):
+    """The same for one token per request (ssu_gated_delta_rule_step): q, k
+    [batch, G, N], v [batch, H, P], log_decay [batch, H] or [H], beta [batch, H] or
+    None. Returns out [batch, H, P] bf16."""
+    if stream is not None:
+        with _on(stream, state):
+            return gated_delta_rule_step(state, q, k, v, log_decay, beta, state_batch_indices, scale, normalize, out)
+    return _native.delta(state, q, k, v, log_decay, None, state_batch_indices, beta, scale, out, None, normalize)
+
+
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
                  k_out=None, v=None, k_cache=None, v_cache=None, slots=None, stream=None):
     """Norm of every query and key head, then the position rotation (see
@@ -658,6 +698,22 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
                                 v_cache, slots)
     return _native.qk(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, v, k_cache, v_cache,
                       slots)
+
+
+def add_rms_norm(x, residual=None, weight=None, eps=1e-6, quantize=False, group=0, out=None, scales=None, stream=None):
+    """Root-mean-square norm with the residual's addition (see include/ssu.h,
+    ssu_add_rms_norm); ``residual`` takes the sum in place.
+
+    x [T, D] bf16 or fp16, D <= 32768; residual [T, D] x's type or fp32, or None;
+    weight [D] x's type or fp32, or None. Returns out [T, D] in x's type (which
+    may be x itself); with quantize (out in float8_e4m3fn, scales fp32), values
+    times their scale being the norm: one scale per token [T, 1], or for each
+    ``group`` (32, 64, 128, 256) of values [T, D / group]. Inference only: no
+    gradient."""
+    if stream is not None:
+        with _on(stream, x):
+            return add_rms_norm(x, residual, weight, eps, quantize, group, out, scales)
+    return _native.norm(x, residual, weight, eps, quantize, group, out, scales)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, return_lse=False, workspace=None,

@@ -1,6 +1,6 @@
 // binding.cpp -- the Python entry points of the sequence operators
-// (linear_attention, linear_attention_step, qk_norm_rope, paged_attention):
-// tensors checked, turned into the views of include/ssu.h and passed on, with
+// (linear_attention, gated_delta_rule, their steps, qk_norm_rope, add_rms_norm,
+// paged_attention): tensors checked, turned into the views of include/ssu.h and passed on, with
 // outputs and workspaces from torch's allocator on torch's current stream.
 // Native because the operators' smallest calls run for 3 to 5 us and checking
 // and packing nine to twelve tensors in Python took 6 to 10.
@@ -60,6 +60,7 @@ int32_t tag_of(at::ScalarType t)
     case at::kHalf: return SSU_F16;
     case at::kInt: return SSU_I32;
     case at::kLong: return SSU_I64;
+    case at::kFloat8_e4m3fn: return SSU_E4M3;
     default: return -1;
     }
 }
@@ -116,6 +117,22 @@ float number(PyObject *o)
     if (x == -1.0 && PyErr_Occurred())
         throw python_error();
     return static_cast<float>(x);
+}
+
+int64_t integer(PyObject *o)
+{
+    const long long n = PyLong_AsLongLong(o);
+    if (n == -1 && PyErr_Occurred())
+        throw python_error();
+    return n;
+}
+
+bool truth(PyObject *o)
+{
+    const int x = PyObject_IsTrue(o);
+    if (x < 0)
+        throw python_error();
+    return x != 0;
 }
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int gpu)
@@ -179,11 +196,23 @@ void count(Py_ssize_t n, Py_ssize_t want)
         refuse(PyExc_TypeError, "expected " + std::to_string(want) + " arguments");
 }
 
-// linear(state, q, k, v, log_decay, cu_seqlens | None, idx, beta | None, scale, out | None, workspace | None)
-PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n)
+// The operators on state slots, over prompts and for single tokens.
+template <typename Args>
+struct Recurrence {
+    ssu_status (*prompts)(const Args *, hipStream_t), (*step)(const Args *, hipStream_t);
+    int64_t (*need)(const Args *);
+    const char *where, *where_step;
+};
+
+constexpr Recurrence<ssu_linear_args> kLinear{&ssu_linear_attention, &ssu_linear_attention_step, &ssu_linear_attention_workspace,
+                                              "ssu_linear_attention", "ssu_linear_attention_step"};
+constexpr Recurrence<ssu_delta_args> kDelta{&ssu_gated_delta_rule, &ssu_gated_delta_rule_step, &ssu_gated_delta_rule_workspace,
+                                            "ssu_gated_delta_rule", "ssu_gated_delta_rule_step"};
+
+// o: state, q, k, v, log_decay, cu_seqlens | None, idx, beta | None, scale, out | None, workspace | None
+template <typename Args>
+PyObject *recurrence(const Recurrence<Args> &fn, Args a, PyObject *const *o)
 {
-    HANDLE_TH_ERRORS
-    count(n, 11);
     const at::Tensor &state = tensor(o[0], "state"), &q = tensor(o[1], "q"), &v = tensor(o[3], "v");
     const at::Tensor &decay = tensor(o[4], "log_decay"), &idx = tensor(o[6], "state_batch_indices");
     const int gpu = gpu_of(state, "state");
@@ -194,7 +223,6 @@ PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n)
     const int64_t H = state.size(1), P = state.size(2), N = state.size(3), T = q.size(0), G = q.size(1), B = idx.size(0);
     if (!prompts && T != B)
         refuse(PyExc_ValueError, "q has " + std::to_string(T) + " tokens for " + std::to_string(B) + " requests");
-    ssu_linear_args a{};
     a.batch = i32(B, "batch");
     a.nheads = i32(H, "H");
     a.headdim = i32(P, "P");
@@ -222,10 +250,72 @@ PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n)
     a.out = view(out, "out", {T, H, P}, {at::kBFloat16}, gpu);
     at::Tensor keep;
     if (prompts)
-        workspace(o[10], ssu_linear_attention_workspace(&a), gpu, a, keep);
-    call(prompts ? &ssu_linear_attention : &ssu_linear_attention_step, a, gpu,
-         prompts ? "ssu_linear_attention" : "ssu_linear_attention_step");
+        workspace(o[10], fn.need(&a), gpu, a, keep);
+    call(prompts ? fn.prompts : fn.step, a, gpu, prompts ? fn.where : fn.where_step);
     return object(o[9], out);
+}
+
+// linear(state, q, k, v, log_decay, cu_seqlens | None, idx, beta | None, scale, out | None, workspace | None)
+PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 11);
+    return recurrence(kLinear, {}, o);
+    END_HANDLE_TH_ERRORS
+}
+
+// delta(the same, normalize)
+PyObject *delta(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 12);
+    ssu_delta_args a{};
+    a.normalize = truth(o[11]);
+    return recurrence(kDelta, a, o);
+    END_HANDLE_TH_ERRORS
+}
+
+// norm(x, residual | None, weight | None, eps, quantize, group, out | None, scales | None)
+PyObject *norm(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 8);
+    const at::Tensor &x = tensor(o[0], "x");
+    const int gpu = gpu_of(x, "x");
+    if (x.dim() != 2)
+        refuse(PyExc_ValueError, "x must be [tokens, D]");
+    const at::ScalarType type = x.scalar_type();
+    const Types half = {type}, wide = {type, at::kFloat}, eight = {at::kFloat8_e4m3fn};
+    if (type != at::kBFloat16 && type != at::kHalf)
+        refuse(PyExc_TypeError, std::string("x: dtype ") + c10::toString(type) + " not supported here");
+    const bool quantize = truth(o[4]);
+    const int64_t T = x.size(0), D = x.size(1), group = integer(o[5]);
+    if (!quantize && (group != 0 || o[7] != Py_None))
+        refuse(PyExc_ValueError, "group and scales go with quantize");
+    if (group < 0 || (group > 0 && D % group))
+        refuse(PyExc_ValueError, "group " + std::to_string(group) + " does not divide D = " + std::to_string(D));
+    ssu_norm_args a{};
+    a.ntokens = T;
+    a.width = i32(D, "D");
+    a.group = i32(group, "group");
+    a.device = gpu;
+    a.eps = number(o[3]);
+    a.x = view(x, "x", {T, D}, half, gpu);
+    a.residual = view_or_none(o[1], "residual", {T, D}, wide, gpu);
+    a.weight = view_or_none(o[2], "weight", {D}, wide, gpu);
+    const at::Tensor out = given_or(o[6], "out", {T, D}, quantize ? at::kFloat8_e4m3fn : type, gpu);
+    a.out = view(out, "out", {T, D}, quantize ? eight : half, gpu);
+    at::Tensor scales;
+    if (quantize) {
+        const int64_t shape[] = {T, group > 0 ? D / group : 1};
+        scales = given_or(o[7], "scales", shape, at::kFloat, gpu);
+        a.scales = view(scales, "scales", shape, {at::kFloat}, gpu);
+    }
+    call(&ssu_add_rms_norm, a, gpu, "ssu_add_rms_norm");
+    if (!quantize)
+        return object(o[6], out);
+    PyObject *const first = object(o[6], out);
+    return Py_BuildValue("(NN)", first, object(o[7], scales));
     END_HANDLE_TH_ERRORS
 }
 
@@ -253,10 +343,7 @@ PyObject *qk(PyObject *, PyObject *const *o, Py_ssize_t n)
     a.nk = i32(nk, "Hk");
     a.headdim = i32(D, "D");
     a.rot = i32(cos_sin.size(1), "rot");
-    const int inter = PyObject_IsTrue(o[7]);
-    if (inter < 0)
-        throw python_error();
-    a.interleaved = inter;
+    a.interleaved = truth(o[7]);
     a.device = gpu;
     a.eps = number(o[6]);
     a.max_pos = cos_sin.size(0);
@@ -330,9 +417,7 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
     a.seq_lens = view(o[4], "seq_lens", {B}, {at::kInt}, gpu);
     const at::Tensor out = given_or(o[6], "out", {B, nq, D}, type, gpu);
     a.out = view(out, "out", {B, nq, D}, half, gpu);
-    const int with_lse = PyObject_IsTrue(o[7]);
-    if (with_lse < 0)
-        throw python_error();
+    const bool with_lse = truth(o[7]);
     at::Tensor lse, keep;
     if (with_lse) {
         lse = make({B, nq}, at::kFloat, gpu);
@@ -347,14 +432,6 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-int64_t integer(PyObject *o)
-{
-    const long long n = PyLong_AsLongLong(o);
-    if (n == -1 && PyErr_Occurred())
-        throw python_error();
-    return n;
-}
-
 PyObject *bytes_of(int64_t n)
 {
     if (n < 0)
@@ -362,19 +439,34 @@ PyObject *bytes_of(int64_t n)
     return PyLong_FromLongLong(n);
 }
 
-// linear_workspace(batch, ntokens, H, P, N, G)
-PyObject *linear_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+template <typename Args>
+PyObject *recurrence_workspace(const Recurrence<Args> &fn, PyObject *const *o)
 {
-    HANDLE_TH_ERRORS
-    count(n, 6);
-    ssu_linear_args a{};
+    Args a{};
     a.batch = i32(integer(o[0]), "batch");
     a.ntokens = integer(o[1]);
     a.nheads = i32(integer(o[2]), "H");
     a.headdim = i32(integer(o[3]), "P");
     a.dstate = i32(integer(o[4]), "N");
     a.ngroups = i32(integer(o[5]), "G");
-    return bytes_of(ssu_linear_attention_workspace(&a));
+    return bytes_of(fn.need(&a));
+}
+
+// linear_workspace(batch, ntokens, H, P, N, G)
+PyObject *linear_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    return recurrence_workspace(kLinear, o);
+    END_HANDLE_TH_ERRORS
+}
+
+// delta_workspace(the same)
+PyObject *delta_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    return recurrence_workspace(kDelta, o);
     END_HANDLE_TH_ERRORS
 }
 
@@ -409,9 +501,12 @@ PyCFunction fast()
 
 PyMethodDef methods[] = {
     {"linear", fast<linear>(), METH_FASTCALL, nullptr},
+    {"delta", fast<delta>(), METH_FASTCALL, nullptr},
+    {"norm", fast<norm>(), METH_FASTCALL, nullptr},
     {"qk", fast<qk>(), METH_FASTCALL, nullptr},
     {"attention", fast<attention>(), METH_FASTCALL, nullptr},
     {"linear_workspace", fast<linear_workspace>(), METH_FASTCALL, nullptr},
+    {"delta_workspace", fast<delta_workspace>(), METH_FASTCALL, nullptr},
     {"attention_workspace", fast<attention_workspace>(), METH_FASTCALL, nullptr},
     {"errors", errors, METH_O, "Set the class that a failed call raises: cls(status, where)."},
     {nullptr, nullptr, 0, nullptr},

@@ -1,0 +1,894 @@
+// gated_delta.hip -- the gated delta rule on MI355X (gfx950):
+// ssu_gated_delta_rule over whole prompts, ssu_gated_delta_rule_step for one
+// token per request. The operation is stated in include/ssu.h.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "host_checks.h"
+#include "internal.h"
+#include "recurrence.h"
+#include "seq_common.h"
+
+namespace ssu {
+namespace {
+
+constexpr float kFaint = 1e-6f;  // beside the squares of q and k that are normalized
+
+__device__ __forceinline__ float inverse_length(float squares) { return 1.0f / sqrtf(squares + kFaint); }
+
+struct StepParams {
+    LinearParams a;
+    int32_t normalize;
+};
+
+// One token per request. One wave owns RPI * R rows p of one (request, head): a
+// row's N values are split over LPR = N / 4 lanes (N = 256: 32 lanes with two
+// chunks), one dwordx4 each, so that one instruction moves 1 KiB of contiguous
+// state. Memory-bound by the state, read and written once, past the caches; what
+// does not depend on the slot is requested first, since vector loads return in order.
+// What a row recalls of k has to be known before the row is written: two sums over
+// its lanes, one behind the other, instead of the one of linear attention.
+template <int N, int R>
+__global__ void __launch_bounds__(64) ssu_delta_step_kernel(const StepParams sp)
+{
+    constexpr int VEC = N > 128 ? N / 128 : 1;
+    constexpr int LPR = N / (4 * VEC);
+    constexpr int RPI = 64 / LPR;
+    static_assert(R <= LPR, "one writer lane per row");
+    const LinearParams &p = sp.a;
+    const int id = xcd_order(static_cast<int>(blockIdx.x), p.total);
+    const int tile = id % p.tiles, bh = id / p.tiles;
+    const int h = __builtin_amdgcn_readfirstlane(bh % p.nheads), b = __builtin_amdgcn_readfirstlane(bh / p.nheads);
+    const int grp = __builtin_amdgcn_readfirstlane(h / p.heads_per_group);
+    const int lane = static_cast<int>(threadIdx.x), c = lane % LPR, sub = lane / LPR;
+    const int row0 = __builtin_amdgcn_readfirstlane(tile * RPI * R) + sub;
+
+    const uint16_t *const qt = p.q + b * p.q_t + grp * p.q_g, *const kt = p.k + b * p.k_t + grp * p.k_g;
+    const uint16_t *const vt = p.v + b * p.v_t + h * p.v_h;
+    u32x2 qw[VEC], kw[VEC];
+    uint16_t vw[R];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        qw[e] = *reinterpret_cast<const u32x2_a2 *>(qt + 4 * c + 128 * e);
+        kw[e] = *reinterpret_cast<const u32x2_a2 *>(kt + 4 * c + 128 * e);
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        vw[j] = vt[min(row0 + j * RPI, p.headdim - 1)];
+
+    const int64_t slot = p.idx64 ? load_ro(static_cast<const int64_t *>(p.idx) + b)
+                                 : static_cast<int64_t>(load_ro(static_cast<const int32_t *>(p.idx) + b));
+    if (slot < 0 || slot >= p.pool_slots)
+        return;  // padding
+    float *const state = p.state + slot * p.s_slot + h * p.s_head + row0 * p.s_row + 4 * c;
+    f32x4 s[R][VEC];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            s[j][e] = row0 + j * RPI < p.headdim ? load4<true>(state + j * RPI * p.s_row + 128 * e) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const float a = exp_f32(load_ro(p.decay + (b * p.d_t + h * p.d_h)));
+    const float beta = p.beta ? load_ro(p.beta + (b * p.b_t + h * p.b_h)) : 1.0f;
+    f32x4 q[VEC], k[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[e][i] = i % 2 ? Bf16::hi(qw[e][i / 2]) : Bf16::lo(qw[e][i / 2]);
+            k[e][i] = i % 2 ? Bf16::hi(kw[e][i / 2]) : Bf16::lo(kw[e][i / 2]);
+        }
+    float qscale = p.scale;
+    if (sp.normalize) {
+        float qq = 0.0f, kk = 0.0f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qq = fmaf(q[e][i], q[e][i], qq);
+                kk = fmaf(k[e][i], k[e][i], kk);
+            }
+        qscale *= inverse_length(sum_lanes<LPR>(qq));
+        const float length = inverse_length(sum_lanes<LPR>(kk));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            k[e] *= length;
+    }
+    float mine = 0.0f;  // row c of this lane's R
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[j][e][i] *= a;
+                x = fmaf(s[j][e][i], k[e][i], x);
+            }
+        const float u = beta * (Bf16::lo(vw[j]) - sum_lanes<LPR>(x));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[j][e][i] = fmaf(u, k[e][i], s[j][e][i]);
+                y = fmaf(s[j][e][i], q[e][i], y);
+            }
+            if (row0 + j * RPI < p.headdim)
+                store4<true>(state + j * RPI * p.s_row + 128 * e, s[j][e]);
+        }
+        y = sum_lanes<LPR>(y);
+        mine = c == j ? y : mine;
+    }
+    if (c < R && row0 + c * RPI < p.headdim)
+        p.out[b * p.o_t + h * p.o_h + row0 + c * RPI] = Bf16::round(qscale * mine);
+}
+
+// Prompts, 32 tokens (a chunk) at a time. With L_i the decays' logarithms summed
+// from the chunk's start, S the state before it and k, q normalized if asked:
+//
+//   u_i = beta_i (v_i - exp(L_i) S k_i - sum_{j < i} exp(L_i - L_j) (k_i . k_j) u_j)
+//
+// is a triangular system in the chunk's u, the same for all columns p of a head:
+// with X its inverse, u = X diag(beta) (v - diag(exp(L)) S k), and
+//
+//   out_i = scale * ( exp(L_i) S q_i + sum_{j <= i} exp(L_i - L_j) (k_j . q_i) u_j )
+//   S     = exp(L_31) S + sum_j exp(L_31 - L_j) u_j k_j^T
+//
+// What does not depend on the state (X diag(beta), the weights of u in out, the
+// exponentials) comes from a first kernel, all chunks and heads at once, as
+// fragments of the second kernel's products in bf16 pieces; the second kernel takes
+// the chunks of a sequence in order.
+constexpr int kFragments = 10;  // 16 bytes a lane: X's two tiles of 16 tokens in 3 pieces, the weights' in 2
+constexpr int kSums = 128;      // floats: exp(L_i) / |k_i|, exp(L_31 - L_i) / |k_i|, scale exp(L_i) / |q_i|, exp(L_31), finite
+
+struct DeltaParams {
+    LinearParams a;
+    u32x4 *fragments;  // [chunks, nheads, kFragments, 64]
+    float *sums;       // [chunks, nheads, kSums]
+    int32_t normalize, dstate;
+};
+
+// Two values as three bf16 each (2^-24 relative).
+__device__ __forceinline__ void split_triple(float x, float y, uint32_t &a, uint32_t &b, uint32_t &c)
+{
+    a = pack2<Bf16>(x, y);
+    const float x1 = x - Bf16::lo(a), y1 = y - Bf16::hi(a);
+    split_pair(x1, y1, b, c);
+}
+
+struct Pieces {
+    u32x4 a, b, c;
+};
+
+__device__ __forceinline__ Pieces split_triple(const f32x4 &x, const f32x4 &y)
+{
+    Pieces p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f32x4 &f = e < 2 ? x : y;
+        uint32_t a, b, c;
+        split_triple(f[2 * e % 4], f[2 * e % 4 + 1], a, b, c);
+        p.a[e] = a;
+        p.b[e] = b;
+        p.c[e] = c;
+    }
+    return p;
+}
+
+__device__ __forceinline__ f32x4 halves(u32x2 w) { return f32x4{Bf16::lo(w[0]), Bf16::hi(w[0]), Bf16::lo(w[1]), Bf16::hi(w[1])}; }
+
+// acc * 0 added up: 0, or NaN if one is not finite.
+__device__ __forceinline__ float unless_finite(const f32x4 &x, float zero)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        zero = fmaf(x[r], 0.0f, zero);
+    return zero;
+}
+
+// A wave per chunk and head. The scores of two tiles of 16 tokens come out of the
+// products with 4 consecutive j per lane and i = its lane % 16, which is how a
+// fragment with rows i wants them. The triangle's diagonal tiles are inverted by
+// substitution (a product of powers would lose digits to keys that repeat), a column
+// per lane; the tile below them is -X11 L10 X00, in fp32 matrix products, taken
+// transposed so that it too comes out as a fragment.
+template <int N>
+__global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaParams p)
+{
+    constexpr int KS = N / 32, PITCH = 20;
+    const LinearParams &a = p.a;
+    __shared__ __attribute__((aligned(16))) float lower[4][2][16 * PITCH + 4], inverse[4][2][16 * PITCH + 4];
+    __shared__ __attribute__((aligned(16))) float lsum[4][32], lrest[4][32], lbeta[4][32], lk[4][32], lq[4][32];
+    __shared__ int owner;
+    __shared__ int64_t found[2];
+
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int blocks = (a.nheads + 3) / 4;
+    const int f = static_cast<int>(blockIdx.x) / blocks, h = static_cast<int>(blockIdx.x) % blocks * 4 + wave;
+
+    // chunk f of all: sequence b's are cu[b] / 32 + b and the following (distinct
+    // for ordered sequences; otherwise the first to come has it)
+    if (tid == 0)
+        owner = -1;
+    __syncthreads();
+    for (int b = tid; b < a.batch; b += 256) {
+        const int64_t slot = load_index(a.idx, a.idx64, b);
+        const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
+        const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
+        const int64_t s = f - (lo / kChunk + b);
+        if (s >= 0 && s * kChunk < hi - lo && slot >= 0 && slot < a.pool_slots && atomicCAS(&owner, -1, b) == -1) {
+            found[0] = lo + s * kChunk;
+            found[1] = min(hi - (lo + s * kChunk), int64_t(kChunk));
+        }
+    }
+    __syncthreads();
+    if (owner < 0 || h >= a.nheads)
+        return;
+    const int64_t begin = uniform(found[0]);
+    const int rows = __builtin_amdgcn_readfirstlane(static_cast<int>(found[1]));
+    const int grp = h / a.heads_per_group;
+
+    // rows behind the sequence's end come from its last row and have no gain
+    u32x4 kf[2][KS], qf[2][KS];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int64_t row = begin + min(16 * t + c, rows - 1);
+        const uint16_t *const kr = a.k + row * a.k_t + grp * a.k_g + 8 * g, *const qr = a.q + row * a.q_t + grp * a.q_g + 8 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const bool in = 32 * s + 8 * g < p.dstate;
+            kf[t][s] = in ? *reinterpret_cast<const u32x4_a2 *>(kr + 32 * s) : u32x4{0, 0, 0, 0};
+            qf[t][s] = in ? *reinterpret_cast<const u32x4_a2 *>(qr + 32 * s) : u32x4{0, 0, 0, 0};
+        }
+    }
+    const int tok = lane % 32;
+    const int64_t own = begin + min(tok, rows - 1);
+    const float decay = a.decay[own * a.d_t + h * a.d_h];
+    const float gain = a.beta ? a.beta[own * a.b_t + h * a.b_h] : 1.0f;
+
+    // L in units of log 2 and fp64, kept as fp32 and what that leaves
+    const bool in = tok < rows;
+    double sum = in ? static_cast<double>(decay < kDecayFloor ? kDecayFloor : decay) * 1.4426950408889634 : 0.0;
+    sum += lanes_up<0x111, 0xf>(sum);
+    sum += lanes_up<0x112, 0xf>(sum);
+    sum += lanes_up<0x114, 0xf>(sum);
+    sum += lanes_up<0x118, 0xf>(sum);
+    sum += lanes_up<0x142, 0xa>(sum);
+    const double all = lane_of(sum, 31);
+    if (lane < 32) {
+        lsum[wave][lane] = static_cast<float>(sum);
+        lrest[wave][lane] = static_cast<float>(sum - static_cast<double>(static_cast<float>(sum)));
+        lbeta[wave][lane] = in ? gain : 0.0f;
+    }
+
+    // scores: rows j (4 g + r of its tile), columns i (c of its)
+    f32x4 k00 = {}, k11 = {}, k10 = {}, q00 = {}, q01 = {}, q11 = {};  // k10: rows 16 + 4 g + r, columns c
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        k00 = Mma<Bf16>::run(kf[0][s], kf[0][s], k00);
+        k11 = Mma<Bf16>::run(kf[1][s], kf[1][s], k11);
+        k10 = Mma<Bf16>::run(kf[1][s], kf[0][s], k10);
+        q00 = Mma<Bf16>::run(kf[0][s], qf[0][s], q00);
+        q01 = Mma<Bf16>::run(kf[0][s], qf[1][s], q01);
+        q11 = Mma<Bf16>::run(kf[1][s], qf[1][s], q11);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        float kk = 0.0f, qq = 0.0f;
+        if (p.normalize) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t kw = kf[t][s][e], qw = qf[t][s][e];
+                    kk = fmaf(Bf16::lo(kw), Bf16::lo(kw), fmaf(Bf16::hi(kw), Bf16::hi(kw), kk));
+                    qq = fmaf(Bf16::lo(qw), Bf16::lo(qw), fmaf(Bf16::hi(qw), Bf16::hi(qw), qq));
+                }
+            kk += __shfl_xor(kk, 16);
+            kk += __shfl_xor(kk, 32);
+            qq += __shfl_xor(qq, 16);
+            qq += __shfl_xor(qq, 32);
+        }
+        if (g == 0) {
+            lk[wave][16 * t + c] = p.normalize ? inverse_length(kk) : 1.0f;
+            lq[wave][16 * t + c] = p.normalize ? inverse_length(qq) : 1.0f;
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+
+    struct Token {
+        float sum, rest, beta, k, q;
+    };
+    auto token = [&](int i) { return Token{lsum[wave][i], lrest[wave][i], lbeta[wave][i], lk[wave][i], lq[wave][i]}; };
+    auto decayed = [](const Token &i, const Token &j) { return __builtin_amdgcn_exp2f((i.sum - j.sum) + (i.rest - j.rest)); };
+    const Token at0 = token(c), at1 = token(16 + c);  // i of the columns
+    f32x4 beta0, beta1;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int j = 4 * g + r;
+        const Token j0 = token(j), j1 = token(16 + j);
+        beta0[r] = j0.beta;
+        beta1[r] = j1.beta;
+        const float d00 = decayed(at0, j0), d11 = decayed(at1, j1), d01 = decayed(at1, j0);
+        float x = k00[r] * (at0.beta * d00) * (at0.k * j0.k), y = k11[r] * (at1.beta * d11) * (at1.k * j1.k);
+        float z = q00[r] * d00 * (at0.q * j0.k), w = q11[r] * d11 * (at1.q * j1.k);
+        asm("" : "+v"(x), "+v"(y), "+v"(z), "+v"(w));  // (selects, not branches around the exponentials)
+        k00[r] = j < c ? x : 0.0f;
+        k11[r] = j < c ? y : 0.0f;
+        q00[r] = a.scale * (j <= c ? z : 0.0f);
+        q11[r] = a.scale * (j <= c ? w : 0.0f);
+        q01[r] = a.scale * (q01[r] * d01 * (at1.q * j0.k));
+        k10[r] = k10[r] * (j1.beta * decayed(j1, at0)) * (j1.k * at0.k);
+    }
+    *reinterpret_cast<f32x4 *>(&lower[wave][0][c * PITCH + 4 * g]) = k00;
+    *reinterpret_cast<f32x4 *>(&lower[wave][1][c * PITCH + 4 * g]) = k11;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+
+    // column c of the inverse of 1 + the tile (of tile g % 2)
+    const float *const tile = lower[wave][g % 2];
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float acc = i == c ? 1.0f : 0.0f;
+#pragma unroll
+        for (int j = 0; j < i; j += 4) {
+            const f32x4 l = *reinterpret_cast<const f32x4 *>(tile + i * PITCH + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < i)
+                    acc = fmaf(-l[e], x[j + e], acc);
+        }
+        x[i] = acc;
+    }
+    if (g < 2)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            inverse[wave][g][i * PITCH + c] = x[i];
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    f32x4 x00 = *reinterpret_cast<const f32x4 *>(&inverse[wave][0][c * PITCH + 4 * g]);
+    f32x4 x11 = *reinterpret_cast<const f32x4 *>(&inverse[wave][1][c * PITCH + 4 * g]);
+    f32x4 m = {}, x10 = {};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        m = __builtin_amdgcn_mfma_f32_16x16x4f32(k10[r], x11[r], m, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        x10 = __builtin_amdgcn_mfma_f32_16x16x4f32(inverse[wave][0][(4 * g + r) * PITCH + c], m[r], x10, 0, 0, 0);
+    x00 *= beta0;
+    x10 *= -beta0;
+    x11 *= beta1;
+
+    const int64_t id = static_cast<int64_t>(f) * a.nheads + h;
+    u32x4 *const out = p.fragments + id * kFragments * 64 + lane;
+    const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+    const Pieces x0 = split_triple(x00, none), x1 = split_triple(x10, x11);
+    out[0] = x0.a;
+    out[64] = x0.b;
+    out[128] = x0.c;
+    out[192] = x1.a;
+    out[256] = x1.b;
+    out[320] = x1.c;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f32x4 &w = e < 2 ? (t == 0 ? q00 : q01) : t == 0 ? none : q11;
+            uint32_t wh, wl;
+            split_pair(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
+            hi[e] = wh;
+            lo[e] = wl;
+        }
+        out[64 * (6 + 2 * t)] = hi;
+        out[64 * (7 + 2 * t)] = lo;
+    }
+    const float grow = __builtin_amdgcn_exp2f(static_cast<float>(sum)), whole = __builtin_amdgcn_exp2f(static_cast<float>(all));
+    const float kept = grow * lk[wave][tok], late = in ? __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) * lk[wave][tok] : 0.0f;
+    const float asked = a.scale * grow * lq[wave][tok];
+    float zero = fmaf(kept, 0.0f, fmaf(late, 0.0f, fmaf(asked, 0.0f, whole * 0.0f)));
+    for (const f32x4 &v : {x00, x10, x11, q00, q01, q11})
+        zero = unless_finite(v, zero);
+    const bool finite = !__any(zero != 0.0f);
+    float *const s = p.sums + id * kSums;
+    if (lane < 32) {
+        s[lane] = kept;
+        s[32 + lane] = late;
+        s[64 + lane] = asked;
+    }
+    if (lane == 0) {
+        s[96] = whole;
+        s[97] = finite ? 1.0f : 0.0f;
+    }
+}
+
+// One workgroup takes one head's 16 CT columns of v (rows p of the state) of a
+// sequence; its WN waves share N out, each with its part of the state in registers,
+// as the result tiles of the update's product: a lane has, of row p = lane % 16, n =
+// 32 s + 8 g + 0 .. 7. Operands are arranged so that nothing is exchanged between lanes:
+// a lane's 8 values are a fragment of the products with k and q, 16 bytes of a row of
+// which are the other; S k comes out with 4 consecutive tokens per lane, and those of two
+// 16-token tiles are a fragment of the products with the inverse, as u is of those with
+// k and the weights. Only k for the update and v are read transposed from LDS. The waves'
+// shares of S k and S q are added up through LDS, one barrier a chunk; what follows from them
+// every wave computes for itself.
+template <int N, int WN, int CT>
+__global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const DeltaParams p)
+{
+    constexpr int NW = N / WN, KS = NW / 32, MT = NW / 16;
+    constexpr int KP = NW + 8, VP = 16 * CT + 8;  // pitches in LDS
+    __shared__ __attribute__((aligned(16))) uint16_t lk[WN][kChunk * KP], lv[WN][kChunk * VP];
+    __shared__ f32x4 shares[WN > 1 ? 2 : 1][WN > 1 ? WN : 1][CT][4][64];
+    __shared__ float single[2][WN][CT + 1][64];
+
+    const LinearParams &a = p.a;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wn = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // workgroups go round the 8 XCDs: the columns of a head, which share its k, q
+    // and fragments, beside each other on one
+    const int id = static_cast<int>(blockIdx.x) / 8, unit = id / a.tiles * 8 + static_cast<int>(blockIdx.x) % 8;
+    if (unit >= a.total)
+        return;
+    const int b = unit / a.nheads, h = unit % a.nheads, grp = h / a.heads_per_group;
+    const int p0 = id % a.tiles * 16 * CT;
+    const int64_t slot = uniform(load_index(a.idx, a.idx64, b));
+    const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
+    const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
+    if (slot < 0 || slot >= a.pool_slots || hi == lo)
+        return;
+    const int total = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo)), chunks = (total + kChunk - 1) / kChunk;
+    const int n0 = wn * NW + 8 * g;
+
+    f32x4 st[CT][MT];
+    float *const pool = a.state + slot * a.s_slot + h * a.s_head + (p0 + c) * a.s_row + n0;
+    const bool in_n = N >= 64 || n0 < p.dstate;  // (N = 16 in a tile of 32)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            st[ct][m] = p0 + 16 * ct < a.headdim && in_n
+                            ? *reinterpret_cast<const f32x4 *>(pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2))
+                            : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // a chunk's operands; rows behind the end come from the last one
+    u32x4 kf[2][KS], qf[2][KS], vf[CT], xf[6], wf[4];
+    f32x4 kept[2], late[2];
+    float asked[2], whole, finite;
+    const uint16_t *const kb = a.k + lo * a.k_t + grp * a.k_g + n0, *const qb = a.q + lo * a.q_t + grp * a.q_g + n0;
+    const uint16_t *const vb = a.v + lo * a.v_t + h * a.v_h;
+    const int64_t first = (lo / kChunk + b) * a.nheads + h;
+    auto request_kq = [&](int i) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int64_t row = min(i * kChunk + 16 * t + c, total - 1);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                kf[t][s] = in_n ? *reinterpret_cast<const u32x4_a2 *>(kb + row * a.k_t + 32 * s) : u32x4{0, 0, 0, 0};
+                qf[t][s] = in_n ? *reinterpret_cast<const u32x4_a2 *>(qb + row * a.q_t + 32 * s) : u32x4{0, 0, 0, 0};
+            }
+        }
+    };
+    constexpr int VT = 32 / CT;  // tokens that one load of v reads
+    const int vtok = lane / (2 * CT), vcol = 8 * (lane % (2 * CT));
+    auto request_v = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < CT; ++e) {
+            const int64_t row = min(i * kChunk + e * VT + vtok, total - 1);
+            vf[e] = p0 + vcol < a.headdim ? *reinterpret_cast<const u32x4_a2 *>(vb + row * a.v_t + p0 + vcol) : u32x4{0, 0, 0, 0};
+        }
+    };
+    auto request_x = [&](int i) {
+        const u32x4 *const src = p.fragments + (first + static_cast<int64_t>(i) * a.nheads) * kFragments * 64 + lane;
+#pragma unroll
+        for (int e = 0; e < 6; ++e)
+            xf[e] = src[64 * e];
+        const float *const s = p.sums + (first + static_cast<int64_t>(i) * a.nheads) * kSums;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            kept[t] = *reinterpret_cast<const f32x4 *>(s + 16 * t + 4 * g);
+        finite = s[97];
+    };
+    auto request_w = [&](int i) {
+        const u32x4 *const src = p.fragments + (first + static_cast<int64_t>(i) * a.nheads) * kFragments * 64 + lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            wf[e] = src[64 * (6 + e)];
+        const float *const s = p.sums + (first + static_cast<int64_t>(i) * a.nheads) * kSums;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            asked[t] = s[64 + 16 * t + c];
+            late[t] = *reinterpret_cast<const f32x4 *>(s + 32 + 16 * t + 4 * g);
+        }
+        whole = s[96];
+    };
+    request_kq(0);
+    request_v(0);
+    request_x(0);
+    request_w(0);
+
+    for (int i = 0; i < chunks; ++i) {
+        const int next = min(i + 1, chunks - 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                *reinterpret_cast<u32x4 *>(&lk[wn][(16 * t + c) * KP + 32 * s + 8 * g]) = kf[t][s];
+#pragma unroll
+        for (int e = 0; e < CT; ++e)
+            *reinterpret_cast<u32x4 *>(&lv[wn][(e * VT + vtok) * VP + vcol]) = vf[e];
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+
+        // S k (rows tokens, columns p) and S q (rows p, columns tokens), this wave's n
+        f32x4 sk[CT][2], sq[CT][2];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sk[ct][t] = sq[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const Pieces f = split_triple(st[ct][2 * s], st[ct][2 * s + 1]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    sk[ct][t] = Mma<Bf16>::run(kf[t][s], f.c, sk[ct][t]);
+                    sq[ct][t] = Mma<Bf16>::run(f.b, qf[t][s], sq[ct][t]);
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    sk[ct][t] = Mma<Bf16>::run(kf[t][s], f.b, sk[ct][t]);
+                    sq[ct][t] = Mma<Bf16>::run(f.a, qf[t][s], sq[ct][t]);
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    sk[ct][t] = Mma<Bf16>::run(kf[t][s], f.a, sk[ct][t]);
+            }
+        request_kq(next);
+        request_v(next);
+        if constexpr (WN > 1) {
+            auto &sh = shares[i & 1];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    sh[wn][ct][t][lane] = sk[ct][t];
+                    sh[wn][ct][2 + t][lane] = sq[ct][t];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    sk[ct][t] = sh[0][ct][t][lane];
+                    sq[ct][t] = sh[0][ct][2 + t][lane];
+#pragma unroll
+                    for (int w = 1; w < WN; ++w) {
+                        sk[ct][t] += sh[w][ct][t][lane];
+                        sq[ct][t] += sh[w][ct][2 + t][lane];
+                    }
+                }
+        }
+
+        // u: rows tokens, columns p
+        f32x4 u[CT][2];
+        float zero = finite - 1.0f;
+        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            f32x4 r[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                r[t] = halves(read_transposed(&lv[wn][vtr + 16 * t * VP + 16 * ct])) - kept[t] * sk[ct][t];
+            const Pieces f = split_triple(r[0], r[1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+                y = Mma<Bf16>::run(xf[3 * t], f.c, y);
+                y = Mma<Bf16>::run(xf[3 * t + 1], f.b, y);
+                y = Mma<Bf16>::run(xf[3 * t + 2], f.a, y);
+                y = Mma<Bf16>::run(xf[3 * t], f.b, y);
+                y = Mma<Bf16>::run(xf[3 * t + 1], f.a, y);
+                y = Mma<Bf16>::run(xf[3 * t], f.a, y);
+                u[ct][t] = y;
+                zero = unless_finite(y, zero);
+            }
+        }
+        if (__builtin_expect(!__any(zero != 0.0f), 1)) {
+            // out: rows p, columns tokens
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (WN > 1 && wn % 2 != t)
+                    continue;
+                if (WN > 2 && wn >= 2)
+                    continue;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    u32x4 uh, ul;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t wh, wl;
+                        split_pair(u[ct][e / 2][2 * e % 4], u[ct][e / 2][2 * e % 4 + 1], wh, wl);
+                        uh[e] = wh;
+                        ul[e] = wl;
+                    }
+                    f32x4 o = asked[t] * sq[ct][t];
+                    o = Mma<Bf16>::run(ul, wf[2 * t], o);
+                    o = Mma<Bf16>::run(uh, wf[2 * t + 1], o);
+                    o = Mma<Bf16>::run(uh, wf[2 * t], o);
+                    const int row = i * kChunk + 16 * t + c;
+                    if (row < total && p0 + 16 * ct < a.headdim)
+                        *reinterpret_cast<u32x2_a2 *>(a.out + (lo + row) * a.o_t + h * a.o_h + p0 + 16 * ct + 4 * g) =
+                            u32x2{pack2<Bf16>(o[0], o[1]), pack2<Bf16>(o[2], o[3])};
+                }
+            }
+            // the state behind the chunk
+            const int ktr = (4 * g + c / 4) * KP + 8 * (c % 4);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const Pieces f = split_triple(late[0] * u[ct][0], late[1] * u[ct][1]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint16_t *const at = &lk[wn][ktr + 32 * (m / 2) + 4 * (m % 2)];
+                    const u32x2 x = read_transposed(at), y = read_transposed(at + 16 * KP);
+                    const u32x4 kt = {x[0], x[1], y[0], y[1]};
+                    f32x4 s = st[ct][m] * whole;
+                    s = Mma<Bf16>::run(kt, f.c, s);
+                    s = Mma<Bf16>::run(kt, f.b, s);
+                    st[ct][m] = Mma<Bf16>::run(kt, f.a, s);
+                }
+            }
+        } else {
+            // Not finite: the pieces in 16 bits make NaN of infinities, and NaN of one
+            // token would reach those before it through the inverse's zeros. Token by
+            // token, as in the kernel of steps (all waves alike: u is the same in each).
+            const int rows = min(total - i * kChunk, kChunk);
+#pragma unroll 1
+            for (int t = 0; t < rows; ++t) {
+                const int64_t tok = lo + i * kChunk + t;
+                const float keep = exp_f32(a.decay[tok * a.d_t + h * a.d_h]);
+                const float beta = a.beta ? a.beta[tok * a.b_t + h * a.b_h] : 1.0f;
+                const uint16_t *const kr = a.k + tok * a.k_t + grp * a.k_g + n0, *const qr = a.q + tok * a.q_t + grp * a.q_g + n0;
+                // sums over this wave's n, then over the waves'
+                auto whole_sums = [&](float (&x)[CT + 1], float (&box)[WN][CT + 1][64]) {
+#pragma unroll
+                    for (int e = 0; e <= CT; ++e) {
+                        x[e] += __shfl_xor(x[e], 16);
+                        x[e] += __shfl_xor(x[e], 32);
+                        if (WN > 1)
+                            box[wn][e][lane] = x[e];
+                    }
+                    if constexpr (WN > 1) {
+                        __syncthreads();
+#pragma unroll
+                        for (int e = 0; e <= CT; ++e) {
+                            x[e] = box[0][e][lane];
+#pragma unroll
+                            for (int w = 1; w < WN; ++w)
+                                x[e] += box[w][e][lane];
+                        }
+                    }
+                };
+                float x[CT + 1] = {}, y[CT + 1] = {}, un[CT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const f32x4 kn = in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(kr + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[CT] = fmaf(kn[e], kn[e], x[CT]);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            st[ct][m][e] *= keep;
+                            x[ct] = fmaf(st[ct][m][e], kn[e], x[ct]);
+                        }
+                    }
+                }
+                whole_sums(x, single[0]);
+                const float length = p.normalize ? inverse_length(x[CT]) : 1.0f;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const float v = Bf16::lo(a.v[tok * a.v_t + h * a.v_h + min(p0 + 16 * ct + c, a.headdim - 1)]);
+                    un[ct] = beta * (v - length * x[ct]);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const f32x4 kn = in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(kr + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
+                    const f32x4 qn = in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(qr + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[CT] = fmaf(qn[e], qn[e], y[CT]);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            if (in_n)  // (an infinite u times the zeros behind N is NaN)
+                                st[ct][m][e] = fmaf(un[ct], length * kn[e], st[ct][m][e]);
+                            y[ct] = fmaf(st[ct][m][e], qn[e], y[ct]);
+                        }
+                    }
+                }
+                whole_sums(y, single[1]);
+                if (wn == 0 && g == 0)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        if (p0 + 16 * ct < a.headdim)
+                            a.out[tok * a.o_t + h * a.o_h + p0 + 16 * ct + c] =
+                                Bf16::round(a.scale * (p.normalize ? inverse_length(y[CT]) : 1.0f) * y[ct]);
+            }
+        }
+        request_x(next);
+        request_w(next);
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            if (p0 + 16 * ct < a.headdim && in_n)
+                *reinterpret_cast<f32x4 *>(pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2)) = st[ct][m];
+}
+
+using StepFn = void (*)(StepParams);
+
+struct StepKernel {
+    StepFn fn;
+    int rows;  // of the state per workgroup
+};
+
+// LOADS dwordx4 of state per lane.
+template <int N, int LOADS>
+constexpr StepKernel step_kernel()
+{
+    constexpr int VEC = N > 128 ? N / 128 : 1;
+    return {&ssu_delta_step_kernel<N, LOADS / VEC>, 64 / (N / (4 * VEC)) * LOADS / VEC};
+}
+
+template <int LOADS>
+StepKernel step_kernel(int N)
+{
+    switch (N) {
+    case 16: return step_kernel<16, LOADS>();
+    case 32: return step_kernel<32, LOADS>();
+    case 64: return step_kernel<64, LOADS>();
+    case 128: return step_kernel<128, LOADS>();
+    default: return step_kernel<256, LOADS>();
+    }
+}
+
+using DeltaFn = void (*)(DeltaParams);
+
+struct ChunkKernel {
+    DeltaFn fn;
+    int waves, columns;
+};
+
+template <int N, int WN, int CT>
+constexpr ChunkKernel chunk_kernel()
+{
+    return {&ssu_delta_chunk_kernel<N, WN, CT>, WN, 16 * CT};
+}
+
+ChunkKernel chunk_kernel(int N, int64_t tiles)
+{
+    const bool many = tiles > 4 * kNumCUs;
+    if (N <= 32)
+        return many ? chunk_kernel<32, 1, 2>() : chunk_kernel<32, 1, 1>();
+    if (N == 64)
+        return many ? chunk_kernel<64, 1, 2>() : chunk_kernel<64, 2, 1>();
+    if (N == 128)
+        return many ? chunk_kernel<128, 2, 2>() : chunk_kernel<128, 4, 1>();
+    return many ? chunk_kernel<256, 4, 2>() : chunk_kernel<256, 4, 1>();
+}
+
+// ------------------------------------------------------------------ host --
+
+ssu_status check_delta(const ssu_delta_args &a, const char *who, bool prompts)
+{
+    if (a.normalize != 0 && a.normalize != 1)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s: normalize must be 0 or 1", who);
+    return check_linear(a, who, prompts);
+}
+
+// Launch of a step as linear attention's, by the bytes of state that it moves one way.
+ssu_status launch_step(const ssu_delta_args &a, hipStream_t stream)
+{
+    const int64_t mib = static_cast<int64_t>(a.batch) * a.nheads * a.headdim * a.dstate >> 18;
+    const StepKernel k = mib < 8 ? step_kernel<2>(a.dstate) : step_kernel<4>(a.dstate);
+    StepParams p{linear_params(a), a.normalize};
+    p.a.tiles = (a.headdim + k.rows - 1) / k.rows;
+    const int64_t groups = static_cast<int64_t>(a.batch) * a.nheads * p.a.tiles;
+    SSU_TRY(check_launch(groups, 64, "ssu_gated_delta_rule_step"));
+    p.a.total = static_cast<int>(groups);
+    DeviceGuard guard;
+    SSU_TRY(guard.enter(a.device));
+    size_t lds = 0;
+    if (mib >= 40) {
+        int dev = 0;
+        if (hipGetDevice(&dev) != hipSuccess)
+            return fail(SSU_ERR_HIP, "hipGetDevice failed");
+        const DeviceLimits lim = device_limits(dev);
+        lds = lds_for_cap(mib < 128 ? 16 : 14, lim.lds_cu, lim.lds_block);
+    }
+    const hipError_t e = launch_kernel(k.fn, p, groups, 64, lds, stream);
+    if (e != hipSuccess)
+        return fail(SSU_ERR_HIP, "launch of the delta rule's step failed: %s", hipGetErrorString(e));
+    return SSU_OK;
+}
+
+int64_t chunks_of(const ssu_delta_args &a) { return a.ntokens / kChunk + a.batch; }
+
+int64_t workspace_of(const ssu_delta_args &a)
+{
+    return a.ntokens == 0 ? 0 : chunks_of(a) * a.nheads * (kFragments * 1024 + kSums * 4);
+}
+
+ssu_status launch_chunks(const ssu_delta_args &a, hipStream_t stream)
+{
+    const int64_t bytes = workspace_of(a);
+    if (!a.workspace || a.workspace_bytes < bytes)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_gated_delta_rule: workspace of %lld bytes, %lld needed",
+                    static_cast<long long>(a.workspace ? a.workspace_bytes : 0), static_cast<long long>(bytes));
+    if (reinterpret_cast<uintptr_t>(a.workspace) % 16)
+        return fail(SSU_ERR_MISALIGNED, "ssu_gated_delta_rule: workspace must be 16-byte aligned");
+    const int64_t units = static_cast<int64_t>(a.batch) * a.nheads;
+    const ChunkKernel k = chunk_kernel(a.dstate, units * (a.headdim / 16));
+    DeltaParams p{};
+    p.a = linear_params(a);
+    p.a.tiles = (a.headdim + k.columns - 1) / k.columns;
+    p.a.total = static_cast<int>(units);
+    p.normalize = a.normalize;
+    p.dstate = a.dstate;
+    p.fragments = static_cast<u32x4 *>(a.workspace);
+    p.sums = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + chunks_of(a) * a.nheads * kFragments * 1024);
+    const int64_t first = chunks_of(a) * ((a.nheads + 3) / 4), second = (units + 7) / 8 * 8 * p.a.tiles;
+    SSU_TRY(check_launch(first, 256, "ssu_gated_delta_rule"));
+    SSU_TRY(check_launch(second, 64 * k.waves, "ssu_gated_delta_rule"));
+    const DeltaFn pairs = a.dstate <= 32 ? &ssu_delta_pairs_kernel<32> : a.dstate == 64 ? &ssu_delta_pairs_kernel<64>
+                        : a.dstate == 128 ? &ssu_delta_pairs_kernel<128> : &ssu_delta_pairs_kernel<256>;
+    DeviceGuard guard;
+    SSU_TRY(guard.enter(a.device));
+    hipError_t e = launch_kernel(pairs, p, first, 256, 0, stream);
+    if (e == hipSuccess)
+        e = launch_kernel(k.fn, p, second, 64 * k.waves, 0, stream);
+    if (e != hipSuccess)
+        return fail(SSU_ERR_HIP, "launch of the chunked delta rule failed: %s", hipGetErrorString(e));
+    return SSU_OK;
+}
+
+}  // namespace
+}  // namespace ssu
+
+extern "C" {
+
+int64_t ssu_gated_delta_rule_workspace(const ssu_delta_args *a)
+{
+    using namespace ssu;
+    if (!a || check_sizes(*a, "ssu_gated_delta_rule_workspace") != SSU_OK)
+        return -1;
+    return workspace_of(*a);
+}
+
+ssu_status ssu_gated_delta_rule(const ssu_delta_args *a, hipStream_t stream)
+{
+    using namespace ssu;
+    if (!a)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_gated_delta_rule: null args");
+    SSU_TRY(check_delta(*a, "ssu_gated_delta_rule", true));
+    if (a->batch == 0 || a->ntokens == 0)
+        return SSU_OK;
+    return launch_chunks(*a, stream);
+}
+
+ssu_status ssu_gated_delta_rule_step(const ssu_delta_args *a, hipStream_t stream)
+{
+    using namespace ssu;
+    if (!a)
+        return fail(SSU_ERR_INVALID_ARGUMENT, "ssu_gated_delta_rule_step: null args");
+    SSU_TRY(check_delta(*a, "ssu_gated_delta_rule_step", false));
+    if (a->batch == 0)
+        return SSU_OK;
+    return launch_step(*a, stream);
+}
+
+}  // extern "C"

@@ -89,6 +89,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((F{lo, hi}), H));
 }
 
+// Two fp32 values as a 16-bit pair each, rounded value and rounded remainder.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack2<Bf16>(x, y);
+    lo = pack2<Bf16>(x - Bf16::lo(hi), y - Bf16::hi(hi));
+}
+
 // The 16-bit halves of two words side by side: the low ones, the high ones.
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
@@ -123,6 +130,42 @@ __device__ __forceinline__ float sum_lanes(float x)
     if constexpr (LANES >= 64)
         x += __shfl_xor(x, 32);
     return x;
+}
+
+// A double from other lanes by DPP (zero where the lane has no source or its
+// row is not in MASK), and one lane's in all.
+template <int CTRL, int MASK>
+__device__ __forceinline__ double lanes_up(double x)
+{
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, MASK, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(v >> 32), CTRL, MASK, 0xf, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double lane_of(double x, int lane)
+{
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(x >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// 4 rows of 16 16-bit values in LDS, the lane's address being that of values
+// 4 (l % 4) .. of row (l % 16) / 4 of its 16 lanes' rows: the lane gets value
+// l % 16 of each.
+__device__ __forceinline__ u32x2 read_transposed(const uint16_t *p)
+{
+    using S4 = short __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) S4 *)(const_cast<uint16_t *>(p))));
 }
 
 // Inclusive sums over the wave's lanes, by DPP: within 16 lanes (lane - 1, - 2,
