@@ -592,6 +592,35 @@ int64_t ssu_paged_attention_workspace(const ssu_attn_args *args);
  * of a launch or more), SSU_ERR_MISALIGNED, SSU_ERR_HIP. */
 ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream);
 
+/* ----------------------------------------- attention over a shared prefix --
+ * ssu_paged_attention for a batch whose requests all begin with the same tokens
+ * (a system prompt, a document): request b attends to the n0 tokens of the
+ * prefix, K_j, V_j row j % page_size of page prefix_table[j / page_size], and then
+ * to its own seq_lens[b] of block_table, as one softmax over both:
+ *
+ *   n0 = min(max(prefix_len[0], 0), prefix_pages * page_size)
+ *
+ * The prefix is read once for the whole batch, and the products with it run on all
+ * requests' query heads of a key head at once. seq_lens[b] = 0: the prefix alone; negative:
+ * padding. Numerics as ssu_paged_attention, but the weights of the prefix's V are
+ * rounded to 16 bits once: 2^-9 (BF16; F16 2^-12) of the weighted mean of |V| at most,
+ * a pair would make half again as many products. All that is said there of
+ * visibility, infinities and repeated calls holds for the prefix.
+ */
+typedef struct ssu_shared_args {
+    ssu_attn_args attn;    /* the requests' own tokens, and all other operands */
+    ssu_view prefix_table; /* [prefix_pages] I32, stride[0] == 1 */
+    ssu_view prefix_len;   /* [1] I32 */
+    int64_t prefix_pages;  /* >= 0 */
+} ssu_shared_args;
+
+/* Bytes of workspace that ssu_shared_prefix_attention needs for `args` (only its
+ * sizes are read; -1 for sizes that it refuses). */
+int64_t ssu_shared_prefix_attention_workspace(const ssu_shared_args *args);
+
+/* Enqueue it on `stream`: conditions and errors of ssu_paged_attention. */
+ssu_status ssu_shared_prefix_attention(const ssu_shared_args *args, hipStream_t stream);
+
 /* ------------------------------------------ norm with the residual added --
  * What stands between the layers: the residual stream takes a layer's output and
  * the next layer's input is its norm, in 16 bits or in 8 with scales. For every

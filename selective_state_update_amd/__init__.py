@@ -582,7 +582,7 @@ def selective_scan(u, delta, A, B, C, state, D=None, delta_bias=None, delta_soft
 # --------------------------------------------------------------------------- #
 # Sequence operators of hybrid models: ssu_linear_attention(_step),
 # ssu_gated_delta_rule(_step), ssu_qk_norm_rope, ssu_add_rms_norm,
-# ssu_paged_attention
+# ssu_paged_attention, ssu_shared_prefix_attention
 # --------------------------------------------------------------------------- #
 # Checked, packed and launched by a native module (csrc/binding.cpp): the
 # smallest of these calls run for a few microseconds.
@@ -739,3 +739,27 @@ def paged_attention_workspace(batch, nq, nk, headdim, page_size, max_pages):
     of nk heads in pages of page_size and a table [batch, max_pages]; 0 where none
     is needed."""
     return _native.attention_workspace(batch, nq, nk, headdim, page_size, max_pages)
+
+
+def shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens, scale=None, out=None,
+                            return_lse=False, workspace=None, stream=None):
+    """paged_attention for a batch whose requests all begin with the same tokens (see
+    include/ssu.h, ssu_shared_prefix_attention), which are read once for all.
+
+    prefix_table [prefix_pages] int32, the prefix's pages; prefix_len [1] int32, its
+    tokens (on the GPU: a captured call sees what it holds at the replay); block_table
+    [batch, max_pages] and seq_lens [batch] are the requests' own tokens behind it
+    (0: the prefix alone; negative: padding). The rest, and what is returned, as in
+    paged_attention; ``workspace`` of shared_prefix_attention_workspace bytes.
+    Inference only: no gradient."""
+    if stream is not None:
+        with _on(stream, q):
+            return shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens, scale, out,
+                                           return_lse, workspace)
+    return _native.shared(q, k_cache, v_cache, block_table, seq_lens, scale, out, return_lse, workspace, prefix_table, prefix_len)
+
+
+def shared_prefix_attention_workspace(batch, nq, nk, headdim, page_size, max_pages, prefix_pages):
+    """Bytes of workspace that shared_prefix_attention needs: sizes as in
+    paged_attention_workspace, and a prefix of prefix_pages."""
+    return _native.shared_workspace(batch, nq, nk, headdim, page_size, max_pages, prefix_pages)

@@ -20,7 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", n) for n in ("ssu.hip", "block_copy.hip", "scan.hip", "linear_attention.hip",
                                                   "gated_delta.hip", "qk_norm_rope.hip", "rms_norm.hip",
-                                                  "paged_attention.hip")]
+                                                  "paged_attention.hip", "shared_prefix_attention.hip")]
 LIB = os.path.join(HERE, "libssu.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

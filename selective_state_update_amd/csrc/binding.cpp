@@ -1,6 +1,6 @@
 // binding.cpp -- the Python entry points of the sequence operators
 // (linear_attention, gated_delta_rule, their steps, qk_norm_rope, add_rms_norm,
-// paged_attention): tensors checked, turned into the views of include/ssu.h and passed on, with
+// paged_attention, shared_prefix_attention): tensors checked, turned into the views of include/ssu.h and passed on, with
 // outputs and workspaces from torch's allocator on torch's current stream.
 // Native because the operators' smallest calls run for 3 to 5 us and checking
 // and packing nine to twelve tensors in Python took 6 to 10.
@@ -384,11 +384,12 @@ PyObject *qk(PyObject *, PyObject *const *o, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// attention(q, k_cache, v_cache, block_table, seq_lens, scale | None, out | None, return_lse, workspace | None)
-PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
+// What both attentions share: o: q, k_cache, v_cache, block_table, seq_lens, scale | None, out | None, return_lse,
+// workspace | None. `fill` sets what only one of them has.
+template <typename Args, typename Fill>
+PyObject *attend(PyObject *const *o, Fill fill, int64_t (*need)(const Args *), ssu_status (*fn)(const Args *, hipStream_t),
+                 const char *where)
 {
-    HANDLE_TH_ERRORS
-    count(n, 9);
     const at::Tensor &q = tensor(o[0], "q"), &cache = tensor(o[1], "k_cache"), &table = tensor(o[3], "block_table");
     const int gpu = gpu_of(q, "q");
     if (q.dim() != 3 || cache.dim() != 4 || table.dim() != 2)
@@ -399,7 +400,8 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
     if (type != at::kBFloat16 && type != at::kHalf)
         refuse(PyExc_TypeError, std::string("q: dtype ") + c10::toString(type) + " not supported here");
     const int64_t B = q.size(0), nq = q.size(1), D = q.size(2);
-    ssu_attn_args a{};
+    Args args{};
+    ssu_attn_args &a = fill(args, gpu);
     a.batch = i32(B, "batch");
     a.nq = i32(nq, "Hq");
     a.nk = i32(cache.size(2), "Hk");
@@ -423,12 +425,40 @@ PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
         lse = make({B, nq}, at::kFloat, gpu);
         a.lse = view(lse, "lse", {B, nq}, {at::kFloat}, gpu);
     }
-    workspace(o[8], ssu_paged_attention_workspace(&a), gpu, a, keep);
-    call(&ssu_paged_attention, a, gpu, "ssu_paged_attention");
+    workspace(o[8], need(&args), gpu, a, keep);
+    call(fn, args, gpu, where);
     if (!with_lse)
         return object(o[6], out);
     PyObject *const first = object(o[6], out);
     return Py_BuildValue("(NN)", first, THPVariable_Wrap(lse));
+}
+
+// attention(as in attend)
+PyObject *attention(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 9);
+    const auto fill = [](ssu_attn_args &a, int) -> ssu_attn_args & { return a; };
+    return attend<ssu_attn_args>(o, fill, &ssu_paged_attention_workspace, &ssu_paged_attention, "ssu_paged_attention");
+    END_HANDLE_TH_ERRORS
+}
+
+// shared(as in attend, prefix_table, prefix_len)
+PyObject *shared(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 11);
+    const auto fill = [o](ssu_shared_args &a, int gpu) -> ssu_attn_args & {
+        const at::Tensor &prefix = tensor(o[9], "prefix_table");
+        if (prefix.dim() != 1)
+            refuse(PyExc_ValueError, "prefix_table must be [prefix_pages]");
+        a.prefix_pages = prefix.size(0);
+        a.prefix_table = view(prefix, "prefix_table", {a.prefix_pages}, {at::kInt}, gpu);
+        a.prefix_len = view(o[10], "prefix_len", {1}, {at::kInt}, gpu);
+        return a.attn;
+    };
+    return attend<ssu_shared_args>(o, fill, &ssu_shared_prefix_attention_workspace, &ssu_shared_prefix_attention,
+                                   "ssu_shared_prefix_attention");
     END_HANDLE_TH_ERRORS
 }
 
@@ -470,11 +500,8 @@ PyObject *delta_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// attention_workspace(batch, Hq, Hk, D, page_size, max_pages)
-PyObject *attention_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+ssu_attn_args attention_sizes(PyObject *const *o)
 {
-    HANDLE_TH_ERRORS
-    count(n, 6);
     ssu_attn_args a{};
     a.batch = i32(integer(o[0]), "batch");
     a.nq = i32(integer(o[1]), "Hq");
@@ -482,6 +509,27 @@ PyObject *attention_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
     a.headdim = i32(integer(o[3]), "D");
     a.page_size = i32(integer(o[4]), "page_size");
     a.max_pages = integer(o[5]);
+    return a;
+}
+
+// shared_workspace(batch, Hq, Hk, D, page_size, max_pages, prefix_pages)
+PyObject *shared_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 7);
+    ssu_shared_args a{};
+    a.attn = attention_sizes(o);
+    a.prefix_pages = integer(o[6]);
+    return bytes_of(ssu_shared_prefix_attention_workspace(&a));
+    END_HANDLE_TH_ERRORS
+}
+
+// attention_workspace(batch, Hq, Hk, D, page_size, max_pages)
+PyObject *attention_workspace(PyObject *, PyObject *const *o, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    const ssu_attn_args a = attention_sizes(o);
     return bytes_of(ssu_paged_attention_workspace(&a));
     END_HANDLE_TH_ERRORS
 }
@@ -505,8 +553,10 @@ PyMethodDef methods[] = {
     {"norm", fast<norm>(), METH_FASTCALL, nullptr},
     {"qk", fast<qk>(), METH_FASTCALL, nullptr},
     {"attention", fast<attention>(), METH_FASTCALL, nullptr},
+    {"shared", fast<shared>(), METH_FASTCALL, nullptr},
     {"linear_workspace", fast<linear_workspace>(), METH_FASTCALL, nullptr},
     {"delta_workspace", fast<delta_workspace>(), METH_FASTCALL, nullptr},
+    {"shared_workspace", fast<shared_workspace>(), METH_FASTCALL, nullptr},
     {"attention_workspace", fast<attention_workspace>(), METH_FASTCALL, nullptr},
     {"errors", errors, METH_O, "Set the class that a failed call raises: cls(status, where)."},
     {nullptr, nullptr, 0, nullptr},
