@@ -142,22 +142,49 @@ __global__ void __launch_bounds__(64) ssu_delta_step_kernel(const StepParams sp)
 // exponentials) comes from a first kernel, all chunks and heads at once, as
 // fragments of the second kernel's products in bf16 pieces; the second kernel takes
 // the chunks of a sequence in order.
-constexpr int kFragments = 10;  // 16 bytes a lane: X's two tiles of 16 tokens in 3 pieces, the weights' in 2
-constexpr int kSums = 128;      // floats: exp(L_i) / |k_i|, exp(L_31 - L_i) / |k_i|, scale exp(L_i) / |q_i|, exp(L_31), finite
+//
+// Of a chunk and head: 10 fragments of 64 lanes, X's two tiles of 16 tokens in 3 pieces
+// each and the weights' in 2, then 128 floats: exp(L_i) / |k_i|, exp(L_31 - L_i) / |k_i|,
+// scale exp(L_i) / |q_i|, exp(L_31), and 1 if all of it is finite.
+constexpr int kFragments = 10;
+constexpr int kUnits = kFragments * 64 + 32;  // of 16 bytes
 
 struct DeltaParams {
     LinearParams a;
-    u32x4 *fragments;  // [chunks, nheads, kFragments, 64]
-    float *sums;       // [chunks, nheads, kSums]
+    u32x4 *chunks;  // [chunks, nheads, kUnits]
     int32_t normalize, dstate;
 };
 
-// Two values as three bf16 each (2^-24 relative).
+// x less the low (high) bf16 of a word, exact: as a dot product of two pairs one
+// instruction instead of two. (The factors come from registers: as constants of the
+// instruction they are not a pair.)
+__device__ __forceinline__ float less_low(float x, uint32_t w)
+{
+    using H = __bf16 __attribute__((ext_vector_type(2)));
+    uint32_t f = 0x0000BF80u;  // -1, 0
+    asm("" : "+s"(f));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(H, w), __builtin_bit_cast(H, f), x, false);
+}
+
+__device__ __forceinline__ float less_high(float x, uint32_t w)
+{
+    using H = __bf16 __attribute__((ext_vector_type(2)));
+    uint32_t f = 0xBF800000u;  // 0, -1
+    asm("" : "+s"(f));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(H, w), __builtin_bit_cast(H, f), x, false);
+}
+
+// Two values as two bf16 each, and as three (2^-24 relative).
+__device__ __forceinline__ void split_double(float x, float y, uint32_t &a, uint32_t &b)
+{
+    a = pack2<Bf16>(x, y);
+    b = pack2<Bf16>(less_low(x, a), less_high(y, a));
+}
+
 __device__ __forceinline__ void split_triple(float x, float y, uint32_t &a, uint32_t &b, uint32_t &c)
 {
     a = pack2<Bf16>(x, y);
-    const float x1 = x - Bf16::lo(a), y1 = y - Bf16::hi(a);
-    split_pair(x1, y1, b, c);
+    split_double(less_low(x, a), less_high(y, a), b, c);
 }
 
 struct Pieces {
@@ -364,7 +391,7 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     x11 *= beta1;
 
     const int64_t id = static_cast<int64_t>(f) * a.nheads + h;
-    u32x4 *const out = p.fragments + id * kFragments * 64 + lane;
+    u32x4 *const out = p.chunks + id * kUnits + lane;
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
     const Pieces x0 = split_triple(x00, none), x1 = split_triple(x10, x11);
     out[0] = x0.a;
@@ -380,7 +407,7 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
         for (int e = 0; e < 4; ++e) {
             const f32x4 &w = e < 2 ? (t == 0 ? q00 : q01) : t == 0 ? none : q11;
             uint32_t wh, wl;
-            split_pair(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
+            split_double(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
             hi[e] = wh;
             lo[e] = wl;
         }
@@ -394,7 +421,7 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     for (const f32x4 &v : {x00, x10, x11, q00, q01, q11})
         zero = unless_finite(v, zero);
     const bool finite = !__any(zero != 0.0f);
-    float *const s = p.sums + id * kSums;
+    float *const s = reinterpret_cast<float *>(p.chunks + id * kUnits + kFragments * 64);
     if (lane < 32) {
         s[lane] = kept;
         s[32 + lane] = late;
@@ -406,35 +433,59 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     }
 }
 
-// One workgroup takes one head's 16 CT columns of v (rows p of the state) of a
-// sequence; its WN waves share N out, each with its part of the state in registers,
-// as the result tiles of the update's product: a lane has, of row p = lane % 16, n =
-// 32 s + 8 g + 0 .. 7. Operands are arranged so that nothing is exchanged between lanes:
-// a lane's 8 values are a fragment of the products with k and q, 16 bytes of a row of
-// which are the other; S k comes out with 4 consecutive tokens per lane, and those of two
-// 16-token tiles are a fragment of the products with the inverse, as u is of those with
-// k and the weights. Only k for the update and v are read transposed from LDS. The waves'
-// shares of S k and S q are added up through LDS, one barrier a chunk; what follows from them
-// every wave computes for itself.
-template <int N, int WN, int CT>
-__global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const DeltaParams p)
+// Where a token's row of k and q in LDS has its 16-byte runs: exchanged by row, so that
+// neither 16 rows of one run nor 4 rows of 4 runs (read transposed) have bank conflicts.
+template <int N>
+__device__ __forceinline__ int run_of(int row, int run)
 {
+    const int f = N >= 128 ? (row & 3) << 2 | (row >> 2 & 3) : N == 64 ? (row & 2) << 1 | (row >> 2 & 3) : row >> 2 & 3;
+    return row * (N / 8) + (run ^ f);
+}
+
+// Chunks in order. Waves hold the state in registers as the result tiles of the update's
+// product: a lane has, of row p = lane % 16, n = 32 s + 8 g + 0 .. 7. Operands are arranged
+// so that nothing is exchanged between lanes: a lane's 8 values are a fragment of the
+// products with k and q, 16 bytes of a row of which are the other; S k comes out with 4
+// consecutive tokens per lane, and those of two 16-token tiles are a fragment of the
+// products with the inverse, as u is of those with k and the weights. Only k for the update
+// and v are read transposed, from LDS.
+//
+// WN > 1, few columns of heads: a chunk's time is the length of its chain. WN waves share the N of 16
+// columns out; their shares of S k and S q are added up through LDS, one barrier a chunk,
+// and what follows every wave computes for itself. Everything goes from memory into the registers
+// where it is used, requested for the next chunk as soon as this one's has been.
+//
+// WN = 1, many: a wave has all N of 16 CT columns, WC waves as many of one head. They share
+// a chunk's operands, which go through LDS, requested two chunks ahead.
+template <int N, int WN, int WC, int CT>
+__global__ void __launch_bounds__(64 * WN * WC, N == 256 ? 1 : 2) ssu_delta_chunk_kernel(const DeltaParams p)
+{
+    static_assert(WN == 1 || WC == 1, "one or the other");
+    constexpr bool ALONE = WN > 1;
+    constexpr int THREADS = 64 * WN * WC;
     constexpr int NW = N / WN, KS = NW / 32, MT = NW / 16;
-    constexpr int KP = NW + 8, VP = 16 * CT + 8;  // pitches in LDS
-    __shared__ __attribute__((aligned(16))) uint16_t lk[WN][kChunk * KP], lv[WN][kChunk * VP];
-    __shared__ f32x4 shares[WN > 1 ? 2 : 1][WN > 1 ? WN : 1][CT][4][64];
+    constexpr int PC = 16 * CT * WC, VP = PC + 16;  // columns, pitch in LDS
+    constexpr int RK = 32 * NW / 8, RV = 32 * PC / 8;  // runs of 16 bytes
+    constexpr int LT = ALONE ? 64 : THREADS;          // threads that load them
+    constexpr int UK = (RK + LT - 1) / LT, UV = (RV + LT - 1) / LT, UX = (kUnits + LT - 1) / LT;
+    struct Stage {
+        u32x4 k[RK], q[ALONE ? 1 : RK], x[ALONE ? 1 : kUnits];
+        uint16_t v[kChunk * VP];
+    };
+    __shared__ __attribute__((aligned(16))) Stage ring[ALONE ? WN : 2];
+    __shared__ f32x4 shares[ALONE ? 2 : 1][WN][CT][4][64];
     __shared__ float single[2][WN][CT + 1][64];
 
     const LinearParams &a = p.a;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
-    const int wn = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wc = wave / WN;
     // workgroups go round the 8 XCDs: the columns of a head, which share its k, q
     // and fragments, beside each other on one
     const int id = static_cast<int>(blockIdx.x) / 8, unit = id / a.tiles * 8 + static_cast<int>(blockIdx.x) % 8;
     if (unit >= a.total)
         return;
     const int b = unit / a.nheads, h = unit % a.nheads, grp = h / a.heads_per_group;
-    const int p0 = id % a.tiles * 16 * CT;
+    const int col0 = id % a.tiles * PC, p0 = col0 + 16 * CT * wc;
     const int64_t slot = uniform(load_index(a.idx, a.idx64, b));
     const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
     const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
@@ -442,10 +493,80 @@ __global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const Delta
         return;
     const int total = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo)), chunks = (total + kChunk - 1) / kChunk;
     const int n0 = wn * NW + 8 * g;
+    const bool in_n = N >= 64 || n0 < p.dstate;  // (N = 16 in a tile of 32)
+
+    // Requests of a chunk; rows behind the end come from the last one, columns behind P
+    // and N from the first. ALONE, k and q as fragments: run 4 s + g of row 16 t + c.
+    const int lt = ALONE ? lane : tid;
+    u32x4 rk[UK], rq[UK], rv[UV], rx[ALONE ? 1 : UX];
+    uint32_t ok[UK], oq[UK], ov[UV];  // byte offsets from a chunk's first row
+    auto row_of_k = [&](int e) { return ALONE ? 16 * (e % 2) + c : (lt + LT * e) / (NW / 8); };
+    auto run_of_k = [&](int e) { return ALONE ? 4 * (e / 2) + g : (lt + LT * e) % (NW / 8); };
+    auto row_of_v = [&](int e) { return (lt + LT * e) / (PC / 8); };
+    auto col_of_v = [&](int e) { return (lt + LT * e) % (PC / 8) * 8; };
+    auto offsets = [&](int last) {  // of a chunk with rows 0 .. last
+#pragma unroll
+        for (int e = 0; e < UK; ++e) {
+            const int n = wn * NW + run_of_k(e) * 8, col = N >= 64 || n < p.dstate ? n : 0;
+            const uint32_t row = min(row_of_k(e), last);
+            ok[e] = 2 * (row * static_cast<uint32_t>(a.k_t) + col);
+            oq[e] = 2 * (row * static_cast<uint32_t>(a.q_t) + col);
+        }
+#pragma unroll
+        for (int e = 0; e < UV; ++e)
+            ov[e] = 2 * (min(row_of_v(e), last) * static_cast<uint32_t>(a.v_t) + (col0 + col_of_v(e) < a.headdim ? col_of_v(e) : 0));
+    };
+    auto at_bytes = [](const uint16_t *base, uint32_t off) {
+        return *reinterpret_cast<const u32x4_a2 *>(reinterpret_cast<const char *>(base) + off);
+    };
+    const uint16_t *const kb = a.k + lo * a.k_t + grp * a.k_g, *const qb = a.q + lo * a.q_t + grp * a.q_g;
+    const uint16_t *const vb = a.v + lo * a.v_t + h * a.v_h + col0;
+    const u32x4 *const xb = p.chunks + ((lo / kChunk + b) * a.nheads + h) * kUnits;
+    auto request = [&](int i) {
+        const int64_t row = static_cast<int64_t>(i) * kChunk;
+        if (total - i * kChunk < kChunk)
+            offsets(total - i * kChunk - 1);
+#pragma unroll
+        for (int e = 0; e < UK; ++e) {
+            rk[e] = at_bytes(kb + row * a.k_t, ok[e]);
+            rq[e] = at_bytes(qb + row * a.q_t, oq[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < UV; ++e)
+            rv[e] = at_bytes(vb + row * a.v_t, ov[e]);
+        if constexpr (!ALONE)
+#pragma unroll
+            for (int e = 0; e < UX; ++e)
+                rx[e] = xb[static_cast<int64_t>(i) * a.nheads * kUnits + min(lt + LT * e, kUnits - 1)];
+    };
+    auto place = [&](Stage &to) {
+#pragma unroll
+        for (int e = 0; e < UK; ++e) {
+            const int row = row_of_k(e), run = run_of_k(e);
+            if (RK % LT == 0 || lt + LT * e < RK) {
+                const bool in = N >= 64 || run * 8 < p.dstate;
+                rk[e] = in ? rk[e] : u32x4{0, 0, 0, 0};
+                rq[e] = in ? rq[e] : u32x4{0, 0, 0, 0};
+                to.k[run_of<NW>(row, run)] = rk[e];
+                if constexpr (!ALONE)
+                    to.q[run_of<NW>(row, run)] = rq[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < UV; ++e)
+            if (RV % LT == 0 || lt + LT * e < RV)
+                *reinterpret_cast<u32x4 *>(to.v + row_of_v(e) * VP + col_of_v(e)) = rv[e];
+        if constexpr (!ALONE)
+#pragma unroll
+            for (int e = 0; e < UX; ++e)
+                if (kUnits % LT == 0 || lt + LT * e < kUnits)
+                    to.x[lt + LT * e] = rx[e];
+    };
+    offsets(kChunk - 1);
+    request(0);
 
     f32x4 st[CT][MT];
     float *const pool = a.state + slot * a.s_slot + h * a.s_head + (p0 + c) * a.s_row + n0;
-    const bool in_n = N >= 64 || n0 < p.dstate;  // (N = 16 in a tile of 32)
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -454,73 +575,78 @@ __global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const Delta
                             ? *reinterpret_cast<const f32x4 *>(pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2))
                             : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // a chunk's operands; rows behind the end come from the last one
-    u32x4 kf[2][KS], qf[2][KS], vf[CT], xf[6], wf[4];
+    // what comes from the first kernel (of the weights a wave of several has one tile)
+    u32x4 xf[2][3], wf[2][2];
     f32x4 kept[2], late[2];
-    float asked[2], whole, finite;
-    const uint16_t *const kb = a.k + lo * a.k_t + grp * a.k_g + n0, *const qb = a.q + lo * a.q_t + grp * a.q_g + n0;
-    const uint16_t *const vb = a.v + lo * a.v_t + h * a.v_h;
-    const int64_t first = (lo / kChunk + b) * a.nheads + h;
-    auto request_kq = [&](int i) {
+    float asked[2], whole = 0.0f, finite = 0.0f;
+    const int mine = ALONE ? wn & 1 : 0;
+    const u32x4 *xs = xb;  // of the chunk; the other's in LDS
+    auto read_x = [&](const u32x4 *x) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int64_t row = min(i * kChunk + 16 * t + c, total - 1);
+            kept[t] = *reinterpret_cast<const f32x4 *>(x + kFragments * 64 + 4 * t + g);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                kf[t][s] = in_n ? *reinterpret_cast<const u32x4_a2 *>(kb + row * a.k_t + 32 * s) : u32x4{0, 0, 0, 0};
-                qf[t][s] = in_n ? *reinterpret_cast<const u32x4_a2 *>(qb + row * a.q_t + 32 * s) : u32x4{0, 0, 0, 0};
-            }
+            for (int e = 0; e < 3; ++e)
+                xf[t][e] = x[64 * (3 * t + e) + lane];
         }
+        finite = reinterpret_cast<const float *>(x + kFragments * 64)[97];
     };
-    constexpr int VT = 32 / CT;  // tokens that one load of v reads
-    const int vtok = lane / (2 * CT), vcol = 8 * (lane % (2 * CT));
-    auto request_v = [&](int i) {
-#pragma unroll
-        for (int e = 0; e < CT; ++e) {
-            const int64_t row = min(i * kChunk + e * VT + vtok, total - 1);
-            vf[e] = p0 + vcol < a.headdim ? *reinterpret_cast<const u32x4_a2 *>(vb + row * a.v_t + p0 + vcol) : u32x4{0, 0, 0, 0};
-        }
-    };
-    auto request_x = [&](int i) {
-        const u32x4 *const src = p.fragments + (first + static_cast<int64_t>(i) * a.nheads) * kFragments * 64 + lane;
-#pragma unroll
-        for (int e = 0; e < 6; ++e)
-            xf[e] = src[64 * e];
-        const float *const s = p.sums + (first + static_cast<int64_t>(i) * a.nheads) * kSums;
+    auto read_late = [&](const u32x4 *x) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            kept[t] = *reinterpret_cast<const f32x4 *>(s + 16 * t + 4 * g);
-        finite = s[97];
+            late[t] = *reinterpret_cast<const f32x4 *>(x + kFragments * 64 + 8 + 4 * t + g);
+        whole = reinterpret_cast<const float *>(x + kFragments * 64)[96];
     };
-    auto request_w = [&](int i) {
-        const u32x4 *const src = p.fragments + (first + static_cast<int64_t>(i) * a.nheads) * kFragments * 64 + lane;
+    auto read_w = [&](const u32x4 *x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            wf[e] = src[64 * (6 + e)];
-        const float *const s = p.sums + (first + static_cast<int64_t>(i) * a.nheads) * kSums;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            asked[t] = s[64 + 16 * t + c];
-            late[t] = *reinterpret_cast<const f32x4 *>(s + 32 + 16 * t + 4 * g);
+        for (int t = 0; t < (ALONE ? 1 : 2); ++t) {
+            const int tile = ALONE ? mine : t;
+            asked[t] = reinterpret_cast<const float *>(x + kFragments * 64)[64 + 16 * tile + c];
+            wf[t][0] = x[64 * (6 + 2 * tile) + lane];
+            wf[t][1] = x[64 * (7 + 2 * tile) + lane];
         }
-        whole = s[96];
     };
-    request_kq(0);
-    request_v(0);
-    request_x(0);
-    request_w(0);
+    if constexpr (ALONE) {
+        read_x(xs);
+        read_late(xs);
+        read_w(xs);
+    } else {
+        place(ring[0]);
+        request(min(1, chunks - 1));
+        __syncthreads();
+    }
 
     for (int i = 0; i < chunks; ++i) {
-        const int next = min(i + 1, chunks - 1);
+        Stage &at = ring[ALONE ? wn : i & 1];
+        // of the next chunk (behind the last one its own again: a condition around the
+        // requests would make every wait for older ones a wait for all)
+        const u32x4 *const next = xb + static_cast<int64_t>(min(i + 1, chunks - 1)) * a.nheads * kUnits;
+        if constexpr (!ALONE)
+            xs = at.x;
+        u32x4 kt[MT];
+        u32x2 vf[CT][2];
+        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4) + 16 * CT * wc;
+        auto read_v = [&] {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-                *reinterpret_cast<u32x4 *>(&lk[wn][(16 * t + c) * KP + 32 * s + 8 * g]) = kf[t][s];
+                for (int ct = 0; ct < CT; ++ct)
+                    vf[ct][t] = read_transposed(at.v + vtr + 16 * t * VP + 16 * ct);
+        };
+        auto read_kt = [&](int m) {
+            const int row = 4 * g + c / 4, run = 4 * (m / 2) + c % 4;
+            auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<NW>(r, run)]) + 4 * (m % 2); };
+            const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
+            kt[m] = u32x4{x[0], x[1], y[0], y[1]};
+        };
+        if constexpr (ALONE) {
+            place(at);
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // (the buffer is this wave's own)
+            read_v();
 #pragma unroll
-        for (int e = 0; e < CT; ++e)
-            *reinterpret_cast<u32x4 *>(&lv[wn][(e * VT + vtok) * VP + vcol]) = vf[e];
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            for (int m = 0; m < MT; ++m)
+                read_kt(m);
+        }
 
         // S k (rows tokens, columns p) and S q (rows p, columns tokens), this wave's n
         f32x4 sk[CT][2], sq[CT][2];
@@ -530,28 +656,33 @@ __global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const Delta
             for (int t = 0; t < 2; ++t)
                 sk[ct][t] = sq[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s) {
+            u32x4 kf[2], qf[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                kf[t] = ALONE ? rk[2 * s + t] : at.k[run_of<NW>(16 * t + c, 4 * s + g)];
+                qf[t] = ALONE ? rq[2 * s + t] : at.q[ALONE ? 0 : run_of<NW>(16 * t + c, 4 * s + g)];
+            }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 const Pieces f = split_triple(st[ct][2 * s], st[ct][2 * s + 1]);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    sk[ct][t] = Mma<Bf16>::run(kf[t][s], f.c, sk[ct][t]);
-                    sq[ct][t] = Mma<Bf16>::run(f.b, qf[t][s], sq[ct][t]);
+                    sk[ct][t] = Mma<Bf16>::run(kf[t], f.c, sk[ct][t]);
+                    sq[ct][t] = Mma<Bf16>::run(f.b, qf[t], sq[ct][t]);
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    sk[ct][t] = Mma<Bf16>::run(kf[t][s], f.b, sk[ct][t]);
-                    sq[ct][t] = Mma<Bf16>::run(f.a, qf[t][s], sq[ct][t]);
+                    sk[ct][t] = Mma<Bf16>::run(kf[t], f.b, sk[ct][t]);
+                    sq[ct][t] = Mma<Bf16>::run(f.a, qf[t], sq[ct][t]);
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    sk[ct][t] = Mma<Bf16>::run(kf[t][s], f.a, sk[ct][t]);
+                    sk[ct][t] = Mma<Bf16>::run(kf[t], f.a, sk[ct][t]);
             }
-        request_kq(next);
-        request_v(next);
-        if constexpr (WN > 1) {
-            auto &sh = shares[i & 1];
+        }
+        auto &sh = shares[ALONE ? i & 1 : 0];
+        if constexpr (ALONE) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -559,100 +690,119 @@ __global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const Delta
                     sh[wn][ct][t][lane] = sk[ct][t];
                     sh[wn][ct][2 + t][lane] = sq[ct][t];
                 }
+            request(min(i + 1, chunks - 1));
             __syncthreads();
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     sk[ct][t] = sh[0][ct][t][lane];
-                    sq[ct][t] = sh[0][ct][2 + t][lane];
 #pragma unroll
-                    for (int w = 1; w < WN; ++w) {
+                    for (int w = 1; w < WN; ++w)
                         sk[ct][t] += sh[w][ct][t][lane];
-                        sq[ct][t] += sh[w][ct][2 + t][lane];
-                    }
                 }
+        } else {
+            place(ring[(i + 1) & 1]);
+            request(min(i + 2, chunks - 1));
+            read_v();
+            read_x(xs);
         }
 
         // u: rows tokens, columns p
         f32x4 u[CT][2];
         float zero = finite - 1.0f;
-        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             f32x4 r[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                r[t] = halves(read_transposed(&lv[wn][vtr + 16 * t * VP + 16 * ct])) - kept[t] * sk[ct][t];
+            for (int t = 0; t < 2; ++t) {
+                r[t] = halves(vf[ct][t]) - kept[t] * sk[ct][t];
+                zero = unless_finite(r[t], zero);
+            }
             const Pieces f = split_triple(r[0], r[1]);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-                y = Mma<Bf16>::run(xf[3 * t], f.c, y);
-                y = Mma<Bf16>::run(xf[3 * t + 1], f.b, y);
-                y = Mma<Bf16>::run(xf[3 * t + 2], f.a, y);
-                y = Mma<Bf16>::run(xf[3 * t], f.b, y);
-                y = Mma<Bf16>::run(xf[3 * t + 1], f.a, y);
-                y = Mma<Bf16>::run(xf[3 * t], f.a, y);
-                u[ct][t] = y;
-                zero = unless_finite(y, zero);
-            }
+            for (int t = 0; t < 2; ++t)
+                u[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // the smallest products first, the two tiles in turn
+#pragma unroll
+            for (int e = 0; e < 6; ++e)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    u[ct][t] = Mma<Bf16>::run(xf[t][e == 1 || e == 4 ? 1 : e == 2 ? 2 : 0], e == 0 ? f.c : e == 1 || e == 3 ? f.b : f.a,
+                                              u[ct][t]);
         }
+        if constexpr (ALONE)
+            read_x(next);
         if (__builtin_expect(!__any(zero != 0.0f), 1)) {
-            // out: rows p, columns tokens
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (WN > 1 && wn % 2 != t)
-                    continue;
-                if (WN > 2 && wn >= 2)
-                    continue;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    u32x4 uh, ul;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t wh, wl;
-                        split_pair(u[ct][e / 2][2 * e % 4], u[ct][e / 2][2 * e % 4 + 1], wh, wl);
-                        uh[e] = wh;
-                        ul[e] = wl;
-                    }
-                    f32x4 o = asked[t] * sq[ct][t];
-                    o = Mma<Bf16>::run(ul, wf[2 * t], o);
-                    o = Mma<Bf16>::run(uh, wf[2 * t + 1], o);
-                    o = Mma<Bf16>::run(uh, wf[2 * t], o);
-                    const int row = i * kChunk + 16 * t + c;
-                    if (row < total && p0 + 16 * ct < a.headdim)
-                        *reinterpret_cast<u32x2_a2 *>(a.out + (lo + row) * a.o_t + h * a.o_h + p0 + 16 * ct + 4 * g) =
-                            u32x2{pack2<Bf16>(o[0], o[1]), pack2<Bf16>(o[2], o[3])};
-                }
-            }
             // the state behind the chunk
-            const int ktr = (4 * g + c / 4) * KP + 8 * (c % 4);
+            if constexpr (!ALONE)
+                read_late(xs);
+            Pieces f[CT];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const Pieces f = split_triple(late[0] * u[ct][0], late[1] * u[ct][1]);
+            for (int ct = 0; ct < CT; ++ct)
+                f[ct] = split_triple(late[0] * u[ct][0], late[1] * u[ct][1]);
+            constexpr int MB = ALONE || MT < 4 ? MT : 4;  // tiles at a time
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint16_t *const at = &lk[wn][ktr + 32 * (m / 2) + 4 * (m % 2)];
-                    const u32x2 x = read_transposed(at), y = read_transposed(at + 16 * KP);
-                    const u32x4 kt = {x[0], x[1], y[0], y[1]};
-                    f32x4 s = st[ct][m] * whole;
-                    s = Mma<Bf16>::run(kt, f.c, s);
-                    s = Mma<Bf16>::run(kt, f.b, s);
-                    st[ct][m] = Mma<Bf16>::run(kt, f.a, s);
-                }
+            for (int m0 = 0; m0 < MT; m0 += MB) {
+                if constexpr (!ALONE)
+#pragma unroll
+                    for (int m = m0; m < m0 + MB; ++m)
+                        read_kt(m);
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+#pragma unroll
+                    for (int m = m0; m < m0 + MB; ++m)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            if (e == 0)
+                                st[ct][m] *= whole;
+                            st[ct][m] = Mma<Bf16>::run(kt[m], e == 0 ? f[ct].c : e == 1 ? f[ct].b : f[ct].a, st[ct][m]);
+                        }
             }
+            // out: rows p, columns tokens
+            if constexpr (!ALONE)
+                read_w(xs);
+            if (!ALONE || wn < 2)
+#pragma unroll
+                for (int t = 0; t < (ALONE ? 1 : 2); ++t)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const int tile = ALONE ? mine : t;
+                        u32x4 uh, ul;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t wh, wl;
+                            split_double(u[ct][e / 2][2 * e % 4], u[ct][e / 2][2 * e % 4 + 1], wh, wl);
+                            uh[e] = wh;
+                            ul[e] = wl;
+                        }
+                        f32x4 o = sq[ct][t];
+                        if constexpr (ALONE) {
+                            o = sh[0][ct][2 + tile][lane];
+#pragma unroll
+                            for (int w = 1; w < WN; ++w)
+                                o += sh[w][ct][2 + tile][lane];
+                        }
+                        o *= asked[t];
+                        o = Mma<Bf16>::run(ul, wf[t][0], o);
+                        o = Mma<Bf16>::run(uh, wf[t][1], o);
+                        o = Mma<Bf16>::run(uh, wf[t][0], o);
+                        const int row = i * kChunk + 16 * tile + c;
+                        if (row < total && p0 + 16 * ct < a.headdim)
+                            *reinterpret_cast<u32x2_a2 *>(a.out + (lo + row) * a.o_t + h * a.o_h + p0 + 16 * ct + 4 * g) =
+                                u32x2{pack2<Bf16>(o[0], o[1]), pack2<Bf16>(o[2], o[3])};
+                    }
         } else {
             // Not finite: the pieces in 16 bits make NaN of infinities, and NaN of one
             // token would reach those before it through the inverse's zeros. Token by
-            // token, as in the kernel of steps (all waves alike: u is the same in each).
+            // token, as in the kernel of steps (all waves alike: r is the same in each).
             const int rows = min(total - i * kChunk, kChunk);
 #pragma unroll 1
             for (int t = 0; t < rows; ++t) {
                 const int64_t tok = lo + i * kChunk + t;
                 const float keep = exp_f32(a.decay[tok * a.d_t + h * a.d_h]);
                 const float beta = a.beta ? a.beta[tok * a.b_t + h * a.b_h] : 1.0f;
-                const uint16_t *const kr = a.k + tok * a.k_t + grp * a.k_g + n0, *const qr = a.q + tok * a.q_t + grp * a.q_g + n0;
+                const uint16_t *const kr = kb + (i * kChunk + t) * a.k_t + n0, *const qr = qb + (i * kChunk + t) * a.q_t + n0;
                 // sums over this wave's n, then over the waves'
                 auto whole_sums = [&](float (&x)[CT + 1], float (&box)[WN][CT + 1][64]) {
 #pragma unroll
@@ -718,8 +868,12 @@ __global__ void __launch_bounds__(64 * WN, 2) ssu_delta_chunk_kernel(const Delta
                                 Bf16::round(a.scale * (p.normalize ? inverse_length(y[CT]) : 1.0f) * y[ct]);
             }
         }
-        request_x(next);
-        request_w(next);
+        if constexpr (ALONE) {
+            read_late(next);
+            read_w(next);
+        } else {
+            __syncthreads();
+        }
     }
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -763,22 +917,22 @@ struct ChunkKernel {
     int waves, columns;
 };
 
-template <int N, int WN, int CT>
+template <int N, int WN, int WC, int CT>
 constexpr ChunkKernel chunk_kernel()
 {
-    return {&ssu_delta_chunk_kernel<N, WN, CT>, WN, 16 * CT};
+    return {&ssu_delta_chunk_kernel<N, WN, WC, CT>, WN * WC, 16 * CT * WC};
 }
 
 ChunkKernel chunk_kernel(int N, int64_t tiles)
 {
-    const bool many = tiles > 4 * kNumCUs;
+    const bool many = tiles > 2 * kNumCUs;
     if (N <= 32)
-        return many ? chunk_kernel<32, 1, 2>() : chunk_kernel<32, 1, 1>();
+        return many ? chunk_kernel<32, 1, 4, 2>() : chunk_kernel<32, 1, 1, 1>();
     if (N == 64)
-        return many ? chunk_kernel<64, 1, 2>() : chunk_kernel<64, 2, 1>();
+        return many ? chunk_kernel<64, 1, 4, 2>() : chunk_kernel<64, 2, 1, 1>();
     if (N == 128)
-        return many ? chunk_kernel<128, 2, 2>() : chunk_kernel<128, 4, 1>();
-    return many ? chunk_kernel<256, 4, 2>() : chunk_kernel<256, 4, 1>();
+        return many ? chunk_kernel<128, 1, 4, 2>() : chunk_kernel<128, 4, 1, 1>();
+    return many ? chunk_kernel<256, 1, 4, 1>() : chunk_kernel<256, 4, 1, 1>();
 }
 
 // ------------------------------------------------------------------ host --
@@ -820,7 +974,7 @@ int64_t chunks_of(const ssu_delta_args &a) { return a.ntokens / kChunk + a.batch
 
 int64_t workspace_of(const ssu_delta_args &a)
 {
-    return a.ntokens == 0 ? 0 : chunks_of(a) * a.nheads * (kFragments * 1024 + kSums * 4);
+    return a.ntokens == 0 ? 0 : chunks_of(a) * a.nheads * kUnits * 16;
 }
 
 ssu_status launch_chunks(const ssu_delta_args &a, hipStream_t stream)
@@ -839,8 +993,7 @@ ssu_status launch_chunks(const ssu_delta_args &a, hipStream_t stream)
     p.a.total = static_cast<int>(units);
     p.normalize = a.normalize;
     p.dstate = a.dstate;
-    p.fragments = static_cast<u32x4 *>(a.workspace);
-    p.sums = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + chunks_of(a) * a.nheads * kFragments * 1024);
+    p.chunks = static_cast<u32x4 *>(a.workspace);
     const int64_t first = chunks_of(a) * ((a.nheads + 3) / 4), second = (units + 7) / 8 * 8 * p.a.tiles;
     SSU_TRY(check_launch(first, 256, "ssu_gated_delta_rule"));
     SSU_TRY(check_launch(second, 64 * k.waves, "ssu_gated_delta_rule"));
