@@ -449,223 +449,548 @@ __device__ __forceinline__ int run_of(int row, int run)
 // consecutive tokens per lane, and those of two 16-token tiles are a fragment of the
 // products with the inverse, as u is of those with k and the weights. Only k for the update
 // and v are read transposed, from LDS.
-//
-// WN > 1, few columns of heads: a chunk's time is the length of its chain. WN waves share the N of 16
-// columns out; their shares of S k and S q are added up through LDS, one barrier a chunk,
-// and what follows every wave computes for itself. Everything goes from memory into the registers
-// where it is used, requested for the next chunk as soon as this one's has been.
-//
-// WN = 1, many: a wave has all N of 16 CT columns, WC waves as many of one head. They share
-// a chunk's operands, which go through LDS, requested two chunks ahead.
-template <int N, int WN, int WC, int CT>
-__global__ void __launch_bounds__(64 * WN * WC, N == 256 ? 1 : 2) ssu_delta_chunk_kernel(const DeltaParams p)
-{
-    static_assert(WN == 1 || WC == 1, "one or the other");
-    constexpr bool ALONE = WN > 1;
-    constexpr int THREADS = 64 * WN * WC;
-    constexpr int NW = N / WN, KS = NW / 32, MT = NW / 16;
-    constexpr int PC = 16 * CT * WC, VP = PC + 16;  // columns, pitch in LDS
-    constexpr int RK = 32 * NW / 8, RV = 32 * PC / 8;  // runs of 16 bytes
-    constexpr int LT = ALONE ? 64 : THREADS;          // threads that load them
-    constexpr int UK = (RK + LT - 1) / LT, UV = (RV + LT - 1) / LT, UX = (kUnits + LT - 1) / LT;
-    struct Stage {
-        u32x4 k[RK], q[ALONE ? 1 : RK], x[ALONE ? 1 : kUnits];
-        uint16_t v[kChunk * VP];
-    };
-    __shared__ __attribute__((aligned(16))) Stage ring[ALONE ? WN : 2];
-    __shared__ f32x4 shares[ALONE ? 2 : 1][WN][CT][4][64];
-    __shared__ float single[2][WN][CT + 1][64];
 
+// What a workgroup has of which sequence.
+struct Stretch {
+    int b, h, col0, total;  // sequence, head, first column, tokens
+    int64_t slot, lo;       // its state, its first row
+    const uint16_t *k, *q, *v;
+    const u32x4 *x;  // its first chunk
+};
+
+// Workgroups go round the 8 XCDs: the columns of a head, which share its k, q and
+// fragments, beside each other on one.
+__device__ __forceinline__ bool stretch_of(const DeltaParams &p, int columns, Stretch &s)
+{
     const LinearParams &a = p.a;
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wc = wave / WN;
-    // workgroups go round the 8 XCDs: the columns of a head, which share its k, q
-    // and fragments, beside each other on one
     const int id = static_cast<int>(blockIdx.x) / 8, unit = id / a.tiles * 8 + static_cast<int>(blockIdx.x) % 8;
     if (unit >= a.total)
+        return false;
+    s.b = unit / a.nheads;
+    s.h = unit % a.nheads;
+    s.col0 = id % a.tiles * columns;
+    s.slot = uniform(load_index(a.idx, a.idx64, s.b));
+    s.lo = min(max(static_cast<int64_t>(a.cu[s.b]), int64_t(0)), a.ntokens);
+    const int64_t hi = min(max(static_cast<int64_t>(a.cu[s.b + 1]), s.lo), a.ntokens);
+    s.total = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - s.lo));
+    const int grp = s.h / a.heads_per_group;
+    s.k = a.k + s.lo * a.k_t + grp * a.k_g;
+    s.q = a.q + s.lo * a.q_t + grp * a.q_g;
+    s.v = a.v + s.lo * a.v_t + s.h * a.v_h;
+    s.x = p.chunks + ((s.lo / kChunk + s.b) * a.nheads + s.h) * kUnits;
+    return s.slot >= 0 && s.slot < a.pool_slots && s.total > 0;
+}
+
+__device__ __forceinline__ u32x4 at_bytes(const uint16_t *base, uint32_t off)
+{
+    return *reinterpret_cast<const u32x4_a2 *>(reinterpret_cast<const char *>(base) + off);
+}
+
+// What does not depend on the state of a chunk, as the first kernel left it.
+__device__ __forceinline__ const float *sums_of(const u32x4 *x) { return reinterpret_cast<const float *>(x + kFragments * 64); }
+
+// The larger of m and x's magnitudes; NaN stays.
+__device__ __forceinline__ float largest(const f32x4 &x, float m)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        m = __builtin_elementwise_maximum(m, fabsf(x[r]));
+    return m;
+}
+
+template <int MT, int CT>
+__device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &s, int p0, int n0, f32x4 (&st)[CT][MT], bool store)
+{
+    const LinearParams &a = p.a;
+    const int c = static_cast<int>(threadIdx.x) & 15;
+    float *const pool = a.state + s.slot * a.s_slot + s.h * a.s_head + (p0 + c) * a.s_row + n0;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float *const at = pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2);
+            const bool in = p0 + 16 * ct < a.headdim && n0 < p.dstate;  // (N = 16 in a tile of 32)
+            if (!store)
+                st[ct][m] = in ? *reinterpret_cast<const f32x4 *>(at) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            else if (in)
+                *reinterpret_cast<f32x4 *>(at) = st[ct][m];
+        }
+}
+
+// The tokens t0 .. of a chunk one after the other, as in the kernel of steps: where a
+// value is not finite the pieces in 16 bits make NaN of infinities, and NaN of one token would
+// reach those before it through the inverse's zeros. All WN waves of a column come here.
+template <int MT, int WN, int CT>
+__device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s, int t0, int p0, int n0, int wn, f32x4 (&st)[CT][MT],
+                                          float (&box)[2][WN][CT + 1][64])
+{
+    const LinearParams &a = p.a;
+    const int lane = static_cast<int>(threadIdx.x) & 63, c = lane & 15, g = lane >> 4;
+    const bool in_n = n0 < p.dstate;
+    const int t1 = min(t0 + kChunk, s.total);
+    // sums over this wave's n, then over the waves'
+    auto whole_sums = [&](float (&x)[CT + 1], float (&to)[WN][CT + 1][64]) {
+#pragma unroll
+        for (int e = 0; e <= CT; ++e) {
+            x[e] += __shfl_xor(x[e], 16);
+            x[e] += __shfl_xor(x[e], 32);
+            if (WN > 1)
+                to[wn][e][lane] = x[e];
+        }
+        if constexpr (WN > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e <= CT; ++e) {
+                x[e] = to[0][e][lane];
+#pragma unroll
+                for (int w = 1; w < WN; ++w)
+                    x[e] += to[w][e][lane];
+            }
+        }
+    };
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t) {
+        const int64_t tok = s.lo + t;
+        const float keep = exp_f32(a.decay[tok * a.d_t + s.h * a.d_h]);
+        const float beta = a.beta ? a.beta[tok * a.b_t + s.h * a.b_h] : 1.0f;
+        const uint16_t *const kr = s.k + t * a.k_t + n0, *const qr = s.q + t * a.q_t + n0;
+        auto values = [&](const uint16_t *row, int m) {
+            return in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(row + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
+        };
+        float x[CT + 1] = {}, y[CT + 1] = {}, u[CT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const f32x4 k = values(kr, m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[CT] = fmaf(k[e], k[e], x[CT]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    st[ct][m][e] *= keep;
+                    x[ct] = fmaf(st[ct][m][e], k[e], x[ct]);
+                }
+            }
+        }
+        whole_sums(x, box[0]);
+        const float length = p.normalize ? inverse_length(x[CT]) : 1.0f;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            u[ct] = beta * (Bf16::lo(s.v[t * a.v_t + min(p0 + 16 * ct + c, a.headdim - 1)]) - length * x[ct]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const f32x4 k = values(kr, m), q = values(qr, m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[CT] = fmaf(q[e], q[e], y[CT]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    if (in_n)  // (an infinite u times the zeros behind N is NaN)
+                        st[ct][m][e] = fmaf(u[ct], length * k[e], st[ct][m][e]);
+                    y[ct] = fmaf(st[ct][m][e], q[e], y[ct]);
+                }
+            }
+        }
+        whole_sums(y, box[1]);
+        if (wn == 0 && g == 0)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                if (p0 + 16 * ct < a.headdim)
+                    a.out[tok * a.o_t + s.h * a.o_h + p0 + 16 * ct + c] =
+                        Bf16::round(a.scale * (p.normalize ? inverse_length(y[CT]) : 1.0f) * y[ct]);
+    }
+}
+
+// The chunk's u (rows tokens, columns p) from r, and its pieces for the update.
+__device__ __forceinline__ void solve(const u32x4 (&x)[2][3], const f32x4 (&r)[2], f32x4 (&u)[2])
+{
+    const Pieces f = split_triple(r[0], r[1]);
+    u[0] = u[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // the smallest products first, the two tiles in turn
+#pragma unroll
+    for (int e = 0; e < 6; ++e)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            u[t] = Mma<Bf16>::run(x[t][e == 1 || e == 4 ? 1 : e == 2 ? 2 : 0], e == 0 ? f.c : e == 1 || e == 3 ? f.b : f.a, u[t]);
+}
+
+// 16 tokens of out (rows p, columns tokens) from S q and u, stored.
+__device__ __forceinline__ void write_out(const DeltaParams &p, const Stretch &s, int row, int p0, const f32x4 &sq, float asked,
+                                          const f32x4 (&u)[2], u32x4 wh, u32x4 wl)
+{
+    const LinearParams &a = p.a;
+    const int g = (static_cast<int>(threadIdx.x) & 63) >> 4;
+    u32x4 uh, ul;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t h, l;
+        split_double(u[e / 2][2 * e % 4], u[e / 2][2 * e % 4 + 1], h, l);
+        uh[e] = h;
+        ul[e] = l;
+    }
+    f32x4 o = asked * sq;
+    o = Mma<Bf16>::run(ul, wh, o);
+    o = Mma<Bf16>::run(uh, wl, o);
+    o = Mma<Bf16>::run(uh, wh, o);
+    if (row < s.total && p0 < a.headdim)
+        *reinterpret_cast<u32x2_a2 *>(a.out + (s.lo + row) * a.o_t + s.h * a.o_h + p0 + 4 * g) =
+            u32x2{pack2<Bf16>(o[0], o[1]), pack2<Bf16>(o[2], o[3])};
+}
+
+// Few columns of heads: a chunk's time is the length of its chain of instructions, one wave on
+// a SIMD, so that what is not part of it is done by others. WN waves share the N of 16
+// columns out; their shares of S k are added up through LDS, one barrier a chunk, and what
+// follows every wave computes for itself. Two waves, a chunk behind, write out what u and the shares of S q
+// give for a tile of 16 tokens each. Two more bring operands into LDS, requested three
+// chunks ahead.
+template <int N, int WN>
+__global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const DeltaParams p)
+{
+    constexpr int NW = N / WN, KS = NW / 32, MT = NW / 16, VP = 32;
+    constexpr int RK = 32 * N / 8, RX = 6 * 64, UK = (RK + 127) / 128, UX = RX / 128;
+    struct Stage {
+        u32x4 k[RK], q[RK], x[RX];
+        float sums[128];
+        uint16_t v[kChunk * VP];
+    };
+    __shared__ __attribute__((aligned(16))) Stage ring[3];
+    __shared__ f32x4 shares_k[WN > 1 ? 2 : 1][WN][2][64], shares_q[3][WN][2][64], lu[2][2][64];
+    __shared__ float bad[2][WN];
+    __shared__ float box[2][WN][2][64];
+
+    const LinearParams &a = p.a;
+    Stretch s;
+    if (!stretch_of(p, 16, s))
         return;
-    const int b = unit / a.nheads, h = unit % a.nheads, grp = h / a.heads_per_group;
-    const int col0 = id % a.tiles * PC, p0 = col0 + 16 * CT * wc;
-    const int64_t slot = uniform(load_index(a.idx, a.idx64, b));
-    const int64_t lo = min(max(static_cast<int64_t>(a.cu[b]), int64_t(0)), a.ntokens);
-    const int64_t hi = min(max(static_cast<int64_t>(a.cu[b + 1]), lo), a.ntokens);
-    if (slot < 0 || slot >= a.pool_slots || hi == lo)
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), chunks = (s.total + kChunk - 1) / kChunk;
+    const int64_t stride = static_cast<int64_t>(a.nheads) * kUnits;
+    auto any_bad = [&](int i) {
+        float y = bad[i & 1][0];
+#pragma unroll
+        for (int w = 1; w < WN; ++w)
+            y += bad[i & 1][w];
+        return __builtin_amdgcn_readfirstlane(__float_as_int(y)) != 0;
+    };
+    // the barriers of a chunk that goes token by token
+    auto stand_by = [&](int i) {
+        if (WN > 1)
+            for (int n = 2 * min(s.total - i * kChunk, kChunk); n > 0; --n)
+                __syncthreads();
+    };
+
+    if (wave >= WN + 2) {  // chunk i + 1 into LDS before barrier i
+        const int lt = tid - 64 * (WN + 2);
+        struct Load {
+            u32x4 k[UK], q[UK], x[UX], v;
+        } even, odd;
+        auto request = [&](int i, Load &l) {  // rows behind the end come from the last one
+            const int i0 = min(i, chunks - 1) * kChunk;
+#pragma unroll
+            for (int e = 0; e < UK; ++e) {
+                const int u = lt + 128 * e, n = u % (N / 8) * 8, col = N >= 64 || n < p.dstate ? n : 0;
+                const int64_t row = min(i0 + u / (N / 8) % 32, s.total - 1);
+                l.k[e] = *reinterpret_cast<const u32x4_a2 *>(s.k + row * a.k_t + col);
+                l.q[e] = *reinterpret_cast<const u32x4_a2 *>(s.q + row * a.q_t + col);
+            }
+            const u32x4 *const x = s.x + min(i, chunks - 1) * stride;
+#pragma unroll
+            for (int e = 0; e < UX; ++e)
+                l.x[e] = x[lt + 128 * e];
+            // v by the first wave, the sums by the second
+            const u32x4_a2 *const v = reinterpret_cast<const u32x4_a2 *>(s.v + min(i0 + lt % 64 / 2, s.total - 1) * a.v_t + s.col0 + 8 * (lt % 2));
+            l.v = lt < 64 ? *v : static_cast<u32x4>(x[kFragments * 64 + lt % 32]);
+        };
+        auto turn = [&](int i, Load &l) {
+            Stage &to = ring[(i + 1) % 3];
+#pragma unroll
+            for (int e = 0; e < UK; ++e) {
+                const int u = lt + 128 * e, row = u / (N / 8), run = u % (N / 8);
+                const bool in = N >= 64 || run * 8 < p.dstate;
+                if (RK % 128 == 0 || u < RK) {
+                    to.k[run_of<N>(row, run)] = in ? l.k[e] : u32x4{0, 0, 0, 0};
+                    to.q[run_of<N>(row, run)] = in ? l.q[e] : u32x4{0, 0, 0, 0};
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < UX; ++e)
+                to.x[lt + 128 * e] = l.x[e];
+            if (lt < 64)
+                *reinterpret_cast<u32x4 *>(&to.v[lt / 2 * VP + 8 * (lt % 2)]) = l.v;
+            else if (lt < 96)
+                reinterpret_cast<u32x4 *>(to.sums)[lt - 64] = l.v;
+            request(i + 3, l);
+            __syncthreads();
+            if (i == chunks)
+                return true;
+            if (i >= 0 && any_bad(i))
+                stand_by(i);
+            return false;
+        };
+        request(0, odd);
+        request(1, even);
+#pragma unroll 1
+        for (int i = -1; !turn(i, odd) && !turn(i + 1, even); i += 2) {
+        }
         return;
-    const int total = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo)), chunks = (total + kChunk - 1) / kChunk;
-    const int n0 = wn * NW + 8 * g;
-    const bool in_n = N >= 64 || n0 < p.dstate;  // (N = 16 in a tile of 32)
+    }
+    if (wave >= WN) {  // out of chunk i - 1 behind barrier i
+        const int t = wave - WN;
+        struct Weights {
+            float asked;
+            u32x4 hi, lo;
+        } even, odd;
+        bool skip = true;
+        auto turn = [&](int i, const Weights &last, Weights &now) {
+            const u32x4 *const x = s.x + min(i, chunks - 1) * stride;
+            now = {sums_of(x)[64 + 16 * t + c], x[64 * (6 + 2 * t) + lane], x[64 * (7 + 2 * t) + lane]};
+            __syncthreads();
+            if (!skip) {
+                const f32x4 u[2] = {lu[(i - 1) & 1][0][lane], lu[(i - 1) & 1][1][lane]};
+                const int from = (i - 1) % 3;
+                f32x4 sq = shares_q[from][0][t][lane];
+#pragma unroll
+                for (int w = 1; w < WN; ++w)
+                    sq += shares_q[from][w][t][lane];
+                write_out(p, s, (i - 1) * kChunk + 16 * t + c, s.col0, sq, last.asked, u, last.hi, last.lo);
+            }
+            if (i == chunks)
+                return true;
+            skip = any_bad(i);
+            if (skip)
+                stand_by(i);
+            return false;
+        };
+        __syncthreads();  // the first chunk's operands
+#pragma unroll 1
+        for (int i = 0; !turn(i, odd, even) && !turn(i + 1, even, odd); i += 2) {
+        }
+        return;
+    }
+
+    const int wn = wave, n0 = wn * NW + 8 * g;
+    f32x4 st[1][MT];
+    load_state<MT, 1>(p, s, s.col0, n0, st, false);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {
+        const Stage &at = ring[i % 3];
+        // S k (rows tokens, columns p) and S q (rows p, columns tokens), this wave's n
+        f32x4 sk[2] = {}, sq[2] = {};
+        u32x4 kf[KS][2], qf[KS][2];
+#pragma unroll
+        for (int e = 0; e < KS; ++e)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                kf[e][t] = at.k[run_of<N>(16 * t + c, wn * (NW / 8) + 4 * e + g)];
+#pragma unroll
+        for (int e = 0; e < KS; ++e)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                qf[e][t] = at.q[run_of<N>(16 * t + c, wn * (NW / 8) + 4 * e + g)];
+        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4);
+        const f32x4 v[2] = {halves(read_transposed(&at.v[vtr])), halves(read_transposed(&at.v[vtr + 16 * VP]))};
+        f32x4 kept[2], late[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            kept[t] = *reinterpret_cast<const f32x4 *>(&at.sums[16 * t + 4 * g]);
+        const float whole = at.sums[96], finite = at.sums[97];
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+            const Pieces f = split_triple(st[0][2 * e], st[0][2 * e + 1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sk[t] = Mma<Bf16>::run(kf[e][t], f.c, sk[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sk[t] = Mma<Bf16>::run(kf[e][t], f.b, sk[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sk[t] = Mma<Bf16>::run(kf[e][t], f.a, sk[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sq[t] = Mma<Bf16>::run(f.b, qf[e][t], sq[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sq[t] = Mma<Bf16>::run(f.a, qf[e][t], sq[t]);
+        }
+        u32x4 xf[2][3], kt[MT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                xf[t][e] = at.x[64 * (3 * t + e) + lane];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int row = 4 * g + c / 4, run = wn * (NW / 8) + 4 * (m / 2) + c % 4;
+            auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<N>(r, run)]) + 4 * (m % 2); };
+            const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
+            kt[m] = u32x4{x[0], x[1], y[0], y[1]};
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            late[t] = *reinterpret_cast<const f32x4 *>(&at.sums[32 + 16 * t + 4 * g]);
+        // whether all of it is finite, and its sums: the other waves know of it as soon
+        // as these do
+        float most = finite == 1.0f ? 0.0f : INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            sk[t] *= kept[t];
+            most = largest(sk[t], largest(v[t], most));
+        }
+        const bool spoilt = __any(!(most <= 0x1p125f));
+        if (lane == 0)
+            bad[i & 1][wn] = spoilt ? 1.0f : 0.0f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (WN > 1)
+                shares_k[i & 1][wn][t][lane] = sk[t];
+            shares_q[i % 3][wn][t][lane] = sq[t];
+        }
+        __syncthreads();
+
+        f32x4 r[2], u[2];
+        const bool slow = any_bad(i);
+        asm volatile("");  // (read here, not where it is asked)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (WN > 1) {
+                sk[t] = shares_k[i & 1][0][t][lane];
+#pragma unroll
+                for (int w = 1; w < WN; ++w)
+                    sk[t] += shares_k[i & 1][w][t][lane];
+            }
+            r[t] = v[t] - sk[t];
+        }
+        solve(xf, r, u);
+        if (__builtin_expect(!slow, 1)) {
+            if (wn == 0) {
+                lu[i & 1][0][lane] = u[0];
+                lu[i & 1][1][lane] = u[1];
+            }
+            const Pieces f = split_triple(late[0] * u[0], late[1] * u[1]);
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (e == 0)
+                        st[0][m] *= whole;
+                    st[0][m] = Mma<Bf16>::run(kt[m], e == 0 ? f.c : e == 1 ? f.b : f.a, st[0][m]);
+                }
+        } else {
+            by_tokens<MT, WN, 1>(p, s, i * kChunk, s.col0, n0, wn, st, box);
+        }
+    }
+    __syncthreads();  // the last u
+    load_state<MT, 1>(p, s, s.col0, n0, st, true);
+}
+
+// Many columns: a wave has all N of 16 CT of them, WC waves as many of one head. They share
+// a chunk's operands, which go through LDS, requested two chunks ahead, one barrier a chunk.
+template <int N, int WC, int CT>
+__global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kernel(const DeltaParams p)
+{
+    constexpr int THREADS = 64 * WC, KS = N / 32, MT = N / 16;
+    constexpr int PC = 16 * CT * WC, VP = PC + 16;     // columns, pitch in LDS
+    constexpr int RK = 32 * N / 8, RV = 32 * PC / 8;  // runs of 16 bytes
+    constexpr int UK = (RK + THREADS - 1) / THREADS, UV = (RV + THREADS - 1) / THREADS, UX = (kUnits + THREADS - 1) / THREADS;
+    struct Stage {
+        u32x4 k[RK], q[RK], x[kUnits];
+        uint16_t v[kChunk * VP];
+    };
+    __shared__ __attribute__((aligned(16))) Stage ring[2];
+    __shared__ float box[2][1][CT + 1][64];
+
+    const LinearParams &a = p.a;
+    Stretch s;
+    if (!stretch_of(p, PC, s))
+        return;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wc = __builtin_amdgcn_readfirstlane(tid >> 6), chunks = (s.total + kChunk - 1) / kChunk;
+    const int p0 = s.col0 + 16 * CT * wc;
 
     // Requests of a chunk; rows behind the end come from the last one, columns behind P
-    // and N from the first. ALONE, k and q as fragments: run 4 s + g of row 16 t + c.
-    const int lt = ALONE ? lane : tid;
-    u32x4 rk[UK], rq[UK], rv[UV], rx[ALONE ? 1 : UX];
+    // and N from the first.
+    u32x4 rk[UK], rq[UK], rv[UV], rx[UX];
     uint32_t ok[UK], oq[UK], ov[UV];  // byte offsets from a chunk's first row
-    auto row_of_k = [&](int e) { return ALONE ? 16 * (e % 2) + c : (lt + LT * e) / (NW / 8); };
-    auto run_of_k = [&](int e) { return ALONE ? 4 * (e / 2) + g : (lt + LT * e) % (NW / 8); };
-    auto row_of_v = [&](int e) { return (lt + LT * e) / (PC / 8); };
-    auto col_of_v = [&](int e) { return (lt + LT * e) % (PC / 8) * 8; };
-    auto offsets = [&](int last) {  // of a chunk with rows 0 .. last
+    auto offsets = [&](int last) {     // of a chunk with rows 0 .. last
 #pragma unroll
         for (int e = 0; e < UK; ++e) {
-            const int n = wn * NW + run_of_k(e) * 8, col = N >= 64 || n < p.dstate ? n : 0;
-            const uint32_t row = min(row_of_k(e), last);
+            const int u = tid + THREADS * e, n = u % (N / 8) * 8, col = N >= 64 || n < p.dstate ? n : 0;
+            const uint32_t row = min(u / (N / 8), last);
             ok[e] = 2 * (row * static_cast<uint32_t>(a.k_t) + col);
             oq[e] = 2 * (row * static_cast<uint32_t>(a.q_t) + col);
         }
 #pragma unroll
-        for (int e = 0; e < UV; ++e)
-            ov[e] = 2 * (min(row_of_v(e), last) * static_cast<uint32_t>(a.v_t) + (col0 + col_of_v(e) < a.headdim ? col_of_v(e) : 0));
+        for (int e = 0; e < UV; ++e) {
+            const int u = tid + THREADS * e, col = s.col0 + u % (PC / 8) * 8;
+            ov[e] = 2 * (min(u / (PC / 8), last) * static_cast<uint32_t>(a.v_t) + (col < a.headdim ? col : 0));
+        }
     };
-    auto at_bytes = [](const uint16_t *base, uint32_t off) {
-        return *reinterpret_cast<const u32x4_a2 *>(reinterpret_cast<const char *>(base) + off);
-    };
-    const uint16_t *const kb = a.k + lo * a.k_t + grp * a.k_g, *const qb = a.q + lo * a.q_t + grp * a.q_g;
-    const uint16_t *const vb = a.v + lo * a.v_t + h * a.v_h + col0;
-    const u32x4 *const xb = p.chunks + ((lo / kChunk + b) * a.nheads + h) * kUnits;
     auto request = [&](int i) {
         const int64_t row = static_cast<int64_t>(i) * kChunk;
-        if (total - i * kChunk < kChunk)
-            offsets(total - i * kChunk - 1);
+        if (s.total - i * kChunk < kChunk)
+            offsets(s.total - i * kChunk - 1);
 #pragma unroll
         for (int e = 0; e < UK; ++e) {
-            rk[e] = at_bytes(kb + row * a.k_t, ok[e]);
-            rq[e] = at_bytes(qb + row * a.q_t, oq[e]);
+            rk[e] = at_bytes(s.k + row * a.k_t, ok[e]);
+            rq[e] = at_bytes(s.q + row * a.q_t, oq[e]);
         }
 #pragma unroll
         for (int e = 0; e < UV; ++e)
-            rv[e] = at_bytes(vb + row * a.v_t, ov[e]);
-        if constexpr (!ALONE)
+            rv[e] = at_bytes(s.v + row * a.v_t, ov[e]);
 #pragma unroll
-            for (int e = 0; e < UX; ++e)
-                rx[e] = xb[static_cast<int64_t>(i) * a.nheads * kUnits + min(lt + LT * e, kUnits - 1)];
+        for (int e = 0; e < UX; ++e)
+            rx[e] = s.x[static_cast<int64_t>(i) * a.nheads * kUnits + min(tid + THREADS * e, kUnits - 1)];
     };
     auto place = [&](Stage &to) {
 #pragma unroll
         for (int e = 0; e < UK; ++e) {
-            const int row = row_of_k(e), run = run_of_k(e);
-            if (RK % LT == 0 || lt + LT * e < RK) {
+            const int u = tid + THREADS * e, row = u / (N / 8), run = u % (N / 8);
+            if (RK % THREADS == 0 || u < RK) {
                 const bool in = N >= 64 || run * 8 < p.dstate;
-                rk[e] = in ? rk[e] : u32x4{0, 0, 0, 0};
-                rq[e] = in ? rq[e] : u32x4{0, 0, 0, 0};
-                to.k[run_of<NW>(row, run)] = rk[e];
-                if constexpr (!ALONE)
-                    to.q[run_of<NW>(row, run)] = rq[e];
+                to.k[run_of<N>(row, run)] = in ? rk[e] : u32x4{0, 0, 0, 0};
+                to.q[run_of<N>(row, run)] = in ? rq[e] : u32x4{0, 0, 0, 0};
             }
         }
 #pragma unroll
-        for (int e = 0; e < UV; ++e)
-            if (RV % LT == 0 || lt + LT * e < RV)
-                *reinterpret_cast<u32x4 *>(to.v + row_of_v(e) * VP + col_of_v(e)) = rv[e];
-        if constexpr (!ALONE)
+        for (int e = 0; e < UV; ++e) {
+            const int u = tid + THREADS * e;
+            if (RV % THREADS == 0 || u < RV)
+                *reinterpret_cast<u32x4 *>(to.v + u / (PC / 8) * VP + u % (PC / 8) * 8) = rv[e];
+        }
 #pragma unroll
-            for (int e = 0; e < UX; ++e)
-                if (kUnits % LT == 0 || lt + LT * e < kUnits)
-                    to.x[lt + LT * e] = rx[e];
+        for (int e = 0; e < UX; ++e) {
+            const int u = tid + THREADS * e;
+            if (kUnits % THREADS == 0 || u < kUnits)
+                to.x[u] = rx[e];
+        }
     };
     offsets(kChunk - 1);
     request(0);
-
     f32x4 st[CT][MT];
-    float *const pool = a.state + slot * a.s_slot + h * a.s_head + (p0 + c) * a.s_row + n0;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            st[ct][m] = p0 + 16 * ct < a.headdim && in_n
-                            ? *reinterpret_cast<const f32x4 *>(pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2))
-                            : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    load_state<MT, CT>(p, s, p0, 8 * g, st, false);
+    place(ring[0]);
+    request(min(1, chunks - 1));
+    __syncthreads();
 
-    // what comes from the first kernel (of the weights a wave of several has one tile)
-    u32x4 xf[2][3], wf[2][2];
-    f32x4 kept[2], late[2];
-    float asked[2], whole = 0.0f, finite = 0.0f;
-    const int mine = ALONE ? wn & 1 : 0;
-    const u32x4 *xs = xb;  // of the chunk; the other's in LDS
-    auto read_x = [&](const u32x4 *x) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            kept[t] = *reinterpret_cast<const f32x4 *>(x + kFragments * 64 + 4 * t + g);
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-                xf[t][e] = x[64 * (3 * t + e) + lane];
-        }
-        finite = reinterpret_cast<const float *>(x + kFragments * 64)[97];
-    };
-    auto read_late = [&](const u32x4 *x) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            late[t] = *reinterpret_cast<const f32x4 *>(x + kFragments * 64 + 8 + 4 * t + g);
-        whole = reinterpret_cast<const float *>(x + kFragments * 64)[96];
-    };
-    auto read_w = [&](const u32x4 *x) {
-#pragma unroll
-        for (int t = 0; t < (ALONE ? 1 : 2); ++t) {
-            const int tile = ALONE ? mine : t;
-            asked[t] = reinterpret_cast<const float *>(x + kFragments * 64)[64 + 16 * tile + c];
-            wf[t][0] = x[64 * (6 + 2 * tile) + lane];
-            wf[t][1] = x[64 * (7 + 2 * tile) + lane];
-        }
-    };
-    if constexpr (ALONE) {
-        read_x(xs);
-        read_late(xs);
-        read_w(xs);
-    } else {
-        place(ring[0]);
-        request(min(1, chunks - 1));
-        __syncthreads();
-    }
-
+#pragma unroll 1
     for (int i = 0; i < chunks; ++i) {
-        Stage &at = ring[ALONE ? wn : i & 1];
-        // of the next chunk (behind the last one its own again: a condition around the
-        // requests would make every wait for older ones a wait for all)
-        const u32x4 *const next = xb + static_cast<int64_t>(min(i + 1, chunks - 1)) * a.nheads * kUnits;
-        if constexpr (!ALONE)
-            xs = at.x;
-        u32x4 kt[MT];
-        u32x2 vf[CT][2];
-        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4) + 16 * CT * wc;
-        auto read_v = [&] {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    vf[ct][t] = read_transposed(at.v + vtr + 16 * t * VP + 16 * ct);
-        };
-        auto read_kt = [&](int m) {
-            const int row = 4 * g + c / 4, run = 4 * (m / 2) + c % 4;
-            auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<NW>(r, run)]) + 4 * (m % 2); };
-            const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
-            kt[m] = u32x4{x[0], x[1], y[0], y[1]};
-        };
-        if constexpr (ALONE) {
-            place(at);
-            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // (the buffer is this wave's own)
-            read_v();
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                read_kt(m);
-        }
+        Stage &at = ring[i & 1];
+        const float *const sums = sums_of(at.x);
 
-        // S k (rows tokens, columns p) and S q (rows p, columns tokens), this wave's n
-        f32x4 sk[CT][2], sq[CT][2];
+        // S k (rows tokens, columns p) and S q (rows p, columns tokens)
+        f32x4 sk[CT][2] = {}, sq[CT][2] = {};
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                sk[ct][t] = sq[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
+        for (int e = 0; e < KS; ++e) {
             u32x4 kf[2], qf[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                kf[t] = ALONE ? rk[2 * s + t] : at.k[run_of<NW>(16 * t + c, 4 * s + g)];
-                qf[t] = ALONE ? rq[2 * s + t] : at.q[ALONE ? 0 : run_of<NW>(16 * t + c, 4 * s + g)];
+                kf[t] = at.k[run_of<N>(16 * t + c, 4 * e + g)];
+                qf[t] = at.q[run_of<N>(16 * t + c, 4 * e + g)];
             }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                const Pieces f = split_triple(st[ct][2 * s], st[ct][2 * s + 1]);
+                const Pieces f = split_triple(st[ct][2 * e], st[ct][2 * e + 1]);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     sk[ct][t] = Mma<Bf16>::run(kf[t], f.c, sk[ct][t]);
@@ -681,206 +1006,75 @@ __global__ void __launch_bounds__(64 * WN * WC, N == 256 ? 1 : 2) ssu_delta_chun
                     sk[ct][t] = Mma<Bf16>::run(kf[t], f.a, sk[ct][t]);
             }
         }
-        auto &sh = shares[ALONE ? i & 1 : 0];
-        if constexpr (ALONE) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    sh[wn][ct][t][lane] = sk[ct][t];
-                    sh[wn][ct][2 + t][lane] = sq[ct][t];
-                }
-            request(min(i + 1, chunks - 1));
-            __syncthreads();
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    sk[ct][t] = sh[0][ct][t][lane];
-#pragma unroll
-                    for (int w = 1; w < WN; ++w)
-                        sk[ct][t] += sh[w][ct][t][lane];
-                }
-        } else {
-            place(ring[(i + 1) & 1]);
-            request(min(i + 2, chunks - 1));
-            read_v();
-            read_x(xs);
-        }
+        place(ring[(i + 1) & 1]);
+        request(min(i + 2, chunks - 1));
 
-        // u: rows tokens, columns p
         f32x4 u[CT][2];
-        float zero = finite - 1.0f;
+        float zero = sums[97] - 1.0f;
+        u32x4 xf[2][3];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                xf[t][e] = at.x[64 * (3 * t + e) + lane];
+        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4) + 16 * CT * wc;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             f32x4 r[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                r[t] = halves(vf[ct][t]) - kept[t] * sk[ct][t];
-                zero = unless_finite(r[t], zero);
+                const f32x4 kept = *reinterpret_cast<const f32x4 *>(sums + 16 * t + 4 * g);
+                r[t] = halves(read_transposed(at.v + vtr + 16 * t * VP + 16 * ct));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    r[t][e] = fmaf(-kept[e], sk[ct][t][e], r[t][e]);
             }
-            const Pieces f = split_triple(r[0], r[1]);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                u[ct][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            // the smallest products first, the two tiles in turn
-#pragma unroll
-            for (int e = 0; e < 6; ++e)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    u[ct][t] = Mma<Bf16>::run(xf[t][e == 1 || e == 4 ? 1 : e == 2 ? 2 : 0], e == 0 ? f.c : e == 1 || e == 3 ? f.b : f.a,
-                                              u[ct][t]);
+            solve(xf, r, u[ct]);
+            // (a zero of the inverse times what is not finite is NaN: any one is in all rows)
+            zero = fmaf(u[ct][0][0], 0.0f, zero);
         }
-        if constexpr (ALONE)
-            read_x(next);
         if (__builtin_expect(!__any(zero != 0.0f), 1)) {
             // the state behind the chunk
-            if constexpr (!ALONE)
-                read_late(xs);
+            const float whole = sums[96];
             Pieces f[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-                f[ct] = split_triple(late[0] * u[ct][0], late[1] * u[ct][1]);
-            constexpr int MB = ALONE || MT < 4 ? MT : 4;  // tiles at a time
+                f[ct] = split_triple(*reinterpret_cast<const f32x4 *>(sums + 32 + 4 * g) * u[ct][0],
+                                     *reinterpret_cast<const f32x4 *>(sums + 48 + 4 * g) * u[ct][1]);
+            constexpr int MB = MT < 4 ? MT : 4;  // tiles at a time
 #pragma unroll
             for (int m0 = 0; m0 < MT; m0 += MB) {
-                if constexpr (!ALONE)
+                u32x4 kt[MB];
 #pragma unroll
-                    for (int m = m0; m < m0 + MB; ++m)
-                        read_kt(m);
+                for (int m = 0; m < MB; ++m) {
+                    const int row = 4 * g + c / 4, run = 4 * ((m0 + m) / 2) + c % 4;
+                    auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<N>(r, run)]) + 4 * (m % 2); };
+                    const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
+                    kt[m] = u32x4{x[0], x[1], y[0], y[1]};
+                }
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
 #pragma unroll
-                    for (int m = m0; m < m0 + MB; ++m)
+                    for (int m = 0; m < MB; ++m)
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) {
                             if (e == 0)
-                                st[ct][m] *= whole;
-                            st[ct][m] = Mma<Bf16>::run(kt[m], e == 0 ? f[ct].c : e == 1 ? f[ct].b : f[ct].a, st[ct][m]);
+                                st[ct][m0 + m] *= whole;
+                            st[ct][m0 + m] = Mma<Bf16>::run(kt[m], e == 0 ? f[ct].c : e == 1 ? f[ct].b : f[ct].a, st[ct][m0 + m]);
                         }
             }
-            // out: rows p, columns tokens
-            if constexpr (!ALONE)
-                read_w(xs);
-            if (!ALONE || wn < 2)
 #pragma unroll
-                for (int t = 0; t < (ALONE ? 1 : 2); ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const int tile = ALONE ? mine : t;
-                        u32x4 uh, ul;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t wh, wl;
-                            split_double(u[ct][e / 2][2 * e % 4], u[ct][e / 2][2 * e % 4 + 1], wh, wl);
-                            uh[e] = wh;
-                            ul[e] = wl;
-                        }
-                        f32x4 o = sq[ct][t];
-                        if constexpr (ALONE) {
-                            o = sh[0][ct][2 + tile][lane];
-#pragma unroll
-                            for (int w = 1; w < WN; ++w)
-                                o += sh[w][ct][2 + tile][lane];
-                        }
-                        o *= asked[t];
-                        o = Mma<Bf16>::run(ul, wf[t][0], o);
-                        o = Mma<Bf16>::run(uh, wf[t][1], o);
-                        o = Mma<Bf16>::run(uh, wf[t][0], o);
-                        const int row = i * kChunk + 16 * tile + c;
-                        if (row < total && p0 + 16 * ct < a.headdim)
-                            *reinterpret_cast<u32x2_a2 *>(a.out + (lo + row) * a.o_t + h * a.o_h + p0 + 16 * ct + 4 * g) =
-                                u32x2{pack2<Bf16>(o[0], o[1]), pack2<Bf16>(o[2], o[3])};
-                    }
+                for (int ct = 0; ct < CT; ++ct)
+                    write_out(p, s, i * kChunk + 16 * t + c, p0 + 16 * ct, sq[ct][t], sums[64 + 16 * t + c], u[ct],
+                              at.x[64 * (6 + 2 * t) + lane], at.x[64 * (7 + 2 * t) + lane]);
         } else {
-            // Not finite: the pieces in 16 bits make NaN of infinities, and NaN of one
-            // token would reach those before it through the inverse's zeros. Token by
-            // token, as in the kernel of steps (all waves alike: r is the same in each).
-            const int rows = min(total - i * kChunk, kChunk);
-#pragma unroll 1
-            for (int t = 0; t < rows; ++t) {
-                const int64_t tok = lo + i * kChunk + t;
-                const float keep = exp_f32(a.decay[tok * a.d_t + h * a.d_h]);
-                const float beta = a.beta ? a.beta[tok * a.b_t + h * a.b_h] : 1.0f;
-                const uint16_t *const kr = kb + (i * kChunk + t) * a.k_t + n0, *const qr = qb + (i * kChunk + t) * a.q_t + n0;
-                // sums over this wave's n, then over the waves'
-                auto whole_sums = [&](float (&x)[CT + 1], float (&box)[WN][CT + 1][64]) {
-#pragma unroll
-                    for (int e = 0; e <= CT; ++e) {
-                        x[e] += __shfl_xor(x[e], 16);
-                        x[e] += __shfl_xor(x[e], 32);
-                        if (WN > 1)
-                            box[wn][e][lane] = x[e];
-                    }
-                    if constexpr (WN > 1) {
-                        __syncthreads();
-#pragma unroll
-                        for (int e = 0; e <= CT; ++e) {
-                            x[e] = box[0][e][lane];
-#pragma unroll
-                            for (int w = 1; w < WN; ++w)
-                                x[e] += box[w][e][lane];
-                        }
-                    }
-                };
-                float x[CT + 1] = {}, y[CT + 1] = {}, un[CT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const f32x4 kn = in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(kr + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[CT] = fmaf(kn[e], kn[e], x[CT]);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            st[ct][m][e] *= keep;
-                            x[ct] = fmaf(st[ct][m][e], kn[e], x[ct]);
-                        }
-                    }
-                }
-                whole_sums(x, single[0]);
-                const float length = p.normalize ? inverse_length(x[CT]) : 1.0f;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const float v = Bf16::lo(a.v[tok * a.v_t + h * a.v_h + min(p0 + 16 * ct + c, a.headdim - 1)]);
-                    un[ct] = beta * (v - length * x[ct]);
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const f32x4 kn = in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(kr + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
-                    const f32x4 qn = in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(qr + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[CT] = fmaf(qn[e], qn[e], y[CT]);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            if (in_n)  // (an infinite u times the zeros behind N is NaN)
-                                st[ct][m][e] = fmaf(un[ct], length * kn[e], st[ct][m][e]);
-                            y[ct] = fmaf(st[ct][m][e], qn[e], y[ct]);
-                        }
-                    }
-                }
-                whole_sums(y, single[1]);
-                if (wn == 0 && g == 0)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        if (p0 + 16 * ct < a.headdim)
-                            a.out[tok * a.o_t + h * a.o_h + p0 + 16 * ct + c] =
-                                Bf16::round(a.scale * (p.normalize ? inverse_length(y[CT]) : 1.0f) * y[ct]);
-            }
+            by_tokens<MT, 1, CT>(p, s, i * kChunk, p0, 8 * g, 0, st, box);
         }
-        if constexpr (ALONE) {
-            read_late(next);
-            read_w(next);
-        } else {
-            __syncthreads();
-        }
+        __syncthreads();
     }
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            if (p0 + 16 * ct < a.headdim && in_n)
-                *reinterpret_cast<f32x4 *>(pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2)) = st[ct][m];
+    load_state<MT, CT>(p, s, p0, 8 * g, st, true);
 }
 
 using StepFn = void (*)(StepParams);
@@ -917,22 +1111,28 @@ struct ChunkKernel {
     int waves, columns;
 };
 
-template <int N, int WN, int WC, int CT>
-constexpr ChunkKernel chunk_kernel()
+template <int N, int WN>
+constexpr ChunkKernel narrow_kernel()
 {
-    return {&ssu_delta_chunk_kernel<N, WN, WC, CT>, WN * WC, 16 * CT * WC};
+    return {&ssu_delta_narrow_kernel<N, WN>, WN + 4, 16};
+}
+
+template <int N, int WC, int CT>
+constexpr ChunkKernel wide_kernel()
+{
+    return {&ssu_delta_wide_kernel<N, WC, CT>, WC, 16 * CT * WC};
 }
 
 ChunkKernel chunk_kernel(int N, int64_t tiles)
 {
     const bool many = tiles > 2 * kNumCUs;
     if (N <= 32)
-        return many ? chunk_kernel<32, 1, 4, 2>() : chunk_kernel<32, 1, 1, 1>();
+        return many ? wide_kernel<32, 4, 2>() : narrow_kernel<32, 1>();
     if (N == 64)
-        return many ? chunk_kernel<64, 1, 4, 2>() : chunk_kernel<64, 2, 1, 1>();
+        return many ? wide_kernel<64, 4, 2>() : narrow_kernel<64, 2>();
     if (N == 128)
-        return many ? chunk_kernel<128, 1, 4, 2>() : chunk_kernel<128, 4, 1, 1>();
-    return many ? chunk_kernel<256, 1, 4, 1>() : chunk_kernel<256, 4, 1, 1>();
+        return many ? wide_kernel<128, 4, 2>() : narrow_kernel<128, 4>();
+    return many ? wide_kernel<256, 4, 1>() : narrow_kernel<256, 2>();
 }
 
 // ------------------------------------------------------------------ host --
