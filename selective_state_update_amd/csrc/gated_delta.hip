@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
         float sums[128];
         uint16_t v[kChunk * VP];
     };
-    __shared__ __attribute__((aligned(16))) Stage ring[3];
+    __shared__ __attribute__((aligned(16))) Stage ring[2];
     __shared__ f32x4 shares_k[WN > 1 ? 2 : 1][WN][2][64], shares_q[3][WN][2][64], lu[2][2][64];
     __shared__ float bad[2][WN];
     __shared__ float box[2][WN][2][64];
@@ -683,25 +683,38 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
         struct Load {
             u32x4 k[UK], q[UK], x[UX], v;
         } even, odd;
-        auto request = [&](int i, Load &l) {  // rows behind the end come from the last one
-            const int i0 = min(i, chunks - 1) * kChunk;
+        // byte offsets from a chunk's first row; rows behind the end come from the last one
+        uint32_t ok[UK], oq[UK], ov = 0;
+        auto offsets = [&](int last) {
 #pragma unroll
             for (int e = 0; e < UK; ++e) {
                 const int u = lt + 128 * e, n = u % (N / 8) * 8, col = N >= 64 || n < p.dstate ? n : 0;
-                const int64_t row = min(i0 + u / (N / 8) % 32, s.total - 1);
-                l.k[e] = *reinterpret_cast<const u32x4_a2 *>(s.k + row * a.k_t + col);
-                l.q[e] = *reinterpret_cast<const u32x4_a2 *>(s.q + row * a.q_t + col);
+                const uint32_t row = min(u / (N / 8) % 32, last);
+                ok[e] = 2 * (row * static_cast<uint32_t>(a.k_t) + col);
+                oq[e] = 2 * (row * static_cast<uint32_t>(a.q_t) + col);
             }
-            const u32x4 *const x = s.x + min(i, chunks - 1) * stride;
+            ov = 2 * (min(lt % 64 / 2, last) * static_cast<uint32_t>(a.v_t) + s.col0 + 8 * (lt % 2));
+        };
+        auto request = [&](int i, Load &l) {
+            const int ci = min(i, chunks - 1);
+            const int64_t row = static_cast<int64_t>(ci) * kChunk;
+            if (s.total - ci * kChunk < kChunk)
+                offsets(s.total - ci * kChunk - 1);
+#pragma unroll
+            for (int e = 0; e < UK; ++e) {
+                l.k[e] = at_bytes(s.k + row * a.k_t, ok[e]);
+                l.q[e] = at_bytes(s.q + row * a.q_t, oq[e]);
+            }
+            const u32x4 *const x = s.x + ci * stride;
 #pragma unroll
             for (int e = 0; e < UX; ++e)
                 l.x[e] = x[lt + 128 * e];
             // v by the first wave, the sums by the second
-            const u32x4_a2 *const v = reinterpret_cast<const u32x4_a2 *>(s.v + min(i0 + lt % 64 / 2, s.total - 1) * a.v_t + s.col0 + 8 * (lt % 2));
-            l.v = lt < 64 ? *v : static_cast<u32x4>(x[kFragments * 64 + lt % 32]);
+            l.v = wave == WN + 2 ? at_bytes(s.v + row * a.v_t, ov) : x[kFragments * 64 + lt % 32];
         };
+        offsets(kChunk - 1);
         auto turn = [&](int i, Load &l) {
-            Stage &to = ring[(i + 1) % 3];
+            Stage &to = ring[(i + 1) & 1];
 #pragma unroll
             for (int e = 0; e < UK; ++e) {
                 const int u = lt + 128 * e, row = u / (N / 8), run = u % (N / 8);
@@ -771,29 +784,55 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
     f32x4 st[1][MT];
     load_state<MT, 1>(p, s, s.col0, n0, st, false);
     __syncthreads();
-#pragma unroll 1
-    for (int i = 0; i < chunks; ++i) {
-        const Stage &at = ring[i % 3];
-        // S k (rows tokens, columns p) and S q (rows p, columns tokens), this wave's n
-        f32x4 sk[2] = {}, sq[2] = {};
-        u32x4 kf[KS][2], qf[KS][2];
+    // what a chunk needs besides the state, read from LDS as soon as the chunk before no
+    // longer needs the registers: nothing of it is waited for
+    u32x4 kf[KS][2], qf[KS][2], xf[2][3], kt[MT];
+    u32x2 vf[2];
+    f32x4 kept[2], late[2];
+    float whole, finite;
+    auto read_first = [&](const Stage &at) {
 #pragma unroll
         for (int e = 0; e < KS; ++e)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
                 kf[e][t] = at.k[run_of<N>(16 * t + c, wn * (NW / 8) + 4 * e + g)];
-#pragma unroll
-        for (int e = 0; e < KS; ++e)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
                 qf[e][t] = at.q[run_of<N>(16 * t + c, wn * (NW / 8) + 4 * e + g)];
-        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4);
-        const f32x4 v[2] = {halves(read_transposed(&at.v[vtr])), halves(read_transposed(&at.v[vtr + 16 * VP]))};
-        f32x4 kept[2], late[2];
+            }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            vf[t] = read_transposed(&at.v[(16 * t + 4 * g + c / 4) * VP + 4 * (c % 4)]);
+            kept[t] = *reinterpret_cast<const f32x4 *>(&at.sums[16 * t + 4 * g]);
+        }
+        finite = at.sums[97];
+    };
+    auto read_x = [&](const Stage &at) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            kept[t] = *reinterpret_cast<const f32x4 *>(&at.sums[16 * t + 4 * g]);
-        const float whole = at.sums[96], finite = at.sums[97];
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                xf[t][e] = at.x[64 * (3 * t + e) + lane];
+    };
+    auto read_last = [&](const Stage &at) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            late[t] = *reinterpret_cast<const f32x4 *>(&at.sums[32 + 16 * t + 4 * g]);
+        whole = at.sums[96];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int row = 4 * g + c / 4, run = wn * (NW / 8) + 4 * (m / 2) + c % 4;
+            auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<N>(r, run)]) + 4 * (m % 2); };
+            const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
+            kt[m] = u32x4{x[0], x[1], y[0], y[1]};
+        }
+    };
+    read_first(ring[0]);
+    read_x(ring[0]);
+    read_last(ring[0]);
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {
+        const Stage &next = ring[(i + 1) & 1];
+        // S k (rows tokens, columns p) and S q (rows p, columns tokens), this wave's n
+        f32x4 sk[2] = {}, sq[2] = {};
 #pragma unroll
         for (int e = 0; e < KS; ++e) {
             const Pieces f = split_triple(st[0][2 * e], st[0][2 * e + 1]);
@@ -813,22 +852,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
             for (int t = 0; t < 2; ++t)
                 sq[t] = Mma<Bf16>::run(f.a, qf[e][t], sq[t]);
         }
-        u32x4 xf[2][3], kt[MT];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-                xf[t][e] = at.x[64 * (3 * t + e) + lane];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int row = 4 * g + c / 4, run = wn * (NW / 8) + 4 * (m / 2) + c % 4;
-            auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<N>(r, run)]) + 4 * (m % 2); };
-            const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
-            kt[m] = u32x4{x[0], x[1], y[0], y[1]};
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            late[t] = *reinterpret_cast<const f32x4 *>(&at.sums[32 + 16 * t + 4 * g]);
+        const f32x4 v[2] = {halves(vf[0]), halves(vf[1])};
         // whether all of it is finite, and its sums: the other waves know of it as soon
         // as these do
         float most = finite == 1.0f ? 0.0f : INFINITY;
@@ -837,9 +861,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
             sk[t] *= kept[t];
             most = largest(sk[t], largest(v[t], most));
         }
-        const bool spoilt = __any(!(most <= 0x1p125f));
-        if (lane == 0)
-            bad[i & 1][wn] = spoilt ? 1.0f : 0.0f;
+        bad[i & 1][wn] = __any(!(most <= 0x1p125f)) ? 1.0f : 0.0f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (WN > 1)
@@ -862,6 +884,8 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
             r[t] = v[t] - sk[t];
         }
         solve(xf, r, u);
+        read_first(next);
+        read_x(next);
         if (__builtin_expect(!slow, 1)) {
             if (wn == 0) {
                 lu[i & 1][0][lane] = u[0];
@@ -879,6 +903,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
         } else {
             by_tokens<MT, WN, 1>(p, s, i * kChunk, s.col0, n0, wn, st, box);
         }
+        read_last(next);
     }
     __syncthreads();  // the last u
     load_state<MT, 1>(p, s, s.col0, n0, st, true);
@@ -1132,7 +1157,7 @@ ChunkKernel chunk_kernel(int N, int64_t tiles)
         return many ? wide_kernel<64, 4, 2>() : narrow_kernel<64, 2>();
     if (N == 128)
         return many ? wide_kernel<128, 4, 2>() : narrow_kernel<128, 4>();
-    return many ? wide_kernel<256, 4, 1>() : narrow_kernel<256, 2>();
+    return many ? wide_kernel<256, 4, 1>() : narrow_kernel<256, 4>();
 }
 
 // ------------------------------------------------------------------ host --
