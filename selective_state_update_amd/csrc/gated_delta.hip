@@ -155,36 +155,27 @@ struct DeltaParams {
     int32_t normalize, dstate;
 };
 
-// x less the low (high) bf16 of a word, exact: as a dot product of two pairs one
-// instruction instead of two. (The factors come from registers: as constants of the
-// instruction they are not a pair.)
-__device__ __forceinline__ float less_low(float x, uint32_t w)
-{
-    using H = __bf16 __attribute__((ext_vector_type(2)));
-    uint32_t f = 0x0000BF80u;  // -1, 0
-    asm("" : "+s"(f));
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(H, w), __builtin_bit_cast(H, f), x, false);
-}
+// Two values as three bf16 each, exactly (their 24 bits in three parts), and as two
+// (2^-17 relative). A part is cut off, not rounded: `and` and a subtraction, whose
+// difference is exact, run at twice the rate of conversions and beside the matrix
+// instructions. (As a dot product of pairs the subtraction is one instruction without the
+// `and`, but runs where the matrix instructions do.)
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
-__device__ __forceinline__ float less_high(float x, uint32_t w)
-{
-    using H = __bf16 __attribute__((ext_vector_type(2)));
-    uint32_t f = 0xBF800000u;  // 0, -1
-    asm("" : "+s"(f));
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(H, w), __builtin_bit_cast(H, f), x, false);
-}
+__device__ __forceinline__ uint32_t cut_pair(float x, float y) { return high_halves(__float_as_uint(x), __float_as_uint(y)); }
 
-// Two values as two bf16 each, and as three (2^-24 relative).
 __device__ __forceinline__ void split_double(float x, float y, uint32_t &a, uint32_t &b)
 {
-    a = pack2<Bf16>(x, y);
-    b = pack2<Bf16>(less_low(x, a), less_high(y, a));
+    a = cut_pair(x, y);
+    b = pack2<Bf16>(x - cut(x), y - cut(y));
 }
 
 __device__ __forceinline__ void split_triple(float x, float y, uint32_t &a, uint32_t &b, uint32_t &c)
 {
-    a = pack2<Bf16>(x, y);
-    split_double(less_low(x, a), less_high(y, a), b, c);
+    a = cut_pair(x, y);
+    const float x1 = x - cut(x), y1 = y - cut(y);
+    b = cut_pair(x1, y1);
+    c = cut_pair(x1 - cut(x1), y1 - cut(y1));
 }
 
 struct Pieces {
@@ -498,7 +489,7 @@ __device__ __forceinline__ float largest(const f32x4 &x, float m)
     return m;
 }
 
-template <int MT, int CT>
+template <int N, int MT, int CT>
 __device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &s, int p0, int n0, f32x4 (&st)[CT][MT], bool store)
 {
     const LinearParams &a = p.a;
@@ -509,7 +500,7 @@ __device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             float *const at = pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2);
-            const bool in = p0 + 16 * ct < a.headdim && n0 < p.dstate;  // (N = 16 in a tile of 32)
+            const bool in = p0 + 16 * ct < a.headdim && (N >= 64 || n0 < p.dstate);  // (N = 16 in a tile of 32)
             if (!store)
                 st[ct][m] = in ? *reinterpret_cast<const f32x4 *>(at) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             else if (in)
@@ -520,13 +511,13 @@ __device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &
 // The tokens t0 .. of a chunk one after the other, as in the kernel of steps: where a
 // value is not finite the pieces in 16 bits make NaN of infinities, and NaN of one token would
 // reach those before it through the inverse's zeros. All WN waves of a column come here.
-template <int MT, int WN, int CT>
+template <int N, int MT, int WN, int CT>
 __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s, int t0, int p0, int n0, int wn, f32x4 (&st)[CT][MT],
                                           float (&box)[2][WN][CT + 1][64])
 {
     const LinearParams &a = p.a;
     const int lane = static_cast<int>(threadIdx.x) & 63, c = lane & 15, g = lane >> 4;
-    const bool in_n = n0 < p.dstate;
+    const bool in_n = N >= 64 || n0 < p.dstate;
     const int t1 = min(t0 + kChunk, s.total);
     // sums over this wave's n, then over the waves'
     auto whole_sums = [&](float (&x)[CT + 1], float (&to)[WN][CT + 1][64]) {
@@ -561,6 +552,7 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const f32x4 k = values(kr, m);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 x[CT] = fmaf(k[e], k[e], x[CT]);
@@ -579,6 +571,7 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const f32x4 k = values(kr, m), q = values(qr, m);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 y[CT] = fmaf(q[e], q[e], y[CT]);
@@ -614,11 +607,11 @@ __device__ __forceinline__ void solve(const u32x4 (&x)[2][3], const f32x4 (&r)[2
 }
 
 // 16 tokens of out (rows p, columns tokens) from S q and u, stored.
-__device__ __forceinline__ void write_out(const DeltaParams &p, const Stretch &s, int row, int p0, const f32x4 &sq, float asked,
+__device__ __forceinline__ void write_out(const DeltaParams &p, const Stretch &s, int row0, int p0, const f32x4 &sq, float asked,
                                           const f32x4 (&u)[2], u32x4 wh, u32x4 wl)
 {
     const LinearParams &a = p.a;
-    const int g = (static_cast<int>(threadIdx.x) & 63) >> 4;
+    const int g = (static_cast<int>(threadIdx.x) & 63) >> 4, c = static_cast<int>(threadIdx.x) & 15;
     u32x4 uh, ul;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -631,8 +624,9 @@ __device__ __forceinline__ void write_out(const DeltaParams &p, const Stretch &s
     o = Mma<Bf16>::run(ul, wh, o);
     o = Mma<Bf16>::run(uh, wl, o);
     o = Mma<Bf16>::run(uh, wh, o);
-    if (row < s.total && p0 < a.headdim)
-        *reinterpret_cast<u32x2_a2 *>(a.out + (s.lo + row) * a.o_t + s.h * a.o_h + p0 + 4 * g) =
+    if (row0 + c < s.total && p0 < a.headdim)
+        *reinterpret_cast<u32x2_a2 *>(reinterpret_cast<char *>(a.out + (s.lo + row0) * a.o_t + s.h * a.o_h + p0) +
+                                      2 * (c * static_cast<uint32_t>(a.o_t) + 4 * g)) =
             u32x2{pack2<Bf16>(o[0], o[1]), pack2<Bf16>(o[2], o[3])};
 }
 
@@ -764,7 +758,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
 #pragma unroll
                 for (int w = 1; w < WN; ++w)
                     sq += shares_q[from][w][t][lane];
-                write_out(p, s, (i - 1) * kChunk + 16 * t + c, s.col0, sq, last.asked, u, last.hi, last.lo);
+                write_out(p, s, (i - 1) * kChunk + 16 * t, s.col0, sq, last.asked, u, last.hi, last.lo);
             }
             if (i == chunks)
                 return true;
@@ -782,7 +776,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
 
     const int wn = wave, n0 = wn * NW + 8 * g;
     f32x4 st[1][MT];
-    load_state<MT, 1>(p, s, s.col0, n0, st, false);
+    load_state<N, MT, 1>(p, s, s.col0, n0, st, false);
     __syncthreads();
     // what a chunk needs besides the state, read from LDS as soon as the chunk before no
     // longer needs the registers: nothing of it is waited for
@@ -901,28 +895,29 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
                     st[0][m] = Mma<Bf16>::run(kt[m], e == 0 ? f.c : e == 1 ? f.b : f.a, st[0][m]);
                 }
         } else {
-            by_tokens<MT, WN, 1>(p, s, i * kChunk, s.col0, n0, wn, st, box);
+            by_tokens<N, MT, WN, 1>(p, s, i * kChunk, s.col0, n0, wn, st, box);
         }
         read_last(next);
     }
     __syncthreads();  // the last u
-    load_state<MT, 1>(p, s, s.col0, n0, st, true);
+    load_state<N, MT, 1>(p, s, s.col0, n0, st, true);
 }
 
 // Many columns: a wave has all N of 16 CT of them, WC waves as many of one head. They share
 // a chunk's operands, which go through LDS, requested two chunks ahead, one barrier a chunk.
 template <int N, int WC, int CT>
-__global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_delta_wide_kernel(const DeltaParams p)
 {
     constexpr int THREADS = 64 * WC, KS = N / 32, MT = N / 16;
     constexpr int PC = 16 * CT * WC, VP = PC + 16;     // columns, pitch in LDS
+    constexpr int KP = N / 8 + (N == 32 ? 1 : 5);      // of k and q: a multiple of 16 runs and 5 (13)
     constexpr int RK = 32 * N / 8, RV = 32 * PC / 8;  // runs of 16 bytes
     constexpr int UK = (RK + THREADS - 1) / THREADS, UV = (RV + THREADS - 1) / THREADS, UX = (kUnits + THREADS - 1) / THREADS;
     struct Stage {
-        u32x4 k[RK], q[RK], x[kUnits];
+        u32x4 k[32 * KP], q[32 * KP], x[kUnits];
         uint16_t v[kChunk * VP];
     };
-    __shared__ __attribute__((aligned(16))) Stage ring[2];
+    __shared__ __attribute__((aligned(16))) Stage at;
     __shared__ float box[2][1][CT + 1][64];
 
     const LinearParams &a = p.a;
@@ -967,40 +962,38 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kern
         for (int e = 0; e < UX; ++e)
             rx[e] = s.x[static_cast<int64_t>(i) * a.nheads * kUnits + min(tid + THREADS * e, kUnits - 1)];
     };
-    auto place = [&](Stage &to) {
+    auto place = [&] {
 #pragma unroll
         for (int e = 0; e < UK; ++e) {
             const int u = tid + THREADS * e, row = u / (N / 8), run = u % (N / 8);
             if (RK % THREADS == 0 || u < RK) {
                 const bool in = N >= 64 || run * 8 < p.dstate;
-                to.k[run_of<N>(row, run)] = in ? rk[e] : u32x4{0, 0, 0, 0};
-                to.q[run_of<N>(row, run)] = in ? rq[e] : u32x4{0, 0, 0, 0};
+                at.k[row * KP + run] = in ? rk[e] : u32x4{0, 0, 0, 0};
+                at.q[row * KP + run] = in ? rq[e] : u32x4{0, 0, 0, 0};
             }
         }
 #pragma unroll
         for (int e = 0; e < UV; ++e) {
             const int u = tid + THREADS * e;
             if (RV % THREADS == 0 || u < RV)
-                *reinterpret_cast<u32x4 *>(to.v + u / (PC / 8) * VP + u % (PC / 8) * 8) = rv[e];
+                *reinterpret_cast<u32x4 *>(at.v + u / (PC / 8) * VP + u % (PC / 8) * 8) = rv[e];
         }
 #pragma unroll
         for (int e = 0; e < UX; ++e) {
             const int u = tid + THREADS * e;
             if (kUnits % THREADS == 0 || u < kUnits)
-                to.x[u] = rx[e];
+                at.x[u] = rx[e];
         }
     };
     offsets(kChunk - 1);
     request(0);
     f32x4 st[CT][MT];
-    load_state<MT, CT>(p, s, p0, 8 * g, st, false);
-    place(ring[0]);
-    request(min(1, chunks - 1));
+    load_state<N, MT, CT>(p, s, p0, 8 * g, st, false);
+    place();
     __syncthreads();
 
 #pragma unroll 1
     for (int i = 0; i < chunks; ++i) {
-        Stage &at = ring[i & 1];
         const float *const sums = sums_of(at.x);
 
         // S k (rows tokens, columns p) and S q (rows p, columns tokens)
@@ -1010,8 +1003,8 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kern
             u32x4 kf[2], qf[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                kf[t] = at.k[run_of<N>(16 * t + c, 4 * e + g)];
-                qf[t] = at.q[run_of<N>(16 * t + c, 4 * e + g)];
+                kf[t] = at.k[(16 * t + c) * KP + 4 * e + g];
+                qf[t] = at.q[(16 * t + c) * KP + 4 * e + g];
             }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
@@ -1031,9 +1024,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kern
                     sk[ct][t] = Mma<Bf16>::run(kf[t], f.a, sk[ct][t]);
             }
         }
-        place(ring[(i + 1) & 1]);
-        request(min(i + 2, chunks - 1));
-
+        __builtin_amdgcn_sched_barrier(0);
         f32x4 u[CT][2];
         float zero = sums[97] - 1.0f;
         u32x4 xf[2][3];
@@ -1058,6 +1049,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kern
             // (a zero of the inverse times what is not finite is NaN: any one is in all rows)
             zero = fmaf(u[ct][0][0], 0.0f, zero);
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (__builtin_expect(!__any(zero != 0.0f), 1)) {
             // the state behind the chunk
             const float whole = sums[96];
@@ -1069,11 +1061,12 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kern
             constexpr int MB = MT < 4 ? MT : 4;  // tiles at a time
 #pragma unroll
             for (int m0 = 0; m0 < MT; m0 += MB) {
+                __builtin_amdgcn_sched_barrier(0);
                 u32x4 kt[MB];
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
                     const int row = 4 * g + c / 4, run = 4 * ((m0 + m) / 2) + c % 4;
-                    auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[run_of<N>(r, run)]) + 4 * (m % 2); };
+                    auto of = [&](int r) { return reinterpret_cast<const uint16_t *>(&at.k[r * KP + run]) + 4 * (m % 2); };
                     const u32x2 x = read_transposed(of(row)), y = read_transposed(of(row + 16));
                     kt[m] = u32x4{x[0], x[1], y[0], y[1]};
                 }
@@ -1088,18 +1081,26 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 1 : 2) ssu_delta_wide_kern
                             st[ct][m0 + m] = Mma<Bf16>::run(kt[m], e == 0 ? f[ct].c : e == 1 ? f[ct].b : f[ct].a, st[ct][m0 + m]);
                         }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            request(min(i + 1, chunks - 1));
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    write_out(p, s, i * kChunk + 16 * t + c, p0 + 16 * ct, sq[ct][t], sums[64 + 16 * t + c], u[ct],
+                    write_out(p, s, i * kChunk + 16 * t, p0 + 16 * ct, sq[ct][t], sums[64 + 16 * t + c], u[ct],
                               at.x[64 * (6 + 2 * t) + lane], at.x[64 * (7 + 2 * t) + lane]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         } else {
-            by_tokens<MT, 1, CT>(p, s, i * kChunk, p0, 8 * g, 0, st, box);
+            by_tokens<N, MT, 1, CT>(p, s, i * kChunk, p0, 8 * g, 0, st, box);
+            request(min(i + 1, chunks - 1));
         }
         __syncthreads();
+        place();
+        __syncthreads();
     }
-    load_state<MT, CT>(p, s, p0, 8 * g, st, true);
+    load_state<N, MT, CT>(p, s, p0, 8 * g, st, true);
 }
 
 using StepFn = void (*)(StepParams);
@@ -1152,11 +1153,11 @@ ChunkKernel chunk_kernel(int N, int64_t tiles)
 {
     const bool many = tiles > 2 * kNumCUs;
     if (N <= 32)
-        return many ? wide_kernel<32, 4, 2>() : narrow_kernel<32, 1>();
+        return many ? wide_kernel<32, 4, 1>() : narrow_kernel<32, 1>();
     if (N == 64)
-        return many ? wide_kernel<64, 4, 2>() : narrow_kernel<64, 2>();
+        return many ? wide_kernel<64, 4, 1>() : narrow_kernel<64, 2>();
     if (N == 128)
-        return many ? wide_kernel<128, 4, 2>() : narrow_kernel<128, 4>();
+        return many ? wide_kernel<128, 4, 1>() : narrow_kernel<128, 4>();
     return many ? wide_kernel<256, 4, 1>() : narrow_kernel<256, 4>();
 }
 
