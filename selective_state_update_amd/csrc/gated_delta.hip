@@ -155,27 +155,16 @@ struct DeltaParams {
     int32_t normalize, dstate;
 };
 
-// Two values as three bf16 each, exactly (their 24 bits in three parts), and as two
-// (2^-17 relative). A part is cut off, not rounded: `and` and a subtraction, whose
-// difference is exact, run at twice the rate of conversions and beside the matrix
-// instructions. (As a dot product of pairs the subtraction is one instruction without the
-// `and`, but runs where the matrix instructions do.)
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-
-__device__ __forceinline__ uint32_t cut_pair(float x, float y) { return high_halves(__float_as_uint(x), __float_as_uint(y)); }
-
-__device__ __forceinline__ void split_double(float x, float y, uint32_t &a, uint32_t &b)
-{
-    a = cut_pair(x, y);
-    b = pack2<Bf16>(x - cut(x), y - cut(y));
-}
-
+// Two values as three bf16 each (2^-24 relative; the last part fits and is cut off).
+// (The rests as dot products of pairs, one instruction each, run where the matrix
+// instructions do and hold them up; all parts cut off, not rounded, cost the two that
+// enter out a bit each.)
 __device__ __forceinline__ void split_triple(float x, float y, uint32_t &a, uint32_t &b, uint32_t &c)
 {
-    a = cut_pair(x, y);
-    const float x1 = x - cut(x), y1 = y - cut(y);
-    b = cut_pair(x1, y1);
-    c = cut_pair(x1 - cut(x1), y1 - cut(y1));
+    a = pack2<Bf16>(x, y);
+    const float x1 = x - Bf16::lo(a), y1 = y - Bf16::hi(a);
+    b = pack2<Bf16>(x1, y1);
+    c = high_halves(__float_as_uint(x1 - Bf16::lo(b)), __float_as_uint(y1 - Bf16::hi(b)));
 }
 
 struct Pieces {
@@ -398,7 +387,7 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
         for (int e = 0; e < 4; ++e) {
             const f32x4 &w = e < 2 ? (t == 0 ? q00 : q01) : t == 0 ? none : q11;
             uint32_t wh, wl;
-            split_double(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
+            split_pair(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
             hi[e] = wh;
             lo[e] = wl;
         }
@@ -616,7 +605,7 @@ __device__ __forceinline__ void write_out(const DeltaParams &p, const Stretch &s
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         uint32_t h, l;
-        split_double(u[e / 2][2 * e % 4], u[e / 2][2 * e % 4 + 1], h, l);
+        split_pair(u[e / 2][2 * e % 4], u[e / 2][2 * e % 4 + 1], h, l);
         uh[e] = h;
         ul[e] = l;
     }
