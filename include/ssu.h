@@ -472,7 +472,7 @@ typedef struct ssu_delta_args {
 } ssu_delta_args;
 
 /* Bytes of workspace that ssu_gated_delta_rule needs for `args` (only its sizes
- * are read; -1 for sizes that it refuses): 10.5 KiB for each head and 32 tokens. */
+ * are read; -1 for sizes that it refuses): 8 KiB for each head and 32 tokens. */
 int64_t ssu_gated_delta_rule_workspace(const ssu_delta_args *args);
 
 /* Enqueue `args`' prompts on `stream`: conditions and errors of

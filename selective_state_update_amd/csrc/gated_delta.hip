@@ -143,11 +143,25 @@ __global__ void __launch_bounds__(64) ssu_delta_step_kernel(const StepParams sp)
 // fragments of the second kernel's products in bf16 pieces; the second kernel takes
 // the chunks of a sequence in order.
 //
-// Of a chunk and head: 10 fragments of 64 lanes, X's two tiles of 16 tokens in 3 pieces
-// each and the weights' in 2, then 128 floats: exp(L_i) / |k_i|, exp(L_31 - L_i) / |k_i|,
+// Of a chunk and head, in units of 16 bytes (8 KiB in all; what a call writes and reads of
+// them is as much as its operands): X's second tile of 16 tokens in 3 pieces, a unit per
+// lane, and its first, which has half the places, in 3 of half a unit per lane; the
+// weights the same in 2; then 128 floats: exp(L_i) / |k_i|, exp(L_31 - L_i) / |k_i|,
 // scale exp(L_i) / |q_i|, exp(L_31), and 1 if all of it is finite.
-constexpr int kFragments = 10;
-constexpr int kUnits = kFragments * 64 + 32;  // of 16 bytes
+constexpr int kXUnits = 3 * 64 + 3 * 32, kSumsAt = kXUnits + 2 * 64 + 2 * 32, kUnits = kSumsAt + 32;
+
+// The fragments of tile t, piece e.
+__device__ __forceinline__ u32x4 first_half(u32x2 x) { return u32x4{x[0], x[1], 0, 0}; }
+
+__device__ __forceinline__ u32x4 x_of(const u32x4 *x, int t, int e, int lane)
+{
+    return t ? x[64 * e + lane] : first_half(reinterpret_cast<const u32x2 *>(x + 192 + 32 * e)[lane]);
+}
+
+__device__ __forceinline__ u32x4 w_of(const u32x4 *x, int t, int e, int lane)
+{
+    return t ? x[kXUnits + 64 * e + lane] : first_half(reinterpret_cast<const u32x2 *>(x + kXUnits + 128 + 32 * e)[lane]);
+}
 
 struct DeltaParams {
     LinearParams a;
@@ -371,29 +385,32 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     x11 *= beta1;
 
     const int64_t id = static_cast<int64_t>(f) * a.nheads + h;
-    u32x4 *const out = p.chunks + id * kUnits + lane;
+    u32x4 *const out = p.chunks + id * kUnits;
+    auto half = [&](int at, uint32_t a, uint32_t b) { reinterpret_cast<u32x2 *>(out + at)[lane] = u32x2{a, b}; };
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
     const Pieces x0 = split_triple(x00, none), x1 = split_triple(x10, x11);
-    out[0] = x0.a;
-    out[64] = x0.b;
-    out[128] = x0.c;
-    out[192] = x1.a;
-    out[256] = x1.b;
-    out[320] = x1.c;
+    out[lane] = x1.a;
+    out[64 + lane] = x1.b;
+    out[128 + lane] = x1.c;
+    half(192, x0.a[0], x0.a[1]);
+    half(192 + 32, x0.b[0], x0.b[1]);
+    half(192 + 64, x0.c[0], x0.c[1]);
+    u32x4 hi, lo;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const f32x4 &w = e < 2 ? (t == 0 ? q00 : q01) : t == 0 ? none : q11;
-            uint32_t wh, wl;
-            split_pair(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
-            hi[e] = wh;
-            lo[e] = wl;
-        }
-        out[64 * (6 + 2 * t)] = hi;
-        out[64 * (7 + 2 * t)] = lo;
+    for (int e = 0; e < 4; ++e) {
+        const f32x4 &w = e < 2 ? q01 : q11;
+        uint32_t wh, wl;
+        split_pair(w[2 * e % 4], w[2 * e % 4 + 1], wh, wl);
+        hi[e] = wh;
+        lo[e] = wl;
     }
+    out[kXUnits + lane] = hi;
+    out[kXUnits + 64 + lane] = lo;
+    uint32_t h0, h1, l0, l1;
+    split_pair(q00[0], q00[1], h0, l0);
+    split_pair(q00[2], q00[3], h1, l1);
+    half(kXUnits + 128, h0, h1);
+    half(kXUnits + 160, l0, l1);
     const float grow = __builtin_amdgcn_exp2f(static_cast<float>(sum)), whole = __builtin_amdgcn_exp2f(static_cast<float>(all));
     const float kept = grow * lk[wave][tok], late = in ? __builtin_amdgcn_exp2f(static_cast<float>(all - sum)) * lk[wave][tok] : 0.0f;
     const float asked = a.scale * grow * lq[wave][tok];
@@ -401,7 +418,7 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     for (const f32x4 &v : {x00, x10, x11, q00, q01, q11})
         zero = unless_finite(v, zero);
     const bool finite = !__any(zero != 0.0f);
-    float *const s = reinterpret_cast<float *>(p.chunks + id * kUnits + kFragments * 64);
+    float *const s = reinterpret_cast<float *>(out + kSumsAt);
     if (lane < 32) {
         s[lane] = kept;
         s[32 + lane] = late;
@@ -467,7 +484,7 @@ __device__ __forceinline__ u32x4 at_bytes(const uint16_t *base, uint32_t off)
 }
 
 // What does not depend on the state of a chunk, as the first kernel left it.
-__device__ __forceinline__ const float *sums_of(const u32x4 *x) { return reinterpret_cast<const float *>(x + kFragments * 64); }
+__device__ __forceinline__ const float *sums_of(const u32x4 *x) { return reinterpret_cast<const float *>(x + kSumsAt); }
 
 // The larger of m and x's magnitudes; NaN stays.
 __device__ __forceinline__ float largest(const f32x4 &x, float m)
@@ -629,9 +646,9 @@ template <int N, int WN>
 __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const DeltaParams p)
 {
     constexpr int NW = N / WN, KS = NW / 32, MT = NW / 16, VP = 32;
-    constexpr int RK = 32 * N / 8, RX = 6 * 64, UK = (RK + 127) / 128, UX = RX / 128;
+    constexpr int RK = 32 * N / 8, UK = (RK + 127) / 128, UX = (kXUnits + 127) / 128;
     struct Stage {
-        u32x4 k[RK], q[RK], x[RX];
+        u32x4 k[RK], q[RK], x[128 * UX];  // (x: as many as the loads; a branch would make their waits longer)
         float sums[128];
         uint16_t v[kChunk * VP];
     };
@@ -691,9 +708,9 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
             const u32x4 *const x = s.x + ci * stride;
 #pragma unroll
             for (int e = 0; e < UX; ++e)
-                l.x[e] = x[lt + 128 * e];
+                l.x[e] = x[min(lt + 128 * e, kXUnits - 1)];
             // v by the first wave, the sums by the second
-            l.v = wave == WN + 2 ? at_bytes(s.v + row * a.v_t, ov) : x[kFragments * 64 + lt % 32];
+            l.v = wave == WN + 2 ? at_bytes(s.v + row * a.v_t, ov) : x[kSumsAt + lt % 32];
         };
         offsets(kChunk - 1);
         auto turn = [&](int i, Load &l) {
@@ -738,7 +755,11 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
         bool skip = true;
         auto turn = [&](int i, const Weights &last, Weights &now) {
             const u32x4 *const x = s.x + min(i, chunks - 1) * stride;
-            now = {sums_of(x)[64 + 16 * t + c], x[64 * (6 + 2 * t) + lane], x[64 * (7 + 2 * t) + lane]};
+            // (both tiles by the same loads: a branch around them would be waited for)
+            const char *const at = reinterpret_cast<const char *>(x + kXUnits + 128 * (1 - t)) + lane * (8 + 8 * t);
+            const u32x2 h = *reinterpret_cast<const u32x2 *>(at), l = *reinterpret_cast<const u32x2 *>(at + 512 + 512 * t);
+            const u32x2 h1 = *reinterpret_cast<const u32x2 *>(at + 8 * t), l1 = *reinterpret_cast<const u32x2 *>(at + 512 + 520 * t);
+            now = {sums_of(x)[64 + 16 * t + c], u32x4{h[0], h[1], h1[0], h1[1]}, u32x4{l[0], l[1], l1[0], l1[1]}};
             __syncthreads();
             if (!skip) {
                 const f32x4 u[2] = {lu[(i - 1) & 1][0][lane], lu[(i - 1) & 1][1][lane]};
@@ -747,7 +768,8 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
 #pragma unroll
                 for (int w = 1; w < WN; ++w)
                     sq += shares_q[from][w][t][lane];
-                write_out(p, s, (i - 1) * kChunk + 16 * t, s.col0, sq, last.asked, u, last.hi, last.lo);
+                write_out(p, s, (i - 1) * kChunk + 16 * t, s.col0, sq, last.asked, u, t ? last.hi : first_half(u32x2{last.hi[0], last.hi[1]}),
+                          t ? last.lo : first_half(u32x2{last.lo[0], last.lo[1]}));
             }
             if (i == chunks)
                 return true;
@@ -793,7 +815,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 3; ++e)
-                xf[t][e] = at.x[64 * (3 * t + e) + lane];
+                xf[t][e] = x_of(at.x, t, e, lane);
     };
     auto read_last = [&](const Stage &at) {
 #pragma unroll
@@ -1021,7 +1043,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 3; ++e)
-                xf[t][e] = at.x[64 * (3 * t + e) + lane];
+                xf[t][e] = x_of(at.x, t, e, lane);
         const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4) + 16 * CT * wc;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
@@ -1078,7 +1100,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
                     write_out(p, s, i * kChunk + 16 * t, p0 + 16 * ct, sq[ct][t], sums[64 + 16 * t + c], u[ct],
-                              at.x[64 * (6 + 2 * t) + lane], at.x[64 * (7 + 2 * t) + lane]);
+                              w_of(at.x, t, 0, lane), w_of(at.x, t, 1, lane));
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
