@@ -298,27 +298,24 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
         q01 = Mma<Bf16>::run(kf[0][s], qf[1][s], q01);
         q11 = Mma<Bf16>::run(kf[1][s], qf[1][s], q11);
     }
+    if (p.normalize) {  // the squares are the products' diagonals, in lanes c of 4 g .. 4 g + 3
+        f32x4 qq0 = {}, qq1 = {};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        float kk = 0.0f, qq = 0.0f;
-        if (p.normalize) {
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t kw = kf[t][s][e], qw = qf[t][s][e];
-                    kk = fmaf(Bf16::lo(kw), Bf16::lo(kw), fmaf(Bf16::hi(kw), Bf16::hi(kw), kk));
-                    qq = fmaf(Bf16::lo(qw), Bf16::lo(qw), fmaf(Bf16::hi(qw), Bf16::hi(qw), qq));
-                }
-            kk += __shfl_xor(kk, 16);
-            kk += __shfl_xor(kk, 32);
-            qq += __shfl_xor(qq, 16);
-            qq += __shfl_xor(qq, 32);
+        for (int s = 0; s < KS; ++s) {
+            qq0 = Mma<Bf16>::run(qf[0][s], qf[0][s], qq0);
+            qq1 = Mma<Bf16>::run(qf[1][s], qf[1][s], qq1);
         }
-        if (g == 0) {
-            lk[wave][16 * t + c] = p.normalize ? inverse_length(kk) : 1.0f;
-            lq[wave][16 * t + c] = p.normalize ? inverse_length(qq) : 1.0f;
+        auto diagonal = [&](const f32x4 &x) { return c % 4 < 2 ? (c % 4 == 0 ? x[0] : x[1]) : c % 4 == 2 ? x[2] : x[3]; };
+        const float k0 = inverse_length(diagonal(k00)), k1 = inverse_length(diagonal(k11));
+        const float q0 = inverse_length(diagonal(qq0)), q1 = inverse_length(diagonal(qq1));
+        if (c / 4 == g) {
+            lk[wave][c] = k0;
+            lk[wave][16 + c] = k1;
+            lq[wave][c] = q0;
+            lq[wave][16 + c] = q1;
         }
+    } else if (lane < 32) {
+        lk[wave][lane] = lq[wave][lane] = 1.0f;
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 
