@@ -121,12 +121,13 @@ __device__ __forceinline__ PrefixCut prefix_cut(const AttnParams &p)
 __device__ __forceinline__ void join_prefix(const AttnParams &p, int pieces, int D, int64_t row, int d, f32x4 &y, float &top, float &sum)
 {
     const float own = top;
+#pragma unroll 8
     for (int i = 0; i < pieces; ++i)
         top = fmaxf(top, p.prefix_stat[2 * (i * p.prefix_rows + row)]);
     const float f = rescale(own, top);
     y *= f;
     sum *= f;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < pieces; ++i) {
         const int64_t at = i * p.prefix_rows + row;
         const float g = rescale(p.prefix_stat[2 * at], top);

@@ -31,22 +31,28 @@ struct PrefixParams {
     int32_t page_shift;
 };
 
-constexpr int kRowsOfWave = 32, kPrefixWaves = 4, kRowsOfGroup = kRowsOfWave * kPrefixWaves;
+constexpr int kRowsOfWave = 32;
 
-// One workgroup takes 128 rows (a request's query head each) of one key head and one
-// piece of the prefix, a wave 32 of them; tiles of 64 tokens go through LDS, two
-// buffers and one barrier a tile. S^T = K Q^T and O^T = V^T P^T: a row's statistics are
+// Waves of a workgroup: two on each SIMD, or one where D = 256 needs all its registers.
+constexpr int prefix_waves(int D) { return D == 256 ? 4 : 8; }
+
+// One workgroup takes 256 rows (a request's query head each; 128 at D = 256) of one key
+// head and one piece of the prefix, a wave 32 of them; tiles of 64 tokens go through LDS, two
+// buffers and one barrier a tile, requested three tiles ahead, or two where registers
+// are short. S^T = K Q^T and O^T = V^T P^T: a row's statistics are
 // one value per lane (and its other half's), its weights lie as the second product's
 // fragment wants them (8 tokens of 16 per lane, whichever they are), and V is read
 // transposed. The rows of LDS are whole rows of K and V, their 16-byte runs
 // exchanged by row so that neither side has bank conflicts.
 template <typename T, int D>
-__global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefix_kernel(const PrefixParams p)
+__global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_prefix_kernel(const PrefixParams p)
 {
+    constexpr int W = prefix_waves(D), WR = kPrefixTile / W, kRowsOfGroup = kRowsOfWave * W;  // (WR: rows of a tile that a wave loads)
     constexpr int KS = D / 16, DT = D / 32, CH = D / 8, SW = CH < 16 ? CH - 1 : 15;
-    constexpr int RPI = 64 / CH, LI = 16 / RPI;  // rows of one load, loads of a wave's 16 rows
+    constexpr bool DEEP = D <= 128;
+    constexpr int RPI = 64 / CH, LI = WR / RPI;  // rows of one load, loads of a wave's rows
     __shared__ u32x4 lk[2][kPrefixTile * CH], lv[2][kPrefixTile * CH];
-    __shared__ __attribute__((aligned(16))) uint32_t lseen[2][kPrefixWaves];
+    __shared__ __attribute__((aligned(16))) uint32_t lseen[2][W];
 
     const AttnParams &a = p.a;
     const PrefixCut cut = prefix_cut(a);
@@ -73,52 +79,58 @@ __global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefi
     for (int s = 0; s < KS; ++s)
         qf[s] = live ? *reinterpret_cast<const u32x4_a2 *>(a.q + b * a.q_b + h * a.q_h + 16 * s + 8 * hl) : u32x4{0, 0, 0, 0};
 
-    // this wave's 16 rows of a tile: the page ids a tile ahead of K and V, those a
-    // tile ahead of the products; behind the end the last token again, as not visible
+    // this wave's rows of a tile: the page ids a tile ahead of K and V (and requested before
+    // the older tile's, since loads return in order), those three (D = 256: two) ahead
+    // of the products; behind the end the last token again, as not visible
     const int sub = lane / CH, ch = lane % CH;
     int32_t page[LI];
-    u32x4 kr[LI], vr[LI];
-    uint32_t good[LI];
-    auto token = [&](int tile, int i) { return static_cast<uint32_t>(begin) + tile * kPrefixTile + 16 * wave + RPI * i + sub; };
+    struct Rows {
+        u32x4 k[LI], v[LI];
+        bool good[LI];
+    } even, odd;  // (odd only if DEEP)
+    auto token = [&](int tile, int i) { return static_cast<uint32_t>(begin) + tile * kPrefixTile + WR * wave + RPI * i + sub; };
     auto place = [&](int tile, int i, int &col, int &off) {
         const uint32_t t = min(token(tile, i), static_cast<uint32_t>(end - 1));
         col = static_cast<int>(static_cast<uint64_t>(t) * p.page_magic >> p.page_shift);
         off = static_cast<int>(t) - col * a.page_size;
     };
-    auto request_ids = [&](int tile) {
+    auto request_ids = [&](int tile, int32_t (&to)[LI]) {
 #pragma unroll
         for (int i = 0; i < LI; ++i) {
             int col, off;
-            place(tile, i, col, off);
-            page[i] = p.table[col];
+            place(min(tile, tiles - 1), i, col, off);
+            to[i] = p.table[col];
         }
     };
-    auto request = [&](int tile) {
+    auto request = [&](int tile, Rows &to) {  // with the next one's page ids
+        int32_t next[LI];
+        request_ids(tile + 1, next);
 #pragma unroll
         for (int i = 0; i < LI; ++i) {
             int col, off;
-            place(tile, i, col, off);
-            good[i] = page[i] >= 0 && page[i] < a.num_pages && token(tile, i) < static_cast<uint32_t>(end);
-            const int64_t pg = page[i] >= 0 && page[i] < a.num_pages ? page[i] : 0;
-            kr[i] = *reinterpret_cast<const u32x4_a2 *>(a.k + pg * a.k_page + off * a.k_row + kh * a.k_h + 8 * ch);
-            vr[i] = *reinterpret_cast<const u32x4_a2 *>(a.v + pg * a.v_page + off * a.v_row + kh * a.v_h + 8 * ch);
+            place(min(tile, tiles - 1), i, col, off);
+            const bool in = page[i] >= 0 && page[i] < a.num_pages;
+            to.good[i] = in && token(min(tile, tiles - 1), i) < static_cast<uint32_t>(end);
+            const int64_t pg = in ? page[i] : 0;
+            to.k[i] = *reinterpret_cast<const u32x4_a2 *>(a.k + pg * a.k_page + off * a.k_row + kh * a.k_h + 8 * ch);
+            to.v[i] = *reinterpret_cast<const u32x4_a2 *>(a.v + pg * a.v_page + off * a.v_row + kh * a.v_h + 8 * ch);
+            page[i] = next[i];
         }
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](int buf, const Rows &from) {
         uint32_t seen = 0;
 #pragma unroll
         for (int i = 0; i < LI; ++i) {
-            const int r = 16 * wave + RPI * i + sub, at = r * CH + (ch ^ (r & SW));
-            const uint64_t ok = __ballot(good[i]);
+            const int r = WR * wave + RPI * i + sub, at = r * CH + (ch ^ (r & SW));
+            const uint64_t ok = __ballot(from.good[i]);
 #pragma unroll
             for (int j = 0; j < RPI; ++j)
                 seen |= static_cast<uint32_t>(ok >> (CH * j) & 1) << (RPI * i + j);
             // what is not visible may be NaN
-            lk[buf][at] = good[i] ? kr[i] : u32x4{0, 0, 0, 0};
-            lv[buf][at] = good[i] ? vr[i] : u32x4{0, 0, 0, 0};
+            lk[buf][at] = from.good[i] ? from.k[i] : u32x4{0, 0, 0, 0};
+            lv[buf][at] = from.good[i] ? from.v[i] : u32x4{0, 0, 0, 0};
         }
-        if (lane == 0)
-            lseen[buf][wave] = seen;
+        lseen[buf][wave] = seen;
     };
 
     f32x16 o[DT];
@@ -127,14 +139,14 @@ __global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefi
         o[d] = f32x16{};
     float m = -INFINITY, l = 0.0f;  // of this lane's row (l: this lane's tokens)
 
-    request_ids(0);
-    request(0);
-    request_ids(min(1, tiles - 1));
-    stage(0);
-    request(min(1, tiles - 1));
-    request_ids(min(2, tiles - 1));
+    request_ids(0, page);
+    request(0, even);
+    if constexpr (DEEP)
+        request(1, odd);
+    stage(0, even);
+    request(DEEP ? 2 : 1, even);
     __syncthreads();
-    for (int tile = 0; tile < tiles; ++tile) {
+    auto turn = [&](int tile, Rows &next) {  // `next` holds tile + 1
         const int buf = tile & 1;
         f32x16 s[2];
         u32x4 w[4];
@@ -146,8 +158,11 @@ __global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefi
                 for (int k = 0; k < KS; ++k)
                     s[t] = mma32<T>(lk[buf][(32 * t + c) * CH + ((2 * k + hl) ^ (c & SW))], qf[k], s[t]);
             }
-            const u32x4 seen = *reinterpret_cast<const u32x4 *>(lseen[buf]);
-            const bool all = ((seen[0] & seen[1]) & (seen[2] & seen[3])) == 0xffffu;
+            uint32_t seen[W], both = ~0u;
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                both &= seen[i] = lseen[buf][i];
+            const bool all = both == (WR == 8 ? 0xffu : 0xffffu);
             float top = m;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -159,8 +174,8 @@ __global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefi
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int at = 8 * (r / 4 % 2) + 4 * hl + r % 4;
-                        s[t][r] = seen[2 * t + r / 8] >> at & 1 ? s[t][r] : -INFINITY;
+                        const int token = 32 * t + 8 * (r / 4) + r % 4;  // (and 4 hl)
+                        s[t][r] = seen[token / WR] >> (token % WR + 4 * hl) & 1 ? s[t][r] : -INFINITY;
                     }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -190,9 +205,8 @@ __global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefi
                 for (int r = 0; r < 16; r += 2)
                     w[2 * t + r / 8][r / 2 % 4] = pack2<T>(s[t][r], s[t][r + 1]);
         }
-        stage(buf ^ 1);
-        request(min(tile + 2, tiles - 1));
-        request_ids(min(tile + 3, tiles - 1));
+        stage(buf ^ 1, next);
+        request(tile + (DEEP ? 3 : 2), next);
         if (busy) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -207,6 +221,12 @@ __global__ void __launch_bounds__(64 * kPrefixWaves, D <= 128 ? 2 : 1) ssu_prefi
                 }
         }
         __syncthreads();
+    };
+#pragma unroll 1
+    for (int tile = 0; tile < tiles; tile += 2) {
+        turn(tile, DEEP ? odd : even);
+        if (tile + 1 < tiles)
+            turn(tile + 1, even);
     }
     if (!busy)
         return;
@@ -286,26 +306,33 @@ PrefixFn prefix_kernel(int D)
 
 struct PrefixPlan {
     Plan own;
-    int pieces, rows, row_tiles;
+    int waves, pieces, rows, row_tiles;
     int64_t part_at, stat_at, bytes;  // workspace, behind the own tokens'
 };
 
-// Pieces of the prefix, all of about the same length: as many as give the workgroups,
-// of which so many are resident, the fewest tiles one after the other, a piece
-// counting two more for its start and its sums.
+// Pieces of the prefix, all of about the same length: as many as take the least time,
+// counted in ns. A workgroup takes its tiles one after the other, each D * (10 + waves
+// with rows) (D = 128: 1.5 us with one, 2.5 us with eight), and two more for its start and
+// end, one workgroup to a compute unit; a piece more costs its sums, written and read at
+// 3.3 TB/s, and 0.2 us of the join. 64 requests of 32 heads (8 of keys), 8192 tokens:
+// 4 pieces 128 us, 8 90, 16 74, 32 73, 64 94, the rule's 16; 2000 tokens: 40, 32, 32, 39, 39;
+// 256 requests of 64 heads behind 30011: 414, 429, 464, the rule's 4; 8 requests of 32
+// heads, 32000 tokens: 247, 134, 79, 55, 71, the rule's 32.
 PrefixPlan prefix_plan_of(const ssu_shared_args &a)
 {
     PrefixPlan p{};
     p.own = plan_of(a.attn);
     const int64_t rows = static_cast<int64_t>(a.attn.batch) * (a.attn.nq / a.attn.nk);
     p.rows = static_cast<int>(rows);
-    p.row_tiles = static_cast<int>((rows + kRowsOfGroup - 1) / kRowsOfGroup);
+    p.waves = prefix_waves(a.attn.headdim);
+    p.row_tiles = static_cast<int>((rows + kRowsOfWave * p.waves - 1) / (kRowsOfWave * p.waves));
     const int64_t tokens = std::min<int64_t>(a.prefix_pages > INT32_MAX ? INT32_MAX : a.prefix_pages * a.attn.page_size, INT32_MAX);
     const int64_t tiles = (tokens + kPrefixTile - 1) / kPrefixTile, groups = static_cast<int64_t>(p.row_tiles) * a.attn.nk;
-    const int64_t resident = (a.attn.headdim <= 128 ? 2 : 1) * kNumCUs;
+    const int64_t tile_ns = a.attn.headdim * (10 + std::min<int64_t>((rows + kRowsOfWave - 1) / kRowsOfWave, p.waves));
+    const int64_t piece_ns = 200 + rows * a.attn.nk * a.attn.headdim / 400;
     int64_t best = INT64_MAX;
     for (int n = 1; n <= 64 && n <= std::max<int64_t>(tiles, 1); ++n) {
-        const int64_t time = (groups * n + resident - 1) / resident * ((tiles + n - 1) / n + 2);
+        const int64_t time = (groups * n + kNumCUs - 1) / kNumCUs * ((tiles + n - 1) / n + 2) * tile_ns + n * piece_ns;
         if (time < best) {
             best = time;
             p.pieces = n;
@@ -384,13 +411,13 @@ ssu_status ssu_shared_prefix_attention(const ssu_shared_args *args, hipStream_t 
     p.page_shift = 31 + bits;
     p.page_magic = static_cast<uint32_t>(((uint64_t(1) << p.page_shift) + a.page_size - 1) / a.page_size);
     const int64_t groups = (static_cast<int64_t>(plan.pieces) * a.nk + 7) / 8 * 8 * plan.row_tiles;
-    SSU_TRY(check_launch(groups, 64 * kPrefixWaves, who));
+    SSU_TRY(check_launch(groups, 64 * plan.waves, who));
     SSU_TRY(check_launch(plan.own.groups, 64 * plan.own.waves, who));
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     if (args->prefix_pages > 0 && a.num_pages > 0) {
         const PrefixFn fn = a.q.dtype == SSU_BF16 ? prefix_kernel<Bf16>(a.headdim) : prefix_kernel<F16>(a.headdim);
-        const hipError_t e = launch_kernel(fn, p, groups, 64 * kPrefixWaves, 0, stream);
+        const hipError_t e = launch_kernel(fn, p, groups, 64 * plan.waves, 0, stream);
         if (e != hipSuccess)
             return fail(SSU_ERR_HIP, "%s: launch of the prefix kernel failed: %s", who, hipGetErrorString(e));
     }

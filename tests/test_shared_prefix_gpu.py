@@ -216,8 +216,9 @@ def test_streams_and_graphs(ssu, lens):
     c = Case(lens, 1003, 8, 2, 64, seed=10)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    got = [x.clone() for x in c.run(ssu, stream=s)]
+    got = c.run(ssu, stream=s)
     torch.cuda.current_stream().wait_stream(s)
+    got = [x.clone() for x in got]
     want = [x.clone() for x in c.run(ssu)]
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     torch.cuda.synchronize()
