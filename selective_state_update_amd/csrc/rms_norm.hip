@@ -77,12 +77,12 @@ __device__ __forceinline__ uint32_t max_over(uint32_t x, int lanes)
     return x;
 }
 
-// n (8: all) 16-bit values from p on, zeros behind them.
-template <typename T>
+// n (8: all) 16-bit values from p on, zeros behind them. With RUNS they are all there.
+template <typename T, bool RUNS>
 __device__ __forceinline__ void load_halves(const uint16_t *p, int n, float (&f)[8])
 {
     u32x4 w = {0, 0, 0, 0};
-    if (n == 8) {
+    if (RUNS || n == 8) {
         w = *reinterpret_cast<const u32x4_a2 *>(p);
     } else {
 #pragma unroll
@@ -95,9 +95,10 @@ __device__ __forceinline__ void load_halves(const uint16_t *p, int n, float (&f)
         f[i] = i % 2 ? T::hi(w[i / 2]) : T::lo(w[i / 2]);
 }
 
+template <bool RUNS>
 __device__ __forceinline__ void load_floats(const float *p, int n, float (&f)[8])
 {
-    if (n == 8) {
+    if (RUNS || n == 8) {
         const f32x4 a = *reinterpret_cast<const f32x4_a4 *>(p), b = *reinterpret_cast<const f32x4_a4 *>(p + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -115,7 +116,8 @@ template <typename T>
 __device__ __forceinline__ void store_halves(uint16_t *p, int n, const float (&f)[8])
 {
     if (n == 8) {
-        *reinterpret_cast<u32x4_a2 *>(p) = u32x4{pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
+        const u32x4 w = {pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2 *>(p));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -127,8 +129,8 @@ __device__ __forceinline__ void store_halves(uint16_t *p, int n, const float (&f
 __device__ __forceinline__ void store_floats(float *p, int n, const float (&f)[8])
 {
     if (n == 8) {
-        *reinterpret_cast<f32x4_a4 *>(p) = f32x4{f[0], f[1], f[2], f[3]};
-        *reinterpret_cast<f32x4_a4 *>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+        __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4_a4 *>(p));
+        __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4_a4 *>(p + 4));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -139,8 +141,13 @@ __device__ __forceinline__ void store_floats(float *p, int n, const float (&f)[8
 
 // Rows of up to 64 runs of 8 values take `lanes` lanes (a power of two) of a wave, longer
 // ones a workgroup of `waves` waves, M runs a lane, `64 * waves` runs apart: each
-// value is read once, kept in fp32 and written once. Memory-bound.
-template <typename T, Residual R, bool Q, int M>
+// value is read once, kept in fp32 and written once, past the L2 (its readers run on all
+// XCDs; 16384 rows of 4096: 78 against 92 us). Memory-bound: 16384 rows of 5120 with an
+// fp32 residual, to 8 bits, 171 us, 5.4 TB/s; a single row 4.5 us, which is the launch,
+// one load's latency and the sum's way through the waves. RUNS: a width of whole runs,
+// whose loads have no branches (a lane without a run reads the last) and whose weights
+// are on their way while the sum is taken; 171 against 179 us.
+template <typename T, Residual R, bool Q, int M, bool RUNS>
 __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
 {
     __shared__ float sums[16];
@@ -153,24 +160,43 @@ __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
     const bool live = t < p.ntokens;
     const int64_t row = live ? t : p.ntokens - 1;
 
-    float s[M][8], r[M][8], sum = 0.0f;
+    float s[M][8], r[M][8], w[M][8], sum = 0.0f;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-        const int at = (first + m * step) * 8, n = min(max(p.width - at, 0), 8);
-        load_halves<T>(p.x + row * p.x_t + at, n, s[m]);
+        const int run = (first + m * step) * 8, n = min(max(p.width - run, 0), 8), at = RUNS ? min(run, p.width - 8) : run;
+        load_halves<T, RUNS>(p.x + row * p.x_t + at, n, s[m]);
         if constexpr (R == Residual::same)
-            load_halves<T>(static_cast<const uint16_t *>(p.residual) + row * p.r_t + at, n, r[m]);
+            load_halves<T, RUNS>(static_cast<const uint16_t *>(p.residual) + row * p.r_t + at, n, r[m]);
         if constexpr (R == Residual::f32)
-            load_floats(static_cast<const float *>(p.residual) + row * p.r_t + at, n, r[m]);
+            load_floats<RUNS>(static_cast<const float *>(p.residual) + row * p.r_t + at, n, r[m]);
     }
+    auto load_weights = [&] {
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+        for (int m = 0; m < M; ++m) {
+            const int run = (first + m * step) * 8, n = min(max(p.width - run, 0), 8), at = RUNS ? min(run, p.width - 8) : run;
+            if (!p.weight)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[m][i] = 1.0f;
+            else if (p.w32)
+                load_floats<RUNS>(static_cast<const float *>(p.weight) + at, n, w[m]);
+            else
+                load_halves<T, RUNS>(static_cast<const uint16_t *>(p.weight) + at, n, w[m]);
+        }
+    };
+    if constexpr (RUNS)
+        load_weights();  // on their way while the sum is taken
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const bool in = !RUNS || (first + m * step) * 8 < p.width;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if constexpr (R != Residual::none)
                 s[m][i] += r[m][i];
+            s[m][i] = in ? s[m][i] : 0.0f;
             sum = fmaf(s[m][i], s[m][i], sum);
         }
+    }
     sum = sum_over(sum, shared ? 64 : p.lanes);
     if (shared) {
         if (tid % 64 == 0)
@@ -182,6 +208,8 @@ __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
     }
     const float scale = 1.0f / sqrtf(sum / static_cast<float>(p.width) + p.eps);
 
+    if constexpr (!RUNS)
+        load_weights();
     uint32_t top[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -192,17 +220,10 @@ __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
         if constexpr (R == Residual::f32)
             if (live)
                 store_floats(static_cast<float *>(p.residual) + row * p.r_t + at, n, s[m]);
-        float w[8];
-        if (p.weight) {
-            if (p.w32)
-                load_floats(static_cast<const float *>(p.weight) + at, n, w);
-            else
-                load_halves<T>(static_cast<const uint16_t *>(p.weight) + at, n, w);
-        }
         top[m] = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            s[m][i] = s[m][i] * scale * (p.weight ? w[i] : 1.0f);
+            s[m][i] = s[m][i] * scale * w[m][i];
             if (i < n)
                 top[m] = max(top[m], __float_as_uint(s[m][i]) & 0x7fffffffu);
         }
@@ -253,7 +274,7 @@ __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
             continue;
         uint8_t *const out = static_cast<uint8_t *>(p.out) + row * p.o_t + at;
         if (n == 8) {
-            *reinterpret_cast<u32x2_a1 *>(out) = q;
+            __builtin_nontemporal_store(q, reinterpret_cast<u32x2_a1 *>(out));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -268,18 +289,27 @@ __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
 
 using NormFn = void (*)(NormParams);
 
-template <typename T, Residual R, bool Q>
+template <typename T, Residual R, bool Q, bool RUNS>
 NormFn norm_kernel(int m)
 {
-    return m == 1 ? &ssu_rms_norm_kernel<T, R, Q, 1> : m == 2 ? &ssu_rms_norm_kernel<T, R, Q, 2> : &ssu_rms_norm_kernel<T, R, Q, 4>;
+    return m == 1 ? &ssu_rms_norm_kernel<T, R, Q, 1, RUNS>
+         : m == 2 ? &ssu_rms_norm_kernel<T, R, Q, 2, RUNS>
+                  : &ssu_rms_norm_kernel<T, R, Q, 4, RUNS>;
+}
+
+template <typename T, Residual R>
+NormFn norm_kernel(bool q, bool runs, int m)
+{
+    return q ? (runs ? norm_kernel<T, R, true, true>(m) : norm_kernel<T, R, true, false>(m))
+             : (runs ? norm_kernel<T, R, false, true>(m) : norm_kernel<T, R, false, false>(m));
 }
 
 template <typename T>
-NormFn norm_kernel(Residual r, bool q, int m)
+NormFn norm_kernel(Residual r, bool q, bool runs, int m)
 {
-    return r == Residual::none ? (q ? norm_kernel<T, Residual::none, true>(m) : norm_kernel<T, Residual::none, false>(m))
-         : r == Residual::same ? (q ? norm_kernel<T, Residual::same, true>(m) : norm_kernel<T, Residual::same, false>(m))
-                               : (q ? norm_kernel<T, Residual::f32, true>(m) : norm_kernel<T, Residual::f32, false>(m));
+    return r == Residual::none ? norm_kernel<T, Residual::none>(q, runs, m)
+         : r == Residual::same ? norm_kernel<T, Residual::same>(q, runs, m)
+                               : norm_kernel<T, Residual::f32>(q, runs, m);
 }
 
 // ------------------------------------------------------------------ host --
@@ -366,6 +396,9 @@ extern "C" ssu_status ssu_add_rms_norm(const ssu_norm_args *args, hipStream_t st
         const int rows = 256 / p.lanes;
         groups = a.ntokens / rows + (a.ntokens % rows != 0);
     } else {
+        // (16384 rows of 640 runs: m = 2 172 us, 1 182, 4 190; of 1024: 171, 186, 183; of 2048:
+        // 395 (m = 2), 414 (4); 16384 rows of 512 runs 92 with 1, 90 with 2, but 509 of
+        // them 6.1 against 6.2: few rows want many waves)
         m = runs <= 512 ? 1 : runs <= 2048 ? 2 : 4;
         p.waves = (runs + 64 * m - 1) / (64 * m);
         threads = 64 * p.waves;
@@ -373,8 +406,8 @@ extern "C" ssu_status ssu_add_rms_norm(const ssu_norm_args *args, hipStream_t st
     }
     SSU_TRY(check_launch(groups, threads, "ssu_add_rms_norm"));
     const Residual r = !p.residual ? Residual::none : a.residual.dtype == SSU_F32 ? Residual::f32 : Residual::same;
-    const bool eight = a.out.dtype == SSU_E4M3;
-    const NormFn fn = a.x.dtype == SSU_BF16 ? norm_kernel<Bf16>(r, eight, m) : norm_kernel<F16>(r, eight, m);
+    const bool eight = a.out.dtype == SSU_E4M3, runs_only = a.width % 8 == 0;
+    const NormFn fn = a.x.dtype == SSU_BF16 ? norm_kernel<Bf16>(r, eight, runs_only, m) : norm_kernel<F16>(r, eight, runs_only, m);
     DeviceGuard guard;
     SSU_TRY(guard.enter(a.device));
     const hipError_t e = launch_kernel(fn, p, groups, threads, 0, stream);
