@@ -50,6 +50,12 @@ __all__ = [
     "qk_norm_rope",
     "paged_attention",
     "paged_attention_workspace",
+    "gated_delta_rule",
+    "gated_delta_rule_step",
+    "gated_delta_rule_workspace",
+    "add_rms_norm",
+    "shared_prefix_attention",
+    "shared_prefix_attention_workspace",
     "tile_fits",
     "tiles",
     "library_path",
