@@ -36,19 +36,26 @@ constexpr int kRowsOfWave = 32;
 // Waves of a workgroup: two on each SIMD, or one where D = 256 needs all its registers.
 constexpr int prefix_waves(int D) { return D == 256 ? 4 : 8; }
 
+// Where row r of a tile has its 16-byte run: exchanged by row, so that neither 16 rows of one
+// run (K) nor 4 rows of 4 runs (V, transposed) have bank conflicts.
+template <int CH>
+__device__ __forceinline__ int run_at(int r, int run)
+{
+    return r * CH + (run ^ (CH == 8 ? (r & 2) << 1 | (r >> 2 & 3) : (r & 3) << 2 | (r >> 2 & 3)));
+}
+
 // One workgroup takes 256 rows (a request's query head each; 128 at D = 256) of one key
 // head and one piece of the prefix, a wave 32 of them; tiles of 64 tokens go through LDS, two
 // buffers and one barrier a tile, requested three tiles ahead, or two where registers
 // are short. S^T = K Q^T and O^T = V^T P^T: a row's statistics are
 // one value per lane (and its other half's), its weights lie as the second product's
 // fragment wants them (8 tokens of 16 per lane, whichever they are), and V is read
-// transposed. The rows of LDS are whole rows of K and V, their 16-byte runs
-// exchanged by row so that neither side has bank conflicts.
+// transposed. The rows of LDS are whole rows of K and V.
 template <typename T, int D>
 __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_prefix_kernel(const PrefixParams p)
 {
     constexpr int W = prefix_waves(D), WR = kPrefixTile / W, kRowsOfGroup = kRowsOfWave * W;  // (WR: rows of a tile that a wave loads)
-    constexpr int KS = D / 16, DT = D / 32, CH = D / 8, SW = CH < 16 ? CH - 1 : 15;
+    constexpr int KS = D / 16, DT = D / 32, CH = D / 8;
     constexpr bool DEEP = D <= 128;
     constexpr int RPI = 64 / CH, LI = WR / RPI;  // rows of one load, loads of a wave's rows
     __shared__ u32x4 lk[2][kPrefixTile * CH], lv[2][kPrefixTile * CH];
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
         uint32_t seen = 0;
 #pragma unroll
         for (int i = 0; i < LI; ++i) {
-            const int r = WR * wave + RPI * i + sub, at = r * CH + (ch ^ (r & SW));
+            const int r = WR * wave + RPI * i + sub, at = run_at<CH>(r, ch);
             const uint64_t ok = __ballot(from.good[i]);
 #pragma unroll
             for (int j = 0; j < RPI; ++j)
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
                 s[t] = f32x16{};
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    s[t] = mma32<T>(lk[buf][(32 * t + c) * CH + ((2 * k + hl) ^ (c & SW))], qf[k], s[t]);
+                    s[t] = mma32<T>(lk[buf][run_at<CH>(32 * t + c, 2 * k + hl)], qf[k], s[t]);
             }
             uint32_t seen[W], both = ~0u;
 #pragma unroll
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
                 for (int d = 0; d < DT; ++d) {
                     const int r0 = 16 * k + 4 * hl + lane % 16 / 4, run = 4 * d + 2 * (lane / 16 % 2) + lane % 4 / 2;
                     auto at = [&](int r) {
-                        return reinterpret_cast<const uint16_t *>(&lv[buf][r * CH + (run ^ (r & SW))]) + 4 * (lane % 2);
+                        return reinterpret_cast<const uint16_t *>(&lv[buf][run_at<CH>(r, run)]) + 4 * (lane % 2);
                     };
                     const u32x2 x = read_transposed(at(r0)), y = read_transposed(at(r0 + 8));
                     o[d] = mma32<T>(u32x4{x[0], x[1], y[0], y[1]}, w[k], o[d]);
