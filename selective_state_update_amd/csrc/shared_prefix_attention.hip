@@ -81,10 +81,15 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     const bool live = row < p.rows;
     const int b = min(row, p.rows - 1) / a.heads_per_kv, h = kh * a.heads_per_kv + min(row, p.rows - 1) % a.heads_per_kv;
     const bool busy = (id % p.row_tiles) * kRowsOfGroup + wave * kRowsOfWave < p.rows;  // (uniform)
+    // Scores stay unscaled, so that the scale is part of the exponent's one fma (2 to 3 %): with
+    // its sign moved into Q, and scores of 0 instead of a scale of 0.
+    const bool flat = a.scale_log2 == 0.0f;
+    const float scale = flat ? 1.0f : fabsf(a.scale_log2);
+    const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
     u32x4 qf[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s)
-        qf[s] = live ? *reinterpret_cast<const u32x4_a2 *>(a.q + b * a.q_b + h * a.q_h + 16 * s + 8 * hl) : u32x4{0, 0, 0, 0};
+        qf[s] = sign ^ (live ? *reinterpret_cast<const u32x4_a2 *>(a.q + b * a.q_b + h * a.q_h + 16 * s + 8 * hl) : u32x4{0, 0, 0, 0});
 
     // this wave's rows of a tile: the page ids a tile ahead of K and V (and requested before
     // the older tile's, since loads return in order), those three (D = 256: two) ahead
@@ -144,7 +149,7 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
 #pragma unroll
     for (int d = 0; d < DT; ++d)
         o[d] = f32x16{};
-    float m = -INFINITY, l = 0.0f;  // of this lane's row (l: this lane's tokens)
+    float m = -INFINITY, l = 0.0f;  // of this lane's row (m: unscaled until the end, l: this lane's tokens)
 
     request_ids(0, page);
     request(0, even);
@@ -155,27 +160,34 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     __syncthreads();
     auto turn = [&](int tile, Rows &next) {  // `next` holds tile + 1
         const int buf = tile & 1;
+        // D = 256: places in LDS are computed for every tile, not kept in registers (they
+        // would be spilled: 256 requests of 32 heads behind 8000 tokens 262 against 491 us)
+        int at_lane = lane;
+        if constexpr (!DEEP)
+            asm volatile("" : "+v"(at_lane));
         f32x16 s[2];
         u32x4 w[4];
         if (busy) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+                // products before the other wave's softmax, the halves one after the other: 1 to 3 %
+                __builtin_amdgcn_s_setprio(1);
                 s[t] = f32x16{};
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    s[t] = mma32<T>(lk[buf][run_at<CH>(32 * t + c, 2 * k + hl)], qf[k], s[t]);
+                    s[t] = mma32<T>(lk[buf][run_at<CH>(32 * t + at_lane % 32, 2 * k + at_lane / 32)], qf[k], s[t]);
             }
+            __builtin_amdgcn_s_setprio(0);
             uint32_t seen[W], both = ~0u;
 #pragma unroll
             for (int i = 0; i < W; ++i)
                 both &= seen[i] = lseen[buf][i];
             const bool all = both == (WR == 8 ? 0xffu : 0xffffu);
             float top = m;
+            if (flat)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[t][r] *= a.scale_log2;
+                for (int t = 0; t < 2; ++t)
+                    s[t] *= 0.0f;
             if (!all)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -191,14 +203,14 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
                     top = fmaxf(top, s[t][r]);
             top = fmaxf(top, __shfl_xor(top, 32));
             const float base = top == -INFINITY ? 0.0f : top;  // scores of -inf weigh nothing
-            const float keep = __builtin_amdgcn_exp2f(m - base);
+            const float keep = __builtin_amdgcn_exp2f((m - base) * scale), shift = fmaf(-base, scale, kShift<T>);
             m = top;
             float sum = 0.0f;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[t][r] = __builtin_amdgcn_exp2f(s[t][r] - base + kShift<T>);
+                    s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], scale, shift));
                     sum += s[t][r];
                 }
             l = fmaf(l, keep, sum);
@@ -219,9 +231,9 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
             for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                    const int r0 = 16 * k + 4 * hl + lane % 16 / 4, run = 4 * d + 2 * (lane / 16 % 2) + lane % 4 / 2;
+                    const int r0 = 16 * k + 4 * (at_lane / 32) + at_lane % 16 / 4, run = 4 * d + 2 * (at_lane / 16 % 2) + at_lane % 4 / 2;
                     auto at = [&](int r) {
-                        return reinterpret_cast<const uint16_t *>(&lv[buf][run_at<CH>(r, run)]) + 4 * (lane % 2);
+                        return reinterpret_cast<const uint16_t *>(&lv[buf][run_at<CH>(r, run)]) + 4 * (at_lane % 2);
                     };
                     const u32x2 x = read_transposed(at(r0)), y = read_transposed(at(r0 + 8));
                     o[d] = mma32<T>(u32x4{x[0], x[1], y[0], y[1]}, w[k], o[d]);
@@ -237,6 +249,7 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     }
     if (!busy)
         return;
+    m *= scale;
 
     // An infinity in V, times a weight that 16 bits round to 0, is not what the formula
     // has: such a row's sums are taken again with whole weights, token by token (the
