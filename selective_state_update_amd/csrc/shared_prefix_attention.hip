@@ -334,10 +334,10 @@ struct PrefixPlan {
 // counted in ns. A workgroup takes its tiles one after the other, each D * (10 + waves
 // with rows) (D = 128: 1.5 us with one, 2.5 us with eight), and two more for its start and
 // end, one workgroup to a compute unit; a piece more costs its sums, written and read at
-// 3.3 TB/s, and 0.2 us of the join. 64 requests of 32 heads (8 of keys), 8192 tokens:
-// 4 pieces 128 us, 8 90, 16 74, 32 73, 64 94, the rule's 16; 2000 tokens: 40, 32, 32, 39, 39;
-// 256 requests of 64 heads behind 30011: 414, 429, 464, the rule's 4; 8 requests of 32
-// heads, 32000 tokens: 247, 134, 79, 55, 71, the rule's 32.
+// 3.3 TB/s, and 0.2 us of the join. 64 requests of 32 heads (8 of keys), 8192 tokens: 4
+// pieces 115 us, 8 83, 16 70, 32 68, 64 85, the rule's 69; 2000 tokens: 37, 28, 27, 31, 31,
+// 28; 256 requests of 64 heads behind 30011: 383, 393, 427, 488, 615, 382; 8 requests of
+// 32 heads, 32000 tokens: 217, 118, 68, 45, 57, 46.
 PrefixPlan prefix_plan_of(const ssu_shared_args &a)
 {
     PrefixPlan p{};
