@@ -442,8 +442,9 @@ ssu_status ssu_linear_attention_step(const ssu_linear_args *args, hipStream_t st
  * fp32; over prompts the products run on bf16 matrix instructions, fp32 operands
  * as three bf16 pieces where they enter the state (2^-24 relative), as two where
  * they enter only the output (2^-17). log_decay below -10000 counts as -10000. A chunk of tokens
- * with a value that is not finite goes through the recurrence token by token, so
- * that prompts leave the infinities and NaN that single steps leave: NaN and
+ * with a value that is not finite, or whose state, keys, queries, gains and decays are so
+ * large that a value might leave fp32 in it, goes through the recurrence token by
+ * token, so that prompts leave the infinities and NaN that single steps leave: NaN and
  * infinite v reach their own and later tokens of their channel p only, NaN and
  * infinite k and beta their own and later tokens, NaN and infinite q their own
  * token. Such chunks take 20 to 100 times as long. The same call gives the same bits.

@@ -147,8 +147,16 @@ __global__ void __launch_bounds__(64) ssu_delta_step_kernel(const StepParams sp)
 // them is as much as its operands): X's second tile of 16 tokens in 3 pieces, a unit per
 // lane, and its first, which has half the places, in 3 of half a unit per lane; the
 // weights the same in 2; then 128 floats: exp(L_i) / |k_i|, exp(L_31 - L_i) / |k_i|,
-// scale exp(L_i) / |q_i|, exp(L_31), and 1 if all of it is finite.
+// scale exp(L_i) / |q_i|, and Limits.
 constexpr int kXUnits = 3 * 64 + 3 * 32, kSumsAt = kXUnits + 2 * 64 + 2 * 32, kUnits = kSumsAt + 32;
+
+// A chunk's exp(L_31), and the bounds within which it is computed from its fragments: of the
+// values that enter the triangle's right side (negative if a fragment is not finite), of the
+// state before it, and what the state can gain of such values. Beyond them its tokens
+// go one after the other, as infinities and NaN have to.
+struct Limits {
+    float whole, most, state, gain;
+};
 
 // The fragments of tile t, piece e.
 __device__ __forceinline__ u32x4 first_half(u32x2 x) { return u32x4{x[0], x[1], 0, 0}; }
@@ -201,6 +209,29 @@ __device__ __forceinline__ Pieces split_triple(const f32x4 &x, const f32x4 &y)
 }
 
 __device__ __forceinline__ f32x4 halves(u32x2 w) { return f32x4{Bf16::lo(w[0]), Bf16::hi(w[0]), Bf16::lo(w[1]), Bf16::hi(w[1])}; }
+
+// The larger of two; of m and x's magnitudes; NaN stays.
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
+__device__ __forceinline__ float largest(const f32x4 &x, float m)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        m = larger(m, fabsf(x[r]));
+    return m;
+}
+
+template <int CT, int MT>
+__device__ __forceinline__ float largest(const f32x4 (&x)[CT][MT])
+{
+    float most = 0.0f;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            most = largest(x[ct][m], most);
+    return most;
+}
 
 // acc * 0 added up: 0, or NaN if one is not finite.
 __device__ __forceinline__ float unless_finite(const f32x4 &x, float zero)
@@ -300,24 +331,25 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
         q01 = Mma<Bf16>::run(kf[0][s], qf[1][s], q01);
         q11 = Mma<Bf16>::run(kf[1][s], qf[1][s], q11);
     }
-    if (p.normalize) {  // the squares are the products' diagonals, in lanes c of 4 g .. 4 g + 3
-        f32x4 qq0 = {}, qq1 = {};
+    // the squares are the products' diagonals, in lanes c of 4 g .. 4 g + 3
+    f32x4 qq0 = {}, qq1 = {};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qq0 = Mma<Bf16>::run(qf[0][s], qf[0][s], qq0);
-            qq1 = Mma<Bf16>::run(qf[1][s], qf[1][s], qq1);
-        }
-        auto diagonal = [&](const f32x4 &x) { return c % 4 < 2 ? (c % 4 == 0 ? x[0] : x[1]) : c % 4 == 2 ? x[2] : x[3]; };
-        const float k0 = inverse_length(diagonal(k00)), k1 = inverse_length(diagonal(k11));
-        const float q0 = inverse_length(diagonal(qq0)), q1 = inverse_length(diagonal(qq1));
-        if (c / 4 == g) {
-            lk[wave][c] = k0;
-            lk[wave][16 + c] = k1;
-            lq[wave][c] = q0;
-            lq[wave][16 + c] = q1;
-        }
-    } else if (lane < 32) {
-        lk[wave][lane] = lq[wave][lane] = 1.0f;
+    for (int s = 0; s < KS; ++s) {
+        qq0 = Mma<Bf16>::run(qf[0][s], qf[0][s], qq0);
+        qq1 = Mma<Bf16>::run(qf[1][s], qf[1][s], qq1);
+    }
+    auto diagonal = [&](const f32x4 &x) { return c % 4 < 2 ? (c % 4 == 0 ? x[0] : x[1]) : c % 4 == 2 ? x[2] : x[3]; };
+    const float kk0 = diagonal(k00), kk1 = diagonal(k11), q0 = diagonal(qq0), q1 = diagonal(qq1);
+    const bool has = c / 4 == g;  // (other lanes: no token's)
+    const float kk = has ? larger(kk0, kk1) : 0.0f, qq = has ? larger(q0, q1) : 0.0f;
+    if (!p.normalize) {
+        if (lane < 32)
+            lk[wave][lane] = lq[wave][lane] = 1.0f;
+    } else if (has) {
+        lk[wave][c] = inverse_length(kk0);
+        lk[wave][16 + c] = inverse_length(kk1);
+        lq[wave][c] = inverse_length(q0);
+        lq[wave][16 + c] = inverse_length(q1);
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 
@@ -417,16 +449,42 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     for (const f32x4 &v : {x00, x10, x11, q00, q01, q11})
         zero = unless_finite(v, zero);
     const bool finite = !__any(zero != 0.0f);
+
+    // How large the state and r may be (Limits) so that whatever the recurrence computes of them, here
+    // or token by token, stays below 2^127. With D the largest decay between two points of the
+    // chunk (1 or more), K, Q the largest lengths of k and q, K' of normalized k, X the largest of
+    // the inverse's values: |u| <= 32 X |r|, a state's value between two tokens is
+    // D (|S| + 32 K' |u|) at most, a sum of N products of it with k or q 16 K or 16 Q times
+    // that, and out |scale| / |q| times it. Of |S| that is 16 D W, of |r| 2^15 X D W K' (what an
+    // inverse length of at most 1000 takes u to is less), W = max(1, K, Q, Q |scale| / |q|).
+    const float xs = largest(x00, largest(x10, largest(x11, 0.0f))), unit = fabsf(a.scale) * lq[wave][tok];
+    float K = 0x1p12f, W = 0x1p22f, X = 0x1p10f, D = 1.0f;  // where no decay grows and all are at most so
+    if (!__all(!(in && decay > 0.0f) && kk <= K * K && qq <= K * K && xs <= X && unit <= 0x1p10f)) {
+        auto of_wave = [](float x) {
+#pragma unroll
+            for (int m = 32; m >= 1; m /= 2)
+                x = larger(x, __shfl_xor(x, m));
+            return x;
+        };
+        float low = fminf(static_cast<float>(sum), 0.0f);  // the least sum of decays up to a token
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2)
+            low = fminf(low, __shfl_up(low, m, 32));
+        D = __builtin_amdgcn_exp2f(of_wave(larger(static_cast<float>(sum) - low, 0.0f)));
+        X = of_wave(larger(xs, 0x1p-10f));  // (r stays finite)
+        K = sqrtf(of_wave(larger(kk, 1.0f)));
+        W = larger(K, sqrtf(of_wave(qq)) * of_wave(larger(unit, 1.0f)));
+    }
+    const float normed = p.normalize ? 1.0f : K, most = 0x1p112f / (0x1p15f * X * D * W * normed);
     float *const s = reinterpret_cast<float *>(out + kSumsAt);
     if (lane < 32) {
         s[lane] = kept;
         s[32 + lane] = late;
         s[64 + lane] = asked;
     }
-    if (lane == 0) {
-        s[96] = whole;
-        s[97] = finite ? 1.0f : 0.0f;
-    }
+    // (r: 2^10 less than it could be, and up to 8 times what is looked at)
+    if (lane == 0)
+        *reinterpret_cast<f32x4 *>(s + 96) = f32x4{whole, finite ? most : -1.0f, 0x1p122f / (16.0f * D * W), 0x1p13f * normed * D * X * most};
 }
 
 // Where a token's row of k and q in LDS has its 16-byte runs: exchanged by row, so that
@@ -485,13 +543,10 @@ __device__ __forceinline__ u32x4 at_bytes(const uint16_t *base, uint32_t off)
 // What does not depend on the state of a chunk, as the first kernel left it.
 __device__ __forceinline__ const float *sums_of(const u32x4 *x) { return reinterpret_cast<const float *>(x + kSumsAt); }
 
-// The larger of m and x's magnitudes; NaN stays.
-__device__ __forceinline__ float largest(const f32x4 &x, float m)
+__device__ __forceinline__ Limits limits_of(const float *sums)
 {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        m = __builtin_elementwise_maximum(m, fabsf(x[r]));
-    return m;
+    const f32x4 x = *reinterpret_cast<const f32x4 *>(sums + 96);
+    return {x[0], x[1], x[2], x[3]};
 }
 
 template <int N, int MT, int CT>
@@ -795,7 +850,8 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
     u32x4 kf[KS][2], qf[KS][2], xf[2][3], kt[MT];
     u32x2 vf[2];
     f32x4 kept[2], late[2];
-    float whole, finite;
+    Limits limits;
+    float whole, reach = INFINITY;  // (reach: no value of this wave's state is larger)
     auto read_first = [&](const Stage &at) {
 #pragma unroll
         for (int e = 0; e < KS; ++e)
@@ -809,7 +865,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
             vf[t] = read_transposed(&at.v[(16 * t + 4 * g + c / 4) * VP + 4 * (c % 4)]);
             kept[t] = *reinterpret_cast<const f32x4 *>(&at.sums[16 * t + 4 * g]);
         }
-        finite = at.sums[97];
+        limits = limits_of(at.sums);
     };
     auto read_x = [&](const Stage &at) {
 #pragma unroll
@@ -859,15 +915,18 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
                 sq[t] = Mma<Bf16>::run(f.a, qf[e][t], sq[t]);
         }
         const f32x4 v[2] = {halves(vf[0]), halves(vf[1])};
-        // whether all of it is finite, and its sums: the other waves know of it as soon
-        // as these do
-        float most = finite == 1.0f ? 0.0f : INFINITY;
+        // whether all of it is within its limits (sk: this wave's share of up to 4), and its sums:
+        // the other waves know of it as soon as these do
+        float most = 0.0f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             sk[t] *= kept[t];
             most = largest(sk[t], largest(v[t], most));
         }
-        bad[i & 1][wn] = __any(!(most <= 0x1p125f)) ? 1.0f : 0.0f;
+        if (__any(!(reach <= limits.state)))
+            reach = largest(st);
+        bad[i & 1][wn] = __any(!(most <= limits.most && reach <= limits.state)) ? 1.0f : 0.0f;
+        reach = fmaf(reach, whole, limits.gain);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (WN > 1)
@@ -908,6 +967,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
                 }
         } else {
             by_tokens<N, MT, WN, 1>(p, s, i * kChunk, s.col0, n0, wn, st, box);
+            reach = INFINITY;
         }
         read_last(next);
     }
@@ -1007,6 +1067,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
     request(0);
     f32x4 st[CT][MT];
     load_state<N, MT, CT>(p, s, p0, 8 * g, st, false);
+    float reach = INFINITY;  // no value of the state is larger
     place();
     __syncthreads();
 
@@ -1044,7 +1105,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         }
         __builtin_amdgcn_sched_barrier(0);
         f32x4 u[CT][2];
-        float zero = sums[97] - 1.0f;
+        float most = 0.0f;
         u32x4 xf[2][3];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -1062,15 +1123,18 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     r[t][e] = fmaf(-kept[e], sk[ct][t][e], r[t][e]);
+                most = largest(r[t], most);
             }
             solve(xf, r, u[ct]);
-            // (a zero of the inverse times what is not finite is NaN: any one is in all rows)
-            zero = fmaf(u[ct][0][0], 0.0f, zero);
         }
+        const Limits limits = limits_of(sums);
+        if (__any(!(reach <= limits.state)))
+            reach = largest(st);
         __builtin_amdgcn_sched_barrier(0);
-        if (__builtin_expect(!__any(zero != 0.0f), 1)) {
+        if (__builtin_expect(__all(most <= limits.most && reach <= limits.state), 1)) {
             // the state behind the chunk
-            const float whole = sums[96];
+            const float whole = limits.whole;
+            reach = fmaf(reach, whole, limits.gain);
             Pieces f[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
@@ -1112,6 +1176,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
             }
         } else {
             by_tokens<N, MT, 1, CT>(p, s, i * kChunk, p0, 8 * g, 0, st, box);
+            reach = INFINITY;
             request(min(i + 1, chunks - 1));
         }
         __syncthreads();
