@@ -618,7 +618,8 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
                 x[CT] = fmaf(k[e], k[e], x[CT]);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    st[ct][m][e] *= keep;
+                    if (in_n)  // (an infinite decay times the zeros behind N is NaN)
+                        st[ct][m][e] *= keep;
                     x[ct] = fmaf(st[ct][m][e], k[e], x[ct]);
                 }
             }
@@ -637,7 +638,7 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
                 y[CT] = fmaf(q[e], q[e], y[CT]);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    if (in_n)  // (an infinite u times the zeros behind N is NaN)
+                    if (in_n)  // (as is an infinite u)
                         st[ct][m][e] = fmaf(u[ct], length * k[e], st[ct][m][e]);
                     y[ct] = fmaf(st[ct][m][e], q[e], y[ct]);
                 }

@@ -127,3 +127,25 @@ def test_a_large_state_decays_before_it_is_asked(ssu, N, many):
     assert b.out.isfinite().all()
     same(a.out, b.out, 2.0 ** -6 * b.out.float().abs(), "out")
     same(a.state, b.state, 2.0 ** -16 * b.state.abs(), "state")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("N", [16, 32, 64])
+def test_infinities_of_one_sign(ssu, N, many):
+    """A decay of infinity over a state, keys and queries of one sign, the gain negative: all that single tokens leave are
+    infinities of one sign. With N = 16 half of a product's places are no state at all."""
+    def change(c):
+        c.state.abs_().add_(0.1)
+        c.q.abs_().add_(0.1)
+        c.k.abs_().add_(0.1)
+        c.v.zero_()
+        c.beta.mul_(-0.01)
+        for b in c.cu[:-1].tolist():
+            c.log_decay[b + 37] = INF
+
+    a, b = pair([50] * (40 if many else 1), 8 if many else 2, 64, N, 2, change)
+    prompts_and_steps(ssu, a, b)
+    assert b.out[:37].isfinite().all() and (b.out[37:50] == INF).all() and (b.state[b.idx.long()] == INF).all()
+    # (the chunk of the tokens 0 to 31 is finite; sums of one sign lose nothing)
+    same(a.out, b.out, 2.0 ** -6 * b.out.float().abs(), "out")
+    same(a.state, b.state, 2.0 ** -10 * b.state.abs(), "state")
