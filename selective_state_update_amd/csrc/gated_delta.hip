@@ -573,16 +573,16 @@ __device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &
 // reach those before it through the inverse's zeros. All WN waves of a column come here.
 template <int N, int MT, int WN, int CT>
 __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s, int t0, int p0, int n0, int wn, f32x4 (&st)[CT][MT],
-                                          float (&box)[2][WN][CT + 1][64])
+                                          float (&box)[2][WN][CT][64])
 {
     const LinearParams &a = p.a;
     const int lane = static_cast<int>(threadIdx.x) & 63, c = lane & 15, g = lane >> 4;
     const bool in_n = N >= 64 || n0 < p.dstate;
     const int t1 = min(t0 + kChunk, s.total);
     // sums over this wave's n, then over the waves'
-    auto whole_sums = [&](float (&x)[CT + 1], float (&to)[WN][CT + 1][64]) {
+    auto whole_sums = [&](float (&x)[CT], float (&to)[WN][CT][64]) {
 #pragma unroll
-        for (int e = 0; e <= CT; ++e) {
+        for (int e = 0; e < CT; ++e) {
             x[e] += __shfl_xor(x[e], 16);
             x[e] += __shfl_xor(x[e], 32);
             if (WN > 1)
@@ -591,7 +591,7 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
         if constexpr (WN > 1) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e <= CT; ++e) {
+            for (int e = 0; e < CT; ++e) {
                 x[e] = to[0][e][lane];
 #pragma unroll
                 for (int w = 1; w < WN; ++w)
@@ -599,58 +599,60 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
             }
         }
     };
+    // of all n of a row: every wave for itself, before anything is multiplied with the row
+    auto length_of = [&](const uint16_t *row) {
+        if (!p.normalize)
+            return 1.0f;
+        const f32x4 x = 4 * lane < p.dstate ? halves(*reinterpret_cast<const u32x2_a2 *>(row + 4 * lane)) : f32x4{};
+        return inverse_length(sum_lanes<64>(fmaf(x[3], x[3], fmaf(x[2], x[2], fmaf(x[1], x[1], x[0] * x[0])))));
+    };
 #pragma unroll 1
     for (int t = t0; t < t1; ++t) {
         const int64_t tok = s.lo + t;
         const float keep = exp_f32(a.decay[tok * a.d_t + s.h * a.d_h]);
         const float beta = a.beta ? a.beta[tok * a.b_t + s.h * a.b_h] : 1.0f;
-        const uint16_t *const kr = s.k + t * a.k_t + n0, *const qr = s.q + t * a.q_t + n0;
+        const uint16_t *const kr = s.k + t * a.k_t, *const qr = s.q + t * a.q_t;
         auto values = [&](const uint16_t *row, int m) {
-            return in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(row + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
+            return in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(row + n0 + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
         };
-        float x[CT + 1] = {}, y[CT + 1] = {}, u[CT];
+        const float klength = length_of(kr), qlength = length_of(qr);
+        float x[CT] = {}, y[CT] = {}, u[CT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const f32x4 k = values(kr, m);
+            const f32x4 k = klength * values(kr, m);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[CT] = fmaf(k[e], k[e], x[CT]);
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     if (in_n)  // (an infinite decay times the zeros behind N is NaN)
                         st[ct][m][e] *= keep;
                     x[ct] = fmaf(st[ct][m][e], k[e], x[ct]);
                 }
-            }
         }
         whole_sums(x, box[0]);
-        const float length = p.normalize ? inverse_length(x[CT]) : 1.0f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            u[ct] = beta * (Bf16::lo(s.v[t * a.v_t + min(p0 + 16 * ct + c, a.headdim - 1)]) - length * x[ct]);
+            u[ct] = beta * (Bf16::lo(s.v[t * a.v_t + min(p0 + 16 * ct + c, a.headdim - 1)]) - x[ct]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const f32x4 k = values(kr, m), q = values(qr, m);
+            const f32x4 k = klength * values(kr, m), q = values(qr, m);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[CT] = fmaf(q[e], q[e], y[CT]);
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     if (in_n)  // (as is an infinite u)
-                        st[ct][m][e] = fmaf(u[ct], length * k[e], st[ct][m][e]);
+                        st[ct][m][e] = fmaf(u[ct], k[e], st[ct][m][e]);
                     y[ct] = fmaf(st[ct][m][e], q[e], y[ct]);
                 }
-            }
         }
         whole_sums(y, box[1]);
         if (wn == 0 && g == 0)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
                 if (p0 + 16 * ct < a.headdim)
-                    a.out[tok * a.o_t + s.h * a.o_h + p0 + 16 * ct + c] =
-                        Bf16::round(a.scale * (p.normalize ? inverse_length(y[CT]) : 1.0f) * y[ct]);
+                    a.out[tok * a.o_t + s.h * a.o_h + p0 + 16 * ct + c] = Bf16::round(a.scale * qlength * y[ct]);
     }
 }
 
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
     __shared__ __attribute__((aligned(16))) Stage ring[2];
     __shared__ f32x4 shares_k[WN > 1 ? 2 : 1][WN][2][64], shares_q[3][WN][2][64], lu[2][2][64];
     __shared__ float bad[2][WN];
-    __shared__ float box[2][WN][2][64];
+    __shared__ float box[2][WN][1][64];
 
     const LinearParams &a = p.a;
     Stretch s;
@@ -997,7 +999,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         uint16_t v[kChunk * VP];
     };
     __shared__ __attribute__((aligned(16))) Stage at;
-    __shared__ float box[2][1][CT + 1][64];
+    __shared__ float box[2][1][CT][64];
 
     const LinearParams &a = p.a;
     Stretch s;

@@ -149,3 +149,26 @@ def test_infinities_of_one_sign(ssu, N, many):
     # (the chunk of the tokens 0 to 31 is finite; sums of one sign lose nothing)
     same(a.out, b.out, 2.0 ** -6 * b.out.float().abs(), "out")
     same(a.state, b.state, 2.0 ** -10 * b.state.abs(), "state")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("N", [32, 64, 128])
+def test_keys_are_normalized_before_they_are_asked(ssu, N, many):
+    """A state near fp32's end and long keys that are normalized: S k of the keys as given would be beyond fp32. A NaN in
+    one query takes the chunk through the tokens."""
+    def change(c):
+        c.state.abs_().add_(1.0).mul_(1e36)
+        c.k.abs_().add_(0.5).mul_(1000.0)
+        c.v.zero_()
+        for b in c.cu[:-1].tolist():
+            c.q[b + 5, 0, 1] = NAN
+
+    a, b = pair([20] * (40 if many else 1), 8 if many else 2, 64, N, 2, change, normalize=True)
+    prompts_and_steps(ssu, a, b)
+    assert b.state.isfinite().all() and b.out[:5].isfinite().all() and b.out[6:20].isfinite().all()
+    assert b.out[5].isnan().any() and not b.out[5].isnan().all()
+    # rows of the state are at most 10e36 sqrt(N) long and no longer behind a token; a token rounds sums of N such products
+    # with a key and a query of length 1: 20 N 2^-24 at most
+    size = 10e36 * N ** 0.5
+    same(a.out, b.out, 2.0 ** -8 * b.out.float().abs() + 2.0 ** -12 * size, "out")
+    same(a.state, b.state, 2.0 ** -12 * size, "state")
