@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     constexpr bool DEEP = D <= 128;
     constexpr int RPI = 64 / CH, LI = WR / RPI;  // rows of one load, loads of a wave's rows
     __shared__ u32x4 lk[2][kPrefixTile * CH], lv[2][kPrefixTile * CH];
-    __shared__ __attribute__((aligned(16))) uint32_t lseen[2][W];
+    __shared__ __attribute__((aligned(16))) uint32_t lseen[2][W], lbusy[W];
 
     const AttnParams &a = p.a;
     const PrefixCut cut = prefix_cut(a);
@@ -77,10 +77,11 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     const int end = static_cast<int>(min(cut.tokens, static_cast<int64_t>(begin) + cut.per * kPrefixTile));
     const int tiles = (end - begin + kPrefixTile - 1) / kPrefixTile;
 
+    // Rows of padding requests count as rows that are not there: whatever their q holds is not used.
     const int row = (id % p.row_tiles) * kRowsOfGroup + wave * kRowsOfWave + c;
-    const bool live = row < p.rows;
     const int b = min(row, p.rows - 1) / a.heads_per_kv, h = kh * a.heads_per_kv + min(row, p.rows - 1) % a.heads_per_kv;
-    const bool busy = (id % p.row_tiles) * kRowsOfGroup + wave * kRowsOfWave < p.rows;  // (uniform)
+    const bool live = row < p.rows && a.lens[b] >= 0;
+    const bool busy = __any(live);  // (uniform)
     // Scores stay unscaled, so that the scale is part of the exponent's one fma (2 to 3 %): with
     // its sign moved into Q, and scores of 0 instead of a scale of 0.
     const bool flat = a.scale_log2 == 0.0f;
@@ -89,7 +90,10 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     u32x4 qf[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s)
-        qf[s] = sign ^ (live ? *reinterpret_cast<const u32x4_a2 *>(a.q + b * a.q_b + h * a.q_h + 16 * s + 8 * hl) : u32x4{0, 0, 0, 0});
+        qf[s] = *reinterpret_cast<const u32x4_a2 *>(a.q + b * a.q_b + h * a.q_h + 16 * s + 8 * hl);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+        qf[s] = sign ^ (live ? qf[s] : u32x4{0, 0, 0, 0});
 
     // this wave's rows of a tile: the page ids a tile ahead of K and V (and requested before
     // the older tile's, since loads return in order), those three (D = 256: two) ahead
@@ -157,7 +161,14 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
         request(1, odd);
     stage(0, even);
     request(DEEP ? 2 : 1, even);
+    lbusy[wave] = busy;
     __syncthreads();
+    uint32_t work = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        work |= lbusy[i];
+    if (__builtin_amdgcn_readfirstlane(static_cast<int>(work)) == 0)
+        return;  // (all of them)
     auto turn = [&](int tile, Rows &next) {  // `next` holds tile + 1
         const int buf = tile & 1;
         // D = 256: places in LDS are computed for every tile, not kept in registers (they
@@ -260,8 +271,8 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             zero = fmaf(o[d][r], 0.0f, zero);
-    if (__any(zero != 0.0f)) {
-        const bool again = zero + __shfl_xor(zero, 32) != 0.0f;
+    if (__any(live && zero != 0.0f)) {
+        const bool again = live && zero + __shfl_xor(zero, 32) != 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
             o[d] = again ? f32x16{} : o[d];
