@@ -265,14 +265,16 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
     // An infinity in V, times a weight that 16 bits round to 0, is not what the formula
     // has: such a row's sums are taken again with whole weights, token by token (the
     // other rows of its wave are other requests' and keep theirs: with a finite row all V is).
+    // A row whose weights add up to NaN is NaN whatever V holds.
+    l += __shfl_xor(l, 32);
     float zero = 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             zero = fmaf(o[d][r], 0.0f, zero);
-    if (__any(live && zero != 0.0f)) {
-        const bool again = live && zero + __shfl_xor(zero, 32) != 0.0f;
+    const bool again = live && l == l && zero + __shfl_xor(zero, 32) != 0.0f;
+    if (__any(again)) {
 #pragma unroll
         for (int d = 0; d < DT; ++d)
             o[d] = again ? f32x16{} : o[d];
@@ -309,7 +311,6 @@ __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_pr
         }
     }
 
-    l += __shfl_xor(l, 32);
     if (!live)
         return;
     const int64_t at = piece * a.prefix_rows + static_cast<int64_t>(b) * a.nk * a.heads_per_kv + h;

@@ -57,7 +57,7 @@ def least_time(f):
     return min(times)
 
 
-@pytest.mark.parametrize("row", ["padding"])
+@pytest.mark.parametrize("row", ["padding", "live"])
 def test_time_of_nan(ssu, row):
     """A NaN in a query does not hold the other requests up. (Token by token, 20 to 100 times as long, would go only rows
     that infinities of V reach.)"""
