@@ -603,9 +603,13 @@ ssu_status ssu_paged_attention(const ssu_attn_args *args, hipStream_t stream);
  *
  * The prefix is read once for the whole batch, and the products with it run on all
  * requests' query heads of a key head at once. seq_lens[b] = 0: the prefix alone; negative:
- * padding. Numerics as ssu_paged_attention, but the weights of the prefix's V are
- * rounded to 16 bits once: 2^-9 (BF16; F16 2^-12) of the weighted mean of |V| at most,
- * a pair would make half again as many products. All that is said there of
+ * padding, of which neither q nor the prefix is used. Numerics as ssu_paged_attention, but
+ * the weights of the prefix's V are rounded to 16 bits once, not kept as a pair: each is off by
+ * half a step at most, out by 2^-8 (BF16; F16 2^-11) of the weighted mean of |V| beside its own
+ * rounding, and with F16 each weight below 2^-28 of its row's largest by up to 2^-39 of that
+ * one. (Whole weights: ssu_paged_attention with the prefix's pages in every request's table.)
+ * Pieces of the prefix in which V holds infinities are read again token by token for rows that see
+ * them, which takes 20 times as long or more. All that is said there of
  * visibility, infinities and repeated calls holds for the prefix.
  */
 typedef struct ssu_shared_args {

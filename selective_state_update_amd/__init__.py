@@ -756,7 +756,8 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_len, block
     tokens (on the GPU: a captured call sees what it holds at the replay); block_table
     [batch, max_pages] and seq_lens [batch] are the requests' own tokens behind it
     (0: the prefix alone; negative: padding). The rest, and what is returned, as in
-    paged_attention; ``workspace`` of shared_prefix_attention_workspace bytes.
+    paged_attention, but the weights of the prefix are rounded once to q's type (half a
+    step); ``workspace`` of shared_prefix_attention_workspace bytes.
     Inference only: no gradient."""
     if stream is not None:
         with _on(stream, q):

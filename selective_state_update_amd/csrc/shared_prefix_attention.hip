@@ -51,6 +51,11 @@ __device__ __forceinline__ int run_at(int r, int run)
 // one value per lane (and its other half's), its weights lie as the second product's
 // fragment wants them (8 tokens of 16 per lane, whichever they are), and V is read
 // transposed. The rows of LDS are whole rows of K and V.
+// Weights are rounded to 16 bits once (half a step: 2^-8, fp16 2^-11, relative), while l adds up
+// whole ones: products with their remainders too, as where a row's tokens are its own, take
+// 256 requests of 64 heads behind 30011 tokens from 375 to 476 us, 64 of 32 behind 8192 from 69
+// to 75, and the root mean square of out's error from 1.30 (fp16 1.38) times the one of its own
+// rounding to 1.00.
 template <typename T, int D>
 __global__ void __launch_bounds__(64 * prefix_waves(D), D <= 128 ? 2 : 1) ssu_prefix_kernel(const PrefixParams p)
 {
