@@ -77,6 +77,27 @@ __device__ __forceinline__ uint32_t max_over(uint32_t x, int lanes)
     return x;
 }
 
+// y / unit for |y| <= 448 unit, rounded as a division is: the product with the rounded reciprocal
+// and one correction by what it leaves, which is exact unless it is below fp32's least. That a
+// quotient halfway between two 8-bit values stays there, and none beside it gets there, holds
+// for all 2^23 significands of unit. 509 rows of 8192 9.3 us, 65536 of 512 in groups of 32 33:
+// the product alone 8.9 and 31, divisions 10.2 and 37.
+__device__ __forceinline__ void over(float (&y)[8], float unit)
+{
+    if (unit > 0x1p-90f && unit < INFINITY) {
+        const float inv = 1.0f / unit;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = y[i] * inv;
+            y[i] = fmaf(-fmaf(q, unit, -y[i]), inv, q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            y[i] /= unit;
+    }
+}
+
 // n (8: all) 16-bit values from p on, zeros behind them. With RUNS they are all there.
 template <typename T, bool RUNS>
 __device__ __forceinline__ void load_halves(const uint16_t *p, int n, float (&f)[8])
@@ -262,12 +283,12 @@ __global__ void __launch_bounds__(1024) ssu_rms_norm_kernel(const NormParams p)
         const int run = first + m * step, at = run * 8, n = min(max(p.width - at, 0), 8);
         const float most = __uint_as_float(top[m]) / kLargest;
         const float unit = most < 0x1p-126f ? 0x1p-126f : most;  // (NaN stays)
-        const float inv = 1.0f / unit;
+        over(s[m], unit);
         u32x2 q;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            int word = __builtin_amdgcn_cvt_pk_fp8_f32(s[m][4 * h] * inv, s[m][4 * h + 1] * inv, 0, false);
-            word = __builtin_amdgcn_cvt_pk_fp8_f32(s[m][4 * h + 2] * inv, s[m][4 * h + 3] * inv, word, true);
+            int word = __builtin_amdgcn_cvt_pk_fp8_f32(s[m][4 * h], s[m][4 * h + 1], 0, false);
+            word = __builtin_amdgcn_cvt_pk_fp8_f32(s[m][4 * h + 2], s[m][4 * h + 3], word, true);
             q[h] = static_cast<uint32_t>(word);
         }
         if (!live)
