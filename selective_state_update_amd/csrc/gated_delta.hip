@@ -221,15 +221,13 @@ __device__ __forceinline__ float largest(const f32x4 &x, float m)
     return m;
 }
 
-template <int CT, int MT>
-__device__ __forceinline__ float largest(const f32x4 (&x)[CT][MT])
+template <int MT>
+__device__ __forceinline__ float largest(const f32x4 (&x)[MT])
 {
     float most = 0.0f;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            most = largest(x[ct][m], most);
+    for (int m = 0; m < MT; ++m)
+        most = largest(x[m], most);
     return most;
 }
 
@@ -549,55 +547,47 @@ __device__ __forceinline__ Limits limits_of(const float *sums)
     return {x[0], x[1], x[2], x[3]};
 }
 
-template <int N, int MT, int CT>
-__device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &s, int p0, int n0, f32x4 (&st)[CT][MT], bool store)
+template <int N, int MT>
+__device__ __forceinline__ void load_state(const DeltaParams &p, const Stretch &s, int p0, int n0, f32x4 (&st)[MT], bool store)
 {
     const LinearParams &a = p.a;
     const int c = static_cast<int>(threadIdx.x) & 15;
     float *const pool = a.state + s.slot * a.s_slot + s.h * a.s_head + (p0 + c) * a.s_row + n0;
+    const bool in = p0 < a.headdim && (N >= 64 || n0 < p.dstate);  // (N = 16 in a tile of 32)
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            float *const at = pool + 16 * ct * a.s_row + 32 * (m / 2) + 4 * (m % 2);
-            const bool in = p0 + 16 * ct < a.headdim && (N >= 64 || n0 < p.dstate);  // (N = 16 in a tile of 32)
-            if (!store)
-                st[ct][m] = in ? *reinterpret_cast<const f32x4 *>(at) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            else if (in)
-                *reinterpret_cast<f32x4 *>(at) = st[ct][m];
-        }
+    for (int m = 0; m < MT; ++m) {
+        float *const at = pool + 32 * (m / 2) + 4 * (m % 2);
+        if (!store)
+            st[m] = in ? *reinterpret_cast<const f32x4 *>(at) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        else if (in)
+            *reinterpret_cast<f32x4 *>(at) = st[m];
+    }
 }
 
 // The tokens t0 .. of a chunk one after the other, as in the kernel of steps: where a
 // value is not finite the pieces in 16 bits make NaN of infinities, and NaN of one token would
 // reach those before it through the inverse's zeros. All WN waves of a column come here.
-template <int N, int MT, int WN, int CT>
-__device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s, int t0, int p0, int n0, int wn, f32x4 (&st)[CT][MT],
-                                          float (&box)[2][WN][CT][64])
+template <int N, int MT, int WN>
+__device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s, int t0, int p0, int n0, int wn, f32x4 (&st)[MT],
+                                          float (*box)[WN][64])
 {
     const LinearParams &a = p.a;
     const int lane = static_cast<int>(threadIdx.x) & 63, c = lane & 15, g = lane >> 4;
     const bool in_n = N >= 64 || n0 < p.dstate;
     const int t1 = min(t0 + kChunk, s.total);
-    // sums over this wave's n, then over the waves'
-    auto whole_sums = [&](float (&x)[CT], float (&to)[WN][CT][64]) {
-#pragma unroll
-        for (int e = 0; e < CT; ++e) {
-            x[e] += __shfl_xor(x[e], 16);
-            x[e] += __shfl_xor(x[e], 32);
-            if (WN > 1)
-                to[wn][e][lane] = x[e];
-        }
+    // the sum over this wave's n, then over the waves' (through box[turn])
+    auto whole_sum = [&](float x, int turn) {
+        x += __shfl_xor(x, 16);
+        x += __shfl_xor(x, 32);
         if constexpr (WN > 1) {
+            box[turn][wn][lane] = x;
             __syncthreads();
+            x = box[turn][0][lane];
 #pragma unroll
-            for (int e = 0; e < CT; ++e) {
-                x[e] = to[0][e][lane];
-#pragma unroll
-                for (int w = 1; w < WN; ++w)
-                    x[e] += to[w][e][lane];
-            }
+            for (int w = 1; w < WN; ++w)
+                x += box[turn][w][lane];
         }
+        return x;
     };
     // of all n of a row: every wave for itself, before anything is multiplied with the row
     auto length_of = [&](const uint16_t *row) {
@@ -616,43 +606,33 @@ __device__ __forceinline__ void by_tokens(const DeltaParams &p, const Stretch &s
             return in_n ? halves(*reinterpret_cast<const u32x2_a2 *>(row + n0 + 32 * (m / 2) + 4 * (m % 2))) : f32x4{};
         };
         const float klength = length_of(kr), qlength = length_of(qr);
-        float x[CT] = {}, y[CT] = {}, u[CT];
+        float x = 0.0f, y = 0.0f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const f32x4 k = klength * values(kr, m);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    if (in_n)  // (an infinite decay times the zeros behind N is NaN)
-                        st[ct][m][e] *= keep;
-                    x[ct] = fmaf(st[ct][m][e], k[e], x[ct]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                if (in_n)  // (an infinite decay times the zeros behind N is NaN)
+                    st[m][e] *= keep;
+                x = fmaf(st[m][e], k[e], x);
+            }
         }
-        whole_sums(x, box[0]);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-            u[ct] = beta * (Bf16::lo(s.v[t * a.v_t + min(p0 + 16 * ct + c, a.headdim - 1)]) - x[ct]);
+        const float u = beta * (Bf16::lo(s.v[t * a.v_t + min(p0 + c, a.headdim - 1)]) - whole_sum(x, 0));
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const f32x4 k = klength * values(kr, m), q = values(qr, m);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    if (in_n)  // (as is an infinite u)
-                        st[ct][m][e] = fmaf(u[ct], k[e], st[ct][m][e]);
-                    y[ct] = fmaf(st[ct][m][e], q[e], y[ct]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                if (in_n)  // (as is an infinite u)
+                    st[m][e] = fmaf(u, k[e], st[m][e]);
+                y = fmaf(st[m][e], q[e], y);
+            }
         }
-        whole_sums(y, box[1]);
-        if (wn == 0 && g == 0)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-                if (p0 + 16 * ct < a.headdim)
-                    a.out[tok * a.o_t + s.h * a.o_h + p0 + 16 * ct + c] = Bf16::round(a.scale * qlength * y[ct]);
+        y = whole_sum(y, 1);
+        if (wn == 0 && g == 0 && p0 < a.headdim)
+            a.out[tok * a.o_t + s.h * a.o_h + p0 + c] = Bf16::round(a.scale * qlength * y);
     }
 }
 
@@ -714,7 +694,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
     __shared__ __attribute__((aligned(16))) Stage ring[2];
     __shared__ f32x4 shares_k[WN > 1 ? 2 : 1][WN][2][64], shares_q[3][WN][2][64], lu[2][2][64];
     __shared__ float bad[2][WN];
-    __shared__ float box[2][WN][1][64];
+    __shared__ float box[2][WN][64];
 
     const LinearParams &a = p.a;
     Stretch s;
@@ -845,8 +825,8 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
     }
 
     const int wn = wave, n0 = wn * NW + 8 * g;
-    f32x4 st[1][MT];
-    load_state<N, MT, 1>(p, s, s.col0, n0, st, false);
+    f32x4 st[MT];
+    load_state<N>(p, s, s.col0, n0, st, false);
     __syncthreads();
     // what a chunk needs besides the state, read from LDS as soon as the chunk before no
     // longer needs the registers: nothing of it is waited for
@@ -900,7 +880,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
         f32x4 sk[2] = {}, sq[2] = {};
 #pragma unroll
         for (int e = 0; e < KS; ++e) {
-            const Pieces f = split_triple(st[0][2 * e], st[0][2 * e + 1]);
+            const Pieces f = split_triple(st[2 * e], st[2 * e + 1]);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
                 sk[t] = Mma<Bf16>::run(kf[e][t], f.c, sk[t]);
@@ -965,20 +945,20 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     if (e == 0)
-                        st[0][m] *= whole;
-                    st[0][m] = Mma<Bf16>::run(kt[m], e == 0 ? f.c : e == 1 ? f.b : f.a, st[0][m]);
+                        st[m] *= whole;
+                    st[m] = Mma<Bf16>::run(kt[m], e == 0 ? f.c : e == 1 ? f.b : f.a, st[m]);
                 }
         } else {
-            by_tokens<N, MT, WN, 1>(p, s, i * kChunk, s.col0, n0, wn, st, box);
+            by_tokens<N, MT, WN>(p, s, i * kChunk, s.col0, n0, wn, st, box);
             reach = INFINITY;
         }
         read_last(next);
     }
     __syncthreads();  // the last u
-    load_state<N, MT, 1>(p, s, s.col0, n0, st, true);
+    load_state<N>(p, s, s.col0, n0, st, true);
 }
 
-// Many columns: a wave has all N of 16 CT of them, WC waves as many of one head. They share
+// Many columns: a wave has all N of 16 of them, kWideWaves waves as many of one head. They share
 // a chunk's operands, which go through one stage in LDS, requested while the chunk before is
 // worked on, two barriers a chunk: what covers a wave's waits is the other waves of its
 // SIMD, two to four of them, and the one stage is what leaves room for them. 16 prompts of up to
@@ -986,11 +966,13 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
 // waves to a stage 337, 32 columns to a wave 373. What bounds it: vector instructions
 // of three waves beside the matrix products (under which the clock falls to 1.7 GHz), and
 // at the end the longest prompt, alone.
-template <int N, int WC, int CT>
-__global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_delta_wide_kernel(const DeltaParams p)
+constexpr int kWideWaves = 4;
+
+template <int N>
+__global__ void __launch_bounds__(64 * kWideWaves, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_delta_wide_kernel(const DeltaParams p)
 {
-    constexpr int THREADS = 64 * WC, KS = N / 32, MT = N / 16;
-    constexpr int PC = 16 * CT * WC, VP = PC + 16;     // columns, pitch in LDS
+    constexpr int THREADS = 64 * kWideWaves, KS = N / 32, MT = N / 16;
+    constexpr int PC = 16 * kWideWaves, VP = PC + 16;  // columns, pitch in LDS
     constexpr int KP = N / 8 + (N == 32 ? 1 : 5);      // of k and q: a multiple of 16 runs and 5 (13)
     constexpr int RK = 32 * N / 8, RV = 32 * PC / 8;  // runs of 16 bytes
     constexpr int UK = (RK + THREADS - 1) / THREADS, UV = (RV + THREADS - 1) / THREADS, UX = (kUnits + THREADS - 1) / THREADS;
@@ -999,7 +981,6 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         uint16_t v[kChunk * VP];
     };
     __shared__ __attribute__((aligned(16))) Stage at;
-    __shared__ float box[2][1][CT][64];
 
     const LinearParams &a = p.a;
     Stretch s;
@@ -1007,7 +988,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         return;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wc = __builtin_amdgcn_readfirstlane(tid >> 6), chunks = (s.total + kChunk - 1) / kChunk;
-    const int p0 = s.col0 + 16 * CT * wc;
+    const int p0 = s.col0 + 16 * wc;
 
     // Requests of a chunk; rows behind the end come from the last one, columns behind P
     // and N from the first.
@@ -1068,8 +1049,8 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
     };
     offsets(kChunk - 1);
     request(0);
-    f32x4 st[CT][MT];
-    load_state<N, MT, CT>(p, s, p0, 8 * g, st, false);
+    f32x4 st[MT];
+    load_state<N>(p, s, p0, 8 * g, st, false);
     float reach = INFINITY;  // no value of the state is larger
     place();
     __syncthreads();
@@ -1079,7 +1060,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         const float *const sums = sums_of(at.x);
 
         // S k (rows tokens, columns p) and S q (rows p, columns tokens)
-        f32x4 sk[CT][2] = {}, sq[CT][2] = {};
+        f32x4 sk[2] = {}, sq[2] = {};
 #pragma unroll
         for (int e = 0; e < KS; ++e) {
             u32x4 kf[2], qf[2];
@@ -1088,26 +1069,23 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
                 kf[t] = at.k[(16 * t + c) * KP + 4 * e + g];
                 qf[t] = at.q[(16 * t + c) * KP + 4 * e + g];
             }
+            const Pieces f = split_triple(st[2 * e], st[2 * e + 1]);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const Pieces f = split_triple(st[ct][2 * e], st[ct][2 * e + 1]);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    sk[ct][t] = Mma<Bf16>::run(kf[t], f.c, sk[ct][t]);
-                    sq[ct][t] = Mma<Bf16>::run(f.b, qf[t], sq[ct][t]);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    sk[ct][t] = Mma<Bf16>::run(kf[t], f.b, sk[ct][t]);
-                    sq[ct][t] = Mma<Bf16>::run(f.a, qf[t], sq[ct][t]);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    sk[ct][t] = Mma<Bf16>::run(kf[t], f.a, sk[ct][t]);
+            for (int t = 0; t < 2; ++t) {
+                sk[t] = Mma<Bf16>::run(kf[t], f.c, sk[t]);
+                sq[t] = Mma<Bf16>::run(f.b, qf[t], sq[t]);
             }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sk[t] = Mma<Bf16>::run(kf[t], f.b, sk[t]);
+                sq[t] = Mma<Bf16>::run(f.a, qf[t], sq[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                sk[t] = Mma<Bf16>::run(kf[t], f.a, sk[t]);
         }
         __builtin_amdgcn_sched_barrier(0);
-        f32x4 u[CT][2];
+        f32x4 r[2], u[2];
         float most = 0.0f;
         u32x4 xf[2][3];
 #pragma unroll
@@ -1115,21 +1093,17 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
 #pragma unroll
             for (int e = 0; e < 3; ++e)
                 xf[t][e] = x_of(at.x, t, e, lane);
-        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4) + 16 * CT * wc;
+        const int vtr = (4 * g + c / 4) * VP + 4 * (c % 4) + 16 * wc;
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            f32x4 r[2];
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 kept = *reinterpret_cast<const f32x4 *>(sums + 16 * t + 4 * g);
+            r[t] = halves(read_transposed(at.v + vtr + 16 * t * VP));
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const f32x4 kept = *reinterpret_cast<const f32x4 *>(sums + 16 * t + 4 * g);
-                r[t] = halves(read_transposed(at.v + vtr + 16 * t * VP + 16 * ct));
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    r[t][e] = fmaf(-kept[e], sk[ct][t][e], r[t][e]);
-                most = largest(r[t], most);
-            }
-            solve(xf, r, u[ct]);
+            for (int e = 0; e < 4; ++e)
+                r[t][e] = fmaf(-kept[e], sk[t][e], r[t][e]);
+            most = largest(r[t], most);
         }
+        solve(xf, r, u);
         const Limits limits = limits_of(sums);
         if (__any(!(reach <= limits.state)))
             reach = largest(st);
@@ -1138,11 +1112,8 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
             // the state behind the chunk
             const float whole = limits.whole;
             reach = fmaf(reach, whole, limits.gain);
-            Pieces f[CT];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-                f[ct] = split_triple(*reinterpret_cast<const f32x4 *>(sums + 32 + 4 * g) * u[ct][0],
-                                     *reinterpret_cast<const f32x4 *>(sums + 48 + 4 * g) * u[ct][1]);
+            const Pieces f = split_triple(*reinterpret_cast<const f32x4 *>(sums + 32 + 4 * g) * u[0],
+                                          *reinterpret_cast<const f32x4 *>(sums + 48 + 4 * g) * u[1]);
             constexpr int MB = MT < 4 ? MT : 4;  // tiles at a time
 #pragma unroll
             for (int m0 = 0; m0 < MT; m0 += MB) {
@@ -1158,27 +1129,23 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
 #pragma unroll
-                    for (int m = 0; m < MB; ++m)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            if (e == 0)
-                                st[ct][m0 + m] *= whole;
-                            st[ct][m0 + m] = Mma<Bf16>::run(kt[m], e == 0 ? f[ct].c : e == 1 ? f[ct].b : f[ct].a, st[ct][m0 + m]);
-                        }
+                    for (int m = 0; m < MB; ++m) {
+                        if (e == 0)
+                            st[m0 + m] *= whole;
+                        st[m0 + m] = Mma<Bf16>::run(kt[m], e == 0 ? f.c : e == 1 ? f.b : f.a, st[m0 + m]);
+                    }
             }
             __builtin_amdgcn_sched_barrier(0);
             request(min(i + 1, chunks - 1));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    write_out(p, s, i * kChunk + 16 * t, p0 + 16 * ct, sq[ct][t], sums[64 + 16 * t + c], u[ct],
-                              w_of(at.x, t, 0, lane), w_of(at.x, t, 1, lane));
+                write_out(p, s, i * kChunk + 16 * t, p0, sq[t], sums[64 + 16 * t + c], u, w_of(at.x, t, 0, lane),
+                          w_of(at.x, t, 1, lane));
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
-            by_tokens<N, MT, 1, CT>(p, s, i * kChunk, p0, 8 * g, 0, st, box);
+            by_tokens<N, MT, 1>(p, s, i * kChunk, p0, 8 * g, 0, st, nullptr);
             reach = INFINITY;
             request(min(i + 1, chunks - 1));
         }
@@ -1186,7 +1153,7 @@ __global__ void __launch_bounds__(64 * WC, N == 256 ? 2 : N == 128 ? 3 : 4) ssu_
         place();
         __syncthreads();
     }
-    load_state<N, MT, CT>(p, s, p0, 8 * g, st, true);
+    load_state<N>(p, s, p0, 8 * g, st, true);
 }
 
 using StepFn = void (*)(StepParams);
@@ -1229,10 +1196,10 @@ constexpr ChunkKernel narrow_kernel()
     return {&ssu_delta_narrow_kernel<N, WN>, WN + 4, 16};
 }
 
-template <int N, int WC, int CT>
+template <int N>
 constexpr ChunkKernel wide_kernel()
 {
-    return {&ssu_delta_wide_kernel<N, WC, CT>, WC, 16 * CT * WC};
+    return {&ssu_delta_wide_kernel<N>, kWideWaves, 16 * kWideWaves};
 }
 
 // tiles: of 16 columns, of all sequences and heads. More than two for each compute unit
@@ -1246,12 +1213,12 @@ ChunkKernel chunk_kernel(int N, int64_t tiles)
 {
     const bool many = tiles > 2 * kNumCUs;
     if (N <= 32)
-        return many ? wide_kernel<32, 4, 1>() : narrow_kernel<32, 1>();
+        return many ? wide_kernel<32>() : narrow_kernel<32, 1>();
     if (N == 64)
-        return many ? wide_kernel<64, 4, 1>() : narrow_kernel<64, 2>();
+        return many ? wide_kernel<64>() : narrow_kernel<64, 2>();
     if (N == 128)
-        return many ? wide_kernel<128, 4, 1>() : narrow_kernel<128, 4>();
-    return many ? wide_kernel<256, 4, 1>() : narrow_kernel<256, 4>();
+        return many ? wide_kernel<128>() : narrow_kernel<128, 4>();
+    return many ? wide_kernel<256>() : narrow_kernel<256, 4>();
 }
 
 // ------------------------------------------------------------------ host --
