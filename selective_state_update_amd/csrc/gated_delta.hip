@@ -455,9 +455,11 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
     // D (|S| + 32 K' |u|) at most, a sum of N products of it with k or q 16 K or 16 Q times
     // that, and out |scale| / |q| times it. Of |S| that is 16 D W, of |r| 2^15 X D W K' (what an
     // inverse length of at most 1000 takes u to is less), W = max(1, K, Q, Q |scale| / |q|).
+    // r has 2^10 less than that, and up to 8 times what is looked at.
     const float xs = largest(x00, largest(x10, largest(x11, 0.0f))), unit = fabsf(a.scale) * lq[wave][tok];
-    float K = 0x1p12f, W = 0x1p22f, X = 0x1p10f, D = 1.0f;  // where no decay grows and all are at most so
-    if (!__all(!(in && decay > 0.0f) && kk <= K * K && qq <= K * K && xs <= X && unit <= 0x1p10f)) {
+    // where no decay grows, K, Q <= 2^12, X, |scale| / |q| <= 2^10
+    f32x4 limits = {whole, p.normalize ? 0x1p65f : 0x1p53f, 0x1p96f, 0x1p88f};
+    if (!__all(!(in && decay > 0.0f) && kk <= 0x1p24f && qq <= 0x1p24f && xs <= 0x1p10f && unit <= 0x1p10f)) {
         auto of_wave = [](float x) {
 #pragma unroll
             for (int m = 32; m >= 1; m /= 2)
@@ -468,21 +470,23 @@ __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaPara
 #pragma unroll
         for (int m = 1; m < 32; m *= 2)
             low = fminf(low, __shfl_up(low, m, 32));
-        D = __builtin_amdgcn_exp2f(of_wave(larger(static_cast<float>(sum) - low, 0.0f)));
-        X = of_wave(larger(xs, 0x1p-10f));  // (r stays finite)
-        K = sqrtf(of_wave(larger(kk, 1.0f)));
-        W = larger(K, sqrtf(of_wave(qq)) * of_wave(larger(unit, 1.0f)));
+        const float D = __builtin_amdgcn_exp2f(of_wave(larger(static_cast<float>(sum) - low, 0.0f)));
+        const float X = of_wave(larger(xs, 0x1p-10f));  // (r stays finite)
+        const float K = sqrtf(of_wave(larger(kk, 1.0f))), normed = p.normalize ? 1.0f : K;
+        const float W = larger(K, sqrtf(of_wave(qq)) * of_wave(larger(unit, 1.0f)));
+        limits[1] = 0x1p112f / (0x1p15f * X * D * W * normed);
+        limits[2] = 0x1p122f / (16.0f * D * W);
+        limits[3] = 0x1p13f * normed * D * X * limits[1];
     }
-    const float normed = p.normalize ? 1.0f : K, most = 0x1p112f / (0x1p15f * X * D * W * normed);
+    limits[1] = finite ? limits[1] : -1.0f;
     float *const s = reinterpret_cast<float *>(out + kSumsAt);
     if (lane < 32) {
         s[lane] = kept;
         s[32 + lane] = late;
         s[64 + lane] = asked;
     }
-    // (r: 2^10 less than it could be, and up to 8 times what is looked at)
     if (lane == 0)
-        *reinterpret_cast<f32x4 *>(s + 96) = f32x4{whole, finite ? most : -1.0f, 0x1p122f / (16.0f * D * W), 0x1p13f * normed * D * X * most};
+        *reinterpret_cast<f32x4 *>(s + 96) = limits;
 }
 
 // Where a token's row of k and q in LDS has its 16-byte runs: exchanged by row, so that
@@ -906,9 +910,11 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
             sk[t] *= kept[t];
             most = largest(sk[t], largest(v[t], most));
         }
-        if (__any(!(reach <= limits.state)))
+        if (__any(!(reach <= limits.state))) {
             reach = largest(st);
-        bad[i & 1][wn] = __any(!(most <= limits.most && reach <= limits.state)) ? 1.0f : 0.0f;
+            most = reach <= limits.state ? most : INFINITY;
+        }
+        bad[i & 1][wn] = __any(!(most <= limits.most)) ? 1.0f : 0.0f;
         reach = fmaf(reach, whole, limits.gain);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -1105,10 +1111,12 @@ __global__ void __launch_bounds__(64 * kWideWaves, N == 256 ? 2 : N == 128 ? 3 :
         }
         solve(xf, r, u);
         const Limits limits = limits_of(sums);
-        if (__any(!(reach <= limits.state)))
+        if (__any(!(reach <= limits.state))) {
             reach = largest(st);
+            most = reach <= limits.state ? most : INFINITY;
+        }
         __builtin_amdgcn_sched_barrier(0);
-        if (__builtin_expect(__all(most <= limits.most && reach <= limits.state), 1)) {
+        if (__builtin_expect(__all(most <= limits.most), 1)) {
             // the state behind the chunk
             const float whole = limits.whole;
             reach = fmaf(reach, whole, limits.gain);
