@@ -501,14 +501,26 @@ __global__ void __launch_bounds__(64 * W, D <= 128 ? 2 : 1) ssu_attn_split_kerne
 
         // An infinity in V, times a weight's remainder or a weight that 16 bits round to
         // 0, is not what the formula has: such a wave's sums are taken again with whole
-        // weights, token by token (the check costs a call 0.2 to 1 us).
+        // weights, token by token (the check costs a call 0.2 to 1 us). A row whose weights
+        // add up to NaN is NaN whatever V holds.
         f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 zero[i] = fmaf(o[e][i], 0.0f, zero[i]);
-        if (__any((zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f)) {
+        bool again = (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f;
+        if (__any(again)) {
+            float sum = l + __shfl_xor(l, 16);
+            sum += __shfl_xor(sum, 32);
+            again = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float own = __shfl(sum, 4 * g + i);
+                again |= zero[i] != 0.0f && own == own;
+            }
+        }
+        if (__any(again)) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 o[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};

@@ -66,3 +66,25 @@ def test_time_of_nan(ssu, row):
     finite = least_time(lambda: c.run(ssu, workspace=ws))
     c.q[1 if row == "padding" else 0] = NAN
     assert least_time(lambda: c.run(ssu, workspace=ws)) <= 4 * finite
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("D,tokens", [(64, 400), (128, 12000), (256, 3000)])
+def test_time_of_nan_among_own_tokens(ssu, D, tokens, shared):
+    """The same for a request's own tokens, here and in paged_attention, in a workgroup of its own and in several."""
+    c = Case([5, tokens, 9], 100, 4, 2, D, seed=2)
+    ws = workspace(ssu, c)
+
+    def call():
+        if shared:
+            return c.run(ssu, workspace=ws)
+        return ssu.paged_attention(c.q, c.kc, c.vc, c.table, c.lens, scale=c.scale, out=c.out, return_lse=True, workspace=ws)
+
+    finite, clean = least_time(call), [x.clone() for x in call()]
+    c.q[1, 2, 3] = NAN
+    slow = least_time(call)
+    out, lse = call()
+    assert out[1, 2].isnan().all() and lse[1, 2].isnan()
+    out[1, 2], lse[1, 2] = clean[0][1, 2], clean[1][1, 2]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+    assert slow <= 4 * finite, (slow, finite)
