@@ -639,7 +639,9 @@ ssu_status ssu_shared_prefix_attention(const ssu_shared_args *args, hipStream_t 
  *
  * fp32 throughout (the norm takes s before it is rounded into the residual),
  * each output rounded once, to nearest even. Rows whose squares add up beyond
- * fp32 become 0. A NaN in a row's s makes its y NaN, a NaN in y its group's scale and values.
+ * fp32 become 0; with eps 0, rows whose squares add up below its least normal number lose
+ * digits, and become infinities and NaN where that sum is 0. A NaN in a row's s makes its
+ * y NaN, a NaN in y its group's scale and values.
  */
 typedef struct ssu_norm_args {
     int64_t ntokens;    /* T >= 0 (0: no-op) */

@@ -246,7 +246,7 @@ __device__ __forceinline__ float unless_finite(const f32x4 &x, float zero)
 // substitution (a product of powers would lose digits to keys that repeat), a column
 // per lane; the tile below them is -X11 L10 X00, in fp32 matrix products, taken
 // transposed so that it too comes out as a fragment. 16384 tokens, 32 heads of 128
-// (16 of keys): 65 us for 268 MB, which a copy moves in 42; between the two are the vector
+// (16 of keys): 62 us for 268 MB, which a copy moves in 42; between the two are the vector
 // instructions of the splitting, the decays and the substitution.
 template <int N>
 __global__ void __launch_bounds__(256, 2) ssu_delta_pairs_kernel(const DeltaParams p)
@@ -682,7 +682,7 @@ __device__ __forceinline__ void write_out(const DeltaParams &p, const Stretch &s
 // columns out; their shares of S k are added up through LDS, one barrier a chunk, and what
 // follows every wave computes for itself. Two waves, a chunk behind, write out what u and the shares of S q
 // give for a tile of 16 tokens each. Two more bring operands into LDS, requested three
-// chunks ahead. One prompt of 16384 tokens, 32 heads of 128 x 128: 530 us, 1 us a chunk,
+// chunks ahead. One prompt of 16384 tokens, 32 heads of 128 x 128: 535 us, 1 us a chunk,
 // about 2300 cycles of a chain wave's instructions, of which a wave alone on its SIMD starts one
 // in 5.6 cycles; with the N on two waves 695 us, on one 878 (both with the first kernel).
 template <int N, int WN>
@@ -968,7 +968,7 @@ __global__ void __launch_bounds__(64 * (WN + 4)) ssu_delta_narrow_kernel(const D
 // a chunk's operands, which go through one stage in LDS, requested while the chunk before is
 // worked on, two barriers a chunk: what covers a wave's waits is the other waves of its
 // SIMD, two to four of them, and the one stage is what leaves room for them. 16 prompts of up to
-// 2048 tokens, 32 heads of 128 x 128: 227 us. Two stages and two waves took 298, eight
+// 2048 tokens, 32 heads of 128 x 128: 224 us. Two stages and two waves took 298, eight
 // waves to a stage 337, 32 columns to a wave 373. What bounds it: vector instructions
 // of three waves beside the matrix products (under which the clock falls to 1.7 GHz), and
 // at the end the longest prompt, alone.

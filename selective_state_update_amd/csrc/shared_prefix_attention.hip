@@ -349,7 +349,7 @@ struct PrefixPlan {
 
 // Pieces of the prefix, all of about the same length: as many as take the least time,
 // counted in ns. A workgroup takes its tiles one after the other, each D * (10 + waves
-// with rows) (D = 128: 1.5 us with one, 2.5 us with eight), and two more for its start and
+// with rows) (D = 128: 1.4 us with one, 2.3 with eight; about 1.5 and 2.5 measured), and two more for its start and
 // end, one workgroup to a compute unit; a piece more costs its sums, written and read at
 // 3.3 TB/s, and 0.2 us of the join. 64 requests of 32 heads (8 of keys), 8192 tokens: 4
 // pieces 115 us, 8 83, 16 70, 32 68, 64 85, the rule's 69; 2000 tokens: 37, 28, 27, 31, 31,
