@@ -447,7 +447,9 @@ ssu_status ssu_linear_attention_step(const ssu_linear_args *args, hipStream_t st
  * token, so that prompts leave the infinities and NaN that single steps leave: NaN and
  * infinite v reach their own and later tokens of their channel p only, NaN and
  * infinite k and beta their own and later tokens, NaN and infinite q their own
- * token. Such chunks take 20 to 100 times as long. The same call gives the same bits.
+ * token. (Where finite terms of a sum over n leave fp32 on the way, it depends on their
+ * order whether an infinity, NaN or a finite value comes of it, and prompts and steps
+ * add up in orders of their own.) Such chunks take 20 to 100 times as long. The same call gives the same bits.
  */
 typedef struct ssu_delta_args {
     int32_t batch;      /* sequences, >= 0 (0: no-op) */
